@@ -321,6 +321,143 @@ PA_API int pa_mixed_step(void *prefill_out, const void *prefill_query, const int
                          int num_blocks, float scale, pa_dtype dtype, int *d_err, void *stream);
 
 /*
+ * pa_rotary_and_cache -- rotate the new tokens' queries and keys by their
+ * positions and write keys and values into their slots: the step before
+ * attention, with pa_reshape_and_cache's cache write in it.  Positions are
+ * explicit and have num_axes coordinates (1 for text; time, height and width
+ * for images and video), so they need not be the tokens' places in the cache.
+ *   angle(t, i) = positions[pair_axis[i]][t] * inv_freq[i],   i < rot_dim / 2
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * where pair i of a head is its dimensions (i, rot_dim/2 + i), or (2i, 2i + 1)
+ * when `interleaved` is non-zero; dimensions from rot_dim on pass unchanged.
+ * The angle is reduced to one turn in 64-bit fixed point (no digits are lost
+ * to a far position), the rotation is fp32, each result is rounded once.
+ *
+ *   query, query_out  [num_tokens][num_heads][head_dim] dtype; query_out may be
+ *                     query itself (same pointer and stride) but must not
+ *                     overlap it otherwise, nor key, value or the caches
+ *   key, value     [num_tokens][num_kv_heads][head_dim] dtype
+ *   *_stride       elements from one token's row to the next, a multiple of 8
+ *                  and at least a row's elements (so slices of one fused
+ *                  projection can be passed as they are); heads are contiguous
+ *   positions      int32 [num_axes][num_tokens], any sign
+ *   slot_mapping   as for pa_reshape_and_cache; a token whose slot is negative
+ *                  still gets its query_out row
+ *   inv_freq       float [rot_dim / 2] (device), finite
+ *   pair_axis      int [rot_dim / 2] in HOST memory, or NULL for axis 0 throughout
+ * Supported: head_dim a multiple of 16 up to 256, rot_dim a multiple of 16 up
+ * to head_dim (0: a plain cache write), up to 8 axes, any block_size.
+ * num_tokens == 0 is a no-op.  The cache write of the values is bit-exact.
+ */
+PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
+                               const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+                               void *k_cache, void *v_cache, const int32_t *positions, const int64_t *slot_mapping,
+                               const float *inv_freq, const int *pair_axis, int num_axes, int rot_dim, int interleaved,
+                               int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                               int num_blocks, pa_dtype dtype, int *d_err, void *stream);
+
+/*
+ * pa_decode_weights -- pa_decode that also adds up how much attention each
+ * cached token receives, the totals pa_evict chooses by:
+ *   weights_out[r][kvh][j] = weights[r][kvh][j] + sum softmax_j(...)
+ * over row r's queries and the query heads of kv head kvh, for every j below
+ * the longest of the row's contexts; entries from there on are left as they
+ * are.  out as from pa_decode (the same kernels and partitions; equal to it up
+ * to rounding).
+ *   weights, weights_out  float [num_seqs / queries_per_row][num_kv_heads]
+ *                  [weights_len]; weights_out may be weights itself, else the
+ *                  two must not overlap
+ *   weights_len    >= max_context_len
+ *   queries_per_row  consecutive sequences r*queries_per_row .. that add to one
+ *                  row: 1 for plain decode; several query positions over one
+ *                  cache (the last positions of a prompt observing it, several
+ *                  new tokens at once) repeat the sequence's block-table row,
+ *                  each with its own context length
+ *   workspace      >= pa_decode_weights_workspace_bytes(...) bytes, 256-byte
+ *                  aligned, scratch: the partials, and every score in fp32
+ *                  (num_seqs * num_heads * max_context_len * 4 bytes)
+ * The weights are fp32 from fp32 scores; sums run in a fixed order.  Keys that
+ * an invalid table entry leaves out of the softmax weigh 0.  Shapes,
+ * partition_tokens, data errors as for pa_decode.
+ */
+PA_API size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                int block_size, int max_context_len, int partition_tokens);
+PA_API int pa_decode_weights(void *out, const void *query, const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                             int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, int max_context_len, float scale, int partition_tokens,
+                             const float *weights, float *weights_out, int weights_len, int queries_per_row,
+                             pa_dtype dtype, void *workspace, size_t workspace_bytes, int *d_err, void *stream);
+
+/*
+ * pa_evict -- cut sequences' caches down to `keep` tokens by their accumulated
+ * attention weight.  Each kv head of a sequence of L tokens chooses for itself:
+ * n = min(L, keep); when L > keep it keeps its first `sink` tokens, its last
+ * `recent`, and of those between the keep - sink - recent with the largest
+ * weights (the lower index first among equals; NaN counts as the least), else
+ * all of them.  The kept tokens keep their order:
+ *   kept[s][h][i]     index of the i-th kept token (int32; -1 from n to keep)
+ *   new K/V row i     = K/V row kept[s][h][i], bit-exact, in the blocks of the
+ *                     sequence's row of new_block_tables; rows past n in the
+ *                     last block are left as they are
+ *   new_weights[s][h][i] = weights[s][h][kept[s][h][i]], 0 from n to weights_len
+ *   new_context_lens[s] = n
+ * The old blocks are only read (other sequences may share them); the caller
+ * drops them afterwards (pa_bm_evict_sequence).  Tokens keep the positions they
+ * were rotated with, so a later token's position is no longer its index.
+ *   weights, new_weights  float [num_seqs][num_kv_heads][weights_len], not
+ *                  overlapping; weights_len >= max_context_len
+ *   block_tables   int32 [num_seqs][max_blocks_per_seq], context_lens int32
+ *   new_block_tables  int32 [num_seqs][new_max_blocks_per_seq], which must hold
+ *                  min(keep, max_context_len) tokens; the entries of a row past
+ *                  ceil(n / block_size) are never read.  A new block named twice, or
+ *                  that one of the call's sequences still reads, sets
+ *                  PA_DEVERR_COPY_PAIR and is not written
+ *   new_context_lens  must not be context_lens
+ *   workspace      >= pa_evict_workspace_bytes(num_blocks) bytes, 16-byte
+ *                  aligned, scratch; its content on entry is ignored
+ * Needs sink + recent <= keep and keep >= 1.  Supported: head_dim in {64, 128},
+ * block_size in {8, 16, 32, 64, 128}.  Invalid lengths are clamped and flagged
+ * as in pa_decode; a row whose old table entry is out of the pool is flagged
+ * and not written.
+ */
+PA_API size_t pa_evict_workspace_bytes(int num_blocks);
+PA_API int pa_evict(void *k_cache, void *v_cache, const float *weights, float *new_weights, int weights_len,
+                    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                    const int32_t *new_block_tables, int new_max_blocks_per_seq, int32_t *new_context_lens,
+                    int32_t *kept, int num_seqs, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                    int max_context_len, int keep, int sink, int recent, pa_dtype dtype, void *workspace,
+                    size_t workspace_bytes, int *d_err, void *stream);
+
+/*
+ * pa_decode_common_prefix -- pa_decode_shared_prefix for groups of any size: a
+ * whole batch behind one long system prompt, tens of samples of a prompt.  The
+ * prefix is attended once for the whole group on the tensor cores, with the
+ * group's queries (group_size times the heads of a kv head) as rows, each
+ * sequence's own tokens as in pa_decode, and the partials are merged.
+ * Arguments, layout and data errors as for pa_decode_shared_prefix (an invalid
+ * entry among a group's prefix blocks is flagged and that group's outputs are
+ * undefined), and:
+ *   group_size     any divisor of num_seqs
+ *   scale          finite and > 0
+ *   partition_tokens  splits the sequences' own tokens (0 = automatic)
+ *   workspace      >= pa_decode_common_prefix_workspace_bytes(...) bytes,
+ *                  256-byte aligned, scratch (needs no clearing)
+ * Supported: head_dim 128, block_size in {16, 32, 64, 128}, num_heads /
+ * num_kv_heads in {1, 2, 4, 8}.  The softmax weights of prefix keys are rounded
+ * to dtype for their product with V, as in pa_prefill_chunk.
+ */
+PA_API size_t pa_decode_common_prefix_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                      int block_size, int max_context_len, int group_size,
+                                                      int prefix_blocks, int partition_tokens);
+PA_API int pa_decode_common_prefix(void *out, const void *query, const void *k_cache, const void *v_cache,
+                                   const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                   int num_seqs, int group_size, int prefix_blocks, int num_heads, int num_kv_heads,
+                                   int head_dim, int block_size, int num_blocks, int max_context_len, float scale,
+                                   int partition_tokens, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   int *d_err, void *stream);
+
+/*
  * Failure detection.  Every wait inside the kernels (on TMA copies, MMA
  * completions, other warps) is bounded: after pa_bounded_wait_polls() polls
  * it gives up, ORs PA_DEVERR_TIMEOUT into *d_err and lets the kernel finish,
@@ -468,6 +605,14 @@ PA_API size_t pa_prefill_workspace_bytes(int num_seqs, int total_chunk_len, int 
  *       tree stay cached (reusable) until evicted; the others are free.
  *       Allocation evicts the least recently released cached leaf block when
  *       no free block is left.
+ *   pa_bm_evict_sequence(m, seq_id, new_len)
+ *       the sequence keeps new_len tokens in fresh private blocks (for
+ *       pa_evict: read the old table first, then call this, then read the new
+ *       one) and drops its references to the old ones, whose contents stay
+ *       valid until work enqueued after the copy writes them.  Its blocks no
+ *       longer spell a prefix, so none of them joins the prefix tree.
+ *       PA_ERR_OUT_OF_RANGE unless 0 <= new_len <= the length; PA_ERR_NO_BLOCKS
+ *       (the sequence unchanged) when the pool runs out.
  *   pa_bm_block_table(m, seq_id, out, max_blocks) -> number of blocks, or
  *       PA_ERR_OUT_OF_RANGE if max_blocks is too small.
  *   pa_bm_seq_len, pa_bm_block_refcount, pa_bm_stats: introspection.  The
@@ -486,6 +631,7 @@ PA_API int pa_bm_fork(pa_block_manager *m, int64_t parent_id, int64_t child_id);
 PA_API int pa_bm_append_token(pa_block_manager *m, int64_t seq_id, int32_t token, int64_t *slot,
                               int64_t *copy_src, int64_t *copy_dst);
 PA_API int pa_bm_free_sequence(pa_block_manager *m, int64_t seq_id);
+PA_API int pa_bm_evict_sequence(pa_block_manager *m, int64_t seq_id, int new_len);
 PA_API int pa_bm_block_table(const pa_block_manager *m, int64_t seq_id, int32_t *out, int max_blocks);
 PA_API int64_t pa_bm_seq_len(const pa_block_manager *m, int64_t seq_id);
 PA_API int pa_bm_block_refcount(const pa_block_manager *m, int block);

@@ -71,6 +71,11 @@ class BlockManager:
     def free_sequence(self, seq_id: int) -> None:
         self._check("pa_bm_free_sequence", self._L.pa_bm_free_sequence(self._h, int(seq_id)))
 
+    def evict_sequence(self, seq_id: int, new_len: int) -> None:
+        """Keep ``new_len`` tokens in fresh private blocks (for ``pa_evict``: read
+        the old table first, call this, then read the new one)."""
+        self._check("pa_bm_evict_sequence", self._L.pa_bm_evict_sequence(self._h, int(seq_id), int(new_len)))
+
     def block_table(self, seq_id: int) -> np.ndarray:
         n = self.seq_len(seq_id)
         cap = max(1, -(-n // self.block_size))

@@ -9,6 +9,7 @@ loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -30,7 +31,10 @@ EXPORTED = ("pa_status_string", "pa_reshape_and_cache", "pa_decode_partition_tok
             "pa_bm_create", "pa_bm_destroy", "pa_bm_add_sequence", "pa_bm_fork", "pa_bm_append_token",
             "pa_bm_free_sequence", "pa_bm_block_table", "pa_bm_seq_len", "pa_bm_block_refcount",
             "pa_bm_stats", "pa_prefill_batch", "pa_decode_step_host_staging_bytes", "pa_decode_step_host",
-            "pa_mixed_step", "pa_mixed_step_workspace_bytes", "pa_bounded_wait_polls", "pa_selftest_bounded_wait")
+            "pa_mixed_step", "pa_mixed_step_workspace_bytes", "pa_bounded_wait_polls", "pa_selftest_bounded_wait",
+            "pa_rotary_and_cache", "pa_decode_weights_workspace_bytes", "pa_decode_weights",
+            "pa_evict_workspace_bytes", "pa_evict", "pa_decode_common_prefix_workspace_bytes",
+            "pa_decode_common_prefix", "pa_bm_evict_sequence")
 PA_ERR_NO_BLOCKS = -8
 PA_ERR_SCRATCH_LIMIT = -7
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -114,6 +118,23 @@ def lib() -> ctypes.CDLL:
         L.pa_mixed_step.restype = i
         L.pa_mixed_step_workspace_bytes.argtypes = [i] * 9
         L.pa_mixed_step_workspace_bytes.restype = sz
+        f = ctypes.c_float
+        L.pa_rotary_and_cache.argtypes = [p, i64, p, i64, p, i64, p, i64, p, p, p, p, p, p] + [i] * 10 + [p, p]
+        L.pa_rotary_and_cache.restype = i
+        L.pa_decode_weights_workspace_bytes.argtypes = [i] * 7
+        L.pa_decode_weights_workspace_bytes.restype = sz
+        L.pa_decode_weights.argtypes = [p, p, p, p, p, i, p, i, i, i, i, i, i, i, f, i, p, p, i, i, i, p, sz, p, p]
+        L.pa_decode_weights.restype = i
+        L.pa_evict_workspace_bytes.argtypes = [i]
+        L.pa_evict_workspace_bytes.restype = sz
+        L.pa_evict.argtypes = [p, p, p, p, i, p, i, p, p, i, p, p] + [i] * 10 + [p, sz, p, p]
+        L.pa_evict.restype = i
+        L.pa_decode_common_prefix_workspace_bytes.argtypes = [i] * 9
+        L.pa_decode_common_prefix_workspace_bytes.restype = sz
+        L.pa_decode_common_prefix.argtypes = [p, p, p, p, p, i, p, i, i, i, i, i, i, i, i, i, f, i, i, p, sz, p, p]
+        L.pa_decode_common_prefix.restype = i
+        L.pa_bm_evict_sequence.argtypes = [p, i64, i]
+        L.pa_bm_evict_sequence.restype = i
         L.pa_bounded_wait_polls.argtypes = []
         L.pa_bounded_wait_polls.restype = i
         L.pa_selftest_bounded_wait.argtypes = [i, p, p, p]
@@ -461,3 +482,220 @@ def pa_prefill_batch(out, query, k_cache, v_cache, block_tables, prefix_lens, ch
                                 block_tables.shape[1], pl.ctypes.data, cl.ctypes.data, n, Hq, Hkv, D, bs, NB,
                                 float(scale), _dt(query), wp, wb, _ptr(d_err), _stream(query, stream))
     _check("pa_prefill_batch", rc)
+
+
+# ---- bounded and shared caches -------------------------------------------------
+
+def _same_device(*ts):
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensor must be on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _on(device):
+    """Make ``device`` current for a call (a no-op object when it already is)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _scratch(device, nbytes, stream):
+    """A uint8 workspace; one made for a call on a given stream stays reserved
+    until that stream is done with it."""
+    w = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        w.record_stream(stream)
+    return w
+
+
+def _token_rows(name, t, heads, head_dim):
+    """Check that ``t`` is [T][heads][head_dim] with contiguous heads; its token stride."""
+    if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
+        raise ValueError(f"{name}: shape mismatch")
+    if (head_dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def pa_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
+                        pair_axis=None, interleaved=False, d_err=None, stream=None):
+    """Rotate queries and keys and write keys and values into their slots.
+    query/query_out [T][Hq][D], key/value [T][Hkv][D] (token rows may be strided,
+    e.g. slices of one projection; query_out may be query); caches [NB][Hkv][bs][D];
+    positions int32 [axes][T] (or [T] for one axis); slot_mapping int64 [T];
+    inv_freq float32 [rot_dim / 2]; pair_axis: host ints [rot_dim / 2], the axis of
+    each pair (None: axis 0)."""
+    dev = _same_device(k_cache, query_out, query, key, value, v_cache, positions, slot_mapping, inv_freq, d_err)
+    _dev(k_cache, v_cache, positions, slot_mapping, inv_freq, d_err)
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if positions.dtype != torch.int32:
+        raise TypeError("positions must be int32")
+    if inv_freq.dtype != torch.float32:
+        raise TypeError("inv_freq must be float32")
+    if not (query_out.dtype == query.dtype == key.dtype == value.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("dtype mismatch")
+    NB, Hkv, bs, D = k_cache.shape
+    T, Hq = query.shape[0], query.shape[1]
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if v_cache.shape != k_cache.shape or query_out.shape[0] != T or key.shape[0] != T or value.shape[0] != T or \
+            slot_mapping.shape != (T,) or positions.dim() not in (1, 2) or positions.shape[-1] != T or \
+            inv_freq.dim() != 1:
+        raise ValueError("shape mismatch")
+    strides = (_token_rows("query_out", query_out, Hq, D), _token_rows("query", query, Hq, D),
+               _token_rows("key", key, Hkv, D), _token_rows("value", value, Hkv, D))
+    half = inv_freq.shape[0]
+    ax = None
+    if pair_axis is not None:
+        ax = np.ascontiguousarray(pair_axis, dtype=np.int32)
+        if ax.shape != (half,):
+            raise ValueError("pair_axis must name an axis for every pair")
+    with _on(dev):
+        rc = lib().pa_rotary_and_cache(
+            _ptr(query_out), strides[0], _ptr(query), strides[1], _ptr(key), strides[2], _ptr(value), strides[3],
+            _ptr(k_cache), _ptr(v_cache), _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq),
+            ax.ctypes.data if ax is not None and half else None, axes, 2 * half, 1 if interleaved else 0, T, Hq, Hkv,
+            D, bs, NB, _dt(k_cache), _ptr(d_err), _stream(k_cache, stream))
+    _check("pa_rotary_and_cache", rc)
+
+
+def pa_decode_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                      partition_tokens=0) -> int:
+    return lib().pa_decode_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                   max_context_len, partition_tokens)
+
+
+def decode_weights_workspace(query, num_kv_heads, block_size, max_context_len, partition_tokens=0, queries_per_row=1,
+                             stream=None):
+    """Allocate (with torch) a workspace big enough for ``pa_decode_weights``
+    (whatever the number of queries per row of totals)."""
+    B, Hq, D = query.shape
+    with _on(query.device):
+        n = pa_decode_weights_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, partition_tokens)
+    return _scratch(query.device, n, stream)
+
+
+def pa_decode_weights(out, query, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, weights,
+                      weights_out=None, queries_per_row=1, partition_tokens=0, workspace=None, d_err=None,
+                      stream=None):
+    """``pa_decode`` that adds each cached token's attention weight to a total:
+    weights float32 [B / queries_per_row][Hkv][W], W >= max_context_len, updated
+    in place unless ``weights_out`` (of the same shape) is given."""
+    if weights_out is None:
+        weights_out = weights
+    dev = _same_device(query, out, k_cache, v_cache, block_tables, context_lens, weights, weights_out, workspace, d_err)
+    _dev(out, query, k_cache, v_cache, block_tables, context_lens, weights, weights_out, workspace, d_err)
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if weights.dtype != torch.float32 or weights_out.dtype != torch.float32:
+        raise TypeError("weights must be float32")
+    NB, Hkv, bs, D = k_cache.shape
+    B, Hq, Dq = query.shape
+    if queries_per_row < 1 or B % queries_per_row:
+        raise ValueError("the number of sequences must be a multiple of queries_per_row")
+    if Dq != D or v_cache.shape != k_cache.shape or out.shape != query.shape or block_tables.dim() != 2 or \
+            block_tables.shape[0] != B or context_lens.shape != (B,) or weights.dim() != 3 or \
+            weights.shape[:2] != (B // queries_per_row, Hkv) or weights_out.shape != weights.shape:
+        raise ValueError("shape mismatch")
+    if not (out.dtype == query.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("dtype mismatch")
+    if workspace is None:
+        workspace = decode_weights_workspace(query, Hkv, bs, max_context_len, partition_tokens, stream=stream)
+    with _on(dev):
+        rc = lib().pa_decode_weights(
+            _ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+            _ptr(context_lens), B, Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), int(partition_tokens),
+            _ptr(weights), _ptr(weights_out), weights.shape[2], int(queries_per_row), _dt(query), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(d_err), _stream(query, stream))
+    _check("pa_decode_weights", rc)
+
+
+def evict_workspace(k_cache, num_seqs=0, keep=0, stream=None):
+    """Allocate (with torch) a workspace for ``pa_evict`` on this pool (its size
+    depends on the pool alone)."""
+    return _scratch(k_cache.device, lib().pa_evict_workspace_bytes(k_cache.shape[0]), stream)
+
+
+def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_context_lens, new_weights,
+             kept, keep, sink, recent, max_context_len, workspace=None, d_err=None, stream=None):
+    """Cut every sequence down to its ``keep`` tokens of the largest totals (the
+    first ``sink`` and last ``recent`` always kept), per kv head, into the blocks
+    of ``new_block_tables``.  weights/new_weights float32 [B][Hkv][W]; kept int32
+    [B][Hkv][keep]; tables int32 [B][MB]; context_lens/new_context_lens int32 [B]."""
+    dev = _same_device(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_context_lens,
+                       new_weights, kept, workspace, d_err)
+    _dev(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_context_lens, new_weights, kept,
+         workspace, d_err)
+    for t in (block_tables, context_lens, new_block_tables, new_context_lens, kept):
+        if t.dtype != torch.int32:
+            raise TypeError("tables, lengths and kept must be int32")
+    if weights.dtype != torch.float32 or new_weights.dtype != torch.float32:
+        raise TypeError("weights must be float32")
+    if k_cache.dtype != v_cache.dtype:
+        raise TypeError("dtype mismatch")
+    NB, Hkv, bs, D = k_cache.shape
+    B = context_lens.shape[0]
+    if v_cache.shape != k_cache.shape or weights.dim() != 3 or weights.shape[:2] != (B, Hkv) or \
+            new_weights.shape != weights.shape or kept.shape != (B, Hkv, keep) or block_tables.dim() != 2 or \
+            block_tables.shape[0] != B or new_block_tables.dim() != 2 or new_block_tables.shape[0] != B or \
+            context_lens.shape != (B,) or new_context_lens.shape != (B,):
+        raise ValueError("shape mismatch")
+    if workspace is None:
+        workspace = evict_workspace(k_cache, stream=stream)
+    with _on(dev):
+        rc = lib().pa_evict(
+            _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(new_weights), weights.shape[2], _ptr(block_tables),
+            block_tables.shape[1], _ptr(context_lens), _ptr(new_block_tables), new_block_tables.shape[1],
+            _ptr(new_context_lens), _ptr(kept), B, Hkv, D, bs, NB, int(max_context_len), int(keep), int(sink),
+            int(recent), _dt(k_cache), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(d_err),
+            _stream(k_cache, stream))
+    _check("pa_evict", rc)
+
+
+def pa_decode_common_prefix_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                            group_size, prefix_blocks, partition_tokens=0) -> int:
+    return lib().pa_decode_common_prefix_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                         max_context_len, group_size, prefix_blocks, partition_tokens)
+
+
+def decode_common_prefix_workspace(query, num_kv_heads, block_size, max_context_len, group_size, prefix_blocks,
+                                   partition_tokens=0, stream=None):
+    """Allocate (with torch) a workspace big enough for ``pa_decode_common_prefix``."""
+    B, Hq, D = query.shape
+    with _on(query.device):
+        n = pa_decode_common_prefix_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, group_size,
+                                                    prefix_blocks, partition_tokens)
+    return _scratch(query.device, n, stream)
+
+
+def pa_decode_common_prefix(out, query, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
+                            group_size, prefix_blocks, partition_tokens=0, workspace=None, d_err=None, stream=None):
+    """``pa_decode`` for batches whose consecutive groups of ``group_size``
+    sequences (any size) share their first ``prefix_blocks`` physical blocks."""
+    dev = _same_device(query, out, k_cache, v_cache, block_tables, context_lens, workspace, d_err)
+    _dev(out, query, k_cache, v_cache, block_tables, context_lens, workspace, d_err)
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    NB, Hkv, bs, D = k_cache.shape
+    B, Hq, Dq = query.shape
+    if Dq != D or v_cache.shape != k_cache.shape or out.shape != query.shape or block_tables.dim() != 2 or \
+            block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("shape mismatch")
+    if not (out.dtype == query.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("dtype mismatch")
+    if workspace is None:
+        workspace = decode_common_prefix_workspace(query, Hkv, bs, max_context_len, group_size, prefix_blocks,
+                                                   partition_tokens, stream=stream)
+    with _on(dev):
+        rc = lib().pa_decode_common_prefix(
+            _ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+            _ptr(context_lens), B, int(group_size), int(prefix_blocks), Hq, Hkv, D, bs, NB, int(max_context_len),
+            float(scale), int(partition_tokens), _dt(query), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(d_err), _stream(query, stream))
+    _check("pa_decode_common_prefix", rc)

@@ -30,6 +30,7 @@
 #include <list>
 #include <map>
 #include <memory>
+#include <new>
 #include <unordered_map>
 #include <vector>
 
@@ -256,6 +257,37 @@ int pa_bm_free_sequence(pa_block_manager *m, int64_t seq_id) {
     const auto &blocks = it->second.blocks;
     for (auto b = blocks.rbegin(); b != blocks.rend(); ++b) m->release(*b);
     m->seqs.erase(it);
+    return PA_OK;
+}
+
+int pa_bm_evict_sequence(pa_block_manager *m, int64_t seq_id, int new_len) {
+    if (!m) return PA_ERR_INVALID_ARG;
+    auto it = m->seqs.find(seq_id);
+    if (it == m->seqs.end()) return PA_ERR_INVALID_ARG;
+    Seq &s = it->second;
+    if (new_len < 0 || new_len > s.len) return PA_ERR_OUT_OF_RANGE;
+    const int need = (int)(((int64_t)new_len + m->block_size - 1) / m->block_size);
+    std::vector<int32_t> fresh;
+    try {
+        fresh.reserve(need);  // so that nothing below can throw half way
+    } catch (const std::bad_alloc &) {
+        return PA_ERR_NO_BLOCKS;
+    }
+    for (int k = 0; k < need; ++k) {
+        const int32_t b = m->alloc();
+        if (b < 0) {
+            for (int32_t f : fresh) m->release(f);
+            return PA_ERR_NO_BLOCKS;
+        }
+        fresh.push_back(b);
+    }
+    for (auto b = s.blocks.rbegin(); b != s.blocks.rend(); ++b) m->release(*b);
+    s.blocks = std::move(fresh);
+    s.len = new_len;
+    // the kept tokens are not consecutive: no block of this sequence is a prefix's from here on
+    s.tail.clear();
+    s.node = nullptr;
+    s.chained = false;
     return PA_OK;
 }
 

@@ -128,10 +128,12 @@ struct WarpState {
 // One K/V tile: QK, online softmax update, PV.
 //   QK layout: lane = (qr, qc): K row step*STEP_ROWS + i*QRP + qr, chunks qc + cc*QL.
 //   PV layout: lane = (grp, c): V row step*STEP_ROWS + i*TPI + grp, chunk c.
-template <typename T, class C, int G>
+//   With kScores each owned score of a valid key also goes to scores[key][head].
+template <typename T, class C, int G, bool kScores>
 __device__ __forceinline__ void attend_tile(const unsigned char *Ks, const unsigned char *Vs, int nvalid,
                                             const float2 (&q2)[G][C::CPL][4], WarpState<G> &st,
-                                            float *pbuf, int lane, int idx0, int h_lane, bool owner) {
+                                            float *pbuf, int lane, int idx0, int h_lane, bool owner,
+                                            float *scores) {
     const int qr = lane / C::QL, qc = lane % C::QL;
     const int grp = lane / C::LPT, c = lane % C::LPT;
     const bool full = nvalid == C::TR;
@@ -170,6 +172,10 @@ __device__ __forceinline__ void attend_tile(const unsigned char *Ks, const unsig
             const int tok = step * C::STEP_ROWS + i * C::QRP + qr;
             sc[f] = (full || tok < nvalid) ? v[f] : -INFINITY;
             need |= sc[f] > st.m_mine + kRescaleThreshold;
+            if constexpr (kScores) {
+                // the warp's stores of one f cover whole 32-byte sectors
+                if (owner && (full || tok < nvalid)) scores[tok * G + h_lane] = v[f];
+            }
         }
         if (__any_sync(kFull, need)) {
             float mymax = sc[0];
@@ -253,7 +259,7 @@ __device__ __forceinline__ int unit_block(int j, int e0, int e1, const int32_t *
 template <int G>
 constexpr int decode_min_ctas() { return G <= 4 ? 3 : 2; }
 
-template <typename T, int D, int BS, int G, int NW, int S>
+template <typename T, int D, int BS, int G, int NW, int S, bool kScores = false>
 __global__ void __launch_bounds__(NW * 32, decode_min_ctas<G>()) decode_kernel(const DecodeParams p) {
     using C = DecodeCfg<D, BS, G, NW, S>;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -414,6 +420,8 @@ __global__ void __launch_bounds__(NW * 32, decode_min_ctas<G>()) decode_kernel(c
     st.l_mine = 0.f;
     bool timed_out = false;
     int consumed = 0;
+    float *scores = nullptr;  // of the unit's first token
+    if constexpr (kScores) scores = p.scores + ((size_t)(s * p.num_kv_heads + kvh) * p.score_stride + tok0) * G;
 
     // ---- step 3 (attend) over this warp's tiles
     for (int j = 0; j < ntile; ++j) {
@@ -427,7 +435,11 @@ __global__ void __launch_bounds__(NW * 32, decode_min_ctas<G>()) decode_kernel(c
         const int nvalid = min(C::TR, ntok - t * C::TR);
         if (sflag[sl]) {
             const unsigned char *Ks = ring + sl * C::STAGE_BYTES;
-            attend_tile<T, C, G>(Ks, Ks + C::TILE_BYTES, nvalid, q2, st, pbuf, lane, idx0, h_lane, owner);
+            attend_tile<T, C, G, kScores>(Ks, Ks + C::TILE_BYTES, nvalid, q2, st, pbuf, lane, idx0, h_lane, owner,
+                                          scores + (kScores ? t * C::TR * G : 0));
+        } else if constexpr (kScores) {
+            // a tile left out of the softmax: its keys weigh nothing
+            for (int i = lane; i < nvalid * G; i += 32) scores[t * C::TR * G + i] = -INFINITY;
         }
         __syncwarp();
         if (j + S < ntile) issue(j + S, sl);
@@ -520,6 +532,9 @@ __global__ void __launch_bounds__(NW * 32, decode_min_ctas<G>()) decode_kernel(c
             for (int e = 0; e < 8; ++e) o[e] *= inv;
             T *orow = static_cast<T *>(p.out) + row * D + ch * 8;
             *reinterpret_cast<uint4 *>(orow) = pack8<T>(o);
+            if constexpr (kScores) {
+                if (ch == 0) p.ws_ml[row * p.slots] = make_float2(M, lsum);
+            }
         } else {
             const size_t slot = row * p.slots + p.part_base + part;
             float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + slot * D + ch * 8);
@@ -587,19 +602,19 @@ __global__ void __launch_bounds__(128) decode_reduce_kernel(const DecodeParams p
 constexpr int kDecodeWarps = 4;
 constexpr int kDecodeStages = 2;
 
-template <typename T, int D, int BS, int G>
+template <typename T, int D, int BS, int G, bool kScores = false>
 int launch_decode_t(const DecodeParams &p, cudaStream_t stream) {
     constexpr int NW = kDecodeWarps;
     constexpr int S = kDecodeStages;
     using C = DecodeCfg<D, BS, G, NW, S>;
-    auto kern = decode_kernel<T, D, BS, G, NW, S>;
+    auto kern = decode_kernel<T, D, BS, G, NW, S, kScores>;
     static std::atomic<uint64_t> attr_done{0};
     if (ensure_smem_attr(kern, C::SMEM, attr_done) != PA_OK) return PA_ERR_CUDA;
     const long long units = (long long)p.max_partitions * p.num_seqs * p.num_kv_heads;
     if (units <= 0) return PA_OK;
     if (units > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
     if (launch_pdl(kern, dim3((unsigned)units), dim3(NW * 32), C::SMEM, stream, p) != cudaSuccess) return PA_ERR_CUDA;
-    if (p.max_partitions > 1 && !p.force_partials) {
+    if (!kScores && p.max_partitions > 1 && !p.force_partials) {
         const int pairs = p.num_seqs * p.num_heads;
         if (launch_pdl(decode_reduce_kernel<T, D>, dim3((pairs + 3) / 4), dim3(128), 0, stream, p) != cudaSuccess)
             return PA_ERR_CUDA;
@@ -618,12 +633,12 @@ int launch_reduce_dtype(int head_dim, const DecodeParams &p, cudaStream_t stream
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-template <typename T>
+template <typename T, bool kScores = false>
 int launch_decode_dtype(int head_dim, int block_size, int group, const DecodeParams &p,
                         cudaStream_t stream) {
 #define PA_DECODE_CASE(DD, BB, GG)                                           \
     if (head_dim == DD && block_size == BB && group == GG)                   \
-        return launch_decode_t<T, DD, BB, GG>(p, stream);
+        return launch_decode_t<T, DD, BB, GG, kScores>(p, stream);
 #define PA_DECODE_GROUPS(DD, BB) \
     PA_DECODE_CASE(DD, BB, 1) PA_DECODE_CASE(DD, BB, 2) PA_DECODE_CASE(DD, BB, 4) PA_DECODE_CASE(DD, BB, 8)
     PA_DECODE_GROUPS(128, 16)

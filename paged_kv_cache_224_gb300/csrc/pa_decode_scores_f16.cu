@@ -1,0 +1,8 @@
+// f16 instances of the CUDA-core decode that keeps its scores (pa_decode_weights).
+#include "pa_decode.cuh"
+
+namespace pa {
+int launch_decode_scores_f16(int head_dim, int block_size, int group, const DecodeParams &p, cudaStream_t stream) {
+    return launch_decode_dtype<__half, true>(head_dim, block_size, group, p, stream);
+}
+}  // namespace pa

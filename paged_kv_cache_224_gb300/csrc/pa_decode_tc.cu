@@ -42,7 +42,7 @@ namespace {
 
 using namespace tcd;
 
-template <typename T, int BS, int G>
+template <typename T, int BS, int G, bool kScores>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv) {
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     tc_fence_after();
     r.tmem = *r.tmem_holder;
-    tc_unit<T, BS, G, kSlotsStandalone>(p, &tmk, &tmv, u, r);
+    tc_unit<T, BS, G, kSlotsStandalone, kScores>(p, &tmk, &tmv, u, r);
     tc_drain<kSlotsStandalone>(r);
     tc_fence_before();
     __syncthreads();
@@ -87,9 +87,9 @@ bool make_pool_map4(CUtensorMap *map, const void *pool, const DecodeParams &p, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int BS, int G>
+template <typename T, int BS, int G, bool kScores>
 int launch_tc_t(const DecodeParams &p, cudaStream_t stream) {
-    auto kern = decode_tc_kernel<T, BS, G>;
+    auto kern = decode_tc_kernel<T, BS, G, kScores>;
     static std::atomic<uint64_t> attr_done{0};
     if (ensure_smem_attr(kern, TcLayout<kSlotsStandalone>::kSmemAlloc, attr_done) != PA_OK) return PA_ERR_CUDA;
     const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -105,35 +105,45 @@ int launch_tc_t(const DecodeParams &p, cudaStream_t stream) {
                : PA_ERR_CUDA;
 }
 
-template <typename T, int G>
+template <typename T, int G, bool kScores>
 int launch_tc_group(int block_size, const DecodeParams &p, cudaStream_t stream) {
     switch (block_size) {
-        case 8: return launch_tc_t<T, 8, G>(p, stream);
-        case 16: return launch_tc_t<T, 16, G>(p, stream);
-        case 32: return launch_tc_t<T, 32, G>(p, stream);
-        case 64: return launch_tc_t<T, 64, G>(p, stream);
-        case 128: return launch_tc_t<T, 128, G>(p, stream);
+        case 8: return launch_tc_t<T, 8, G, kScores>(p, stream);
+        case 16: return launch_tc_t<T, 16, G, kScores>(p, stream);
+        case 32: return launch_tc_t<T, 32, G, kScores>(p, stream);
+        case 64: return launch_tc_t<T, 64, G, kScores>(p, stream);
+        case 128: return launch_tc_t<T, 128, G, kScores>(p, stream);
         default: return PA_ERR_UNSUPPORTED;
     }
 }
 
-template <typename T>
+template <typename T, bool kScores>
 int launch_tc_dtype(int block_size, int group, const DecodeParams &p, cudaStream_t stream) {
     switch (group) {
-        case 8: return launch_tc_group<T, 8>(block_size, p, stream);
+        case 8: return launch_tc_group<T, 8, kScores>(block_size, p, stream);
         default: return PA_ERR_UNSUPPORTED;
     }
+}
+
+template <bool kScores>
+int launch_tc(pa_dtype dt, int head_dim, int block_size, int group, const DecodeParams &p, cudaStream_t stream) {
+    if (head_dim != kTD || !decode_tc_group(group)) return PA_ERR_UNSUPPORTED;
+    // TMA coordinates are 32-bit
+    if ((long long)p.num_blocks * p.num_kv_heads * (block_size / 8) >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
+    return dt == PA_BF16 ? launch_tc_dtype<__nv_bfloat16, kScores>(block_size, group, p, stream)
+                         : launch_tc_dtype<__half, kScores>(block_size, group, p, stream);
 }
 
 }  // namespace
 
 int launch_decode_tc(pa_dtype dt, int head_dim, int block_size, int group, const DecodeParams &p,
                      cudaStream_t stream) {
-    if (head_dim != kTD || !decode_tc_group(group)) return PA_ERR_UNSUPPORTED;
-    // TMA coordinates are 32-bit
-    if ((long long)p.num_blocks * p.num_kv_heads * (block_size / 8) >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
-    return dt == PA_BF16 ? launch_tc_dtype<__nv_bfloat16>(block_size, group, p, stream)
-                         : launch_tc_dtype<__half>(block_size, group, p, stream);
+    return launch_tc<false>(dt, head_dim, block_size, group, p, stream);
+}
+
+int launch_decode_tc_scores(pa_dtype dt, int head_dim, int block_size, int group, const DecodeParams &p,
+                            cudaStream_t stream) {
+    return launch_tc<true>(dt, head_dim, block_size, group, p, stream);
 }
 
 }  // namespace pa

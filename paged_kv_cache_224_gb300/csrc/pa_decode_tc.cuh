@@ -244,7 +244,7 @@ __device__ __forceinline__ void tc_drain(const TcRun &r) {
 
 // One unit with keys, by the instance's six warps; the ring, the barrier
 // phases and TMEM continue from the previous unit (r's counts advance).
-template <typename T, int BS, int G, int S>
+template <typename T, int BS, int G, int S, bool kScores = false>
 __device__ __forceinline__ void tc_unit(const DecodeParams &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
                                         const TcUnit &u, TcRun &r) {
     using Lay = TcLayout<S>;
@@ -395,6 +395,15 @@ __device__ __forceinline__ void tc_unit(const DecodeParams &p, const CUtensorMap
             const bool valid = key < ntok && ent >= 0 && ent < p.num_blocks;
 #pragma unroll
             for (int h = 0; h < kTG; ++h) sc[h] = valid ? sc[h] * csc : -INFINITY;
+            if constexpr (kScores) {
+                static_assert(G % 4 == 0, "a key's scores are stored as vectors of four");
+                if (key < ntok) {
+                    float4 *dst = reinterpret_cast<float4 *>(
+                        p.scores + ((size_t)(u.s * p.num_kv_heads + kvh) * p.score_stride + u.tok0 + key) * G);
+#pragma unroll
+                    for (int h = 0; h < G; h += 4) dst[h / 4] = make_float4(sc[h], sc[h + 1], sc[h + 2], sc[h + 3]);
+                }
+            }
             // each head's maximum over the tile's 128 keys
             const float wmax = warp_scatter8<true>(sc, lane);
             if ((lane & 3) == 0) r.xmax[(b * 4 + sw) * kTG + (lane >> 2)] = wmax;
@@ -515,6 +524,9 @@ __device__ __forceinline__ void tc_unit(const DecodeParams &p, const CUtensorMap
                 const uint32_t w2 = Elem<T>::pack2(o[h] * inv, 0.f);
                 *reinterpret_cast<uint16_t *>(static_cast<T *>(p.out) + tc_row(p, u, h) * kTD + d) =
                     (uint16_t)(w2 & 0xffffu);
+                if constexpr (kScores) {
+                    if (d == h) p.ws_ml[tc_row(p, u, h) * p.slots] = make_float2(m_run[h], lsum[h]);
+                }
             }
         } else {
 #pragma unroll

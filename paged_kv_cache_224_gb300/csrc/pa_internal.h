@@ -64,6 +64,12 @@ struct DecodeParams {
     int slots;                   // ... of `slots` per (row); the reduce merges slots
     int force_partials;          // write partials even for one-partition units; no reduce
     int red_fixed_slots;         // reduce: slots before the per-sequence ones
+    // Kept scores (the kernels instantiated with kScores): the scaled score, in
+    // log2 units, of every (token, head of the group), as [sequence][kv head]
+    // [score_stride tokens][G] (-inf for a key left out), and ws_ml is written
+    // for whole-sequence units too.
+    float *scores;
+    long long score_stride;
 };
 
 // One sequence's chunk in a prefill launch.  Its work units are (kv head,
@@ -97,6 +103,7 @@ struct PrefillParams {
     float2 *part_ml;             // split: [2 * CTAs][2 Q tiles][128 rows] (running max, sum)
     unsigned *counters;          // split: [units][2 Q tiles] segments counted so far; zero on entry, and
                                  // the merging segment resets its unit's to zero before the call ends
+    int part_slots;              // shared prefix: part_o and part_ml are [row][Hq][part_slots], one slot per piece
     PrefillSeq seqs[kPrefillMaxSeqs];
 };
 
@@ -109,6 +116,43 @@ struct MixedParams {
     int prefill_ctas;
     int decode_units;            // sequences x kv heads
     unsigned *decode_next;       // the decode CTAs' shared unit queue (0 between launches)
+};
+
+// One launch of the rotary cache write.
+constexpr int kRotaryMaxDim = 256;   // largest head_dim
+constexpr int kRotaryMaxAxes = 8;
+struct RotaryParams {
+    void *query_out;             // [T][Hq][D], token stride query_out_stride
+    const void *query;           // [T][Hq][D], token stride query_stride
+    const void *key;             // [T][Hkv][D]
+    const void *value;
+    void *k_cache;               // [NB][Hkv][bs][D]
+    void *v_cache;
+    const int32_t *positions;    // [axes][T]
+    const int64_t *slots;        // [T]
+    const float *inv_freq;       // [rot_dim / 2]
+    int *d_err;
+    long long query_out_stride, query_stride, key_stride, value_stride;  // elements
+    int num_tokens, num_heads, num_kv_heads, head_dim, rot_dim, interleaved;
+    int block_size, num_blocks;
+    uint8_t pair_axis[kRotaryMaxDim / 2];
+};
+
+// One eviction (see pa_evict): the kernels mark, select and copy.
+struct EvictParams {
+    void *k_cache;               // [NB][Hkv][bs][D]
+    void *v_cache;
+    const float *weights;        // [B][Hkv][width]
+    float *new_weights;          // [B][Hkv][width]
+    const int32_t *block_tables; // [B][max_blocks]
+    const int32_t *new_block_tables;  // [B][new_max_blocks]
+    const int32_t *context_lens; // [B]
+    int32_t *new_context_lens;   // [B]
+    int32_t *kept;               // [B][Hkv][keep]
+    int *owner;                  // workspace: [NB]
+    int *d_err;
+    int num_seqs, num_kv_heads, head_dim, block_size, num_blocks, max_blocks, new_max_blocks;
+    int width, max_context_len, keep, sink, recent;
 };
 
 // Split-K partition length for the automatic setting.
@@ -128,11 +172,26 @@ inline bool decode_tc_group(int group) { return group == 8; }
 // refuses the kernel's tensor maps.
 int launch_decode_tc(pa_dtype dt, int head_dim, int block_size, int group, const DecodeParams &p,
                      cudaStream_t stream);
+// The decode kernels that keep their scores (p.scores), without a merge of the
+// partials: launch_weights_merge does that together with the totals.
+int launch_decode_scores(pa_dtype dt, int head_dim, int block_size, int group, const DecodeParams &p,
+                         cudaStream_t stream);
+int launch_decode_scores_bf16(int head_dim, int block_size, int group, const DecodeParams &p, cudaStream_t stream);
+int launch_decode_scores_f16(int head_dim, int block_size, int group, const DecodeParams &p, cudaStream_t stream);
+int launch_decode_tc_scores(pa_dtype dt, int head_dim, int block_size, int group, const DecodeParams &p,
+                            cudaStream_t stream);
+// After launch_decode_scores: merges split sequences' partials into p.out and
+// adds every token's weights to its row's total, queries_per_row sequences to
+// a row of `width` totals.
+int launch_weights_merge(pa_dtype dt, int head_dim, int group, const DecodeParams &p, const float *weights,
+                         float *weights_out, int width, int queries_per_row, cudaStream_t stream);
 // Log-sum-exp merge of the partials in p's workspace into p.out.
 int launch_decode_reduce(pa_dtype dt, int head_dim, const DecodeParams &p, cudaStream_t stream);
 int launch_reshape_and_cache(const void *key, const void *value, void *k_cache, void *v_cache,
                              const int64_t *slots, int num_tokens, int num_kv_heads, int head_dim,
                              int block_size, int num_blocks, int *d_err, cudaStream_t stream);
+int launch_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream);
+int launch_evict(const EvictParams &p, cudaStream_t stream);
 // Copies of up to kGatherMax buffers in one launch, each from memory the
 // device can address (pinned host memory through its device view included)
 // to device memory: 16-byte vectors where both ends and the size allow,
@@ -155,6 +214,22 @@ size_t prefill_workspace_bytes(int num_seqs, long long total_chunk_len, int grou
 // workspace may be NULL (or too small): each CTA then computes one whole unit.
 int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const PrefillParams &p,
                    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+// Attention of a batch over long shared prefixes (pa_decode_common_prefix):
+// `groups` groups of group_size consecutive sequences, each over the first
+// prefix_tokens tokens of its first sequence's table.  A unit's key tiles are
+// shared out over the CTAs as in the stream-K prefill, and each piece of a
+// unit leaves an unnormalised partial in its own slot; prefix_pieces is the
+// most pieces a unit can be cut into.
+int prefix_pieces(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads);
+struct PrefixParams {
+    DecodeParams d;              // the tail pass's parameters: d.slots, d.part_base (= pieces), d.len_offset
+    int groups, group_size, prefix_tokens;
+};
+int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp, float scale_log2,
+                  cudaStream_t stream);
+int launch_prefix_merge(pa_dtype dt, int group, const PrefixParams &pp, cudaStream_t stream);
+int launch_prefix_bf16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
+int launch_prefix_f16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
 // Whether launch_mixed has a kernel for these (head_dim 128, a tensor-core
 // decode group, block_size 16..128).
 bool mixed_supported(int head_dim, int block_size, int group);

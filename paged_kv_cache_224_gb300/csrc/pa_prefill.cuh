@@ -64,6 +64,12 @@
 //             copies and then syncs with the MMA warp before it issues the PV
 //             of tile j and the QK of tile j+1.
 // All waits are bounded; a wait that gives up flags PA_DEVERR_TIMEOUT.
+//
+// kPrefix instances serve decode batches that share a long prefix
+// (pa_prefix.cuh): the "chunk" is the group's sequences, one query position
+// each, no row is ahead of another (prefix_len is the last key of them all),
+// and every segment leaves its partial in its rows' workspace slots for a
+// later merge with the sequences' own tokens.
 #pragma once
 
 #include <cuda.h>
@@ -101,8 +107,16 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kBarP = 3;
 constexpr int kBarL = kBarP + kQT;
 
+// Last key that chunk position i sees.
+template <bool kPrefix>
+__host__ __device__ __forceinline__ int last_key(int prefix_len, int i) {
+    return kPrefix ? prefix_len : prefix_len + i;
+}
+
 // Key tiles of row tile r of sequence q: up to the last key its last row sees.
+template <bool kPrefix = false>
 __host__ __device__ __forceinline__ int unit_tiles(int prefix_len, int chunk_len, int G, int r) {
+    if (kPrefix) return prefix_len / kNK + 1;
     const int last_row = min(chunk_len * G, (r + 1) * kUnitRows) - 1;
     return (prefix_len + last_row / G) / kNK + 1;
 }
@@ -117,7 +131,7 @@ struct Seg {
 };
 
 // The segment that starts at global tile x and ends at x_end or at the end of its unit.
-template <int G>
+template <int G, bool kPrefix>
 __device__ __forceinline__ Seg seg_at(const PrefillParams &p, int x, int x_end) {
     int si = 0;
     for (int i = 1; i < p.num_seqs; ++i)
@@ -128,11 +142,11 @@ __device__ __forceinline__ Seg seg_at(const PrefillParams &p, int x, int x_end) 
     s.si = si;
     s.h = off / q.tiles_per_head;
     int rem = off - s.h * q.tiles_per_head;
-    int r = 0, n = unit_tiles(q.prefix_len, q.chunk_len, G, 0);
+    int r = 0, n = unit_tiles<kPrefix>(q.prefix_len, q.chunk_len, G, 0);
     while (rem >= n) {
         rem -= n;
         ++r;
-        n = unit_tiles(q.prefix_len, q.chunk_len, G, r);
+        n = unit_tiles<kPrefix>(q.prefix_len, q.chunk_len, G, r);
     }
     s.r = r;
     s.n = n;
@@ -297,7 +311,7 @@ __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, uns
 // share of the key tiles; without, unit `cta` (all of the CTA's threads call this).
 // Returns the CTA's TMEM base; with kKeepTmem (the one-launch step, whose
 // prefill CTAs go on to decode) the allocation is left for the caller to free.
-template <typename T, int BS, int G, bool kKeepTmem = false>
+template <typename T, int BS, int G, bool kKeepTmem = false, bool kPrefix = false>
 __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CUtensorMap &tmk,
                                                 const CUtensorMap &tmv, const CUtensorMap &tmq, int cta, int ncta) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -325,7 +339,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
     // this CTA's key tiles [x0, x1) of the global order
     int x0, x1;
     const long long W = p.total_tiles, N = ncta;
-    if (p.split) {
+    if (kPrefix || p.split) {
         x0 = (int)(W * cta / N);
         x1 = (int)(W * (cta + 1) / N);
     } else {
@@ -399,10 +413,10 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
         };
         int sc = 0;
         for (int x = x0; x < x1; ++sc) {
-            const Seg sg = seg_at<G>(p, x, x1);
+            const Seg sg = seg_at<G, kPrefix>(p, x, x1);
             const PrefillSeq &q = p.seqs[sg.si];
             const int32_t *table = q.block_table;
-            const int kend = q.prefix_len + min(q.chunk_len - 1, ((sg.r + 1) * kUnitRows - 1) / G);
+            const int kend = last_key<kPrefix>(q.prefix_len, min(q.chunk_len - 1, ((sg.r + 1) * kUnitRows - 1) / G));
             // Table entries come 32 at a time, one per lane, a whole chunk ahead
             // of use (a chunk covers 32 / kBlocksPerTile tiles); lane b <
             // kBlocksPerTile handles block b of a tile.
@@ -454,7 +468,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             const uint32_t v_lo0 = desc_lo(sb + kOffKV, 1024);   // MN-major: second 64-dim half 1 KB on
             int tc = 0;  // tiles of earlier segments
             for (int x = x0, sc = 0; x < x1; ++sc) {
-                const Seg sg = seg_at<G>(p, x, x1);
+                const Seg sg = seg_at<G, kPrefix>(p, x, x1);
                 const int nt = sg.t1 - sg.t0;
                 if (lane == 0) wait_or_flag(q_full, (uint32_t)sc & 1u, p.d_err);
                 for (int k = 0; k <= nt; ++k) {
@@ -512,7 +526,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
         // steady state
         int gt = 0;
         for (int x = x0; x < x1;) {
-            const Seg sg = seg_at<G>(p, x, x1);
+            const Seg sg = seg_at<G, kPrefix>(p, x, x1);
             const int nt = sg.t1 - sg.t0;
             for (int k = 0; k < nt; ++k, ++gt) {
                 if (lane == 0) {
@@ -549,7 +563,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             rw.valid = gr < q.chunk_len * G;
             rw.ipos = rw.valid ? gr / G : 0;
             rw.head = rw.valid ? gr % G : 0;
-            rw.plim = q.prefix_len + min(gr / G, q.chunk_len - 1);
+            rw.plim = last_key<kPrefix>(q.prefix_len, min(gr / G, q.chunk_len - 1));
             return rw;
         };
         // O (TMEM) times inv, rounded once, into this thread's output row if
@@ -574,21 +588,36 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             }
         };
 
+        // O as it stands into a workspace row, likewise
+        [[maybe_unused]] auto store_partial = [&](float *dst, bool valid) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float v[32];
+                tmem_ld32(tO + c * 32, v);
+                tmem_wait_ld();
+                if (valid) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(dst + c * 32 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+            }
+        };
+
         // Only what the tile loop needs stays live across it; the segment is
         // computed again for its epilogue (the softmax runs at the register limit).
         int gt = 0;  // this CTA's tile count: ring items and barrier phases
         for (int x = x0, sc = 0; x < x1; ++sc) {
             int nt, j0, jn, plim, plim_min, kend;
             {
-                const Seg sg = seg_at<G>(p, x, x1);
+                const Seg sg = seg_at<G, kPrefix>(p, x, x1);
                 const PrefillSeq &q = p.seqs[sg.si];
                 nt = sg.t1 - sg.t0;
                 j0 = sg.t0;
                 jn = sg.n - 1;  // the unit's last key tile
                 plim = row_of(sg).plim;
                 // smallest limit in the Q tile, and the unit's last key
-                plim_min = q.prefix_len + min((sg.r * kUnitRows + g * kM) / G, q.chunk_len - 1);
-                kend = q.prefix_len + min(q.chunk_len - 1, ((sg.r + 1) * kUnitRows - 1) / G);
+                plim_min = last_key<kPrefix>(q.prefix_len, min((sg.r * kUnitRows + g * kM) / G, q.chunk_len - 1));
+                kend = last_key<kPrefix>(q.prefix_len, min(q.chunk_len - 1, ((sg.r + 1) * kUnitRows - 1) / G));
             }
 
             float m_run = -INFINITY;  // running max in scaled log2 units
@@ -716,12 +745,16 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             const float l_run =
                 ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) + ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
             {
-                const Seg sg = seg_at<G>(p, x, x1);
+                const Seg sg = seg_at<G, kPrefix>(p, x, x1);
                 const PrefillSeq &q = p.seqs[sg.si];
                 const Row rw = row_of(sg);
-                T *orow = static_cast<T *>(p.out) +
-                          ((size_t)(q.row_start + rw.ipos) * p.num_heads + sg.h * G + rw.head) * kD;
-                if (sg.t0 == 0 && sg.t1 == sg.n) {
+                const size_t out_row = (size_t)(q.row_start + rw.ipos) * p.num_heads + sg.h * G + rw.head;
+                T *orow = static_cast<T *>(p.out) + out_row * kD;
+                if constexpr (kPrefix) {
+                    const size_t slot = out_row * p.part_slots + (cta - cta_of(sg.x_unit, W, N));
+                    store_partial(p.part_o + slot * kD, rw.valid);
+                    if (rw.valid) p.part_ml[slot] = make_float2(m_run, l_run);
+                } else if (sg.t0 == 0 && sg.t1 == sg.n) {
                     // the whole unit: normalise, round once, store
                     store_out(orow, l_run > 0.f ? 1.f / l_run : 0.f, rw.valid);
                 } else {
@@ -805,6 +838,7 @@ inline PrefillWs prefill_ws(long long ctas, long long units) {
 
 // Units in (sequence, kv head, row tile) order and their key tiles laid end to
 // end: fills the schedule fields of p.  Returns PA_OK, or an error.
+template <bool kPrefix = false>
 inline int prefill_schedule(PrefillParams &p, int group, long long *units_out) {
     long long tiles = 0, units = 0;
     for (int i = 0; i < p.num_seqs; ++i) {
@@ -812,7 +846,7 @@ inline int prefill_schedule(PrefillParams &p, int group, long long *units_out) {
         const long long rows = (long long)q.chunk_len * group;
         const int row_tiles = (int)((rows + kUnitRows - 1) / kUnitRows);
         long long per_head = 0;
-        for (int r = 0; r < row_tiles; ++r) per_head += unit_tiles(q.prefix_len, q.chunk_len, group, r);
+        for (int r = 0; r < row_tiles; ++r) per_head += unit_tiles<kPrefix>(q.prefix_len, q.chunk_len, group, r);
         if (per_head > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
         q.row_tiles = row_tiles;
         q.tiles_per_head = (int)per_head;

@@ -1,0 +1,8 @@
+// bf16 instances of the shared-prefix pass.
+#include "pa_prefix.cuh"
+
+namespace pa {
+int launch_prefix_bf16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream) {
+    return pfx::launch_prefix_dtype<__nv_bfloat16>(block_size, group, p, grid, stream);
+}
+}  // namespace pa

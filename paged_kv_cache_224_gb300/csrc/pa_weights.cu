@@ -1,0 +1,205 @@
+// Accumulated attention weights: what follows the decode kernels that keep
+// their scores (pa_decode_weights).
+//
+// A softmax weight is known only once the sequence's maximum and sum are, and
+// those only once all its partitions are done.  Reading K a second time to
+// recompute the scores would cost half of the decode's traffic again; keeping
+// the fp32 scores costs 8 bytes (one write, one read) per (token, query head)
+// against 4 D bytes of K and V per (token, kv head): 1.6% of it at one query
+// head per kv head and head_dim 128, 12.5% at eight.
+//
+// One kernel, two kinds of CTA:
+//   merge    the log-sum-exp merge of a split sequence's partials, one warp per
+//            (sequence, head): out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p;
+//   totals   one CTA per (row of totals, kv head, chunk of tokens): each
+//            token's weight is sum_h 2^(score_h - M_h) / l_h over the group's
+//            heads, added up over the row's sequences in their order (so the
+//            result does not depend on scheduling) and then to its total.
+#include <algorithm>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kItems = 4;  // tokens per thread
+constexpr int kChunk = kThreads * kItems;
+
+// the decode kernels' clamping of a sequence's length
+__device__ __forceinline__ int clamped_len(const DecodeParams &p, int s) {
+    const int cap = (int)min((long long)p.max_context_len, (long long)p.max_blocks_per_seq * p.block_size);
+    return max(0, min(p.context_lens[s], cap));
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void merge_row(const DecodeParams &p, int pair, int lane) {
+    constexpr int VPL = D / 32;  // values per lane
+    const int s = pair / p.num_heads;
+    const int L = clamped_len(p, s);
+    const int nparts = (L + p.partition_tokens - 1) / p.partition_tokens;
+    if (nparts <= 1) return;  // the decode kernel wrote the output
+    const size_t base = (size_t)pair * p.slots;
+    float M = -INFINITY;
+    for (int i = lane; i < nparts; i += 32) M = fmaxf(M, p.ws_ml[base + i].x);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, m));
+    float lsum = 0.f, o[VPL];
+#pragma unroll
+    for (int d = 0; d < VPL; ++d) o[d] = 0.f;
+    if (M != -INFINITY) {  // else every key was left out: zeros
+#pragma unroll 4
+        for (int i = 0; i < nparts; ++i) {
+            const float2 ml = p.ws_ml[base + i];
+            const float w = fast_exp2(ml.x - M);
+            lsum = fmaf(w, ml.y, lsum);
+            const float *a = p.ws_acc + (base + i) * D + lane * VPL;
+            if constexpr (VPL == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(a);
+                o[0] = fmaf(w, x.x, o[0]); o[1] = fmaf(w, x.y, o[1]);
+                o[2] = fmaf(w, x.z, o[2]); o[3] = fmaf(w, x.w, o[3]);
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(a);
+                o[0] = fmaf(w, x.x, o[0]); o[1] = fmaf(w, x.y, o[1]);
+            }
+        }
+    }
+    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    T *orow = static_cast<T *>(p.out) + (size_t)pair * D + lane * VPL;
+    if constexpr (VPL == 4) {
+        uint2 u;
+        u.x = Elem<T>::pack2(o[0] * inv, o[1] * inv);
+        u.y = Elem<T>::pack2(o[2] * inv, o[3] * inv);
+        *reinterpret_cast<uint2 *>(orow) = u;
+    } else {
+        *reinterpret_cast<uint32_t *>(orow) = Elem<T>::pack2(o[0] * inv, o[1] * inv);
+    }
+}
+
+template <int G>
+__device__ __forceinline__ void load_scores(const float *a, float (&x)[G]) {
+    if constexpr (G == 1) {
+        x[0] = *a;
+    } else if constexpr (G == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(a);
+        x[0] = v.x, x[1] = v.y;
+    } else {
+#pragma unroll
+        for (int h = 0; h < G; h += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(a + h);
+            x[h] = v.x, x[h + 1] = v.y, x[h + 2] = v.z, x[h + 3] = v.w;
+        }
+    }
+}
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kThreads)
+    weights_merge_kernel(const __grid_constant__ DecodeParams p, const float *weights, float *weights_out, int width,
+                         int queries_per_row, int chunks, int merge_ctas) {
+    __shared__ float2 s_ml[G];  // a member's (maximum, 1 / sum) per head
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();  // the decode kernel's scores and partials are complete and visible
+    pdl_trigger();
+    if ((int)blockIdx.x < merge_ctas) {
+        const int pair = blockIdx.x * (kThreads / 32) + warp;
+        if (pair < p.num_seqs * p.num_heads) merge_row<T, D>(p, pair, lane);
+        return;
+    }
+    const int u = blockIdx.x - merge_ctas;
+    const int chunk = u % chunks, rh = u / chunks;
+    const int r = rh / p.num_kv_heads, kvh = rh - r * p.num_kv_heads;
+    const int j0 = chunk * kChunk;
+    float acc[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) acc[i] = 0.f;
+    int longest = 0;
+    for (int m = 0; m < queries_per_row; ++m) {
+        const int s = r * queries_per_row + m;
+        const int L = clamped_len(p, s);
+        longest = max(longest, L);
+        if (j0 >= L) continue;  // the same in every thread
+        const int nparts = (L + p.partition_tokens - 1) / p.partition_tokens;
+        __syncthreads();  // the previous member's s_ml is read
+        for (int h = warp; h < G; h += kThreads / 32) {
+            const float2 *ml = p.ws_ml + ((size_t)s * p.num_heads + kvh * G + h) * p.slots;
+            float M = -INFINITY;
+            for (int i = lane; i < nparts; i += 32) M = fmaxf(M, ml[i].x);
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+            float sum = 0.f;
+            if (M != -INFINITY)
+                for (int i = lane; i < nparts; i += 32) sum = fmaf(fast_exp2(ml[i].x - M), ml[i].y, sum);
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
+            // no key attended: 2^(-inf - 0) = 0 for every one of them
+            if (lane == 0) s_ml[h] = M == -INFINITY ? make_float2(0.f, 0.f) : make_float2(M, 1.f / sum);
+        }
+        __syncthreads();
+        float2 ml[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) ml[h] = s_ml[h];
+        const float *sc = p.scores + ((size_t)(s * p.num_kv_heads + kvh) * p.score_stride + j0) * G;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int j = i * kThreads + tid;
+            if (j0 + j < L) {
+                float x[G];
+                load_scores<G>(sc + (size_t)j * G, x);
+#pragma unroll
+                for (int h = 0; h < G; ++h) acc[i] = fmaf(fast_exp2(x[h] - ml[h].x), ml[h].y, acc[i]);
+            }
+        }
+    }
+    const size_t at = (size_t)rh * width + j0;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int j = i * kThreads + tid;
+        if (j0 + j < longest) weights_out[at + j] = weights[at + j] + acc[i];
+    }
+}
+
+template <typename T, int D, int G>
+int launch_merge_t(const DecodeParams &p, const float *weights, float *weights_out, int width, int queries_per_row,
+                   cudaStream_t stream) {
+    const int chunks = std::max(1, (p.max_context_len + kChunk - 1) / kChunk);
+    const long long pairs = (long long)p.num_seqs * p.num_heads;
+    const long long merge = p.max_partitions > 1 ? (pairs + kThreads / 32 - 1) / (kThreads / 32) : 0;
+    const long long total = merge + (long long)(p.num_seqs / queries_per_row) * p.num_kv_heads * chunks;
+    if (total > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    return launch_pdl(weights_merge_kernel<T, D, G>, dim3((unsigned)total), dim3(kThreads), 0, stream, p, weights,
+                      weights_out, width, queries_per_row, chunks, (int)merge) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+template <typename T>
+int launch_merge_dtype(int head_dim, int group, const DecodeParams &p, const float *weights, float *weights_out,
+                       int width, int queries_per_row, cudaStream_t stream) {
+#define PA_MERGE_CASE(DD, GG)                \
+    if (head_dim == DD && group == GG)       \
+        return launch_merge_t<T, DD, GG>(p, weights, weights_out, width, queries_per_row, stream);
+    PA_MERGE_CASE(64, 1) PA_MERGE_CASE(64, 2) PA_MERGE_CASE(64, 4) PA_MERGE_CASE(64, 8)
+    PA_MERGE_CASE(128, 1) PA_MERGE_CASE(128, 2) PA_MERGE_CASE(128, 4) PA_MERGE_CASE(128, 8)
+#undef PA_MERGE_CASE
+    return PA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+int launch_decode_scores(pa_dtype dt, int head_dim, int block_size, int group, const DecodeParams &p,
+                         cudaStream_t stream) {
+    const int rc = launch_decode_tc_scores(dt, head_dim, block_size, group, p, stream);
+    if (rc != PA_ERR_UNSUPPORTED) return rc;
+    return dt == PA_BF16 ? launch_decode_scores_bf16(head_dim, block_size, group, p, stream)
+                         : launch_decode_scores_f16(head_dim, block_size, group, p, stream);
+}
+
+int launch_weights_merge(pa_dtype dt, int head_dim, int group, const DecodeParams &p, const float *weights,
+                         float *weights_out, int width, int queries_per_row, cudaStream_t stream) {
+    return dt == PA_BF16
+               ? launch_merge_dtype<__nv_bfloat16>(head_dim, group, p, weights, weights_out, width, queries_per_row, stream)
+               : launch_merge_dtype<__half>(head_dim, group, p, weights, weights_out, width, queries_per_row, stream);
+}
+
+}  // namespace pa
