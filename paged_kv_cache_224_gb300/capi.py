@@ -9,7 +9,6 @@ loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -486,23 +485,52 @@ def pa_prefill_batch(out, query, k_cache, v_cache, block_tables, prefix_lens, ch
 
 # ---- bounded and shared caches -------------------------------------------------
 
-def _same_device(*ts):
-    dev = None
+# These calls are short enough on the GPU that a small batch waits for the host,
+# so the marshalling is kept lean: plain integers for pointers, one pass over
+# the tensors for device and contiguity, no stream or device objects.
+
+def _index(t) -> int:
+    """The CUDA device index of ``t``."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("tensor must be on a CUDA device")
+    return i
+
+
+def _checked(index, *ts) -> None:
+    """Every tensor that is given is contiguous and on device ``index``."""
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("tensor must be on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors must be on one device")
-    return dev
+        if t.get_device() != index:
+            raise ValueError("tensors must be on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
 
 
-def _on(device):
-    """Make ``device`` current for a call (a no-op object when it already is)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _typed(dtype, what, *ts) -> None:
+    for t in ts:
+        if t.dtype is not dtype:
+            raise TypeError(what)
+
+
+def _call(name, index, *args) -> None:
+    """Call a C entry point with ``index`` as the current device."""
+    if torch._C._cuda_getDevice() == index:
+        rc = getattr(_lib or lib(), name)(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = getattr(_lib or lib(), name)(*args)
+    if rc:
+        raise PAError(name, rc)
+
+
+def _raw_stream(index, stream):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(device, nbytes, stream):
@@ -514,13 +542,16 @@ def _scratch(device, nbytes, stream):
     return w
 
 
-def _token_rows(name, t, heads, head_dim):
-    """Check that ``t`` is [T][heads][head_dim] with contiguous heads; its token stride."""
-    if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
-        raise ValueError(f"{name}: shape mismatch")
-    if (head_dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != head_dim):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+def _token_rows(index, t, tokens, heads, head_dim):
+    """Check that ``t`` is [tokens][heads][head_dim] with contiguous heads; its token stride."""
+    if t.get_device() != index:
+        raise ValueError("tensors must be on one CUDA device")
+    if t.shape != (tokens, heads, head_dim):
+        raise ValueError("shape mismatch")
+    st = t.stride()
+    if (head_dim > 1 and st[2] != 1) or (heads > 1 and st[1] != head_dim):
+        raise ValueError("the heads of a token must be contiguous")
+    return st[0] if tokens > 1 else heads * head_dim
 
 
 def pa_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
@@ -531,38 +562,36 @@ def pa_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, position
     positions int32 [axes][T] (or [T] for one axis); slot_mapping int64 [T];
     inv_freq float32 [rot_dim / 2]; pair_axis: host ints [rot_dim / 2], the axis of
     each pair (None: axis 0)."""
-    dev = _same_device(k_cache, query_out, query, key, value, v_cache, positions, slot_mapping, inv_freq, d_err)
-    _dev(k_cache, v_cache, positions, slot_mapping, inv_freq, d_err)
-    if slot_mapping.dtype != torch.int64:
-        raise TypeError("slot_mapping must be int64")
-    if positions.dtype != torch.int32:
-        raise TypeError("positions must be int32")
-    if inv_freq.dtype != torch.float32:
-        raise TypeError("inv_freq must be float32")
-    if not (query_out.dtype == query.dtype == key.dtype == value.dtype == k_cache.dtype == v_cache.dtype):
-        raise TypeError("dtype mismatch")
-    NB, Hkv, bs, D = k_cache.shape
-    T, Hq = query.shape[0], query.shape[1]
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    if v_cache.shape != k_cache.shape or query_out.shape[0] != T or key.shape[0] != T or value.shape[0] != T or \
-            slot_mapping.shape != (T,) or positions.dim() not in (1, 2) or positions.shape[-1] != T or \
-            inv_freq.dim() != 1:
+    dev = _index(k_cache)
+    _checked(dev, k_cache, v_cache, positions, slot_mapping, inv_freq, d_err)
+    _typed(torch.int64, "slot_mapping must be int64", slot_mapping)
+    _typed(torch.int32, "positions must be int32", positions)
+    _typed(torch.float32, "inv_freq must be float32", inv_freq)
+    _typed(k_cache.dtype, "dtype mismatch", v_cache, query_out, query, key, value)
+    NB, Hkv, bs, D = shape = k_cache.shape
+    if query.dim() != 3 or v_cache.shape != shape or inv_freq.dim() != 1:
         raise ValueError("shape mismatch")
-    strides = (_token_rows("query_out", query_out, Hq, D), _token_rows("query", query, Hq, D),
-               _token_rows("key", key, Hkv, D), _token_rows("value", value, Hkv, D))
-    half = inv_freq.shape[0]
+    T, Hq, _ = query.shape
+    axes = 1
+    if positions.dim() == 2:
+        axes = positions.shape[0]
+        if positions.shape[1] != T:
+            raise ValueError("shape mismatch")
+    elif positions.shape != (T,):
+        raise ValueError("shape mismatch")
+    if slot_mapping.shape != (T,):
+        raise ValueError("shape mismatch")
+    half = inv_freq.numel()
     ax = None
     if pair_axis is not None:
         ax = np.ascontiguousarray(pair_axis, dtype=np.int32)
         if ax.shape != (half,):
             raise ValueError("pair_axis must name an axis for every pair")
-    with _on(dev):
-        rc = lib().pa_rotary_and_cache(
-            _ptr(query_out), strides[0], _ptr(query), strides[1], _ptr(key), strides[2], _ptr(value), strides[3],
-            _ptr(k_cache), _ptr(v_cache), _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq),
-            ax.ctypes.data if ax is not None and half else None, axes, 2 * half, 1 if interleaved else 0, T, Hq, Hkv,
-            D, bs, NB, _dt(k_cache), _ptr(d_err), _stream(k_cache, stream))
-    _check("pa_rotary_and_cache", rc)
+    _call("pa_rotary_and_cache", dev, query_out.data_ptr(), _token_rows(dev, query_out, T, Hq, D), query.data_ptr(),
+          _token_rows(dev, query, T, Hq, D), key.data_ptr(), _token_rows(dev, key, T, Hkv, D), value.data_ptr(),
+          _token_rows(dev, value, T, Hkv, D), k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(),
+          slot_mapping.data_ptr(), inv_freq.data_ptr(), ax.ctypes.data if ax is not None and half else None, axes,
+          2 * half, 1 if interleaved else 0, T, Hq, Hkv, D, bs, NB, _dt(k_cache), _opt(d_err), _raw_stream(dev, stream))
 
 
 def pa_decode_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
@@ -576,7 +605,7 @@ def decode_weights_workspace(query, num_kv_heads, block_size, max_context_len, p
     """Allocate (with torch) a workspace big enough for ``pa_decode_weights``
     (whatever the number of queries per row of totals)."""
     B, Hq, D = query.shape
-    with _on(query.device):
+    with torch.cuda.device(query.device):
         n = pa_decode_weights_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, partition_tokens)
     return _scratch(query.device, n, stream)
 
@@ -589,31 +618,28 @@ def pa_decode_weights(out, query, k_cache, v_cache, block_tables, context_lens, 
     in place unless ``weights_out`` (of the same shape) is given."""
     if weights_out is None:
         weights_out = weights
-    dev = _same_device(query, out, k_cache, v_cache, block_tables, context_lens, weights, weights_out, workspace, d_err)
-    _dev(out, query, k_cache, v_cache, block_tables, context_lens, weights, weights_out, workspace, d_err)
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise TypeError("block_tables and context_lens must be int32")
-    if weights.dtype != torch.float32 or weights_out.dtype != torch.float32:
-        raise TypeError("weights must be float32")
-    NB, Hkv, bs, D = k_cache.shape
-    B, Hq, Dq = query.shape
+    dev = _index(query)
+    _checked(dev, query, out, k_cache, v_cache, block_tables, context_lens, weights, weights_out, workspace, d_err)
+    _typed(torch.int32, "block_tables and context_lens must be int32", block_tables, context_lens)
+    _typed(torch.float32, "weights must be float32", weights, weights_out)
+    _typed(query.dtype, "dtype mismatch", out, k_cache, v_cache)
+    NB, Hkv, bs, D = shape = k_cache.shape
+    qshape = query.shape
+    B, Hq, Dq = qshape
     if queries_per_row < 1 or B % queries_per_row:
         raise ValueError("the number of sequences must be a multiple of queries_per_row")
-    if Dq != D or v_cache.shape != k_cache.shape or out.shape != query.shape or block_tables.dim() != 2 or \
-            block_tables.shape[0] != B or context_lens.shape != (B,) or weights.dim() != 3 or \
-            weights.shape[:2] != (B // queries_per_row, Hkv) or weights_out.shape != weights.shape:
+    wshape = weights.shape
+    if Dq != D or v_cache.shape != shape or out.shape != qshape or block_tables.dim() != 2 or \
+            block_tables.shape[0] != B or context_lens.shape != (B,) or len(wshape) != 3 or \
+            wshape[0] != B // queries_per_row or wshape[1] != Hkv or weights_out.shape != wshape:
         raise ValueError("shape mismatch")
-    if not (out.dtype == query.dtype == k_cache.dtype == v_cache.dtype):
-        raise TypeError("dtype mismatch")
     if workspace is None:
         workspace = decode_weights_workspace(query, Hkv, bs, max_context_len, partition_tokens, stream=stream)
-    with _on(dev):
-        rc = lib().pa_decode_weights(
-            _ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
-            _ptr(context_lens), B, Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), int(partition_tokens),
-            _ptr(weights), _ptr(weights_out), weights.shape[2], int(queries_per_row), _dt(query), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(d_err), _stream(query, stream))
-    _check("pa_decode_weights", rc)
+    _call("pa_decode_weights", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB,
+          int(max_context_len), float(scale), int(partition_tokens), weights.data_ptr(), weights_out.data_ptr(), wshape[2],
+          int(queries_per_row), _dt(query), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _opt(d_err), _raw_stream(dev, stream))
 
 
 def evict_workspace(k_cache, num_seqs=0, keep=0, stream=None):
@@ -628,34 +654,28 @@ def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, new_block_ta
     first ``sink`` and last ``recent`` always kept), per kv head, into the blocks
     of ``new_block_tables``.  weights/new_weights float32 [B][Hkv][W]; kept int32
     [B][Hkv][keep]; tables int32 [B][MB]; context_lens/new_context_lens int32 [B]."""
-    dev = _same_device(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_context_lens,
-                       new_weights, kept, workspace, d_err)
-    _dev(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_context_lens, new_weights, kept,
-         workspace, d_err)
-    for t in (block_tables, context_lens, new_block_tables, new_context_lens, kept):
-        if t.dtype != torch.int32:
-            raise TypeError("tables, lengths and kept must be int32")
-    if weights.dtype != torch.float32 or new_weights.dtype != torch.float32:
-        raise TypeError("weights must be float32")
-    if k_cache.dtype != v_cache.dtype:
-        raise TypeError("dtype mismatch")
-    NB, Hkv, bs, D = k_cache.shape
-    B = context_lens.shape[0]
-    if v_cache.shape != k_cache.shape or weights.dim() != 3 or weights.shape[:2] != (B, Hkv) or \
-            new_weights.shape != weights.shape or kept.shape != (B, Hkv, keep) or block_tables.dim() != 2 or \
+    dev = _index(k_cache)
+    _checked(dev, k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_context_lens,
+             new_weights, kept, workspace, d_err)
+    _typed(torch.int32, "tables, lengths and kept must be int32", block_tables, context_lens, new_block_tables,
+           new_context_lens, kept)
+    _typed(torch.float32, "weights must be float32", weights, new_weights)
+    _typed(k_cache.dtype, "dtype mismatch", v_cache)
+    NB, Hkv, bs, D = shape = k_cache.shape
+    B = context_lens.numel()
+    wshape = weights.shape
+    if v_cache.shape != shape or len(wshape) != 3 or wshape[0] != B or wshape[1] != Hkv or \
+            new_weights.shape != wshape or kept.shape != (B, Hkv, keep) or block_tables.dim() != 2 or \
             block_tables.shape[0] != B or new_block_tables.dim() != 2 or new_block_tables.shape[0] != B or \
-            context_lens.shape != (B,) or new_context_lens.shape != (B,):
+            context_lens.dim() != 1 or new_context_lens.shape != (B,):
         raise ValueError("shape mismatch")
     if workspace is None:
         workspace = evict_workspace(k_cache, stream=stream)
-    with _on(dev):
-        rc = lib().pa_evict(
-            _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(new_weights), weights.shape[2], _ptr(block_tables),
-            block_tables.shape[1], _ptr(context_lens), _ptr(new_block_tables), new_block_tables.shape[1],
-            _ptr(new_context_lens), _ptr(kept), B, Hkv, D, bs, NB, int(max_context_len), int(keep), int(sink),
-            int(recent), _dt(k_cache), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(d_err),
-            _stream(k_cache, stream))
-    _check("pa_evict", rc)
+    _call("pa_evict", dev, k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), new_weights.data_ptr(),
+          wshape[2], block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+          new_block_tables.data_ptr(), new_block_tables.shape[1], new_context_lens.data_ptr(), kept.data_ptr(), B, Hkv,
+          D, bs, NB, int(max_context_len), int(keep), int(sink), int(recent), _dt(k_cache), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _opt(d_err), _raw_stream(dev, stream))
 
 
 def pa_decode_common_prefix_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
@@ -668,7 +688,7 @@ def decode_common_prefix_workspace(query, num_kv_heads, block_size, max_context_
                                    partition_tokens=0, stream=None):
     """Allocate (with torch) a workspace big enough for ``pa_decode_common_prefix``."""
     B, Hq, D = query.shape
-    with _on(query.device):
+    with torch.cuda.device(query.device):
         n = pa_decode_common_prefix_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, group_size,
                                                     prefix_blocks, partition_tokens)
     return _scratch(query.device, n, stream)
@@ -678,24 +698,20 @@ def pa_decode_common_prefix(out, query, k_cache, v_cache, block_tables, context_
                             group_size, prefix_blocks, partition_tokens=0, workspace=None, d_err=None, stream=None):
     """``pa_decode`` for batches whose consecutive groups of ``group_size``
     sequences (any size) share their first ``prefix_blocks`` physical blocks."""
-    dev = _same_device(query, out, k_cache, v_cache, block_tables, context_lens, workspace, d_err)
-    _dev(out, query, k_cache, v_cache, block_tables, context_lens, workspace, d_err)
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise TypeError("block_tables and context_lens must be int32")
-    NB, Hkv, bs, D = k_cache.shape
-    B, Hq, Dq = query.shape
-    if Dq != D or v_cache.shape != k_cache.shape or out.shape != query.shape or block_tables.dim() != 2 or \
+    dev = _index(query)
+    _checked(dev, query, out, k_cache, v_cache, block_tables, context_lens, workspace, d_err)
+    _typed(torch.int32, "block_tables and context_lens must be int32", block_tables, context_lens)
+    _typed(query.dtype, "dtype mismatch", out, k_cache, v_cache)
+    NB, Hkv, bs, D = shape = k_cache.shape
+    qshape = query.shape
+    B, Hq, Dq = qshape
+    if Dq != D or v_cache.shape != shape or out.shape != qshape or block_tables.dim() != 2 or \
             block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("shape mismatch")
-    if not (out.dtype == query.dtype == k_cache.dtype == v_cache.dtype):
-        raise TypeError("dtype mismatch")
     if workspace is None:
         workspace = decode_common_prefix_workspace(query, Hkv, bs, max_context_len, group_size, prefix_blocks,
                                                    partition_tokens, stream=stream)
-    with _on(dev):
-        rc = lib().pa_decode_common_prefix(
-            _ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
-            _ptr(context_lens), B, int(group_size), int(prefix_blocks), Hq, Hkv, D, bs, NB, int(max_context_len),
-            float(scale), int(partition_tokens), _dt(query), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(d_err), _stream(query, stream))
-    _check("pa_decode_common_prefix", rc)
+    _call("pa_decode_common_prefix", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, int(group_size),
+          int(prefix_blocks), Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), int(partition_tokens), _dt(query),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _opt(d_err), _raw_stream(dev, stream))

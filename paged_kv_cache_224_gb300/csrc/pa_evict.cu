@@ -9,16 +9,21 @@
 //
 // Three launches:
 //   mark    each new block's table entry writes its index into owner[block];
-//   select  one CTA per (sequence, kv head): the threshold total by radix
-//           selection (four histograms of 8 bits over an order-preserving
-//           integer image of the fp32 totals), then one pass in index order
-//           that emits the kept indices and their totals.  The CTAs of kv head
-//           0 also look for new blocks named twice or still read, and strike
-//           them from owner[];
+//   select  one CTA, or a cluster of 2 to 8, per (sequence, kv head): the
+//           threshold total by radix selection (four histograms of 8 bits over
+//           an order-preserving integer image of the fp32 totals), then one
+//           pass in index order that emits the kept indices and their totals.
+//           The totals are read once, into registers (up to 4096 or 8192 a CTA;
+//           rows of more than 65536 read them again in every pass); a cluster's CTAs read each
+//           other's histograms and counts through distributed shared memory.
+//           The CTAs of kv head 0 also look for new blocks named twice or still
+//           read, and strike them from owner[];
 //   copy    HBM-bound: 16-byte vectors of the kept rows, K and V, to the new
 //           blocks that owner[] still grants.
 // owner[] needs no clearing: an entry e counts for block b only if the new
 // table's entry e names b, so a stale value proves nothing by itself.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -26,6 +31,7 @@
 
 namespace pa {
 namespace {
+namespace cg = cooperative_groups;
 
 constexpr int kStruck = -1;
 
@@ -63,33 +69,63 @@ __device__ __forceinline__ unsigned order_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelItems = 4;  // tokens per thread and chunk of the emitting pass
-
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ unsigned s_hist[256];
-    __shared__ unsigned s_warp[kSelWarps];
+// A row's tokens go to its CL CTAs of kSelThreads threads in rounds of kSelItems
+// tokens a thread (one round, unless the row is longer than that); in a round
+// CTA `rank` takes a contiguous segment, its warps contiguous segments of that,
+// a warp's lanes neighbours.
+template <int CL, int kSelThreads, int kSelItems>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int kSelWarps = kSelThreads / 32;
+    constexpr int kSelCap = kSelThreads * kSelItems;
+    __shared__ unsigned s_hist[4][256];
+    __shared__ unsigned s_sum[256];
+    __shared__ uint2 s_warp[kSelWarps];
+    __shared__ uint2 s_cta[2];      // this CTA's counts of a round (alternating), read by the others
     __shared__ unsigned s_pick[2];  // the digit, and how many are still to be taken below it
-    const int h = blockIdx.x % p.num_kv_heads, s = blockIdx.x / p.num_kv_heads;
+    const int rank = CL > 1 ? blockIdx.x % CL : 0;
+    const int row = blockIdx.x / CL;
+    const int s = row / p.num_kv_heads, h = row - s * p.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto all_sync = [] {
+        if constexpr (CL > 1) cg::this_cluster().sync();
+        else __syncthreads();
+    };
+    for (int i = tid; i < 4 * 256; i += kSelThreads) (&s_hist[0][0])[i] = 0u;
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
     bool bad;
     const int L = evict_len(p, s, &bad);
     const int n = min(L, p.keep);
-    const size_t row = ((size_t)s * p.num_kv_heads + h);
-    const float *w = p.weights + row * p.width;
-    float *nw = p.new_weights + row * p.width;
-    int *kept = p.kept + row * p.keep;
+    const float *w = p.weights + (size_t)row * p.width;
+    float *nw = p.new_weights + (size_t)row * p.width;
+    int *kept = p.kept + (size_t)row * p.keep;
+
+    const int rounds = max(1, (L + CL * kSelCap - 1) / (CL * kSelCap));
+    // tokens of a warp in a full round: a multiple of 32
+    const int wseg = rounds > 1 ? kSelItems * 32 : ((L + CL * kSelWarps - 1) / (CL * kSelWarps) + 31) / 32 * 32;
+    const int first = (rank * kSelWarps + warp) * wseg + lane;  // in round 0, item 0
+    const int round_len = CL * kSelWarps * wseg;
+    const int lo = min(p.sink, L), hi = max(lo, L - p.recent);  // the tokens that are ranked
+    const bool cut = L > p.keep;
+
+    unsigned key[kSelItems];
+    auto load = [&](int r) {
+#pragma unroll
+        for (int i = 0; i < kSelItems; ++i) {
+            const int j = r * round_len + first + i * 32;
+            key[i] = i * 32 < wseg && j < L ? order_key(w[j]) : 0u;
+        }
+    };
+    load(0);
 
     if (h == 0) {
-        if (tid == 0) {
+        if (tid == 0 && rank == 0) {
             if (bad) flag_error(p.d_err, PA_DEVERR_CONTEXT_RANGE);
             p.new_context_lens[s] = n;
         }
         // a new block that two entries name belongs to neither
-        for (int j = tid; j < blocks_of(n, p.block_size); j += kSelThreads) {
+        for (int j = rank * kSelThreads + tid; j < blocks_of(n, p.block_size); j += CL * kSelThreads) {
             const int e = s * p.new_max_blocks + j, b = p.new_block_tables[e];
             if (b >= 0 && b < p.num_blocks && p.owner[b] != e) {
                 p.owner[b] = kStruck;
@@ -97,7 +133,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             }
         }
         // nor does one that this sequence's table reads
-        for (int j = tid; j < blocks_of(L, p.block_size); j += kSelThreads) {
+        for (int j = rank * kSelThreads + tid; j < blocks_of(L, p.block_size); j += CL * kSelThreads) {
             const int b = p.block_tables[(size_t)s * p.max_blocks + j];
             if (b < 0 || b >= p.num_blocks) {
                 flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
@@ -116,118 +152,153 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 
     // ---- threshold: the `want` largest of the tokens [lo, hi)
     unsigned thr = 0u, eq_take = 0u;  // keys above thr are kept, and the first eq_take equal to it
-    const int lo = min(p.sink, L), hi = max(lo, L - p.recent);
-    const bool cut = L > p.keep;
-    if (cut) {
-        unsigned want = (unsigned)(p.keep - p.sink - p.recent);
-        if (want == 0) {
-            thr = 0xffffffffu;  // no key is above it, and none equal to it is taken
-        } else {
-            unsigned prefix = 0u;
-            for (int shift = 24; shift >= 0; shift -= 8) {
-                if (tid < 256) s_hist[tid] = 0u;
-                __syncthreads();
-                for (int j = lo + tid; j < hi; j += kSelThreads) {
-                    const unsigned k = order_key(w[j]);
-                    if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&s_hist[(k >> shift) & 255u], 1u);
-                }
-                __syncthreads();
-                // digit of the want-th largest: counts from the top, by one warp, 8 digits a lane
-                if (warp == 0) {
-                    unsigned c[8], sum = 0u;
+    unsigned want = (unsigned)(p.keep - p.sink - p.recent);
+    if (cut && want == 0) thr = 0xffffffffu;  // no key is above it, and none equal to it is taken
+    if (cut && want > 0) {
+        unsigned prefix = 0u;
+#pragma unroll 1
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            for (int r = 0; r < rounds; ++r) {
+                if (rounds > 1) load(r);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        c[i] = s_hist[255 - (lane * 8 + i)];
-                        sum += c[i];
-                    }
-                    unsigned before = sum;
-#pragma unroll
-                    for (int m = 1; m < 32; m <<= 1) {
-                        const unsigned up = __shfl_up_sync(kFull, before, m);
-                        if (lane >= m) before += up;
-                    }
-                    before -= sum;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (before < want && want <= before + c[i]) {
-                            s_pick[0] = 255u - (unsigned)(lane * 8 + i);
-                            s_pick[1] = want - before;
-                        }
-                        before += c[i];
+                for (int i = 0; i < kSelItems; ++i) {
+                    if (i * 32 >= wseg) break;
+                    const int j = r * round_len + first + i * 32;
+                    const bool in = j >= lo && j < hi && (pass == 0 || (key[i] >> (shift + 8)) == prefix);
+                    const unsigned act = __ballot_sync(kFull, in);
+                    if (!act) continue;
+                    const unsigned digit = (key[i] >> shift) & 255u;
+                    // totals are often all alike (no attention yet): then one add for the warp
+                    const unsigned one = __shfl_sync(kFull, digit, __ffs(act) - 1);
+                    if (__all_sync(kFull, !in || digit == one)) {
+                        if (lane == 0) atomicAdd(&s_hist[pass][one], (unsigned)__popc(act));
+                    } else if (in) {
+                        atomicAdd(&s_hist[pass][digit], 1u);
                     }
                 }
-                __syncthreads();
-                prefix = (prefix << 8) | s_pick[0];
-                want = s_pick[1];
             }
-            thr = prefix;
-            eq_take = want;
+            all_sync();
+            if constexpr (CL > 1) {
+                if (tid < 256) {
+                    unsigned sum = 0u;
+#pragma unroll
+                    for (int c = 0; c < CL; ++c) sum += *cg::this_cluster().map_shared_rank(&s_hist[pass][tid], c);
+                    s_sum[tid] = sum;
+                }
+                __syncthreads();
+            }
+            // digit of the want-th largest: counts from the top, by one warp, 8 digits a lane
+            if (warp == 0) {
+                unsigned c[8], sum = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    c[i] = (CL > 1 ? s_sum : s_hist[pass])[255 - (lane * 8 + i)];
+                    sum += c[i];
+                }
+                unsigned before = sum;
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const unsigned up = __shfl_up_sync(kFull, before, m);
+                    if (lane >= m) before += up;
+                }
+                before -= sum;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (before < want && want <= before + c[i]) {
+                        s_pick[0] = 255u - (unsigned)(lane * 8 + i);
+                        s_pick[1] = want - before;
+                    }
+                    before += c[i];
+                }
+            }
+            __syncthreads();
+            prefix = (prefix << 8) | s_pick[0];
+            want = s_pick[1];
         }
+        thr = prefix;
+        eq_take = want;
     }
 
-    // ---- emit in index order.  Of a token's predecessors, the sure ones (low
-    // half of a packed count) and those at the threshold (high half) give its
-    // place: sure + min(equal, eq_take).
-    unsigned base_sure = 0u, base_eq = 0u;
-    for (int j0 = 0; j0 < L; j0 += kSelThreads * kSelItems) {
-        unsigned cls[kSelItems], mine = 0u;  // 1: kept, 1 << 16: at the threshold
-        float x[kSelItems];
+    // ---- emit in index order.  A token's place is the count of sure ones
+    // before it plus that of those at the threshold, at most eq_take.
+    uint2 base = make_uint2(0u, 0u);  // (sure, at the threshold) in earlier rounds
+    for (int r = 0; r < rounds; ++r) {
+        if (rounds > 1) load(r);
+        unsigned sure[kSelItems], at[kSelItems];  // the warp's ballots
+        uint2 mine = make_uint2(0u, 0u);
 #pragma unroll
         for (int i = 0; i < kSelItems; ++i) {
-            const int j = j0 + tid * kSelItems + i;
-            cls[i] = 0u;
-            x[i] = 0.f;
-            if (j < L) {
-                x[i] = w[j];
-                const unsigned k = order_key(x[i]);
-                if (!cut || j < lo || j >= hi || k > thr) cls[i] = 1u;
-                else if (k == thr) cls[i] = 1u << 16;
+            sure[i] = at[i] = 0u;
+            if (i * 32 < wseg) {
+                const int j = r * round_len + first + i * 32;
+                const bool ranked = cut && j >= lo && j < hi;
+                sure[i] = __ballot_sync(kFull, j < L && (!ranked || key[i] > thr));
+                at[i] = __ballot_sync(kFull, j < L && ranked && key[i] == thr);
             }
-            mine += cls[i];
+            mine.x += __popc(sure[i]);
+            mine.y += __popc(at[i]);
         }
-        unsigned scan = mine;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const unsigned up = __shfl_up_sync(kFull, scan, m);
-            if (lane >= m) scan += up;
-        }
-        __syncthreads();  // the previous chunk's totals are read
-        if (lane == 31) s_warp[warp] = scan;
+        if (lane == 0) s_warp[warp] = mine;
         __syncthreads();
-        unsigned before = scan - mine, total = 0u;
+        uint2 before = base, total = make_uint2(0u, 0u);
 #pragma unroll
         for (int q = 0; q < kSelWarps; ++q) {
-            const unsigned v = s_warp[q];
-            if (q < warp) before += v;
-            total += v;
+            const uint2 v = s_warp[q];
+            if (q < warp) before.x += v.x, before.y += v.y;
+            total.x += v.x, total.y += v.y;
         }
-        unsigned sure = base_sure + (before & 0xffffu), eq = base_eq + (before >> 16);
+        if constexpr (CL > 1) {
+            if (tid == 0) s_cta[r & 1] = total;
+            cg::this_cluster().sync();
+            uint2 round = make_uint2(0u, 0u);
+#pragma unroll
+            for (int c = 0; c < CL; ++c) {
+                const uint2 v = *cg::this_cluster().map_shared_rank(&s_cta[r & 1], c);
+                if (c < rank) before.x += v.x, before.y += v.y;
+                round.x += v.x, round.y += v.y;
+            }
+            total = round;
+        } else {
+            __syncthreads();  // s_warp is read
+        }
+        const unsigned below = (1u << lane) - 1u;
 #pragma unroll
         for (int i = 0; i < kSelItems; ++i) {
-            const bool at = cls[i] >> 16;
-            if (cls[i] == 1u || (at && eq < eq_take)) {
-                const unsigned pos = sure + min(eq, eq_take);
-                kept[pos] = j0 + tid * kSelItems + i;
-                nw[pos] = x[i];
+            if (i * 32 >= wseg) break;
+            const unsigned eq = before.y + __popc(at[i] & below);
+            const unsigned pos = before.x + __popc(sure[i] & below) + min(eq, eq_take);
+            const bool is_at = at[i] >> lane & 1u;
+            if ((sure[i] >> lane & 1u) || (is_at && eq < eq_take)) {
+                const int j = r * round_len + first + i * 32;
+                kept[pos] = j;
+                nw[pos] = w[j];
             }
-            sure += cls[i] & 1u;
-            eq += at;
+            before.x += __popc(sure[i]);
+            before.y += __popc(at[i]);
         }
-        base_sure += total & 0xffffu;
-        base_eq += total >> 16;
+        base.x += total.x;
+        base.y += total.y;
     }
-    for (int j = n + tid; j < p.keep; j += kSelThreads) kept[j] = -1;
-    for (int j = n + tid; j < p.width; j += kSelThreads) nw[j] = 0.f;
+    for (int j = n + rank * kSelThreads + tid; j < p.keep; j += CL * kSelThreads) kept[j] = -1;
+    for (int j = n + rank * kSelThreads + tid; j < p.width; j += CL * kSelThreads) nw[j] = 0.f;
+    if constexpr (CL > 1) cg::this_cluster().sync();  // nobody leaves while its counts are being read
 }
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyRows = 64;  // rows of one (sequence, kv head) per CTA
+constexpr int kCopyRows = kCopyThreads;  // rows of one (sequence, kv head) per CTA
 
-// LPR lanes (16 bytes each) per row.
+// Finding a row takes four loads, each waiting for the one before (length, kept
+// index, table entries, owner); so a thread finds one row, all rows of the CTA
+// at once, and then the CTA moves them, LPR lanes (16 bytes each) per row, four
+// rows' K and V of each lane in flight.
 template <int LPR>
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_constant__ EvictParams p, int chunks) {
     constexpr int kRowsPass = kCopyThreads / LPR;
-    constexpr int kPasses = kCopyRows / kRowsPass > 0 ? kCopyRows / kRowsPass : 1;
+    constexpr int kPasses = kCopyRows / kRowsPass;
+    constexpr int kFly = 4;
+    static_assert(kPasses % kFly == 0, "passes in steps of kFly");
+    __shared__ longlong2 s_row[kCopyRows];  // (from, to) in rows of the pool; from -1: no copy
     const int chunk = blockIdx.x % chunks;
     const int sh = blockIdx.x / chunks;
     const int s = sh / p.num_kv_heads, h = sh - s * p.num_kv_heads;
@@ -237,44 +308,67 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
     const int n = min(evict_len(p, s, &bad), p.keep);
     const int r0 = chunk * kCopyRows;
     if (r0 >= n) return;
-    const int bs = p.block_size;
-    const int c = threadIdx.x % LPR;
-    const int32_t *kept = p.kept + (size_t)sh * p.keep;
-    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
-    const int32_t *new_table = p.new_block_tables + (size_t)s * p.new_max_blocks;
+    const int bs = p.block_size, shift = 31 - __clz(bs);  // a power of two
+    {
+        const int r = r0 + threadIdx.x;
+        longlong2 x = make_longlong2(-1, 0);
+        if (r < n) {
+            const int j = p.kept[(size_t)sh * p.keep + r];
+            const int nb = p.new_block_tables[(size_t)s * p.new_max_blocks + (r >> shift)];
+            const int b = p.block_tables[(size_t)s * p.max_blocks + (j >> shift)];
+            if (b >= 0 && b < p.num_blocks && nb >= 0 && nb < p.num_blocks &&
+                p.owner[nb] == s * p.new_max_blocks + (r >> shift)) {
+                x.x = ((long long)b * p.num_kv_heads + h) * bs + (j & (bs - 1));
+                x.y = ((long long)nb * p.num_kv_heads + h) * bs + (r & (bs - 1));
+            }
+        }
+        s_row[threadIdx.x] = x;
+    }
+    __syncthreads();
+    const int c = threadIdx.x % LPR, first = threadIdx.x / LPR;
+    const int passes = (min(n - r0, kCopyRows) + kRowsPass - 1) / kRowsPass;
     const uint4 *ks = static_cast<const uint4 *>(p.k_cache), *vs = static_cast<const uint4 *>(p.v_cache);
     uint4 *kd = static_cast<uint4 *>(p.k_cache), *vd = static_cast<uint4 *>(p.v_cache);
-    long long src[kPasses], dst[kPasses];  // 16-byte units; src -1: no copy
+    for (int p0 = 0; p0 < passes; p0 += kFly) {
+        longlong2 x[kFly];
+        uint4 k[kFly], v[kFly];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const int r = r0 + i * kRowsPass + threadIdx.x / LPR;
-        src[i] = -1;
-        dst[i] = 0;
-        if (r < n) {
-            const int j = kept[r];
-            const int nj = r / bs, b = table[j / bs], nb = new_table[nj];
-            const bool ok = b >= 0 && b < p.num_blocks && nb >= 0 && nb < p.num_blocks;
-            if (ok && p.owner[nb] == s * p.new_max_blocks + nj) {
-                src[i] = (((long long)b * p.num_kv_heads + h) * bs + j % bs) * LPR + c;
-                dst[i] = (((long long)nb * p.num_kv_heads + h) * bs + r % bs) * LPR + c;
+        for (int i = 0; i < kFly; ++i) {
+            x[i] = s_row[(p0 + i) * kRowsPass + first];
+            if (x[i].x >= 0) {
+                k[i] = ks[x[i].x * LPR + c];
+                v[i] = vs[x[i].x * LPR + c];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            if (x[i].x >= 0) {
+                kd[x[i].y * LPR + c] = k[i];
+                vd[x[i].y * LPR + c] = v[i];
             }
         }
     }
-    uint4 k[kPasses], v[kPasses];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        if (src[i] >= 0) {
-            k[i] = ks[src[i]];
-            v[i] = vs[src[i]];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        if (src[i] >= 0) {
-            kd[dst[i]] = k[i];
-            vd[dst[i]] = v[i];
-        }
-    }
+}
+
+constexpr int kNarrow = 256, kNarrowItems = 16;
+constexpr int kWide = 1024, kWideItems = 8;
+
+template <int CL, int kThreads, int kItems>
+int launch_select(const EvictParams &p, long long rows, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * CL));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CL;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<CL, kThreads, kItems>, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -285,8 +379,22 @@ int launch_evict(const EvictParams &p, cudaStream_t stream) {
     const int most = std::min(p.keep, std::min(p.max_context_len, p.width));
     const int chunks = std::max(1, (most + kCopyRows - 1) / kCopyRows);
     if (rows * chunks > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-    if (launch_pdl(evict_select_kernel, dim3((unsigned)rows), dim3(kSelThreads), 0, stream, p) != cudaSuccess)
-        return PA_ERR_CUDA;
+    // CTAs per row: as many as hold it in registers, and more while the rows
+    // leave SMs idle and each CTA still has 2048 tokens.  Rows that need more
+    // than eight CTAs of 256 threads get CTAs of 1024.
+    const int longest = std::min(p.max_context_len, p.width);
+    int cl = 1;
+    while (cl < 8 && ((long long)cl * kNarrow * kNarrowItems < longest ||
+                      (rows * cl * 2 <= sm_count() && longest >= 2 * cl * 2048)))
+        cl *= 2;
+    if (rows * cl > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    const bool wide = (long long)cl * kNarrow * kNarrowItems < longest;
+    const int rc = wide      ? launch_select<8, kWide, kWideItems>(p, rows, stream)
+                   : cl == 1 ? launch_select<1, kNarrow, kNarrowItems>(p, rows, stream)
+                   : cl == 2 ? launch_select<2, kNarrow, kNarrowItems>(p, rows, stream)
+                   : cl == 4 ? launch_select<4, kNarrow, kNarrowItems>(p, rows, stream)
+                             : launch_select<8, kNarrow, kNarrowItems>(p, rows, stream);
+    if (rc != PA_OK) return rc;
     const dim3 grid((unsigned)(rows * chunks)), block(kCopyThreads);
     cudaError_t e;
     switch (p.head_dim) {

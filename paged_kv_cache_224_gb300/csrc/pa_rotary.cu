@@ -14,11 +14,14 @@
 // Its top 32 bits go to sincospi: the angle is within 2^-25 turns' worth of
 // fp32 rounding plus |position| * 2^-55 turns of the exact product.
 //
-// HBM-bound: every row is read and written once.  One CTA per token; its
-// cosines and sines are computed once, one pair per thread, into shared memory
-// and serve every head.  A thread moves units of two 16-byte vectors (8 pairs),
-// and a thread's place in the head is the same for every head it takes, so it
-// reads its 8 cosines and sines once.
+// HBM-bound: every row is read and written once.  A CTA walks tokens
+// blockIdx.x, + gridDim.x, ...; a token's cosines and sines are computed once,
+// one pair per thread, into one of two shared buffers and serve every head,
+// and while its rows move, the next token's first vectors are on their way and
+// its angles are computed.  A thread moves units of two 16-byte vectors (8
+// pairs); its place in the head is the same for every head it takes, so it
+// reads its 8 cosines and sines once per token, and pair i's turns per
+// position stay in one thread's register throughout.
 #include <algorithm>
 #include <type_traits>
 
@@ -36,143 +39,181 @@ __device__ __forceinline__ uint4 ldg_stream(const void *p) {
     return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(1024) rotary_kernel(const __grid_constant__ RotaryParams p) {
-    // cosines of pairs 8c .. 8c+3, 8c+4 .. 8c+7, then the sines alike, [4][unit c]: a warp's reads are consecutive
-    __shared__ float4 s_cs[4][kRotaryMaxDim / 16];
-    __shared__ long long s_dst;  // element offset of kv head 0's row in the caches, -1: not written
-    const int t = blockIdx.x;
+// A token's kv head 0 row: element offset in the caches, or -1 for none.
+__device__ __forceinline__ long long cache_row(const RotaryParams &p, long long slot) {
+    if (slot < 0) return -1;
+    if (slot >= (long long)p.num_blocks * p.block_size) {
+        flag_error(p.d_err, PA_DEVERR_SLOT_RANGE);
+        return -1;
+    }
+    // most pools have fewer than 2^32 slots, and a 32-bit division costs a third
+    const long long blk = (slot >> 32) ? slot / p.block_size : (long long)((unsigned)slot / (unsigned)p.block_size);
+    return (blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size)) * p.head_dim;
+}
+
+constexpr int kMaxThreads = 640;
+
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kMaxThreads, 2) rotary_kernel(const __grid_constant__ RotaryParams p) {
+    // [2 tokens]: cosines of pairs 8c .. 8c+3, 8c+4 .. 8c+7, then the sines
+    // alike, [4][unit c], so that a warp's reads are consecutive
+    __shared__ float4 s_cs[2][4][kRotaryMaxDim / 16];
+    __shared__ long long s_dst[2];
     const int tid = threadIdx.x;
     const int upr = p.head_dim / 16;  // units of a head; the first rot_dim / 16 are turned
-    const int nrot = p.rot_dim / 16;
+    const int half = p.rot_dim / 2;
     const int c = tid % upr;
     const int row0 = tid / upr, rows_step = blockDim.x / upr;
-    const int rows = p.num_heads + 2 * p.num_kv_heads;
-    const bool turned = c < nrot;
-    // element offsets of the unit's two vectors inside a head
-    const int e0 = turned ? (p.interleaved ? c * 16 : c * 8) : c * 16;
-    const int e1 = turned && !p.interleaved ? p.rot_dim / 2 + c * 8 : e0 + 8;
+    const int rows_qk = p.num_heads + p.num_kv_heads, rows = rows_qk + p.num_kv_heads;
+    const bool turned = c < p.rot_dim / 16;
+    // element offsets of the unit's two vectors inside a head (the values' too: e0 and e1 cover the row either way)
+    const int e0 = turned && !kInterleaved ? c * 8 : c * 16;
+    const int e1 = turned && !kInterleaved ? half + c * 8 : e0 + 8;
+    const bool active = row0 < rows_step;  // threads past the last whole row of units move nothing
 
     pdl_wait();
     pdl_trigger();  // what follows may be placed; it waits for these writes
-    auto src_of = [&](int row) {
-        const T *base;
-        if (row < p.num_heads) base = static_cast<const T *>(p.query) + t * p.query_stride + (long long)row * p.head_dim;
-        else if (row < p.num_heads + p.num_kv_heads)
-            base = static_cast<const T *>(p.key) + t * p.key_stride + (long long)(row - p.num_heads) * p.head_dim;
-        else
-            base = static_cast<const T *>(p.value) + t * p.value_stride +
-                   (long long)(row - p.num_heads - p.num_kv_heads) * p.head_dim;
-        return base;
-    };
-    // the first row's vectors are on their way while the angles are computed
-    uint4 va = make_uint4(0, 0, 0, 0), vb = va;
-    int row = row0 < rows_step ? row0 : rows;  // threads past the last whole row of units take none
-    if (row < rows) {
-        const T *s = src_of(row);
-        va = ldg_stream(s + e0);
-        vb = ldg_stream(s + e1);
-    }
-    for (int i = tid; i < p.rot_dim / 2; i += blockDim.x) {
+
+    // threads [0, half) of the block's upper end turn pair `mine`, the last
+    // warp's first lane looks the slot up: not the threads with most rows
+    const int mine = (int)blockDim.x - 1 - tid;
+    long long frac = 0, frac2 = 0;  // turns per position in 2^-64, of pair `mine` (and mine + blockDim.x)
+    bool finite = true, finite2 = true;
+    auto turns_of = [&](int i, bool &ok) {
         const float f = p.inv_freq[i];
-        const int pos = p.positions[(long long)p.pair_axis[i] * p.num_tokens + t];
+        ok = isfinite(f);
         double turns = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
         turns -= rint(turns);
-        const long long frac = __double2ll_rn(turns * 18446744073709551616.0);  // of a turn, in 2^-64
-        const unsigned long long ang = (unsigned long long)frac * (unsigned long long)(long long)pos;
+        return __double2ll_rn(turns * 18446744073709551616.0);
+    };
+    if (mine < half) frac = turns_of(mine, finite);
+    if (mine + (int)blockDim.x < half) frac2 = turns_of(mine + blockDim.x, finite2);
+    auto angle = [&](int i, long long fr, bool ok, int pos, int buf) {
+        const unsigned long long ang = (unsigned long long)fr * (unsigned long long)(long long)pos;
         const int top = (int)(unsigned)((ang + 0x80000000ull) >> 32);
         float sn, cs;
         sincospif((float)top * 4.656612873077393e-10f, &sn, &cs);  // top * 2^-31 half turns
-        if (!isfinite(f)) sn = cs = __int_as_float(0x7fc00000);
-        float *q = reinterpret_cast<float *>(s_cs);
+        if (!ok) sn = cs = __int_as_float(0x7fc00000);
+        float *q = reinterpret_cast<float *>(s_cs[buf]);
         constexpr int plane = kRotaryMaxDim / 16 * 4;
         const int u = i >> 3, k = (i >> 2) & 1;
         q[k * plane + u * 4 + (i & 3)] = cs;
         q[(2 + k) * plane + u * 4 + (i & 3)] = sn;
+    };
+    auto prepare = [&](int t, int buf) {
+        if (mine < half)
+            angle(mine, frac, finite, p.positions[(long long)p.pair_axis[mine] * p.num_tokens + t], buf);
+        if (mine + (int)blockDim.x < half)
+            angle(mine + blockDim.x, frac2, finite2,
+                  p.positions[(long long)p.pair_axis[mine + blockDim.x] * p.num_tokens + t], buf);
+        if (tid == 0) s_dst[buf] = cache_row(p, p.slots[t]);
+    };
+    auto src_of = [&](int t, int row) {
+        if (row < p.num_heads) return static_cast<const T *>(p.query) + t * p.query_stride + row * p.head_dim;
+        if (row < rows_qk) return static_cast<const T *>(p.key) + t * p.key_stride + (row - p.num_heads) * p.head_dim;
+        return static_cast<const T *>(p.value) + t * p.value_stride + (row - rows_qk) * p.head_dim;
+    };
+
+    int t = blockIdx.x, buf = 0;
+    uint4 va = make_uint4(0, 0, 0, 0), vb = va;
+    if (active && row0 < rows) {
+        const T *s = src_of(t, row0);
+        va = ldg_stream(s + e0);
+        vb = ldg_stream(s + e1);
     }
-    if (tid == 0) {
-        const long long slot = p.slots[t];
-        long long dst = -1;
-        if (slot >= (long long)p.num_blocks * p.block_size) {
-            flag_error(p.d_err, PA_DEVERR_SLOT_RANGE);
-        } else if (slot >= 0) {
-            const long long blk = slot / p.block_size;
-            dst = (blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size)) * p.head_dim;
-        }
-        s_dst = dst;
-    }
+    prepare(t, 0);
     __syncthreads();
-    const long long dst = s_dst;
-    float cs[8], sn[8];
-    if (turned) {
+    for (; t < p.num_tokens; t += gridDim.x, buf ^= 1) {
+        const int t_next = t + gridDim.x;
+        if (active) {
+            const long long dst = s_dst[buf];
+            float cs[8], sn[8];
+            if (turned) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float4 x = s_cs[k][c], y = s_cs[2 + k][c];
-            cs[4 * k] = x.x, cs[4 * k + 1] = x.y, cs[4 * k + 2] = x.z, cs[4 * k + 3] = x.w;
-            sn[4 * k] = y.x, sn[4 * k + 1] = y.y, sn[4 * k + 2] = y.z, sn[4 * k + 3] = y.w;
-        }
-    }
-    while (row < rows) {
-        const int next = row + rows_step;
-        uint4 na = va, nb = vb;
-        if (next < rows) {
-            const T *s = src_of(next);
-            na = ldg_stream(s + e0);
-            nb = ldg_stream(s + e1);
-        }
-        if (turned && row < p.num_heads + p.num_kv_heads) {
-            float a[8], b[8];
-            unpack8<T>(va, a);
-            unpack8<T>(vb, b);
-            if (p.interleaved) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = a[2 * k], y = a[2 * k + 1], z = b[2 * k], w = b[2 * k + 1];
-                    a[2 * k] = fmaf(x, cs[k], -(y * sn[k]));
-                    a[2 * k + 1] = fmaf(y, cs[k], x * sn[k]);
-                    b[2 * k] = fmaf(z, cs[4 + k], -(w * sn[4 + k]));
-                    b[2 * k + 1] = fmaf(w, cs[4 + k], z * sn[4 + k]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float x = a[k], y = b[k];
-                    a[k] = fmaf(x, cs[k], -(y * sn[k]));
-                    b[k] = fmaf(y, cs[k], x * sn[k]);
+                for (int k = 0; k < 2; ++k) {
+                    const float4 x = s_cs[buf][k][c], y = s_cs[buf][2 + k][c];
+                    cs[4 * k] = x.x, cs[4 * k + 1] = x.y, cs[4 * k + 2] = x.z, cs[4 * k + 3] = x.w;
+                    sn[4 * k] = y.x, sn[4 * k + 1] = y.y, sn[4 * k + 2] = y.z, sn[4 * k + 3] = y.w;
                 }
             }
-            va = pack8<T>(a);
-            vb = pack8<T>(b);
+            for (int row = row0; row < rows; row += rows_step) {
+                // the next unit's vectors, of this token or the next
+                const bool more = row + rows_step < rows;
+                uint4 na = va, nb = vb;
+                if (more || t_next < p.num_tokens) {
+                    const T *s = more ? src_of(t, row + rows_step) : src_of(t_next, row0);
+                    na = ldg_stream(s + e0);
+                    nb = ldg_stream(s + e1);
+                }
+                if (turned && row < rows_qk) {
+                    float a[8], b[8];
+                    unpack8<T>(va, a);
+                    unpack8<T>(vb, b);
+                    if (kInterleaved) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float x = a[2 * k], y = a[2 * k + 1], z = b[2 * k], w = b[2 * k + 1];
+                            a[2 * k] = fmaf(x, cs[k], -(y * sn[k]));
+                            a[2 * k + 1] = fmaf(y, cs[k], x * sn[k]);
+                            b[2 * k] = fmaf(z, cs[4 + k], -(w * sn[4 + k]));
+                            b[2 * k + 1] = fmaf(w, cs[4 + k], z * sn[4 + k]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float x = a[k], y = b[k];
+                            a[k] = fmaf(x, cs[k], -(y * sn[k]));
+                            b[k] = fmaf(y, cs[k], x * sn[k]);
+                        }
+                    }
+                    va = pack8<T>(a);
+                    vb = pack8<T>(b);
+                }
+                T *out = nullptr;
+                if (row < p.num_heads) {
+                    out = static_cast<T *>(p.query_out) + t * p.query_out_stride + row * p.head_dim;
+                } else if (dst >= 0) {
+                    const bool is_v = row >= rows_qk;
+                    const long long h = row - (is_v ? rows_qk : p.num_heads);
+                    out = static_cast<T *>(is_v ? p.v_cache : p.k_cache) + dst + h * p.block_size * p.head_dim;
+                }
+                if (out) {
+                    *reinterpret_cast<uint4 *>(out + e0) = va;
+                    *reinterpret_cast<uint4 *>(out + e1) = vb;
+                }
+                va = na;
+                vb = nb;
+            }
         }
-        T *out = nullptr;
-        if (row < p.num_heads) {
-            out = static_cast<T *>(p.query_out) + t * p.query_out_stride + (long long)row * p.head_dim;
-        } else if (dst >= 0) {
-            const bool is_v = row >= p.num_heads + p.num_kv_heads;
-            const long long h = row - p.num_heads - (is_v ? p.num_kv_heads : 0);
-            out = static_cast<T *>(is_v ? p.v_cache : p.k_cache) + dst + h * p.block_size * p.head_dim;
-        }
-        if (out) {
-            // values have no turned units: their two vectors lie side by side all the same, e0 and e1 cover the row
-            *reinterpret_cast<uint4 *>(out + e0) = va;
-            *reinterpret_cast<uint4 *>(out + e1) = vb;
-        }
-        va = na;
-        vb = nb;
-        row = next;
+        if (t_next < p.num_tokens) prepare(t_next, buf ^ 1);
+        __syncthreads();  // the next token's angles are written, and this one's read
     }
+}
+
+template <typename T, bool kInterleaved>
+int launch_t(const RotaryParams &p, int threads, cudaStream_t stream) {
+    auto kern = rotary_kernel<T, kInterleaved>;
+    static std::atomic<int> resident[kMaxThreads / 32 + 1];  // CTAs an SM holds, by block size; asked for once
+    int n = resident[threads / 32].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess || n < 1) return PA_ERR_CUDA;
+        resident[threads / 32].store(n, std::memory_order_relaxed);
+    }
+    const int grid = std::min(p.num_tokens, sm_count() * n);
+    return launch_pdl(kern, dim3(grid), dim3(threads), 0, stream, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
 
 int launch_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream) {
-    // enough threads that a token's units take one pass, up to 640
+    // A token's units take one pass of up to kMaxThreads threads; the grid
+    // is one wave of resident CTAs, which walk the tokens.
     const int units = (p.num_heads + 2 * p.num_kv_heads) * (p.head_dim / 16);
-    const int threads = std::min(640, std::max(64, (units + 31) / 32 * 32));
-    cudaError_t e;
-    if (dt == PA_BF16) e = launch_pdl(rotary_kernel<__nv_bfloat16>, dim3(p.num_tokens), dim3(threads), 0, stream, p);
-    else e = launch_pdl(rotary_kernel<__half>, dim3(p.num_tokens), dim3(threads), 0, stream, p);
-    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    const int passes = (units + kMaxThreads - 1) / kMaxThreads;
+    const int threads = std::max(64, ((units + passes - 1) / passes + 31) / 32 * 32);
+    if (dt == PA_BF16) return p.interleaved ? launch_t<__nv_bfloat16, true>(p, threads, stream)
+                                             : launch_t<__nv_bfloat16, false>(p, threads, stream);
+    return p.interleaved ? launch_t<__half, true>(p, threads, stream) : launch_t<__half, false>(p, threads, stream);
 }
 
 }  // namespace pa

@@ -24,8 +24,7 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = 4;  // tokens per thread
-constexpr int kChunk = kThreads * kItems;
+constexpr int kMembers = 16;  // sequences of a row taken together
 
 // the decode kernels' clamping of a sequence's length
 __device__ __forceinline__ int clamped_len(const DecodeParams &p, int s) {
@@ -93,11 +92,15 @@ __device__ __forceinline__ void load_scores(const float *a, float (&x)[G]) {
     }
 }
 
-template <typename T, int D, int G>
+// kItems tokens per thread: 4 (2 at eight heads, for registers), or 1 when the
+// rows are too few to fill the GPU.
+// kMany: several sequences add to a row.
+template <typename T, int D, int G, int kItems, bool kMany>
 __global__ void __launch_bounds__(kThreads)
     weights_merge_kernel(const __grid_constant__ DecodeParams p, const float *weights, float *weights_out, int width,
                          int queries_per_row, int chunks, int merge_ctas) {
-    __shared__ float2 s_ml[G];  // a member's (maximum, 1 / sum) per head
+    __shared__ float2 s_ml[(kMany ? kMembers : 1) * G];  // (maximum, 1 / sum) per sequence and head
+    __shared__ int s_len[kMany ? kMembers : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();  // the decode kernel's scores and partials are complete and visible
     pdl_trigger();
@@ -109,65 +112,121 @@ __global__ void __launch_bounds__(kThreads)
     const int u = blockIdx.x - merge_ctas;
     const int chunk = u % chunks, rh = u / chunks;
     const int r = rh / p.num_kv_heads, kvh = rh - r * p.num_kv_heads;
-    const int j0 = chunk * kChunk;
+    const int j0 = chunk * kThreads * kItems + tid;  // this thread's tokens: j0 + i * kThreads
+    const int s0 = r * queries_per_row;
     float acc[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) acc[i] = 0.f;
-    int longest = 0;
-    for (int m = 0; m < queries_per_row; ++m) {
-        const int s = r * queries_per_row + m;
-        const int L = clamped_len(p, s);
-        longest = max(longest, L);
-        if (j0 >= L) continue;  // the same in every thread
-        const int nparts = (L + p.partition_tokens - 1) / p.partition_tokens;
-        __syncthreads();  // the previous member's s_ml is read
-        for (int h = warp; h < G; h += kThreads / 32) {
-            const float2 *ml = p.ws_ml + ((size_t)s * p.num_heads + kvh * G + h) * p.slots;
-            float M = -INFINITY;
-            for (int i = lane; i < nparts; i += 32) M = fmaxf(M, ml[i].x);
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
-            float sum = 0.f;
-            if (M != -INFINITY)
-                for (int i = lane; i < nparts; i += 32) sum = fmaf(fast_exp2(ml[i].x - M), ml[i].y, sum);
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
-            // no key attended: 2^(-inf - 0) = 0 for every one of them
-            if (lane == 0) s_ml[h] = M == -INFINITY ? make_float2(0.f, 0.f) : make_float2(M, 1.f / sum);
-        }
-        __syncthreads();
-        float2 ml[G];
-#pragma unroll
-        for (int h = 0; h < G; ++h) ml[h] = s_ml[h];
+    auto load = [&](int s, int L, float (&x)[kItems][G]) {
         const float *sc = p.scores + ((size_t)(s * p.num_kv_heads + kvh) * p.score_stride + j0) * G;
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int j = i * kThreads + tid;
-            if (j0 + j < L) {
-                float x[G];
-                load_scores<G>(sc + (size_t)j * G, x);
+            if (j0 + i * kThreads < L) {
+                load_scores<G>(sc + (size_t)i * kThreads * G, x[i]);
+            } else {
 #pragma unroll
-                for (int h = 0; h < G; ++h) acc[i] = fmaf(fast_exp2(x[h] - ml[h].x), ml[h].y, acc[i]);
+                for (int h = 0; h < G; ++h) x[i][h] = -INFINITY;
             }
         }
-    }
-    const size_t at = (size_t)rh * width + j0;
+    };
+    // (maximum, 1 / sum) of a sequence's head over its partitions, by a warp
+    auto max_sum = [&](int s, int h, int L) {
+        const int nparts = (L + p.partition_tokens - 1) / p.partition_tokens;
+        const float2 *ml = p.ws_ml + ((size_t)s * p.num_heads + kvh * G + h) * p.slots;
+        const float2 mine = lane < nparts ? ml[lane] : make_float2(-INFINITY, 0.f);
+        float M = mine.x;
+        for (int i = lane + 32; i < nparts; i += 32) M = fmaxf(M, ml[i].x);
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int j = i * kThreads + tid;
-        if (j0 + j < longest) weights_out[at + j] = weights[at + j] + acc[i];
+        for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
+        if (M == -INFINITY) return make_float2(0.f, 0.f);  // no key attended: 2^(-inf - 0) = 0 for every one of them
+        float sum = fast_exp2(mine.x - M) * mine.y;
+        for (int i = lane + 32; i < nparts; i += 32) sum = fmaf(fast_exp2(ml[i].x - M), ml[i].y, sum);
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
+        return make_float2(M, 1.f / sum);
+    };
+    const size_t at = (size_t)rh * width + j0;
+    if constexpr (!kMany) {
+        // everything that does not depend on the maxima and sums is under way while they are put together
+        const int L = clamped_len(p, s0);
+        if (j0 - tid >= L) return;
+        float x[kItems][G], w[kItems];
+        load(s0, L, x);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) w[i] = j0 + i * kThreads < L ? weights[at + i * kThreads] : 0.f;
+        if (warp < G) {
+            const float2 ml = max_sum(s0, warp, L);
+            if (lane == 0) s_ml[warp] = ml;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float2 ml = s_ml[h];
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) acc[i] = fmaf(fast_exp2(x[i][h] - ml.x), ml.y, acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+            if (j0 + i * kThreads < L) weights_out[at + i * kThreads] = w[i] + acc[i];
+    } else {
+        int longest = 0;
+        for (int m0 = 0; m0 < queries_per_row; m0 += kMembers) {
+            const int nm = min(kMembers, queries_per_row - m0);
+            float x[kItems][G];
+            load(s0 + m0, clamped_len(p, s0 + m0), x);
+            if (m0) __syncthreads();  // the previous sequences' values are read
+            for (int mh = warp; mh < nm * G; mh += kThreads / 32) {
+                const int s = s0 + m0 + mh / G, h = mh % G;
+                const int L = clamped_len(p, s);
+                const float2 ml = max_sum(s, h, L);
+                if (lane == 0) {
+                    s_ml[mh] = ml;
+                    if (h == 0) s_len[mh / G] = L;
+                }
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int m = 0; m < nm; ++m) {
+                longest = max(longest, s_len[m]);
+                float y[kItems][G];
+                const bool more = m + 1 < nm;
+                if (more) load(s0 + m0 + m + 1, s_len[m + 1], y);
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    const float2 ml = s_ml[m * G + h];
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) acc[i] = fmaf(fast_exp2(x[i][h] - ml.x), ml.y, acc[i]);
+                }
+                if (more) {
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                        for (int h = 0; h < G; ++h) x[i][h] = y[i][h];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+            if (j0 + i * kThreads < longest) weights_out[at + i * kThreads] = weights[at + i * kThreads] + acc[i];
     }
 }
 
 template <typename T, int D, int G>
 int launch_merge_t(const DecodeParams &p, const float *weights, float *weights_out, int width, int queries_per_row,
                    cudaStream_t stream) {
-    const int chunks = std::max(1, (p.max_context_len + kChunk - 1) / kChunk);
+    const long long rows = (long long)(p.num_seqs / queries_per_row) * p.num_kv_heads;
+    constexpr int kMost = G == 8 ? 2 : 4;
+    const bool few = rows * ((p.max_context_len + kMost * kThreads - 1) / (kMost * kThreads)) < 2 * sm_count();
+    const int chunk = few ? kThreads : kMost * kThreads;
+    const int chunks = std::max(1, (p.max_context_len + chunk - 1) / chunk);
     const long long pairs = (long long)p.num_seqs * p.num_heads;
     const long long merge = p.max_partitions > 1 ? (pairs + kThreads / 32 - 1) / (kThreads / 32) : 0;
-    const long long total = merge + (long long)(p.num_seqs / queries_per_row) * p.num_kv_heads * chunks;
+    const long long total = merge + rows * chunks;
     if (total > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-    return launch_pdl(weights_merge_kernel<T, D, G>, dim3((unsigned)total), dim3(kThreads), 0, stream, p, weights,
+    auto kern = queries_per_row > 1
+                    ? (few ? weights_merge_kernel<T, D, G, 1, true> : weights_merge_kernel<T, D, G, kMost, true>)
+                    : (few ? weights_merge_kernel<T, D, G, 1, false> : weights_merge_kernel<T, D, G, kMost, false>);
+    return launch_pdl(kern, dim3((unsigned)total), dim3(kThreads), 0, stream, p, weights,
                       weights_out, width, queries_per_row, chunks, (int)merge) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;

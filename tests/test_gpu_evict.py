@@ -90,6 +90,9 @@ CASES = [
     ([9000], 8999, 1, 1, 1, 64, 32, "f16", "ties"),            # one token goes
     ([9000, 20000], 70, 4, 32, 1, 64, 8, "bf16", "odd"),
     ([20000], 20001, 0, 0, 1, 64, 16, "bf16", "random"),       # nothing goes: moved as it is
+    ([33000, 5], 15000, 7, 900, 1, 64, 64, "f16", "ties"),     # rows spread over eight CTAs, one of them all but empty
+    ([65537], 30000, 7, 900, 1, 64, 128, "bf16", "equal"),     # one token more than eight CTAs hold at once
+    ([150001], 70001, 0, 33, 1, 64, 128, "f16", "odd"),
 ]
 
 
