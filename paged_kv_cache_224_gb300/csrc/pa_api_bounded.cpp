@@ -75,16 +75,20 @@ struct PrefixWs {
              int group_size, int prefix_blocks, int partition_tokens) {
         const int prefix = prefix_blocks * block_size;
         const int longest = max_context_len - prefix;
-        pt = partition_for(num_seqs, num_heads, num_kv_heads, block_size, longest, partition_tokens);
-        ok = pt > 0;
+        ok = partition_tokens >= 0 && partition_tokens % block_size == 0;
         if (!ok) return;
-        pieces = pa::prefix_pieces(num_seqs / group_size, group_size, prefix, num_heads / num_kv_heads, num_kv_heads);
-        slots = pieces + std::max(1, (int)(((long long)longest + pt - 1) / pt));
+        pt = partition_tokens ? partition_tokens
+                              : pa::prefix_partition_tokens(num_seqs, num_kv_heads, block_size, longest);
+        const int partitions = std::max(1, (int)(((long long)longest + pt - 1) / pt));
+        pieces = pa::prefix_pieces(num_seqs / group_size, group_size, prefix, num_heads / num_kv_heads, num_kv_heads,
+                                   longest, partitions, num_seqs);
+        slots = pieces + partitions;
         const PartialWs w(num_seqs, num_heads, head_dim, slots);
         acc = w.acc;
         ml = w.ml;
     }
-    size_t total() const { return acc + ml; }
+    // ... and the decode instances' queue counter
+    size_t total() const { return acc + ml + 256; }
 };
 
 bool prefix_sizes_ok(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
@@ -332,9 +336,8 @@ int pa_decode_common_prefix(void *out, const void *query, const void *k_cache, c
     d.max_partitions = w.slots - w.pieces;
     d.force_partials = 1;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int rc = pa::launch_prefix(dtype, block_size, group, pp, d.scale_log2, st);
-    if (rc != PA_OK) return rc;
-    rc = pa::launch_decode(dtype, head_dim, block_size, group, d, st);
+    pp.queue = reinterpret_cast<unsigned *>(static_cast<char *>(workspace) + w.acc + w.ml);
+    const int rc = pa::launch_prefix(dtype, block_size, group, pp, st);
     if (rc != PA_OK) return rc;
     return pa::launch_prefix_merge(dtype, group, pp, st);
 }

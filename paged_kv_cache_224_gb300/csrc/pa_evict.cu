@@ -16,8 +16,8 @@
 //           The totals are read once, into registers (up to 4096 or 8192 a CTA;
 //           rows of more than 65536 read them again in every pass); a cluster's CTAs read each
 //           other's histograms and counts through distributed shared memory.
-//           The CTAs of kv head 0 also look for new blocks named twice or still
-//           read, and strike them from owner[];
+//           Beside them one CTA per sequence looks for new blocks named twice
+//           or still read, and strikes them from owner[];
 //   copy    HBM-bound: 16-byte vectors of the kept rows, K and V, to the new
 //           blocks that owner[] still grants.
 // owner[] needs no clearing: an entry e counts for block b only if the new
@@ -61,6 +61,42 @@ __global__ void __launch_bounds__(128) evict_mark_kernel(const __grid_constant__
     }
 }
 
+// One CTA per sequence, beside the selecting ones: its new length, and the new
+// blocks that cannot be written.
+__device__ __forceinline__ void check_blocks(const EvictParams &p, int s) {
+    bool bad;
+    const int L = evict_len(p, s, &bad);
+    const int n = min(L, p.keep);
+    if (threadIdx.x == 0) {
+        if (bad) flag_error(p.d_err, PA_DEVERR_CONTEXT_RANGE);
+        p.new_context_lens[s] = n;
+    }
+    // a new block that two entries name belongs to neither
+    for (int j = threadIdx.x; j < blocks_of(n, p.block_size); j += blockDim.x) {
+        const int e = s * p.new_max_blocks + j, b = p.new_block_tables[e];
+        if (b >= 0 && b < p.num_blocks && p.owner[b] != e) {
+            p.owner[b] = kStruck;
+            flag_error(p.d_err, PA_DEVERR_COPY_PAIR);
+        }
+    }
+    // nor does one that this sequence's table reads
+    for (int j = threadIdx.x; j < blocks_of(L, p.block_size); j += blockDim.x) {
+        const int b = p.block_tables[(size_t)s * p.max_blocks + j];
+        if (b < 0 || b >= p.num_blocks) {
+            flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
+            continue;
+        }
+        const int e = p.owner[b];
+        if (e < 0 || e >= p.num_seqs * p.new_max_blocks || p.new_block_tables[e] != b) continue;
+        const int es = e / p.new_max_blocks;
+        bool eb;
+        if (e - es * p.new_max_blocks < blocks_of(min(evict_len(p, es, &eb), p.keep), p.block_size)) {
+            p.owner[b] = kStruck;
+            flag_error(p.d_err, PA_DEVERR_COPY_PAIR);
+        }
+    }
+}
+
 // Totals as unsigned integers of the same order; NaN sorts below everything,
 // and the two zeros are one value.
 __device__ __forceinline__ unsigned order_key(float x) {
@@ -81,10 +117,10 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     __shared__ unsigned s_sum[256];
     __shared__ uint2 s_warp[kSelWarps];
     __shared__ uint2 s_cta[2];      // this CTA's counts of a round (alternating), read by the others
-    __shared__ unsigned s_pick[2];  // the digit, and how many are still to be taken below it
+    __shared__ unsigned s_pick[3];  // the digit, how many of its keys are to be taken, and how many there are
     const int rank = CL > 1 ? blockIdx.x % CL : 0;
     const int row = blockIdx.x / CL;
-    const int s = row / p.num_kv_heads, h = row - s * p.num_kv_heads;
+    const int s = row / p.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto all_sync = [] {
         if constexpr (CL > 1) cg::this_cluster().sync();
@@ -94,6 +130,11 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     __syncthreads();
     pdl_wait();
     pdl_trigger();
+    if (row >= p.num_seqs * p.num_kv_heads) {  // clusters that do not select (and so never sync)
+        const int seq = blockIdx.x - p.num_seqs * p.num_kv_heads * CL;
+        if (seq < p.num_seqs) check_blocks(p, seq);
+        return;
+    }
     bool bad;
     const int L = evict_len(p, s, &bad);
     const int n = min(L, p.keep);
@@ -109,46 +150,22 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     const int lo = min(p.sink, L), hi = max(lo, L - p.recent);  // the tokens that are ranked
     const bool cut = L > p.keep;
 
+    // Loads first, without conditions on j (a clamped index instead), so that
+    // all of them are in flight at once.
+    auto fetch = [&](int r, float (&x)[kSelItems]) {
+#pragma unroll
+        for (int i = 0; i < kSelItems; ++i)
+            if (i * 32 < wseg) x[i] = w[min(r * round_len + first + i * 32, L - 1)];
+    };
     unsigned key[kSelItems];
     auto load = [&](int r) {
+        float x[kSelItems];
+        fetch(r, x);
 #pragma unroll
-        for (int i = 0; i < kSelItems; ++i) {
-            const int j = r * round_len + first + i * 32;
-            key[i] = i * 32 < wseg && j < L ? order_key(w[j]) : 0u;
-        }
+        for (int i = 0; i < kSelItems; ++i)
+            if (i * 32 < wseg) key[i] = order_key(x[i]);
     };
-    load(0);
-
-    if (h == 0) {
-        if (tid == 0 && rank == 0) {
-            if (bad) flag_error(p.d_err, PA_DEVERR_CONTEXT_RANGE);
-            p.new_context_lens[s] = n;
-        }
-        // a new block that two entries name belongs to neither
-        for (int j = rank * kSelThreads + tid; j < blocks_of(n, p.block_size); j += CL * kSelThreads) {
-            const int e = s * p.new_max_blocks + j, b = p.new_block_tables[e];
-            if (b >= 0 && b < p.num_blocks && p.owner[b] != e) {
-                p.owner[b] = kStruck;
-                flag_error(p.d_err, PA_DEVERR_COPY_PAIR);
-            }
-        }
-        // nor does one that this sequence's table reads
-        for (int j = rank * kSelThreads + tid; j < blocks_of(L, p.block_size); j += CL * kSelThreads) {
-            const int b = p.block_tables[(size_t)s * p.max_blocks + j];
-            if (b < 0 || b >= p.num_blocks) {
-                flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
-                continue;
-            }
-            const int e = p.owner[b];
-            if (e < 0 || e >= p.num_seqs * p.new_max_blocks || p.new_block_tables[e] != b) continue;
-            const int es = e / p.new_max_blocks;
-            bool eb;
-            if (e - es * p.new_max_blocks < blocks_of(min(evict_len(p, es, &eb), p.keep), p.block_size)) {
-                p.owner[b] = kStruck;
-                flag_error(p.d_err, PA_DEVERR_COPY_PAIR);
-            }
-        }
-    }
+    if (L > 0) load(0);  // (an empty row has no segments either)
 
     // ---- threshold: the `want` largest of the tokens [lo, hi)
     unsigned thr = 0u, eq_take = 0u;  // keys above thr are kept, and the first eq_take equal to it
@@ -208,6 +225,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
                     if (before < want && want <= before + c[i]) {
                         s_pick[0] = 255u - (unsigned)(lane * 8 + i);
                         s_pick[1] = want - before;
+                        s_pick[2] = c[i];
                     }
                     before += c[i];
                 }
@@ -215,29 +233,40 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
             __syncthreads();
             prefix = (prefix << 8) | s_pick[0];
             want = s_pick[1];
+            if (want == s_pick[2]) {
+                // all keys that begin with these digits are taken: no more digits needed
+                prefix <<= shift;
+                thr = prefix ? prefix - 1u : 0u;
+                eq_take = prefix ? 0u : 0xffffffffu;
+                break;
+            }
+            thr = prefix;
+            eq_take = want;
         }
-        thr = prefix;
-        eq_take = want;
     }
 
     // ---- emit in index order.  A token's place is the count of sure ones
     // before it plus that of those at the threshold, at most eq_take.
     uint2 base = make_uint2(0u, 0u);  // (sure, at the threshold) in earlier rounds
-    for (int r = 0; r < rounds; ++r) {
+    for (int r = 0; r < rounds && L > 0; ++r) {
+        float x[kSelItems];
+        fetch(r, x);  // the totals to move, while the counts are put together
         if (rounds > 1) load(r);
-        unsigned sure[kSelItems], at[kSelItems];  // the warp's ballots
+        // the warp's tokens of item i that are kept for sure, and those at the threshold
+        auto ballots = [&](int i, unsigned &sure, unsigned &at) {
+            const int j = r * round_len + first + i * 32;
+            const bool ranked = cut && j >= lo && j < hi;
+            sure = __ballot_sync(kFull, j < L && (!ranked || key[i] > thr));
+            at = __ballot_sync(kFull, j < L && ranked && key[i] == thr);
+        };
         uint2 mine = make_uint2(0u, 0u);
 #pragma unroll
         for (int i = 0; i < kSelItems; ++i) {
-            sure[i] = at[i] = 0u;
-            if (i * 32 < wseg) {
-                const int j = r * round_len + first + i * 32;
-                const bool ranked = cut && j >= lo && j < hi;
-                sure[i] = __ballot_sync(kFull, j < L && (!ranked || key[i] > thr));
-                at[i] = __ballot_sync(kFull, j < L && ranked && key[i] == thr);
-            }
-            mine.x += __popc(sure[i]);
-            mine.y += __popc(at[i]);
+            if (i * 32 >= wseg) break;
+            unsigned sure, at;
+            ballots(i, sure, at);
+            mine.x += __popc(sure);
+            mine.y += __popc(at);
         }
         if (lane == 0) s_warp[warp] = mine;
         __syncthreads();
@@ -266,16 +295,16 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
 #pragma unroll
         for (int i = 0; i < kSelItems; ++i) {
             if (i * 32 >= wseg) break;
-            const unsigned eq = before.y + __popc(at[i] & below);
-            const unsigned pos = before.x + __popc(sure[i] & below) + min(eq, eq_take);
-            const bool is_at = at[i] >> lane & 1u;
-            if ((sure[i] >> lane & 1u) || (is_at && eq < eq_take)) {
-                const int j = r * round_len + first + i * 32;
-                kept[pos] = j;
-                nw[pos] = w[j];
+            unsigned sure, at;
+            ballots(i, sure, at);
+            const unsigned eq = before.y + __popc(at & below);
+            const unsigned pos = before.x + __popc(sure & below) + min(eq, eq_take);
+            if ((sure >> lane & 1u) || ((at >> lane & 1u) && eq < eq_take)) {
+                kept[pos] = r * round_len + first + i * 32;
+                nw[pos] = x[i];
             }
-            before.x += __popc(sure[i]);
-            before.y += __popc(at[i]);
+            before.x += __popc(sure);
+            before.y += __popc(at);
         }
         base.x += total.x;
         base.y += total.y;
@@ -351,12 +380,13 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
 }
 
 constexpr int kNarrow = 256, kNarrowItems = 16;
-constexpr int kWide = 1024, kWideItems = 8;
+constexpr int kWide = 512, kWideItems = 16;
 
 template <int CL, int kThreads, int kItems>
 int launch_select(const EvictParams &p, long long rows, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * CL));
+    // a CTA per sequence beside them, in whole clusters
+    cfg.gridDim = dim3((unsigned)(rows * CL + (p.num_seqs + CL - 1) / CL * CL));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -381,13 +411,13 @@ int launch_evict(const EvictParams &p, cudaStream_t stream) {
     if (rows * chunks > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
     // CTAs per row: as many as hold it in registers, and more while the rows
     // leave SMs idle and each CTA still has 2048 tokens.  Rows that need more
-    // than eight CTAs of 256 threads get CTAs of 1024.
+    // than eight CTAs of 256 threads get CTAs of 512.
     const int longest = std::min(p.max_context_len, p.width);
     int cl = 1;
     while (cl < 8 && ((long long)cl * kNarrow * kNarrowItems < longest ||
                       (rows * cl * 2 <= sm_count() && longest >= 2 * cl * 2048)))
         cl *= 2;
-    if (rows * cl > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    if (rows * cl + p.num_seqs + cl > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
     const bool wide = (long long)cl * kNarrow * kNarrowItems < longest;
     const int rc = wide      ? launch_select<8, kWide, kWideItems>(p, rows, stream)
                    : cl == 1 ? launch_select<1, kNarrow, kNarrowItems>(p, rows, stream)

@@ -216,20 +216,33 @@ int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const P
                    void *workspace, size_t workspace_bytes, cudaStream_t stream);
 // Attention of a batch over long shared prefixes (pa_decode_common_prefix):
 // `groups` groups of group_size consecutive sequences, each over the first
-// prefix_tokens tokens of its first sequence's table.  A unit's key tiles are
-// shared out over the CTAs as in the stream-K prefill, and each piece of a
-// unit leaves an unnormalised partial in its own slot; prefix_pieces is the
-// most pieces a unit can be cut into.
-int prefix_pieces(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads);
+// prefix_tokens tokens of its first sequence's table, and every sequence over
+// its own tokens.  A unit's key tiles are shared out over the CTAs as in the
+// stream-K prefill, and each piece of a unit leaves an unnormalised partial in
+// its own slot; prefix_pieces is the most pieces a unit can be cut into.
 struct PrefixParams {
-    DecodeParams d;              // the tail pass's parameters: d.slots, d.part_base (= pieces), d.len_offset
+    DecodeParams d;              // of the own tokens: d.slots, d.part_base (= pieces), d.len_offset
     int groups, group_size, prefix_tokens;
+    unsigned *queue;             // the decode instances' shared unit queue, one counter
 };
-int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp, float scale_log2,
-                  cudaStream_t stream);
+// One launch: the prefixes of up to kPrefillMaxSeqs groups; the last one also
+// runs the own tokens of every sequence.
+struct PrefixLaunch {
+    PrefillParams pp;
+    DecodeParams dp;
+    int prefix_ctas, decode_units;
+    unsigned *decode_next;
+};
+int prefix_pieces(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads, int longest_own,
+                  int partitions, int num_seqs);
+// Partition length of the own tokens when the caller leaves it open: the
+// decode instances take units from a queue, so a sequence is split only as far
+// as it takes to give each about four.
+int prefix_partition_tokens(int num_seqs, int num_kv_heads, int block_size, int longest_own);
+int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp, cudaStream_t stream);
 int launch_prefix_merge(pa_dtype dt, int group, const PrefixParams &pp, cudaStream_t stream);
-int launch_prefix_bf16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
-int launch_prefix_f16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
+int launch_prefix_bf16(int block_size, int group, const PrefixLaunch &pl, unsigned grid, cudaStream_t stream);
+int launch_prefix_f16(int block_size, int group, const PrefixLaunch &pl, unsigned grid, cudaStream_t stream);
 // Whether launch_mixed has a kernel for these (head_dim 128, a tensor-core
 // decode group, block_size 16..128).
 bool mixed_supported(int head_dim, int block_size, int group);

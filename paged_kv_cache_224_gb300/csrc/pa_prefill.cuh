@@ -597,8 +597,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 tmem_wait_ld();
                 if (valid) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(dst + c * 32 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int e = 0; e < 32; e += 8) st_global_v8(dst + c * 32 + e, v + e);
                 }
             }
         };

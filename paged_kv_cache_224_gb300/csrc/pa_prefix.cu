@@ -1,6 +1,6 @@
 // Decode attention for batches that share a long prefix
-// (pa_decode_common_prefix): the schedule of the prefix pass (pa_prefix.cuh)
-// and the merge of its partials with those of the sequences' own tokens.
+// (pa_decode_common_prefix): the schedule of the step (pa_prefix.cuh) and the
+// merge of its partials.
 //
 // With x = the keys of the prefix and of the sequence's own tokens, cut into
 // pieces, a piece's partial is (acc, m, l) = (sum 2^(s_j - m) V_j, max s_j,
@@ -16,6 +16,41 @@ using namespace pfx;
 
 constexpr int kMergeWarps = 4;
 
+// Prefix CTAs of a launch, the rest decoding from the start, by a time model
+// (figures measured on a GB300).  A prefix CTA takes about 5 us to its first
+// tile, 1.8 us for a 128-key tile of 256 rows, and 3 us for the end of each
+// segment, so counts that cut units evenly are better than those that leave
+// every CTA pieces of two.  A decode instance, two to a CTA, takes about 3.2 us
+// for a unit's chain of loads (its number, length, table entries, keys) and
+// then 40 GB/s, all together at most 6.4 TB/s.  A CTA whose prefix tiles are
+// done decodes, some 4 us later.  The count is even (a prefix CTA that shares
+// its SM pair with a decoding one runs a third longer).  Measured on 256
+// sequences after 8192 tokens, own tokens up to 512, 64/8 heads: 123 us at 64
+// prefix CTAs (one unit each), 129 at 96, 136 at 152, 223 at 32.
+int split_ctas(long long tiles, int unit_tiles, double units, double unit_bytes) {
+    const int sms = sm_count();
+    const double t_unit = 3.2e-6 + unit_bytes / 40e9;
+    auto rate = [&](int ctas) {  // units per second
+        const double r = 2.0 * ctas / t_unit;
+        return unit_bytes > 0 ? std::min(r, 6.4e12 / unit_bytes) : r;
+    };
+    int best = 2;
+    double best_t = 1e30;
+    for (int n = 2; n <= sms; n += 2) {
+        const long long q = (tiles + n - 1) / n;
+        const bool even = tiles % n == 0 && (q % unit_tiles == 0 || unit_tiles % q == 0);
+        const double segments = (double)((q + unit_tiles - 1) / unit_tiles) + (even ? 0.0 : 1.0);
+        const double tp = 5e-6 + q * 1.8e-6 + segments * 3e-6;
+        const double done = rate(sms - n) * tp;
+        const double t = units <= done ? tp : tp + 4e-6 + std::max(t_unit, (units - done) / rate(sms));
+        if (t < best_t) {
+            best_t = t;
+            best = n;
+        }
+    }
+    return best;
+}
+
 // Schedule of one launch of `groups` groups (at most kPrefillMaxSeqs).
 struct PrefixSchedule {
     long long tiles;  // key tiles of all units
@@ -23,13 +58,37 @@ struct PrefixSchedule {
     int n;            // key tiles per unit
     int ctas;
 };
-PrefixSchedule prefix_schedule(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads) {
+PrefixSchedule prefix_schedule(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads,
+                               double units, double unit_bytes) {
     PrefixSchedule s;
     s.row_tiles = (int)(((long long)group_size * group + kUnitRows - 1) / kUnitRows);
     s.n = (prefix_tokens + kNK - 1) / kNK;
     s.tiles = (long long)groups * num_kv_heads * s.row_tiles * s.n;
-    s.ctas = (int)std::min<long long>(sm_count(), s.tiles);
+    s.ctas = (int)std::min<long long>(split_ctas(s.tiles, s.n, units, unit_bytes), s.tiles);
     return s;
+}
+
+// The launches of a call: full ones, whose CTAs have nothing to decode, and the
+// last, with the own tokens of all sequences.
+struct Schedules {
+    PrefixSchedule full, last;
+    int last_groups;
+};
+Schedules schedules(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads, int longest_own,
+                    int partitions, int num_seqs) {
+    Schedules x;
+    x.last_groups = (groups - 1) % kPrefillMaxSeqs + 1;
+    x.full = prefix_schedule(kPrefillMaxSeqs, group_size, prefix_tokens, group, num_kv_heads, 0.0, 0.0);
+    // the own tokens' lengths are on the device: half of the longest each
+    const double bytes = 0.5 * longest_own * (2 * kD * 2) * num_kv_heads * num_seqs;
+    const double units = longest_own > 0 ? (double)num_seqs * num_kv_heads * std::max(1.0, 0.5 * partitions) : 0.0;
+    x.last = prefix_schedule(x.last_groups, group_size, prefix_tokens, group, num_kv_heads, units,
+                             units > 0 ? bytes / units : 0.0);
+    return x;
+}
+Schedules schedules(const PrefixParams &pp, int group) {
+    return schedules(pp.groups, pp.group_size, pp.prefix_tokens, group, pp.d.num_kv_heads,
+                     pp.d.max_context_len - pp.prefix_tokens, pp.d.max_partitions, pp.d.num_seqs);
 }
 
 // Where the merge finds a row's prefix partials.
@@ -69,32 +128,57 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const long long W = last ? mp.last_tiles : mp.full_tiles, N = last ? mp.last_ctas : mp.full_ctas;
     const int r = (k * mp.head_group + hq % mp.head_group) / kUnitRows;
     const int x = ((gl * p.num_kv_heads + kvh) * mp.row_tiles + r) * mp.n;
-    const int pre = cta_of(x + mp.n - 1, W, N) - cta_of(x, W, N) + 1;
+    // (a 32-bit division where the numbers allow it: a third of the 64-bit one's time)
+    const int pre = W * N < (1LL << 31)
+                        ? (int)(((unsigned)(x + mp.n) * (unsigned)N - 1u) / (unsigned)W -
+                                ((unsigned)(x + 1) * (unsigned)N - 1u) / (unsigned)W) + 1
+                        : cta_of(x + mp.n - 1, W, N) - cta_of(x, W, N) + 1;
+    // The prefix partials do not depend on the sequence's length: they are on
+    // their way while it is fetched, and the first of its own while their
+    // maxima are compared.
+    constexpr int kAhead = 4;
+    const size_t base = (size_t)pair * p.slots;
+    auto acc_of = [&](size_t sl) { return *reinterpret_cast<const float4 *>(p.ws_acc + sl * kD + lane * VPL); };
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float2 none = make_float2(-INFINITY, 0.f);
+    float4 a[kAhead], b[kAhead / 2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) a[i] = i < pre ? acc_of(base + i) : zero;
+    const float2 ml_pre = lane < pre ? p.ws_ml[base + lane] : none;
     // the sequence's own partitions, clamped like the decode kernels
     const int cap = (int)min((long long)p.max_context_len, (long long)p.max_blocks_per_seq * p.block_size) - p.len_offset;
     const int L = max(0, min(p.context_lens[s] - p.len_offset, cap));
     const int own = (L + p.partition_tokens - 1) / p.partition_tokens;
-    const int total = pre + own;
-    const size_t base = (size_t)pair * p.slots;
-    auto slot = [&](int i) { return base + (i < pre ? i : p.part_base + i - pre); };
-    float M = -INFINITY;
-    for (int i = lane; i < total; i += 32) M = fmaxf(M, p.ws_ml[slot(i)].x);
+    const size_t own_base = base + p.part_base;
+#pragma unroll
+    for (int i = 0; i < kAhead / 2; ++i) b[i] = i < own ? acc_of(own_base + i) : zero;
+    const float2 ml_own = lane < own ? p.ws_ml[own_base + lane] : none;
+    float M = fmaxf(ml_pre.x, ml_own.x);
+    for (int i = lane + 32; i < pre; i += 32) M = fmaxf(M, p.ws_ml[base + i].x);
+    for (int i = lane + 32; i < own; i += 32) M = fmaxf(M, p.ws_ml[own_base + i].x);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, m));
     float lsum = 0.f, o[VPL];
 #pragma unroll
     for (int d = 0; d < VPL; ++d) o[d] = 0.f;
+    auto add = [&](float2 ml, float4 x) {
+        const float w = fast_exp2(ml.x - M);
+        lsum = fmaf(w, ml.y, lsum);
+        o[0] = fmaf(w, x.x, o[0]); o[1] = fmaf(w, x.y, o[1]);
+        o[2] = fmaf(w, x.z, o[2]); o[3] = fmaf(w, x.w, o[3]);
+    };
+    auto lane_ml = [&](const float2 &ml, int i) {
+        return make_float2(__shfl_sync(kFull, ml.x, i), __shfl_sync(kFull, ml.y, i));
+    };
     if (M != -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) add(lane_ml(ml_pre, i), a[i]);  // (past the last: weight 0)
 #pragma unroll 4
-        for (int i = 0; i < total; ++i) {
-            const size_t sl = slot(i);
-            const float2 ml = p.ws_ml[sl];
-            const float w = fast_exp2(ml.x - M);
-            lsum = fmaf(w, ml.y, lsum);
-            const float4 a = *reinterpret_cast<const float4 *>(p.ws_acc + sl * kD + lane * VPL);
-            o[0] = fmaf(w, a.x, o[0]); o[1] = fmaf(w, a.y, o[1]);
-            o[2] = fmaf(w, a.z, o[2]); o[3] = fmaf(w, a.w, o[3]);
-        }
+        for (int i = kAhead; i < pre; ++i) add(p.ws_ml[base + i], acc_of(base + i));
+#pragma unroll
+        for (int i = 0; i < kAhead / 2; ++i) add(lane_ml(ml_own, i), b[i]);
+#pragma unroll 4
+        for (int i = kAhead / 2; i < own; ++i) add(p.ws_ml[own_base + i], acc_of(own_base + i));
     }
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
     uint2 u;
@@ -105,24 +189,35 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 
 }  // namespace
 
-int prefix_pieces(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads) {
-    int most = 1;
-    // the full launches' schedule and the last one's
-    for (int g : {std::min(groups, kPrefillMaxSeqs), (groups - 1) % kPrefillMaxSeqs + 1}) {
-        const PrefixSchedule s = prefix_schedule(g, group_size, prefix_tokens, group, num_kv_heads);
-        // a unit's first and last pieces, and whole ranges of at least q tiles between them
+int prefix_pieces(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads, int longest_own,
+                  int partitions, int num_seqs) {
+    const Schedules x =
+        schedules(groups, group_size, prefix_tokens, group, num_kv_heads, longest_own, partitions, num_seqs);
+    // a unit's first and last pieces, and whole ranges of at least q tiles between them
+    auto most = [](const PrefixSchedule &s) {
         const long long q = s.tiles / s.ctas;
-        if (s.n > 1) most = std::max<int>(most, (int)std::min<long long>(s.ctas, 2 + (s.n - 2) / q));
-    }
-    return most;
+        return s.n > 1 ? (int)std::min<long long>(s.ctas, 2 + (s.n - 2) / q) : 1;
+    };
+    return groups > kPrefillMaxSeqs ? std::max(most(x.full), most(x.last)) : most(x.last);
 }
 
-int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp, float scale_log2,
-                  cudaStream_t stream) {
+int prefix_partition_tokens(int num_seqs, int num_kv_heads, int block_size, int longest_own) {
+    const long long want = 4LL * 2 * sm_count(), have = (long long)num_seqs * num_kv_heads;
+    const long long parts = std::max(1LL, want / have);
+    const long long pt = std::max<long long>(256, (std::max(longest_own, 1) + parts - 1) / parts);
+    return (int)((pt + block_size - 1) / block_size * block_size);
+}
+
+int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp, cudaStream_t stream) {
     const DecodeParams &d = pp.d;
     // TMA row coordinates are 32-bit
     if ((long long)d.num_blocks * d.num_kv_heads * block_size >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
-    PrefillParams p{};
+    const bool any_own = d.max_context_len > pp.prefix_tokens;
+    const long long units = any_own ? (long long)d.max_partitions * d.num_seqs * d.num_kv_heads : 0;
+    if (units > 0x3fffffffLL) return PA_ERR_UNSUPPORTED;
+    const Schedules x = schedules(pp, group);
+    PrefixLaunch pl{};
+    PrefillParams &p = pl.pp;
     p.query = d.query;
     p.k_cache = d.k_cache;
     p.v_cache = d.v_cache;
@@ -130,13 +225,17 @@ int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp
     p.num_heads = d.num_heads;
     p.num_kv_heads = d.num_kv_heads;
     p.num_blocks = d.num_blocks;
-    p.scale_log2 = scale_log2;
+    p.scale_log2 = d.scale_log2;
     p.query_rows = d.num_seqs;
     p.part_o = d.ws_acc;
     p.part_ml = d.ws_ml;
     p.part_slots = d.slots;
+    pl.dp = d;
+    pl.decode_next = pp.queue;
+    if (cudaMemsetAsync(pp.queue, 0, sizeof(unsigned), stream) != cudaSuccess) return PA_ERR_CUDA;
     for (int g0 = 0; g0 < pp.groups; g0 += kPrefillMaxSeqs) {
-        p.num_seqs = std::min(kPrefillMaxSeqs, pp.groups - g0);
+        const bool last = g0 + kPrefillMaxSeqs >= pp.groups;
+        p.num_seqs = last ? x.last_groups : kPrefillMaxSeqs;
         for (int i = 0; i < p.num_seqs; ++i) {
             PrefillSeq &q = p.seqs[i];
             q.row_start = (g0 + i) * pp.group_size;
@@ -144,12 +243,14 @@ int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp
             q.prefix_len = pp.prefix_tokens - 1;
             q.chunk_len = pp.group_size;
         }
-        long long units = 0;
-        int rc = prefill_schedule<true>(p, group, &units);
+        long long rows_units = 0;
+        int rc = prefill_schedule<true>(p, group, &rows_units);
         if (rc != PA_OK) return rc;
-        const PrefixSchedule s = prefix_schedule(p.num_seqs, pp.group_size, pp.prefix_tokens, group, d.num_kv_heads);
-        rc = dt == PA_BF16 ? launch_prefix_bf16(block_size, group, p, (unsigned)s.ctas, stream)
-                           : launch_prefix_f16(block_size, group, p, (unsigned)s.ctas, stream);
+        pl.prefix_ctas = last ? x.last.ctas : x.full.ctas;
+        pl.decode_units = last ? (int)units : 0;
+        const unsigned grid = last && any_own ? (unsigned)sm_count() : (unsigned)pl.prefix_ctas;
+        rc = dt == PA_BF16 ? launch_prefix_bf16(block_size, group, pl, grid, stream)
+                           : launch_prefix_f16(block_size, group, pl, grid, stream);
         if (rc != PA_OK) return rc;
     }
     return PA_OK;
@@ -157,20 +258,18 @@ int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp
 
 int launch_prefix_merge(pa_dtype dt, int group, const PrefixParams &pp, cudaStream_t stream) {
     const DecodeParams &d = pp.d;
+    const Schedules x = schedules(pp, group);
     MergeParams mp{};
     mp.group_size = pp.group_size;
     mp.head_group = group;
     mp.prefix_blocks = pp.prefix_tokens / d.block_size;
-    const int last = (pp.groups - 1) % kPrefillMaxSeqs + 1;
-    const PrefixSchedule f = prefix_schedule(kPrefillMaxSeqs, pp.group_size, pp.prefix_tokens, group, d.num_kv_heads);
-    const PrefixSchedule l = prefix_schedule(last, pp.group_size, pp.prefix_tokens, group, d.num_kv_heads);
-    mp.row_tiles = l.row_tiles;
-    mp.n = l.n;
-    mp.full_tiles = pp.groups > kPrefillMaxSeqs ? (int)f.tiles : 1;
-    mp.full_ctas = pp.groups > kPrefillMaxSeqs ? f.ctas : 1;
-    mp.last_first = pp.groups - last;
-    mp.last_tiles = (int)l.tiles;
-    mp.last_ctas = l.ctas;
+    mp.row_tiles = x.last.row_tiles;
+    mp.n = x.last.n;
+    mp.full_tiles = pp.groups > kPrefillMaxSeqs ? (int)x.full.tiles : 1;
+    mp.full_ctas = pp.groups > kPrefillMaxSeqs ? x.full.ctas : 1;
+    mp.last_first = pp.groups - x.last_groups;
+    mp.last_tiles = (int)x.last.tiles;
+    mp.last_ctas = x.last.ctas;
     const long long pairs = (long long)d.num_seqs * d.num_heads;
     const long long merge = (pairs + kMergeWarps - 1) / kMergeWarps;
     if (merge + d.num_seqs > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;

@@ -1,8 +1,8 @@
-// f16 instances of the shared-prefix pass.
+// f16 instances of the shared-prefix step.
 #include "pa_prefix.cuh"
 
 namespace pa {
-int launch_prefix_f16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream) {
-    return pfx::launch_prefix_dtype<__half>(block_size, group, p, grid, stream);
+int launch_prefix_f16(int block_size, int group, const PrefixLaunch &pl, unsigned grid, cudaStream_t stream) {
+    return pfx::launch_prefix_dtype<__half>(block_size, group, pl, grid, stream);
 }
 }  // namespace pa
