@@ -372,7 +372,17 @@ PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const 
  *                  row: 1 for plain decode; several query positions over one
  *                  cache (the last positions of a prompt observing it, several
  *                  new tokens at once) repeat the sequence's block-table row,
- *                  each with its own context length
+ *                  each with its own context length, and need scale > 0.  From
+ *                  16 query rows (positions times heads per kv head) on, at
+ *                  head_dim 128 and block_size >= 16, they are attended together
+ *                  on the tensor cores: the row of the first position is the one
+ *                  that is read (another that differs in a position's context
+ *                  sets PA_DEVERR_PREFIX, outputs and totals undefined), the
+ *                  softmax weights are rounded to dtype for their product with
+ *                  V as in pa_prefill_chunk (the totals take them in fp32),
+ *                  partition_tokens has no effect, and a V row that holds a NaN
+ *                  or infinity within the longest of the contexts reaches the
+ *                  outputs of the others
  *   workspace      >= pa_decode_weights_workspace_bytes(...) bytes, 256-byte
  *                  aligned, scratch: the partials, and every score in fp32
  *                  (num_seqs * num_heads * max_context_len * 4 bytes)
@@ -381,7 +391,8 @@ PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const 
  * partition_tokens, data errors as for pa_decode.
  */
 PA_API size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                                                int block_size, int max_context_len, int partition_tokens);
+                                                int block_size, int max_context_len, int queries_per_row,
+                                                int partition_tokens);
 PA_API int pa_decode_weights(void *out, const void *query, const void *k_cache, const void *v_cache,
                              const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
                              int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,

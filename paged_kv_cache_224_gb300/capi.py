@@ -120,7 +120,7 @@ def lib() -> ctypes.CDLL:
         f = ctypes.c_float
         L.pa_rotary_and_cache.argtypes = [p, i64, p, i64, p, i64, p, i64, p, p, p, p, p, p] + [i] * 10 + [p, p]
         L.pa_rotary_and_cache.restype = i
-        L.pa_decode_weights_workspace_bytes.argtypes = [i] * 7
+        L.pa_decode_weights_workspace_bytes.argtypes = [i] * 8
         L.pa_decode_weights_workspace_bytes.restype = sz
         L.pa_decode_weights.argtypes = [p, p, p, p, p, i, p, i, i, i, i, i, i, i, f, i, p, p, i, i, i, p, sz, p, p]
         L.pa_decode_weights.restype = i
@@ -595,18 +595,18 @@ def pa_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, position
 
 
 def pa_decode_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
-                                      partition_tokens=0) -> int:
+                                      queries_per_row=1, partition_tokens=0) -> int:
     return lib().pa_decode_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
-                                                   max_context_len, partition_tokens)
+                                                   max_context_len, queries_per_row, partition_tokens)
 
 
 def decode_weights_workspace(query, num_kv_heads, block_size, max_context_len, partition_tokens=0, queries_per_row=1,
                              stream=None):
-    """Allocate (with torch) a workspace big enough for ``pa_decode_weights``
-    (whatever the number of queries per row of totals)."""
+    """Allocate (with torch) a workspace big enough for ``pa_decode_weights``."""
     B, Hq, D = query.shape
     with torch.cuda.device(query.device):
-        n = pa_decode_weights_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, partition_tokens)
+        n = pa_decode_weights_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, queries_per_row,
+                                              partition_tokens)
     return _scratch(query.device, n, stream)
 
 
@@ -634,7 +634,7 @@ def pa_decode_weights(out, query, k_cache, v_cache, block_tables, context_lens, 
             wshape[0] != B // queries_per_row or wshape[1] != Hkv or weights_out.shape != wshape:
         raise ValueError("shape mismatch")
     if workspace is None:
-        workspace = decode_weights_workspace(query, Hkv, bs, max_context_len, partition_tokens, stream=stream)
+        workspace = decode_weights_workspace(query, Hkv, bs, max_context_len, partition_tokens, queries_per_row, stream)
     _call("pa_decode_weights", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB,
           int(max_context_len), float(scale), int(partition_tokens), weights.data_ptr(), weights_out.data_ptr(), wshape[2],

@@ -46,22 +46,32 @@ struct PartialWs {
     }
 };
 
-// Decode over the kept scores: the partials, then the scores.
+// Decode with kept scores: the partials, then the scores.  `window`: the rows of
+// several queries are attended together.
 struct WeightsWs {
-    int pt, slots;
-    long long stride;  // tokens of a (sequence, kv head)'s scores
+    int pt = 1, slots;
+    long long stride;  // tokens of a query row's scores
     size_t acc, ml, scores;
-    bool ok;
+    bool window, ok;
     WeightsWs(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
-              int partition_tokens) {
-        pt = partition_for(num_seqs, num_heads, num_kv_heads, block_size, max_context_len, partition_tokens);
-        ok = pt > 0;
-        if (!ok) return;
-        slots = std::max(1, (int)(((long long)max_context_len + pt - 1) / pt));
+              int queries_per_row, int partition_tokens) {
+        const int group = num_heads / num_kv_heads;
+        window = pa::window_supported(head_dim, block_size, group, queries_per_row);
+        if (window) {
+            ok = partition_tokens >= 0 && partition_tokens % block_size == 0;
+            if (!ok) return;
+            slots = pa::window_pieces(num_seqs / queries_per_row, queries_per_row, group, num_kv_heads, max_context_len);
+            stride = pa::window_score_stride(max_context_len);
+        } else {
+            pt = partition_for(num_seqs, num_heads, num_kv_heads, block_size, max_context_len, partition_tokens);
+            ok = pt > 0;
+            if (!ok) return;
+            slots = std::max(1, (int)(((long long)max_context_len + pt - 1) / pt));
+            stride = ((long long)max_context_len + 3) / 4 * 4;
+        }
         const PartialWs w(num_seqs, num_heads, head_dim, slots);
-        acc = slots > 1 ? w.acc : 0;
+        acc = slots > 1 || window ? w.acc : 0;
         ml = w.ml;
-        stride = ((long long)max_context_len + 3) / 4 * 4;
         scores = round256((size_t)num_seqs * num_heads * stride * sizeof(float));
     }
     size_t total() const { return acc + ml + scores; }
@@ -184,11 +194,12 @@ int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const void *q
 }
 
 size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                                         int max_context_len, int partition_tokens) {
+                                         int max_context_len, int queries_per_row, int partition_tokens) {
     if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
-        block_size <= 0 || max_context_len < 0)
+        block_size <= 0 || max_context_len < 0 || queries_per_row <= 0 || num_seqs % queries_per_row)
         return 0;
-    const WeightsWs w(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_tokens);
+    const WeightsWs w(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, queries_per_row,
+                      partition_tokens);
     return w.ok ? w.total() : 0;
 }
 
@@ -203,6 +214,7 @@ int pa_decode_weights(void *out, const void *query, const void *k_cache, const v
         return PA_ERR_INVALID_ARG;
     if (num_heads % num_kv_heads || num_seqs % queries_per_row) return PA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || max_context_len > weights_len) return PA_ERR_OUT_OF_RANGE;
+    if (queries_per_row > 1 && !(scale > 0.f)) return PA_ERR_OUT_OF_RANGE;
     if (num_seqs == 0) return PA_OK;
     if (!out || !query || !k_cache || !v_cache || !block_tables || !context_lens ||
         (weights_len > 0 && (!weights || !weights_out)))
@@ -212,7 +224,8 @@ int pa_decode_weights(void *out, const void *query, const void *k_cache, const v
     if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGNMENT;
     const size_t totals = (size_t)(num_seqs / queries_per_row) * num_kv_heads * weights_len * sizeof(float);
     if (weights != weights_out && overlap(weights, totals, weights_out, totals)) return PA_ERR_INVALID_ARG;
-    const WeightsWs w(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_tokens);
+    const WeightsWs w(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, queries_per_row,
+                      partition_tokens);
     if (!w.ok) return PA_ERR_OUT_OF_RANGE;
     if (!workspace || workspace_bytes < w.total()) return PA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return PA_ERR_ALIGNMENT;
@@ -227,6 +240,8 @@ int pa_decode_weights(void *out, const void *query, const void *k_cache, const v
     p.scores = reinterpret_cast<float *>(base + w.acc + w.ml);
     p.score_stride = w.stride;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (w.window)
+        return pa::launch_window(dtype, block_size, group, p, queries_per_row, weights, weights_out, weights_len, st);
     const int rc = pa::launch_decode_scores(dtype, head_dim, block_size, group, p, st);
     if (rc != PA_OK) return rc;
     return pa::launch_weights_merge(dtype, head_dim, group, p, weights, weights_out, weights_len, queries_per_row, st);

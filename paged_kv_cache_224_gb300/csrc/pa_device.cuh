@@ -118,13 +118,6 @@ __device__ __forceinline__ uint4 lds128(const void *p) {
     return v;
 }
 
-// Eight floats to a 32-byte aligned global address in one store: a whole sector.
-__device__ __forceinline__ void st_global_v8(float *p, const float *v) {
-    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
-}
-
 // ---------------------------------------------------------------- 16-bit data
 
 template <typename T> struct Elem;

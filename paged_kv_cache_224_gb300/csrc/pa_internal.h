@@ -104,6 +104,13 @@ struct PrefillParams {
     unsigned *counters;          // split: [units][2 Q tiles] segments counted so far; zero on entry, and
                                  // the merging segment resets its unit's to zero before the call ends
     int part_slots;              // shared prefix: part_o and part_ml are [row][Hq][part_slots], one slot per piece
+    // several queries over one cache (kWindow): query row r of the call has
+    // context_lens[r] tokens, at most len_cap; the scores (not scaled) go to
+    // [row_base + entry of seqs][kv head][chunk_len * G rows][score_stride]
+    const int32_t *context_lens;
+    int len_cap, row_base;
+    float *scores;
+    long long score_stride;
     PrefillSeq seqs[kPrefillMaxSeqs];
 };
 
@@ -243,6 +250,18 @@ int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp
 int launch_prefix_merge(pa_dtype dt, int group, const PrefixParams &pp, cudaStream_t stream);
 int launch_prefix_bf16(int block_size, int group, const PrefixLaunch &pl, unsigned grid, cudaStream_t stream);
 int launch_prefix_f16(int block_size, int group, const PrefixLaunch &pl, unsigned grid, cudaStream_t stream);
+// Several query positions over one cache, with the totals of their weights
+// (pa_decode_weights with enough queries per row): every row of queries_per_row
+// consecutive sequences is attended together on the tensor cores, its scores
+// kept (window_score_stride floats per query row and head), and then merged and
+// added up.  window_pieces: the most pieces (partials) of a unit.
+bool window_supported(int head_dim, int block_size, int group, int queries_per_row);
+int window_pieces(int rows, int queries_per_row, int group, int num_kv_heads, int max_context_len);
+inline long long window_score_stride(int max_context_len) { return ((long long)max_context_len + 127) / 128 * 128; }
+int launch_window(pa_dtype dt, int block_size, int group, const DecodeParams &d, int queries_per_row,
+                  const float *weights, float *weights_out, int width, cudaStream_t stream);
+int launch_window_bf16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
+int launch_window_f16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
 // Whether launch_mixed has a kernel for these (head_dim 128, a tensor-core
 // decode group, block_size 16..128).
 bool mixed_supported(int head_dim, int block_size, int group);

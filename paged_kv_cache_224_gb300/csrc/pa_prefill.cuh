@@ -69,7 +69,9 @@
 // (pa_prefix.cuh): the "chunk" is the group's sequences, one query position
 // each, no row is ahead of another (prefix_len is the last key of them all),
 // and every segment leaves its partial in its rows' workspace slots for a
-// later merge with the sequences' own tokens.
+// later merge with the sequences' own tokens.  kWindow instances on top of that
+// serve several query positions over one cache (pa_window.cuh): each position
+// has its own context length, on the device, and every score is kept.
 #pragma once
 
 #include <cuda.h>
@@ -128,10 +130,22 @@ struct Seg {
     int n;
     int x_unit;    // global index of the unit's first key tile
     int unit;      // global index of the unit
+    int adv;       // tiles of the schedule: t1 - t0, unless kWindow's lengths end before t1
+    int longest;   // kWindow: tokens of the longest context
 };
 
+// kWindow: context length of query row s, and the longest of a sequence's rows (by a whole warp).
+__device__ __forceinline__ int window_len(const PrefillParams &p, int s) {
+    return max(0, min(p.context_lens[s], p.len_cap));
+}
+__device__ __forceinline__ int window_longest(const PrefillParams &p, const PrefillSeq &q) {
+    int m = 0;
+    for (int i = threadIdx.x & 31; i < q.chunk_len; i += 32) m = max(m, window_len(p, q.row_start + i));
+    return __reduce_max_sync(kFull, m);
+}
+
 // The segment that starts at global tile x and ends at x_end or at the end of its unit.
-template <int G, bool kPrefix>
+template <int G, bool kPrefix, bool kWindow>
 __device__ __forceinline__ Seg seg_at(const PrefillParams &p, int x, int x_end) {
     int si = 0;
     for (int i = 1; i < p.num_seqs; ++i)
@@ -154,6 +168,13 @@ __device__ __forceinline__ Seg seg_at(const PrefillParams &p, int x, int x_end) 
     s.t1 = min(n, rem + (x_end - x));
     s.x_unit = x - rem;
     s.unit = q.unit_start + s.h * q.row_tiles + r;
+    s.adv = s.t1 - s.t0;
+    if constexpr (kWindow) {
+        // the schedule is laid out for the longest context allowed: a segment
+        // ends where the sequence does, and may be empty
+        s.longest = window_longest(p, q);
+        s.t1 = max(s.t0, min(s.t1, (s.longest + kNK - 1) / kNK));
+    }
     return s;
 }
 
@@ -305,19 +326,41 @@ __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, uns
     if (t == 0) *counter = 0u;  // ready for the next call
 }
 
+// kPrefix: a segment's partial -- O as it stands (the calling thread's TMEM lane
+// at tO), maximum and sum -- into the slot of its piece, if the row exists;
+// every lane runs the warp-collective TMEM loads.  Out of line like
+// finish_partial.
+static __device__ __noinline__ void store_partial(float *part_o, float2 *part_ml, size_t first_slot, bool valid, uint32_t tO,
+                                           int cta, int x_unit, int W, int N, float m_run, float l_run) {
+    const size_t slot = first_slot + (cta - cta_of(x_unit, W, N));
+    float *dst = part_o + slot * kD;
+    if (valid) part_ml[slot] = make_float2(m_run, l_run);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_ld32_wait(tO + c * 32, v);
+        if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4 *>(dst + c * 32 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+    }
+}
+
 // ---- the kernel ------------------------------------------------------------
 
 // The prefill work of CTA `cta` of `ncta`: with the stream-K schedule, its
 // share of the key tiles; without, unit `cta` (all of the CTA's threads call this).
 // Returns the CTA's TMEM base; with kKeepTmem (the one-launch step, whose
 // prefill CTAs go on to decode) the allocation is left for the caller to free.
-template <typename T, int BS, int G, bool kKeepTmem = false, bool kPrefix = false>
+template <typename T, int BS, int G, bool kKeepTmem = false, bool kPrefix = false, bool kWindow = false>
 __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CUtensorMap &tmk,
                                                 const CUtensorMap &tmv, const CUtensorMap &tmq, int cta, int ncta) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr int kBlocksPerTile = kNK / BS;
     static_assert(kNK % BS == 0 && BS % 8 == 0 && 32 % kBlocksPerTile == 0, "block_size");
     static_assert(kM % G == 0, "group");
+    static_assert(kPrefix || !kWindow, "a window leaves partials");
 
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -413,10 +456,17 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
         };
         int sc = 0;
         for (int x = x0; x < x1; ++sc) {
-            const Seg sg = seg_at<G, kPrefix>(p, x, x1);
+            const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
+            if (kWindow && sg.t1 == sg.t0) {
+                x += sg.adv;
+                --sc;
+                continue;
+            }
             const PrefillSeq &q = p.seqs[sg.si];
             const int32_t *table = q.block_table;
-            const int kend = last_key<kPrefix>(q.prefix_len, min(q.chunk_len - 1, ((sg.r + 1) * kUnitRows - 1) / G));
+            const int kend = kWindow ? sg.longest - 1
+                                     : last_key<kPrefix>(q.prefix_len,
+                                                         min(q.chunk_len - 1, ((sg.r + 1) * kUnitRows - 1) / G));
             // Table entries come 32 at a time, one per lane, a whole chunk ahead
             // of use (a chunk covers 32 / kBlocksPerTile tiles); lane b <
             // kBlocksPerTile handles block b of a tile.
@@ -443,12 +493,12 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 // segment its slots free up only as the previous one ends
                 if (j == sg.t0) load_q(sg, sc);
             }
-            x += sg.t1 - sg.t0;
+            x += sg.adv;
         }
         // every copy has normally been consumed by now; after a timeout, let
         // the ones in flight land before the CTA can exit
         if (lane == 0)
-            for (int i = max(0, nitems - kSlots); i < nitems; ++i) mbar_wait(&full[i % kSlots], (uint32_t)(i / kSlots) & 1u);
+            for (int i = max(0, item - kSlots); i < item; ++i) mbar_wait(&full[i % kSlots], (uint32_t)(i / kSlots) & 1u);
     } else if (warp == 1) {
         // ============================================================ MMA issuer
         // One thread issues; the whole warp takes the P announcements, which
@@ -468,8 +518,13 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             const uint32_t v_lo0 = desc_lo(sb + kOffKV, 1024);   // MN-major: second 64-dim half 1 KB on
             int tc = 0;  // tiles of earlier segments
             for (int x = x0, sc = 0; x < x1; ++sc) {
-                const Seg sg = seg_at<G, kPrefix>(p, x, x1);
+                const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
                 const int nt = sg.t1 - sg.t0;
+                if (kWindow && nt == 0) {
+                    x += sg.adv;
+                    --sc;
+                    continue;
+                }
                 if (lane == 0) wait_or_flag(q_full, (uint32_t)sc & 1u, p.d_err);
                 for (int k = 0; k <= nt; ++k) {
                     const int gt = tc + k;  // this CTA's tile count
@@ -514,7 +569,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     }
                 }
                 tc += nt;
-                x += nt;
+                x += sg.adv;
             }
         }
     } else if (warp == 2 + 4 * kQT) {
@@ -526,7 +581,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
         // steady state
         int gt = 0;
         for (int x = x0; x < x1;) {
-            const Seg sg = seg_at<G, kPrefix>(p, x, x1);
+            const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
             const int nt = sg.t1 - sg.t0;
             for (int k = 0; k < nt; ++k, ++gt) {
                 if (lane == 0) {
@@ -540,7 +595,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 __syncwarp();
                 named_bar_sync(kBarL, 64);
             }
-            x += nt;
+            x += sg.adv;
         }
     } else if (warp < 2 + 4 * kQT) {
         // ============================================================ softmax
@@ -564,6 +619,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             rw.ipos = rw.valid ? gr / G : 0;
             rw.head = rw.valid ? gr % G : 0;
             rw.plim = last_key<kPrefix>(q.prefix_len, min(gr / G, q.chunk_len - 1));
+            if constexpr (kWindow) rw.plim = window_len(p, q.row_start + min(gr / G, q.chunk_len - 1)) - 1;
             return rw;
         };
         // O (TMEM) times inv, rounded once, into this thread's output row if
@@ -588,35 +644,50 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             }
         };
 
-        // O as it stands into a workspace row, likewise
-        [[maybe_unused]] auto store_partial = [&](float *dst, bool valid) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[32];
-                tmem_ld32(tO + c * 32, v);
-                tmem_wait_ld();
-                if (valid) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) st_global_v8(dst + c * 32 + e, v + e);
-                }
-            }
-        };
-
         // Only what the tile loop needs stays live across it; the segment is
         // computed again for its epilogue (the softmax runs at the register limit).
         int gt = 0;  // this CTA's tile count: ring items and barrier phases
         for (int x = x0, sc = 0; x < x1; ++sc) {
             int nt, j0, jn, plim, plim_min, kend;
+            [[maybe_unused]] int adv;                       // kWindow: tiles of the schedule
+            [[maybe_unused]] float *srow = nullptr;         // kWindow: this row's kept scores, or none
+            [[maybe_unused]] const int32_t *wtable = nullptr;
             {
-                const Seg sg = seg_at<G, kPrefix>(p, x, x1);
+                const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
                 const PrefillSeq &q = p.seqs[sg.si];
                 nt = sg.t1 - sg.t0;
+                if constexpr (kWindow) adv = sg.adv;
                 j0 = sg.t0;
                 jn = sg.n - 1;  // the unit's last key tile
-                plim = row_of(sg).plim;
+                const Row rw = row_of(sg);
+                plim = rw.plim;
                 // smallest limit in the Q tile, and the unit's last key
                 plim_min = last_key<kPrefix>(q.prefix_len, min((sg.r * kUnitRows + g * kM) / G, q.chunk_len - 1));
                 kend = last_key<kPrefix>(q.prefix_len, min(q.chunk_len - 1, ((sg.r + 1) * kUnitRows - 1) / G));
+                if constexpr (kWindow) {
+                    const size_t rows = (size_t)q.chunk_len * G;
+                    const size_t gr = (size_t)sg.r * kUnitRows + g * kM + t;
+                    if (rw.valid)
+                        srow = p.scores + ((size_t)((p.row_base + sg.si) * p.num_kv_heads + sg.h) * rows + gr) * p.score_stride;
+                    wtable = q.block_table;
+                    plim_min = __reduce_min_sync(kFull, plim);
+                    kend = sg.longest - 1;
+                    jn = kend / kNK;
+                }
+            }
+            if constexpr (kWindow) {
+                if (nt == 0) {
+                    // nothing of the sequence here: an empty partial
+                    const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
+                    const Row rw = row_of(sg);
+                    if (rw.valid)
+                        p.part_ml[((size_t)(p.seqs[sg.si].row_start + rw.ipos) * p.num_heads + sg.h * G + rw.head) *
+                                      p.part_slots + (cta - cta_of(sg.x_unit, p.total_tiles, ncta))] =
+                            make_float2(-INFINITY, 0.f);
+                    x += adv;
+                    --sc;
+                    continue;
+                }
             }
 
             float m_run = -INFINITY;  // running max in scaled log2 units
@@ -625,6 +696,12 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             for (int e = 0; e < 4; ++e) l2[e] = make_float2(0.f, 0.f);
             for (int k = 0; k < nt; ++k, ++gt) {
                 const int j = j0 + k;  // key tile of the unit
+                [[maybe_unused]] int went = -1;  // kWindow: the tile's table entry `lane`, fetched behind the wait
+                if constexpr (kWindow) {
+                    const int b = j * kBlocksPerTile + lane;
+                    if (lane < kBlocksPerTile && b * BS <= kend) went = wtable[b];
+                    else went = 0;
+                }
                 wait_or_flag(&s_full[g], (uint32_t)gt & 1u, p.d_err);
                 tc_fence_after();
                 if (g == kQT - 1 && t == 0) {
@@ -647,9 +724,23 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 tmem_ld32p(tS + 64, s + 64);
                 tmem_ld32p(tS + 96, s + 96);
                 tmem_wait_ld();
+                if constexpr (kWindow) tie(s);  // the scores go straight to stores
                 if (need_mask) {
 #pragma unroll
                     for (int c = 0; c < kNK; ++c) s[c] = (kb + c <= plim) ? s[c] : -INFINITY;
+                }
+                if constexpr (kWindow) {
+                    // keys whose table entry is out of the pool (flagged by the producer) are left out
+                    const unsigned bad = __ballot_sync(kFull, went < 0 || went >= p.num_blocks);
+                    if (bad) {
+#pragma unroll
+                        for (int c = 0; c < kNK; ++c) s[c] = (bad >> (c / BS) & 1u) ? -INFINITY : s[c];
+                    }
+                    if (srow) {
+#pragma unroll
+                        for (int c = 0; c < kNK; c += 4)
+                            *reinterpret_cast<float4 *>(srow + kb + c) = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
+                    }
                 }
                 // row max with three-input maxima: 8 chains over the 128 columns
                 float mx8[8];
@@ -740,19 +831,19 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             // tensor pipe already works on the next segment's first S.
             wait_or_flag(&o_done[g], (uint32_t)sc & 1u, p.d_err);
             tc_fence_after();
-            const int x_next = x + nt;
+            int x_next = x + nt;
+            if constexpr (kWindow) x_next = x + adv;
             const float l_run =
                 ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) + ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
             {
-                const Seg sg = seg_at<G, kPrefix>(p, x, x1);
+                const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
                 const PrefillSeq &q = p.seqs[sg.si];
                 const Row rw = row_of(sg);
                 const size_t out_row = (size_t)(q.row_start + rw.ipos) * p.num_heads + sg.h * G + rw.head;
                 T *orow = static_cast<T *>(p.out) + out_row * kD;
                 if constexpr (kPrefix) {
-                    const size_t slot = out_row * p.part_slots + (cta - cta_of(sg.x_unit, W, N));
-                    store_partial(p.part_o + slot * kD, rw.valid);
-                    if (rw.valid) p.part_ml[slot] = make_float2(m_run, l_run);
+                    store_partial(p.part_o, p.part_ml, out_row * p.part_slots, rw.valid, tO, cta, sg.x_unit,
+                                  p.total_tiles, ncta, m_run, l_run);
                 } else if (sg.t0 == 0 && sg.t1 == sg.n) {
                     // the whole unit: normalise, round once, store
                     store_out(orow, l_run > 0.f ? 1.f / l_run : 0.f, rw.valid);

@@ -59,13 +59,17 @@ def test_decode_weights_refusals(lib):
     assert weights(lib, D=96) == -2 and weights(lib, bs=24) == -2 and weights(lib, Hq=32) == -2
     assert weights(lib, q=BUF + 2) == -6
     assert weights(lib, wo=BUF + 4) == -1            # overlapping, but not the same
-    need = lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 0)
+    need = lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 1, 0)
     # (max, sum) pairs of 32 (sequence, head)s, then 100 scores each
     assert need == 256 + 4 * 8 * 100 * 4
     assert weights(lib, ws=0) == -5 and weights(lib, wsb=need - 1) == -5
     assert weights(lib, ws=BUF + 16) == -6
-    assert lib.pa_decode_weights_workspace_bytes(4, 7, 2, 128, 16, 100, 0) == 0
-    assert lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 24) == 0
+    assert lib.pa_decode_weights_workspace_bytes(4, 7, 2, 128, 16, 100, 1, 0) == 0
+    assert lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 1, 24) == 0
+    assert lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 3, 0) == 0
+    # four positions of four heads are attended together: one piece of 128 values, (max, sum), 128 scores
+    assert lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 4, 0) == 4 * 8 * (128 + 2 + 128) * 4
+    assert weights(lib, qpr=4, scale=-0.1) == -3 and weights(lib, qpr=4, pt=24) == -3
 
 
 def evict(lib, k=BUF, v=BUF, w=BUF, nw=2 * BUF, W=100, bt=BUF, mb=8, lens=BUF, nbt=BUF, nmb=4, nl=2 * BUF, kept=BUF, B=2,

@@ -106,6 +106,104 @@ def test_several_queries_add_to_one_row_in_place(w, G):
     check(setup([3, 700, 0, 64], w, 2 * G, 2, 128, 16, "f16", seed=w), in_place=True)
 
 
+WINDOWS = [
+    # (cache lengths, positions, G, Hkv, bs, dtype): attended together on the tensor cores
+    ([300], 16, 1, 1, 16, "bf16"),
+    ([2000, 3, 640], 8, 4, 2, 16, "f16"),          # lengths far apart: CTAs with nothing to do
+    ([129, 128, 127], 4, 8, 1, 64, "bf16"),
+    ([900], 70, 4, 1, 32, "f16"),                  # 280 query rows: a second row tile of 24
+    ([40, 0, 1], 33, 8, 1, 128, "bf16"),           # more positions than tokens, no tokens, one token
+    ([700, 1500], 20, 2, 3, 16, "bf16"),
+    ([33] * 70, 16, 1, 1, 16, "f16"),              # more rows than one launch takes
+    ([1, 400], 9, 8, 2, 16, "f16"),
+]
+
+
+@pytest.mark.parametrize("rows,w,G,Hkv,bs,dtype", WINDOWS)
+@pytest.mark.parametrize("in_place", [False, True])
+def test_windows(rows, w, G, Hkv, bs, dtype, in_place):
+    check(setup(rows, w, G * Hkv, Hkv, 128, bs, dtype, seed=w + G), in_place=in_place)
+
+
+def test_window_positions_in_any_order_and_apart():
+    c = setup([700, 500], 6, 8, 2, 128, 16, "bf16", seed=31)
+    c["ctx"] = [700, 1, 350, 0, 129, 128, 20, 500, 499, 17, 16, 256]
+    c["lens"] = torch.as_tensor(c["ctx"], dtype=torch.int32, device=DEV)
+    check(c)
+
+
+def test_window_garbage_past_the_contexts_does_not_reach_anything():
+    c = setup([300, 45], 8, 4, 1, 128, 16, "f16", seed=32)
+    a, wa = call(c)
+    for r, n in enumerate((300, 45)):
+        b = int(c["bt"][r * 8, (n - 1) // 16])
+        c["kc"][b, :, n % 16:] = float("nan")
+        c["vc"][b, :, n % 16:] = float("inf")
+    b, wb = call(c)
+    assert torch.equal(a, b) and torch.equal(wa, wb)
+
+
+def test_window_bad_entries_weigh_nothing_and_broken_promises_are_flagged():
+    c = setup([300], 5, 8, 2, 128, 32, "bf16", seed=33)
+    bad = c["bt"].clone()
+    bad[:, 3] = 10 ** 6
+    bad[:, 5] = -9
+
+    def run(bt, lens):
+        out, new = torch.empty_like(c["q"]), torch.full_like(c["tot"], -7.0)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        pa.pa_decode_weights(out, c["q"], c["kc"], c["vc"], bt, lens, c["scale"], c["ml"], c["tot"], new,
+                             queries_per_row=5, d_err=err)
+        torch.cuda.synchronize()
+        return out, new, int(err.item())
+    out, new, err = run(bad, c["lens"])
+    assert err == pa.capi.DEVERR["block_range"]
+    tot, tol, ref = c["tot"][0].cpu().double().clone(), torch.zeros_like(c["tot"][0].cpu().double()), []
+    for i, n in enumerate(c["ctx"]):
+        keep = [j for j in range(n) if j // 32 not in (3, 5)]
+        K, V = gather(c["kc"], c["bt"][i], n)[keep], gather(c["vc"], c["bt"][i], n)[keep]
+        o, p, size = attend(c["q"][i].cpu().double(), K, V, c["scale"])
+        ref.append(o)
+        tot[:, keep] += p
+        tol[:, keep] += p * (2 * 128 * 2.0 ** -23 * size + 2.0 ** -19) + tot[:, keep] * 2.0 ** -23
+    check_attention(to_f64(out), torch.stack(ref).numpy(), "bf16", "kept keys")
+    assert bool(((new[0].cpu().double() - tot).abs() <= tol).all())
+    # a position whose table row is another's
+    odd = c["bt"].clone()
+    odd[2, 1] = c["bt"][0, 0]
+    assert run(odd, c["lens"])[2] == pa.capi.DEVERR["prefix"]
+    # lengths out of range are clamped
+    lens = c["lens"].clone()
+    lens[4], lens[1] = 10000, -1
+    out2, _, err = run(c["bt"], lens)
+    assert err == pa.capi.DEVERR["context_range"]
+    good, _, _ = run(c["bt"], c["lens"])
+    assert torch.equal(out2[4], good[4]) and not bool(out2[1].any())
+
+
+def test_window_workspace_content_capture_and_another_stream():
+    c = setup([900, 77], 16, 4, 1, 128, 16, "bf16", seed=34)
+    ref, wref = call(c)
+    ws = pa.decode_weights_workspace(c["q"], 1, 16, c["ml"], queries_per_row=16)
+    ws.fill_(255)
+    out, new = torch.zeros_like(ref), torch.full_like(wref, -7.0)
+    args = (out, c["q"], c["kc"], c["vc"], c["bt"], c["lens"], c["scale"], c["ml"], c["tot"], new)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pa.pa_decode_weights(*args, queries_per_row=16, workspace=ws, stream=s)
+    s.synchronize()
+    assert torch.equal(out, ref) and torch.equal(new, wref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_decode_weights(*args, queries_per_row=16, workspace=ws)
+    for _ in range(2):
+        out.zero_()
+        new.fill_(-7.0)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and torch.equal(new, wref)
+
+
 def test_a_row_of_totals_wider_than_the_contexts():
     check(setup([40, 5], 1, 4, 2, 64, 16, "bf16", seed=3, width=77))
 
