@@ -372,10 +372,10 @@ PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const 
  *                  row: 1 for plain decode; several query positions over one
  *                  cache (the last positions of a prompt observing it, several
  *                  new tokens at once) repeat the sequence's block-table row,
- *                  each with its own context length, and need scale > 0.  From
- *                  16 query rows (positions times heads per kv head) on, at
- *                  head_dim 128 and block_size >= 16, they are attended together
- *                  on the tensor cores: the row of the first position is the one
+ *                  each with its own context length, and need scale > 0.  From 4
+ *                  positions and 16 query rows (positions times heads per kv head)
+ *                  on, at head_dim 128 and block_size >= 16, they are attended
+ *                  together on the tensor cores: the row of the first position is the one
  *                  that is read (another that differs in a position's context
  *                  sets PA_DEVERR_PREFIX, outputs and totals undefined), the
  *                  softmax weights are rounded to dtype for their product with

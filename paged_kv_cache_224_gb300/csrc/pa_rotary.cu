@@ -51,10 +51,10 @@ __device__ __forceinline__ long long cache_row(const RotaryParams &p, long long 
     return (blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size)) * p.head_dim;
 }
 
-constexpr int kMaxThreads = 640;
+constexpr int kMaxThreads = 320;
 
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kMaxThreads, 2) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
     // [2 tokens]: cosines of pairs 8c .. 8c+3, 8c+4 .. 8c+7, then the sines
     // alike, [4][unit c], so that a warp's reads are consecutive
     __shared__ float4 s_cs[2][4][kRotaryMaxDim / 16];

@@ -98,7 +98,7 @@ __device__ __forceinline__ void load_scores(const float *a, float (&x)[G]) {
 template <typename T, int D, int G, int kItems, bool kMany>
 __global__ void __launch_bounds__(kThreads)
     weights_merge_kernel(const __grid_constant__ DecodeParams p, const float *weights, float *weights_out, int width,
-                         int queries_per_row, int chunks, int merge_ctas) {
+                         int queries_per_row, int loops, int chunks, int merge_ctas) {
     __shared__ float2 s_ml[(kMany ? kMembers : 1) * G];  // (maximum, 1 / sum) per sequence and head
     __shared__ int s_len[kMany ? kMembers : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads)
     const int u = blockIdx.x - merge_ctas;
     const int chunk = u % chunks, rh = u / chunks;
     const int r = rh / p.num_kv_heads, kvh = rh - r * p.num_kv_heads;
-    const int j0 = chunk * kThreads * kItems + tid;  // this thread's tokens: j0 + i * kThreads
+    const int j0 = chunk * loops * kThreads * kItems + tid;  // this thread's first tokens: j0 + i * kThreads
     const int s0 = r * queries_per_row;
     float acc[kItems];
 #pragma unroll
@@ -147,9 +147,12 @@ __global__ void __launch_bounds__(kThreads)
     };
     const size_t at = (size_t)rh * width + j0;
     if constexpr (!kMany) {
-        // everything that does not depend on the maxima and sums is under way while they are put together
+        // Everything that does not depend on the maxima and sums is under way
+        // while they are put together, and the next tokens' while these are
+        // summed.
         const int L = clamped_len(p, s0);
         if (j0 - tid >= L) return;
+        const float *sc = p.scores + ((size_t)rh * p.score_stride + j0) * G;
         float x[kItems][G], w[kItems];
         load(s0, L, x);
 #pragma unroll
@@ -159,15 +162,40 @@ __global__ void __launch_bounds__(kThreads)
             if (lane == 0) s_ml[warp] = ml;
         }
         __syncthreads();
+        constexpr int kStep = kThreads * kItems;
+        for (int it = 0; it < loops; ++it) {
+            const int j = j0 + it * kStep, next = j + kStep;
+            float y[kItems][G], v[kItems];
+            const bool more = it + 1 < loops && next - tid < L;
+            if (more) {
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const float2 ml = s_ml[h];
+                for (int i = 0; i < kItems; ++i) {
+                    v[i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) acc[i] = fmaf(fast_exp2(x[i][h] - ml.x), ml.y, acc[i]);
+                    for (int h = 0; h < G; ++h) y[i][h] = -INFINITY;
+                    if (next + i * kThreads < L) {
+                        load_scores<G>(sc + (size_t)((it + 1) * kStep + i * kThreads) * G, y[i]);
+                        v[i] = weights[at + (it + 1) * kStep + i * kThreads];
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                const float2 ml = s_ml[h];
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) acc[i] = fmaf(fast_exp2(x[i][h] - ml.x), ml.y, h ? acc[i] : 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                if (j + i * kThreads < L) weights_out[at + it * kStep + i * kThreads] = w[i] + acc[i];
+            if (!more) break;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                w[i] = v[i];
+#pragma unroll
+                for (int h = 0; h < G; ++h) x[i][h] = y[i][h];
+            }
         }
-#pragma unroll
-        for (int i = 0; i < kItems; ++i)
-            if (j0 + i * kThreads < L) weights_out[at + i * kThreads] = w[i] + acc[i];
     } else {
         int longest = 0;
         for (int m0 = 0; m0 < queries_per_row; m0 += kMembers) {
@@ -218,7 +246,11 @@ int launch_merge_t(const DecodeParams &p, const float *weights, float *weights_o
     constexpr int kMost = G == 8 ? 2 : 4;
     const bool few = rows * ((p.max_context_len + kMost * kThreads - 1) / (kMost * kThreads)) < 2 * sm_count();
     const int chunk = few ? kThreads : kMost * kThreads;
-    const int chunks = std::max(1, (p.max_context_len + chunk - 1) / chunk);
+    int chunks = std::max(1, (p.max_context_len + chunk - 1) / chunk);
+    // with many chunks a CTA takes several of a row's, the next one's loads ahead
+    const int loops =
+        queries_per_row > 1 ? 1 : (int)std::min<long long>(std::min(chunks, 8), std::max(1LL, rows * chunks / (8 * sm_count())));
+    chunks = (chunks + loops - 1) / loops;
     const long long pairs = (long long)p.num_seqs * p.num_heads;
     const long long merge = p.max_partitions > 1 ? (pairs + kThreads / 32 - 1) / (kThreads / 32) : 0;
     const long long total = merge + rows * chunks;
@@ -227,7 +259,7 @@ int launch_merge_t(const DecodeParams &p, const float *weights, float *weights_o
                     ? (few ? weights_merge_kernel<T, D, G, 1, true> : weights_merge_kernel<T, D, G, kMost, true>)
                     : (few ? weights_merge_kernel<T, D, G, 1, false> : weights_merge_kernel<T, D, G, kMost, false>);
     return launch_pdl(kern, dim3((unsigned)total), dim3(kThreads), 0, stream, p, weights,
-                      weights_out, width, queries_per_row, chunks, (int)merge) == cudaSuccess
+                      weights_out, width, queries_per_row, loops, chunks, (int)merge) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }
