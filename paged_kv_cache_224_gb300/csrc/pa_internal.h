@@ -106,7 +106,7 @@ struct PrefillParams {
     int part_slots;              // shared prefix: part_o and part_ml are [row][Hq][part_slots], one slot per piece
     // several queries over one cache (kWindow): query row r of the call has
     // context_lens[r] tokens, at most len_cap; the scores (not scaled) go to
-    // [row_base + entry of seqs][kv head][chunk_len * G rows][score_stride]
+    // [row_base + entry of seqs][kv head][score_stride keys][chunk_len * G rows]
     const int32_t *context_lens;
     int len_cap, row_base;
     float *scores;

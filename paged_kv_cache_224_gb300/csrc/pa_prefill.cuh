@@ -651,6 +651,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             int nt, j0, jn, plim, plim_min, kend;
             [[maybe_unused]] int adv;                       // kWindow: tiles of the schedule
             [[maybe_unused]] float *srow = nullptr;         // kWindow: this row's kept scores, or none
+            [[maybe_unused]] int srows = 0;                 // query rows of the unit's sequence: floats per key
             [[maybe_unused]] const int32_t *wtable = nullptr;
             {
                 const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
@@ -668,7 +669,8 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     const size_t rows = (size_t)q.chunk_len * G;
                     const size_t gr = (size_t)sg.r * kUnitRows + g * kM + t;
                     if (rw.valid)
-                        srow = p.scores + ((size_t)((p.row_base + sg.si) * p.num_kv_heads + sg.h) * rows + gr) * p.score_stride;
+                        srow = p.scores + (size_t)((p.row_base + sg.si) * p.num_kv_heads + sg.h) * p.score_stride * rows + gr;
+                    srows = (int)rows;
                     wtable = q.block_table;
                     plim_min = __reduce_min_sync(kFull, plim);
                     kend = sg.longest - 1;
@@ -736,10 +738,14 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
 #pragma unroll
                         for (int c = 0; c < kNK; ++c) s[c] = (bad >> (c / BS) & 1u) ? -INFINITY : s[c];
                     }
+                    // rows side by side for a key: a warp's store is one line
                     if (srow) {
+                        float *dst = srow + (size_t)kb * srows;
 #pragma unroll
-                        for (int c = 0; c < kNK; c += 4)
-                            *reinterpret_cast<float4 *>(srow + kb + c) = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
+                        for (int c = 0; c < kNK; ++c) {
+                            *dst = s[c];
+                            dst += srows;
+                        }
                     }
                 }
                 // row max with three-input maxima: 8 chains over the 128 columns

@@ -3,9 +3,12 @@
 //
 // One kernel follows, with three kinds of CTA:
 //   merge    one warp per (sequence, head): the log-sum-exp merge of its pieces;
-//   totals   one CTA per (row of totals, kv head, chunk of tokens): a token's
-//            weight is sum_r 2^(score_r - M_r) / l_r over the row's query rows
-//            (positions x heads) that see it, in their order;
+//   totals   one CTA per (row of totals, kv head, 128 tokens): a token's weight
+//            is sum_r 2^(score_r - M_r) / l_r over the row's query rows
+//            (positions x heads) that see it.  A warp takes 32 tokens, a lane
+//            every 32nd query row: its loads are lines of 32 rows' scores of a
+//            key, and the lanes' sums for 32 tokens change places in 31
+//            shuffles, in a fixed order;
 //   check    one CTA per sequence: its length, and that its table row is the
 //            one its row of totals is attended over.
 #include <algorithm>
@@ -16,7 +19,7 @@ namespace pa {
 namespace {
 using namespace wnd;
 
-constexpr int kTotThreads = 128;  // tokens of a totals CTA
+constexpr int kTotThreads = 128;  // tokens of a totals CTA, 32 to a warp
 constexpr int kBatch = 128;       // query rows whose maxima and sums are held at a time
 
 struct WindowSchedule {
@@ -68,39 +71,66 @@ __global__ void __launch_bounds__(kTotThreads)
         // ---------------------------------------------------------------- totals
         const int chunk = blockIdx.x % mp.chunks, rh = blockIdx.x / mp.chunks;
         const int i = rh / p.num_kv_heads, kvh = rh - i * p.num_kv_heads;
-        const int j = chunk * kTotThreads + tid;
+        const int j0 = chunk * kTotThreads + warp * 32;  // the warp's first token
         const int rows = w * G;
+        const int j = j0 + lane;
         const size_t at = (size_t)rh * mp.width + j;
-        float acc = 0.f;
+        const float was = j < p.max_context_len ? mp.weights[at] : 0.f;
+        float sum[32];  // per token, over this lane's query rows
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sum[k] = 0.f;
         int longest = 0;
         for (int r0 = 0; r0 < rows; r0 += kBatch) {
             const int nr = min(kBatch, rows - r0);
+            // the first 32 rows' scores (inside the tile-rounded buffer whatever the lengths are)
+            const float *sc = p.scores + ((size_t)rh * p.score_stride + j0) * rows + r0 + lane;
+            float x[32];
+            auto fetch = [&](int b) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = b * 32 + lane < nr ? __ldcs(sc + (size_t)k * rows + b * 32) : 0.f;
+            };
+            fetch(0);
             if (r0) __syncthreads();  // the previous rows' values are read
             if (tid < nr) {
                 const int gr = r0 + tid, s = i * w + gr / G;
                 const float2 *ml = p.ws_ml + ((size_t)s * p.num_heads + kvh * G + gr % G) * p.slots;
                 const int np = pieces_of(p, mp, i, kvh, gr);
                 const int L = clamped_len(p, s);
-                float M = -INFINITY, sum = 0.f;
+                float M = -INFINITY, l = 0.f;
+#pragma unroll 8
                 for (int k = 0; k < np; ++k) M = fmaxf(M, ml[k].x);
-                if (M != -INFINITY)
-                    for (int k = 0; k < np; ++k) sum = fmaf(fast_exp2(ml[k].x - M), ml[k].y, sum);
+                if (M != -INFINITY) {
+#pragma unroll 8
+                    for (int k = 0; k < np; ++k) l = fmaf(fast_exp2(ml[k].x - M), ml[k].y, l);
+                }
                 // no key attended: 2^(-inf) = 0 for every one of them
-                s_ml[tid] = M == -INFINITY ? make_float2(0.f, 0.f) : make_float2(M, 1.f / sum);
+                s_ml[tid] = M == -INFINITY ? make_float2(0.f, 0.f) : make_float2(M, 1.f / l);
                 s_len[tid] = L;
             }
             __syncthreads();
-            const float *sc = p.scores + ((size_t)rh * rows + r0) * p.score_stride + j;
-#pragma unroll 8
-            for (int r = 0; r < nr; ++r) {
-                longest = max(longest, s_len[r]);
-                if (j < s_len[r]) {
-                    const float2 ml = s_ml[r];
-                    acc = fmaf(fast_exp2(fmaf(__ldcs(sc + (size_t)r * p.score_stride), p.scale_log2, -ml.x)), ml.y, acc);
-                }
+            for (int b = 0; b * 32 < nr; ++b) {
+                if (b) fetch(b);
+                const int r = b * 32 + lane;
+                const float2 ml = r < nr ? s_ml[r] : make_float2(0.f, 0.f);
+                const int left = (r < nr ? s_len[r] : 0) - j0;  // of the warp's tokens, those this row sees
+                longest = max(longest, left);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    if (k < left) sum[k] = fmaf(fast_exp2(fmaf(x[k], p.scale_log2, -ml.x)), ml.y, sum[k]);
             }
         }
-        if (j < longest) mp.weights_out[at] = mp.weights[at] + acc;
+        // the lanes' 32 sums: halves change places until lane k holds token k's
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) {
+            const bool up = lane & m;
+#pragma unroll
+            for (int k = 0; k < m; ++k) {
+                const float keep = up ? sum[k + m] : sum[k], send = up ? sum[k] : sum[k + m];
+                sum[k] = keep + __shfl_xor_sync(kFull, send, m);
+            }
+        }
+        longest = __reduce_max_sync(kFull, longest);
+        if (lane < longest) mp.weights_out[at] = was + sum[0];
         return;
     }
     const int b = blockIdx.x - mp.total_ctas;
