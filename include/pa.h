@@ -385,7 +385,8 @@ PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const 
  *                  outputs of the others
  *   workspace      >= pa_decode_weights_workspace_bytes(...) bytes, 256-byte
  *                  aligned, scratch: the partials, and every score in fp32
- *                  (num_seqs * num_heads * max_context_len * 4 bytes)
+ *                  (num_seqs * num_heads * max_context_len * 4 bytes; rows that are
+ *                  attended together take whole sets of 32 query rows)
  * The weights are fp32 from fp32 scores; sums run in a fixed order.  Keys that
  * an invalid table entry leaves out of the softmax weigh 0.  Shapes,
  * partition_tokens, data errors as for pa_decode.

@@ -50,7 +50,7 @@ struct PartialWs {
 // several queries are attended together.
 struct WeightsWs {
     int pt = 1, slots;
-    long long stride;  // tokens of a query row's scores
+    long long stride;  // tokens of a row's scores
     size_t acc, ml, scores;
     bool window, ok;
     WeightsWs(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
@@ -72,7 +72,10 @@ struct WeightsWs {
         const PartialWs w(num_seqs, num_heads, head_dim, slots);
         acc = slots > 1 || window ? w.acc : 0;
         ml = w.ml;
-        scores = round256((size_t)num_seqs * num_heads * stride * sizeof(float));
+        scores = round256((window ? pa::window_score_floats(num_seqs / queries_per_row, num_kv_heads, queries_per_row * group,
+                                                            max_context_len)
+                                  : (size_t)num_seqs * num_heads * stride) *
+                          sizeof(float));
     }
     size_t total() const { return acc + ml + scores; }
 };

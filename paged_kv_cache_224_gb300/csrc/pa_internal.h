@@ -106,7 +106,7 @@ struct PrefillParams {
     int part_slots;              // shared prefix: part_o and part_ml are [row][Hq][part_slots], one slot per piece
     // several queries over one cache (kWindow): query row r of the call has
     // context_lens[r] tokens, at most len_cap; the scores (not scaled) go to
-    // [row_base + entry of seqs][kv head][score_stride keys][chunk_len * G rows]
+    // [row_base + entry of seqs][kv head][plane of 32 query rows][score_stride keys][32]
     const int32_t *context_lens;
     int len_cap, row_base;
     float *scores;
@@ -253,11 +253,13 @@ int launch_prefix_f16(int block_size, int group, const PrefixLaunch &pl, unsigne
 // Several query positions over one cache, with the totals of their weights
 // (pa_decode_weights with enough queries per row): every row of queries_per_row
 // consecutive sequences is attended together on the tensor cores, its scores
-// kept (window_score_stride floats per query row and head), and then merged and
-// added up.  window_pieces: the most pieces (partials) of a unit.
+// kept (window_score_floats in all), and then merged and added up.  window_pieces: the most pieces (partials) of a unit.
 bool window_supported(int head_dim, int block_size, int group, int queries_per_row);
 int window_pieces(int rows, int queries_per_row, int group, int num_kv_heads, int max_context_len);
 inline long long window_score_stride(int max_context_len) { return ((long long)max_context_len + 127) / 128 * 128; }
+inline size_t window_score_floats(int rows, int num_kv_heads, int query_rows, int max_context_len) {
+    return (size_t)rows * num_kv_heads * (((size_t)query_rows + 31) / 32 * 32) * window_score_stride(max_context_len);
+}
 int launch_window(pa_dtype dt, int block_size, int group, const DecodeParams &d, int queries_per_row,
                   const float *weights, float *weights_out, int width, cudaStream_t stream);
 int launch_window_bf16(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);

@@ -651,7 +651,6 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             int nt, j0, jn, plim, plim_min, kend;
             [[maybe_unused]] int adv;                       // kWindow: tiles of the schedule
             [[maybe_unused]] float *srow = nullptr;         // kWindow: this row's kept scores, or none
-            [[maybe_unused]] int srows = 0;                 // query rows of the unit's sequence: floats per key
             [[maybe_unused]] const int32_t *wtable = nullptr;
             {
                 const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
@@ -666,11 +665,13 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 plim_min = last_key<kPrefix>(q.prefix_len, min((sg.r * kUnitRows + g * kM) / G, q.chunk_len - 1));
                 kend = last_key<kPrefix>(q.prefix_len, min(q.chunk_len - 1, ((sg.r + 1) * kUnitRows - 1) / G));
                 if constexpr (kWindow) {
-                    const size_t rows = (size_t)q.chunk_len * G;
-                    const size_t gr = (size_t)sg.r * kUnitRows + g * kM + t;
+                    // [sequence][kv head][32 rows][key][row]: this warp's plane
+                    const int planes = (q.chunk_len * G + 31) / 32;
+                    const int plane = sg.r * (kUnitRows / 32) + g * (kM / 32) + quarter;
                     if (rw.valid)
-                        srow = p.scores + (size_t)((p.row_base + sg.si) * p.num_kv_heads + sg.h) * p.score_stride * rows + gr;
-                    srows = (int)rows;
+                        srow = p.scores +
+                               ((size_t)((p.row_base + sg.si) * p.num_kv_heads + sg.h) * planes + plane) * p.score_stride * 32 +
+                               lane;
                     wtable = q.block_table;
                     plim_min = __reduce_min_sync(kFull, plim);
                     kend = sg.longest - 1;
@@ -738,14 +739,14 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
 #pragma unroll
                         for (int c = 0; c < kNK; ++c) s[c] = (bad >> (c / BS) & 1u) ? -INFINITY : s[c];
                     }
-                    // rows side by side for a key: a warp's store is one line
+                    // 32 rows side by side for a key: a warp's store is one line, at a
+                    // constant distance from the last (an address register of its
+                    // own for each of 128 stores made a tile's stores take 2 us:
+                    // few registers are free, and each waits for its store)
                     if (srow) {
-                        float *dst = srow + (size_t)kb * srows;
+                        float *dst = srow + (size_t)kb * 32;
 #pragma unroll
-                        for (int c = 0; c < kNK; ++c) {
-                            *dst = s[c];
-                            dst += srows;
-                        }
+                        for (int c = 0; c < kNK; ++c) dst[c * 32] = s[c];
                     }
                 }
                 // row max with three-input maxima: 8 chains over the 128 columns

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kTotThreads)
         const int chunk = blockIdx.x % mp.chunks, rh = blockIdx.x / mp.chunks;
         const int i = rh / p.num_kv_heads, kvh = rh - i * p.num_kv_heads;
         const int j0 = chunk * kTotThreads + warp * 32;  // the warp's first token
-        const int rows = w * G;
+        const int rows = w * G, planes = (rows + 31) / 32;
         const int j = j0 + lane;
         const size_t at = (size_t)rh * mp.width + j;
         const float was = j < p.max_context_len ? mp.weights[at] : 0.f;
@@ -83,11 +83,11 @@ __global__ void __launch_bounds__(kTotThreads)
         for (int r0 = 0; r0 < rows; r0 += kBatch) {
             const int nr = min(kBatch, rows - r0);
             // the first 32 rows' scores (inside the tile-rounded buffer whatever the lengths are)
-            const float *sc = p.scores + ((size_t)rh * p.score_stride + j0) * rows + r0 + lane;
+            const float *sc = p.scores + (((size_t)rh * planes + r0 / 32) * p.score_stride + j0) * 32 + lane;
             float x[32];
             auto fetch = [&](int b) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = b * 32 + lane < nr ? __ldcs(sc + (size_t)k * rows + b * 32) : 0.f;
+                for (int k = 0; k < 32; ++k) x[k] = b * 32 + lane < nr ? __ldcs(sc + (size_t)b * p.score_stride * 32 + k * 32) : 0.f;
             };
             fetch(0);
             if (r0) __syncthreads();  // the previous rows' values are read

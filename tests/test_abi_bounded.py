@@ -67,8 +67,9 @@ def test_decode_weights_refusals(lib):
     assert lib.pa_decode_weights_workspace_bytes(4, 7, 2, 128, 16, 100, 1, 0) == 0
     assert lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 1, 24) == 0
     assert lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 3, 0) == 0
-    # four positions of four heads are attended together: one piece of 128 values, (max, sum), 128 scores
-    assert lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 4, 0) == 4 * 8 * (128 + 2 + 128) * 4
+    # four positions of four heads are attended together: one piece of 128 values and (max, sum) each, and
+    # 128 scores for each of two kv heads' 16 query rows, rounded up to 32
+    assert lib.pa_decode_weights_workspace_bytes(4, 8, 2, 128, 16, 100, 4, 0) == 4 * 8 * (128 + 2) * 4 + 2 * 32 * 128 * 4
     assert weights(lib, qpr=4, scale=-0.1) == -3 and weights(lib, qpr=4, pt=24) == -3
 
 
