@@ -454,7 +454,12 @@ PA_API int pa_evict(void *k_cache, void *v_cache, const float *weights, float *n
  *   scale          finite and > 0
  *   partition_tokens  splits the sequences' own tokens (0 = automatic)
  *   workspace      >= pa_decode_common_prefix_workspace_bytes(...) bytes,
- *                  256-byte aligned, scratch (needs no clearing)
+ *                  256-byte aligned, ZERO-FILLED before its first use (its first
+ *                  256 bytes hold a counter that every call that completes
+ *                  leaves at zero again, so one workspace serves every later
+ *                  call whose sizes it covers; after a call that set
+ *                  PA_DEVERR_TIMEOUT, zero-fill it again).  It must not be shared
+ *                  with work that overlaps the call on the device
  * Supported: head_dim 128, block_size in {16, 32, 64, 128}, num_heads /
  * num_kv_heads in {1, 2, 4, 8}.  The softmax weights of prefix keys are rounded
  * to dtype for their product with V, as in pa_prefill_chunk.

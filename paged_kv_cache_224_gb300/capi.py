@@ -9,6 +9,7 @@ loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -489,6 +490,12 @@ def pa_prefill_batch(out, query, k_cache, v_cache, block_tables, prefix_lens, ch
 # so the marshalling is kept lean: plain integers for pointers, one pass over
 # the tensors for device and contiguity, no stream or device objects.
 
+_fns: dict = {}
+# (absent from a torch built without CUDA, where every call raises before them)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _index(t) -> int:
     """The CUDA device index of ``t``."""
     i = t.get_device()
@@ -516,17 +523,20 @@ def _typed(dtype, what, *ts) -> None:
 
 def _call(name, index, *args) -> None:
     """Call a C entry point with ``index`` as the current device."""
-    if torch._C._cuda_getDevice() == index:
-        rc = getattr(_lib or lib(), name)(*args)
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    if _current_device() == index:
+        rc = fn(*args)
     else:
         with torch.cuda.device(index):
-            rc = getattr(_lib or lib(), name)(*args)
+            rc = fn(*args)
     if rc:
         raise PAError(name, rc)
 
 
 def _raw_stream(index, stream):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return _current_stream(index) if stream is None else stream.cuda_stream
 
 
 def _opt(t):
@@ -542,16 +552,19 @@ def _scratch(device, nbytes, stream):
     return w
 
 
-def _token_rows(index, t, tokens, heads, head_dim):
-    """Check that ``t`` is [tokens][heads][head_dim] with contiguous heads; its token stride."""
+def _token_rows(index, dtype, t, shape, row) -> int:
+    """Check that ``t`` is [tokens][heads][head_dim] (``shape``; ``row`` values a
+    token) with contiguous heads; its token stride."""
     if t.get_device() != index:
         raise ValueError("tensors must be on one CUDA device")
-    if t.shape != (tokens, heads, head_dim):
+    if t.dtype is not dtype:
+        raise TypeError("dtype mismatch")
+    if t.shape != shape:
         raise ValueError("shape mismatch")
     st = t.stride()
-    if (head_dim > 1 and st[2] != 1) or (heads > 1 and st[1] != head_dim):
+    if (st[2] != 1 and shape[2] > 1) or (st[1] != shape[2] and shape[1] > 1):
         raise ValueError("the heads of a token must be contiguous")
-    return st[0] if tokens > 1 else heads * head_dim
+    return st[0] if shape[0] > 1 else row
 
 
 def pa_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
@@ -567,31 +580,31 @@ def pa_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, position
     _typed(torch.int64, "slot_mapping must be int64", slot_mapping)
     _typed(torch.int32, "positions must be int32", positions)
     _typed(torch.float32, "inv_freq must be float32", inv_freq)
-    _typed(k_cache.dtype, "dtype mismatch", v_cache, query_out, query, key, value)
+    dt = k_cache.dtype
+    _typed(dt, "dtype mismatch", v_cache)
     NB, Hkv, bs, D = shape = k_cache.shape
     if query.dim() != 3 or v_cache.shape != shape or inv_freq.dim() != 1:
         raise ValueError("shape mismatch")
-    T, Hq, _ = query.shape
-    axes = 1
-    if positions.dim() == 2:
-        axes = positions.shape[0]
-        if positions.shape[1] != T:
-            raise ValueError("shape mismatch")
-    elif positions.shape != (T,):
+    qshape = query.shape
+    T, Hq, _ = qshape
+    pshape = positions.shape
+    axes = pshape[0] if len(pshape) == 2 else 1
+    if len(pshape) not in (1, 2) or pshape[-1] != T or slot_mapping.shape != (T,) or qshape[2] != D:
         raise ValueError("shape mismatch")
-    if slot_mapping.shape != (T,):
-        raise ValueError("shape mismatch")
-    half = inv_freq.numel()
+    half = inv_freq.shape[0]
     ax = None
     if pair_axis is not None:
-        ax = np.ascontiguousarray(pair_axis, dtype=np.int32)
+        ax = np.asarray(pair_axis, dtype=np.int32)
         if ax.shape != (half,):
             raise ValueError("pair_axis must name an axis for every pair")
-    _call("pa_rotary_and_cache", dev, query_out.data_ptr(), _token_rows(dev, query_out, T, Hq, D), query.data_ptr(),
-          _token_rows(dev, query, T, Hq, D), key.data_ptr(), _token_rows(dev, key, T, Hkv, D), value.data_ptr(),
-          _token_rows(dev, value, T, Hkv, D), k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(),
-          slot_mapping.data_ptr(), inv_freq.data_ptr(), ax.ctypes.data if ax is not None and half else None, axes,
-          2 * half, 1 if interleaved else 0, T, Hq, Hkv, D, bs, NB, _dt(k_cache), _opt(d_err), _raw_stream(dev, stream))
+        ax = ax.tobytes()
+    qrow, krow, kshape = Hq * D, Hkv * D, (T, Hkv, D)
+    _call("pa_rotary_and_cache", dev, query_out.data_ptr(), _token_rows(dev, dt, query_out, qshape, qrow),
+          query.data_ptr(), _token_rows(dev, dt, query, qshape, qrow), key.data_ptr(),
+          _token_rows(dev, dt, key, kshape, krow), value.data_ptr(), _token_rows(dev, dt, value, kshape, krow),
+          k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(),
+          ax, axes, 2 * half, 1 if interleaved else 0, T, Hq, Hkv, D, bs, NB, _dt(k_cache), _opt(d_err),
+          _raw_stream(dev, stream))
 
 
 def pa_decode_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
@@ -686,12 +699,14 @@ def pa_decode_common_prefix_workspace_bytes(num_seqs, num_heads, num_kv_heads, h
 
 def decode_common_prefix_workspace(query, num_kv_heads, block_size, max_context_len, group_size, prefix_blocks,
                                    partition_tokens=0, stream=None):
-    """Allocate (with torch) a workspace big enough for ``pa_decode_common_prefix``."""
+    """A zero-filled workspace big enough for ``pa_decode_common_prefix``
+    (zero-filled once; the calls keep it usable)."""
     B, Hq, D = query.shape
     with torch.cuda.device(query.device):
         n = pa_decode_common_prefix_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, group_size,
                                                     prefix_blocks, partition_tokens)
-    return _scratch(query.device, n, stream)
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        return torch.zeros(max(n, 1), dtype=torch.uint8, device=query.device)
 
 
 def pa_decode_common_prefix(out, query, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,

@@ -80,6 +80,8 @@ struct WeightsWs {
     size_t total() const { return acc + ml + scores; }
 };
 
+// The shared-prefix step: the decode instances' queue counter, then the partials.
+constexpr size_t kQueueBytes = 256;
 struct PrefixWs {
     int pt, pieces, slots;
     size_t acc, ml;
@@ -100,8 +102,7 @@ struct PrefixWs {
         acc = w.acc;
         ml = w.ml;
     }
-    // ... and the decode instances' queue counter
-    size_t total() const { return acc + ml + 256; }
+    size_t total() const { return kQueueBytes + acc + ml; }
 };
 
 bool prefix_sizes_ok(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
@@ -346,15 +347,17 @@ int pa_decode_common_prefix(void *out, const void *query, const void *k_cache, c
     pp.d = decode_params(out, query, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
                          num_heads, num_kv_heads, block_size, num_blocks, max_context_len, scale, w.pt, d_err);
     pa::DecodeParams &d = pp.d;
-    d.ws_acc = static_cast<float *>(workspace);
-    d.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + w.acc);
+    // the queue's counter comes first, so that it stays put whatever the call's sizes
+    char *base = static_cast<char *>(workspace);
+    pp.queue = reinterpret_cast<unsigned *>(base);
+    d.ws_acc = reinterpret_cast<float *>(base + kQueueBytes);
+    d.ws_ml = reinterpret_cast<float2 *>(base + kQueueBytes + w.acc);
     d.len_offset = pp.prefix_tokens;
     d.part_base = w.pieces;
     d.slots = w.slots;
     d.max_partitions = w.slots - w.pieces;
     d.force_partials = 1;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    pp.queue = reinterpret_cast<unsigned *>(static_cast<char *>(workspace) + w.acc + w.ml);
     const int rc = pa::launch_prefix(dtype, block_size, group, pp, st);
     if (rc != PA_OK) return rc;
     return pa::launch_prefix_merge(dtype, group, pp, st);

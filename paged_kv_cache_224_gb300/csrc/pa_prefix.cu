@@ -232,7 +232,6 @@ int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp
     p.part_slots = d.slots;
     pl.dp = d;
     pl.decode_next = pp.queue;
-    if (cudaMemsetAsync(pp.queue, 0, sizeof(unsigned), stream) != cudaSuccess) return PA_ERR_CUDA;
     for (int g0 = 0; g0 < pp.groups; g0 += kPrefillMaxSeqs) {
         const bool last = g0 + kPrefillMaxSeqs >= pp.groups;
         p.num_seqs = last ? x.last_groups : kPrefillMaxSeqs;

@@ -112,7 +112,7 @@ def test_common_prefix_refusals(lib):
     assert prefix(lib, k=BUF + 8) == -6
     need = lib.pa_decode_common_prefix_workspace_bytes(12, 8, 2, 128, 16, 100, 6, 2, 0)
     # 2 groups x 2 kv heads x one row tile of one key tile: one piece each, and one partition of own tokens;
-    # then the queue's counter
+    # before them the queue's counter
     assert need == 12 * 8 * 2 * (128 + 2) * 4 + 256
     assert prefix(lib, ws=0) == -5 and prefix(lib, wsb=need - 1) == -5 and prefix(lib, ws=BUF + 16) == -6
     assert lib.pa_decode_common_prefix_workspace_bytes(12, 8, 2, 128, 16, 100, 5, 2, 0) == 0

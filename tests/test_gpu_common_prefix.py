@@ -146,11 +146,11 @@ def test_broken_promises_are_flagged():
     assert torch.equal(out[10:], good[10:])
 
 
-def test_results_repeat_bit_for_bit_with_any_workspace_content_captured_and_on_another_stream():
+def test_results_repeat_bit_for_bit_whatever_the_workspace_holds_captured_and_on_another_stream():
     c = setup(1, 24, 70, list(range(24)), 8, 2, 16, "bf16", seed=26)
     ref, _ = call(c)
     ws = pa.decode_common_prefix_workspace(c["q"], 2, 16, c["ml"], 24, 70)
-    ws.fill_(255)
+    ws[256:].fill_(255)    # past the counter its content is ignored
     out = torch.zeros_like(ref)
     lens = torch.as_tensor(c["lens"], dtype=torch.int32, device=DEV)
     args = (out, c["q"], c["kc"], c["vc"], c["bt"], lens, c["scale"], c["ml"], 24, 70)
@@ -167,6 +167,18 @@ def test_results_repeat_bit_for_bit_with_any_workspace_content_captured_and_on_a
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
+
+
+def test_one_workspace_serves_calls_of_other_sizes():
+    big = setup(2, 40, 30, list(range(80)), 8, 2, 16, "f16", seed=28)
+    small = setup(1, 3, 2, [5, 0, 40], 8, 2, 16, "f16", seed=29)
+    none = setup(1, 4, 3, [0] * 4, 8, 2, 16, "f16", seed=30)
+    ws = pa.decode_common_prefix_workspace(big["q"], 2, 16, big["ml"], 40, 30)
+    want = [call(c)[0] for c in (big, small, none)]
+    for _ in range(2):
+        for c, w in zip((big, small, none), want):
+            out, err = call(c, workspace=ws)
+            assert err == 0 and torch.equal(out, w)
 
 
 def test_wrong_tensors_are_refused():
