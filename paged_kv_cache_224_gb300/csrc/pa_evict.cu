@@ -49,7 +49,7 @@ __device__ __forceinline__ int blocks_of(int tokens, int bs) { return (tokens + 
 
 __global__ void __launch_bounds__(128) evict_mark_kernel(const __grid_constant__ EvictParams p) {
     pdl_wait();
-    pdl_trigger();
+    pdl_trigger();  // after the wait: the selecting CTAs rely on it
     const int s = blockIdx.x;
     bool bad;
     const int n = min(evict_len(p, s, &bad), p.keep);
@@ -128,9 +128,12 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     };
     for (int i = tid; i < 4 * 256; i += kSelThreads) (&s_hist[0][0])[i] = 0u;
     __syncthreads();
-    pdl_wait();
+    // This grid starts once every CTA of the marking one has got past its own
+    // wait, so whatever came before that one on the stream is complete: only
+    // the CTAs that read the marks wait for them.
     pdl_trigger();
     if (row >= p.num_seqs * p.num_kv_heads) {  // clusters that do not select (and so never sync)
+        pdl_wait();
         const int seq = blockIdx.x - p.num_seqs * p.num_kv_heads * CL;
         if (seq < p.num_seqs) check_blocks(p, seq);
         return;
