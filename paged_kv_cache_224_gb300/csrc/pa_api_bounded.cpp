@@ -246,8 +246,14 @@ int pa_decode_weights(void *out, const void *query, const void *k_cache, const v
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (w.window)
         return pa::launch_window(dtype, block_size, group, p, queries_per_row, weights, weights_out, weights_len, st);
+    const bool whole = w.slots == 1 && queries_per_row == 1;  // every sequence is one unit
+    if (whole) {
+        p.weights = weights;
+        p.weights_out = weights_out;
+        p.weights_width = weights_len;
+    }
     const int rc = pa::launch_decode_scores(dtype, head_dim, block_size, group, p, st);
-    if (rc != PA_OK) return rc;
+    if (rc != PA_OK || whole) return rc;
     return pa::launch_weights_merge(dtype, head_dim, group, p, weights, weights_out, weights_len, queries_per_row, st);
 }
 

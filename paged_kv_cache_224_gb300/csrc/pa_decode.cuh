@@ -500,6 +500,8 @@ __global__ void __launch_bounds__(NW * 32, decode_min_ctas<G>()) decode_kernel(c
     __syncthreads();
 
     const int tid = threadIdx.x;
+    // kScores: (maximum, 1 / sum) of each head, in the first warp's P buffer
+    [[maybe_unused]] float2 *s_ml = reinterpret_cast<float2 *>(smem + C::OFF_PBUF);
     if (tid < G * (D / 8)) {
         const int h = tid / (D / 8);
         const int ch = tid % (D / 8);
@@ -534,6 +536,7 @@ __global__ void __launch_bounds__(NW * 32, decode_min_ctas<G>()) decode_kernel(c
             *reinterpret_cast<uint4 *>(orow) = pack8<T>(o);
             if constexpr (kScores) {
                 if (ch == 0) p.ws_ml[row * p.slots] = make_float2(M, lsum);
+                if (ch == 0) s_ml[h] = max_inv(M, lsum);
             }
         } else {
             const size_t slot = row * p.slots + p.part_base + part;
@@ -541,6 +544,20 @@ __global__ void __launch_bounds__(NW * 32, decode_min_ctas<G>()) decode_kernel(c
             dst[0] = make_float4(o[0], o[1], o[2], o[3]);
             dst[1] = make_float4(o[4], o[5], o[6], o[7]);
             if (ch == 0) p.ws_ml[slot] = make_float2(M, lsum);
+        }
+    }
+    if constexpr (kScores) {
+        if (p.weights_out) {  // the unit is the whole sequence
+            __syncthreads();  // s_ml, and every warp's scores (the barrier before the merge)
+            float2 ml[G];
+#pragma unroll
+            for (int h = 0; h < G; ++h) ml[h] = s_ml[h];
+            const size_t at = (size_t)(s * p.num_kv_heads + kvh) * p.weights_width;
+            for (int j = tid; j < ntok; j += NW * 32) {
+                float x[G];
+                load_scores<G>(scores + (size_t)j * G, x);
+                p.weights_out[at + j] = p.weights[at + j] + weight_of<G>(x, ml);
+            }
         }
     }
 }

@@ -517,6 +517,20 @@ __device__ __forceinline__ void tc_unit(const DecodeParams &p, const CUtensorMap
         // the next unit's row sums land in xsum only after every warp read
         // this unit's (its first tile has a barrier first)
         const int d = t;  // O^T row = dimension
+        if constexpr (kScores) {
+            if (p.weights_out) {  // the unit is the whole sequence; each thread wrote its keys' scores itself
+                float2 ml[G];
+#pragma unroll
+                for (int h = 0; h < G; ++h) ml[h] = max_inv(m_run[h], lsum[h]);
+                const size_t row = (size_t)(u.s * p.num_kv_heads + kvh);
+                for (int key = t; key < ntok; key += kTK) {
+                    float x[G];
+                    load_scores<G>(p.scores + (row * p.score_stride + key) * G, x);
+                    p.weights_out[row * p.weights_width + key] =
+                        p.weights[row * p.weights_width + key] + weight_of<G>(x, ml);
+                }
+            }
+        }
         if (u.direct) {
 #pragma unroll
             for (int h = 0; h < G; ++h) {

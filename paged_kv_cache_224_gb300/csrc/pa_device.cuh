@@ -203,4 +203,37 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// The G scores that are kept of one key.
+template <int G>
+__device__ __forceinline__ void load_scores(const float *a, float (&x)[G]) {
+    if constexpr (G == 1) {
+        x[0] = *a;
+    } else if constexpr (G == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(a);
+        x[0] = v.x, x[1] = v.y;
+    } else {
+#pragma unroll
+        for (int h = 0; h < G; h += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(a + h);
+            x[h] = v.x, x[h + 1] = v.y, x[h + 2] = v.z, x[h + 3] = v.w;
+        }
+    }
+}
+
+// A key's attention weight, summed over the G heads: scores x, each head's
+// (maximum, 1 / sum) in ml.
+template <int G>
+__device__ __forceinline__ float weight_of(const float (&x)[G], const float2 (&ml)[G]) {
+    float w = 0.f;
+#pragma unroll
+    for (int h = 0; h < G; ++h) w = fmaf(fast_exp2(x[h] - ml[h].x), ml[h].y, w);
+    return w;
+}
+
+// (maximum, 1 / sum) for weight_of; (0, 0) where no key was attended, so that
+// 2^(-inf - 0) = 0 is every key's weight.
+__device__ __forceinline__ float2 max_inv(float m, float l) {
+    return m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(m, 1.f / l);
+}
+
 }  // namespace pa

@@ -70,6 +70,11 @@ struct DecodeParams {
     // for whole-sequence units too.
     float *scores;
     long long score_stride;
+    // With weights_out set (every sequence is one unit, one sequence to a row of
+    // weights_width totals), the unit adds its weights to the totals itself.
+    const float *weights;
+    float *weights_out;
+    int weights_width;
 };
 
 // One sequence's chunk in a prefill launch.  Its work units are (kv head,

@@ -8,7 +8,9 @@
 // against 4 D bytes of K and V per (token, kv head): 1.6% of it at one query
 // head per kv head and head_dim 128, 12.5% at eight.
 //
-// One kernel, two kinds of CTA:
+// Where every sequence is a single unit the decode kernel adds the weights up
+// itself, from scores it has just written (one launch less: 2 us of a short
+// batch's 12).  Otherwise one kernel, two kinds of CTA:
 //   merge    the log-sum-exp merge of a split sequence's partials, one warp per
 //            (sequence, head): out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p;
 //   totals   one CTA per (row of totals, kv head, chunk of tokens): each
@@ -73,22 +75,6 @@ __device__ __forceinline__ void merge_row(const DecodeParams &p, int pair, int l
         *reinterpret_cast<uint2 *>(orow) = u;
     } else {
         *reinterpret_cast<uint32_t *>(orow) = Elem<T>::pack2(o[0] * inv, o[1] * inv);
-    }
-}
-
-template <int G>
-__device__ __forceinline__ void load_scores(const float *a, float (&x)[G]) {
-    if constexpr (G == 1) {
-        x[0] = *a;
-    } else if constexpr (G == 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(a);
-        x[0] = v.x, x[1] = v.y;
-    } else {
-#pragma unroll
-        for (int h = 0; h < G; h += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(a + h);
-            x[h] = v.x, x[h + 1] = v.y, x[h + 2] = v.z, x[h + 3] = v.w;
-        }
     }
 }
 
