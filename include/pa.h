@@ -346,7 +346,8 @@ PA_API int pa_mixed_step(void *prefill_out, const void *prefill_query, const int
  *   inv_freq       float [rot_dim / 2] (device), finite
  *   pair_axis      int [rot_dim / 2] in HOST memory, or NULL for axis 0 throughout
  * Supported: head_dim a multiple of 16 up to 256, rot_dim a multiple of 16 up
- * to head_dim (0: a plain cache write), up to 8 axes, any block_size.
+ * to head_dim (0: a plain cache write, positions and inv_freq may be NULL), up
+ * to 8 axes, any block_size.
  * num_tokens == 0 is a no-op.  The cache write of the values is bit-exact.
  */
 PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
@@ -427,7 +428,8 @@ PA_API int pa_decode_weights(void *out, const void *query, const void *k_cache, 
  *                  PA_DEVERR_COPY_PAIR and is not written
  *   new_context_lens  must not be context_lens
  *   workspace      >= pa_evict_workspace_bytes(num_blocks) bytes, 16-byte
- *                  aligned, scratch; its content on entry is ignored
+ *                  aligned, scratch; its content on entry is ignored; not to be
+ *                  shared with work that overlaps the call on the device
  * Needs sink + recent <= keep and keep >= 1.  Supported: head_dim in {64, 128},
  * block_size in {8, 16, 32, 64, 128}.  Invalid lengths are clamped and flagged
  * as in pa_decode; a row whose old table entry is out of the pool is flagged

@@ -8,6 +8,11 @@
 // against 4 D bytes of K and V per (token, kv head): 1.6% of it at one query
 // head per kv head and head_dim 128, 12.5% at eight.
 //
+// Measured: 256 sequences of up to 4096 tokens, 32/8 heads, bf16, 361 us, 6.05 TB/s
+// of what the call cannot do without (90% of the copy rate), 326 of them the
+// decode kernel with its score stores, 25 this one; 8 of 16384 to 65536, 64/8
+// heads, 286 us (88%), 256 and 27.
+//
 // Where every sequence is a single unit the decode kernel adds the weights up
 // itself, from scores it has just written (one launch less: 2 us of a short
 // batch's 12).  Otherwise one kernel, two kinds of CTA:

@@ -101,6 +101,7 @@ CASES = [
     (7, 64, 8, 16, 16, 3, 16, "bf16", True, True),       # one unit a head
     (300, 40, 40, 128, 128, 1, 16, "f16", False, True),  # more units than threads
     (9, 8, 8, 64, 0, 1, 16, "bf16", False, True),        # nothing rotated: a plain cache write
+    (45, 4, 2, 64, 32, 2, 5, "f16", False, True),        # any block size
     (2100, 2, 1, 64, 64, 3, 16, "bf16", False, True),    # more tokens than CTAs: each walks several
     (1300, 1, 1, 256, 256, 2, 32, "f16", True, False),   # more pairs than threads
 ]

@@ -106,6 +106,12 @@ def test_several_queries_add_to_one_row_in_place(w, G):
     check(setup([3, 700, 0, 64], w, 2 * G, 2, 128, 16, "f16", seed=w), in_place=True)
 
 
+@pytest.mark.parametrize("D,bs,G,dtype", [(64, 16, 4, "bf16"), (64, 128, 8, "f16"), (128, 8, 8, "bf16"), (128, 16, 1, "f16")])
+def test_several_queries_one_after_the_other(D, bs, G, dtype):
+    # shapes that are not attended together; more positions than are summed at once
+    check(setup([600, 37], 20 if G * 20 < 16 or D == 64 or bs == 8 else 3, G, 1, D, bs, dtype, seed=D + G))
+
+
 WINDOWS = [
     # (cache lengths, positions, G, Hkv, bs, dtype): attended together on the tensor cores
     ([300], 16, 1, 1, 16, "bf16"),
