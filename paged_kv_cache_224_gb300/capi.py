@@ -491,6 +491,7 @@ def pa_prefill_batch(out, query, k_cache, v_cache, block_tables, prefix_lens, ch
 # the tensors for device and contiguity, no stream or device objects.
 
 _fns: dict = {}
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 # (absent from a torch built without CUDA, where every call raises before them)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -513,12 +514,6 @@ def _checked(index, *ts) -> None:
             raise ValueError("tensors must be on one CUDA device")
         if not t.is_contiguous():
             raise ValueError("tensor must be contiguous")
-
-
-def _typed(dtype, what, *ts) -> None:
-    for t in ts:
-        if t.dtype is not dtype:
-            raise TypeError(what)
 
 
 def _call(name, index, *args) -> None:
@@ -577,11 +572,15 @@ def pa_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, position
     each pair (None: axis 0)."""
     dev = _index(k_cache)
     _checked(dev, k_cache, v_cache, positions, slot_mapping, inv_freq, d_err)
-    _typed(torch.int64, "slot_mapping must be int64", slot_mapping)
-    _typed(torch.int32, "positions must be int32", positions)
-    _typed(torch.float32, "inv_freq must be float32", inv_freq)
+    if slot_mapping.dtype is not _I64:
+        raise TypeError("slot_mapping must be int64")
+    if positions.dtype is not _I32:
+        raise TypeError("positions must be int32")
+    if inv_freq.dtype is not _F32:
+        raise TypeError("inv_freq must be float32")
     dt = k_cache.dtype
-    _typed(dt, "dtype mismatch", v_cache)
+    if v_cache.dtype is not dt:
+        raise TypeError("dtype mismatch")
     NB, Hkv, bs, D = shape = k_cache.shape
     if query.dim() != 3 or v_cache.shape != shape or inv_freq.dim() != 1:
         raise ValueError("shape mismatch")
@@ -633,9 +632,13 @@ def pa_decode_weights(out, query, k_cache, v_cache, block_tables, context_lens, 
         weights_out = weights
     dev = _index(query)
     _checked(dev, query, out, k_cache, v_cache, block_tables, context_lens, weights, weights_out, workspace, d_err)
-    _typed(torch.int32, "block_tables and context_lens must be int32", block_tables, context_lens)
-    _typed(torch.float32, "weights must be float32", weights, weights_out)
-    _typed(query.dtype, "dtype mismatch", out, k_cache, v_cache)
+    if block_tables.dtype is not _I32 or context_lens.dtype is not _I32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if weights.dtype is not _F32 or weights_out.dtype is not _F32:
+        raise TypeError("weights must be float32")
+    dt = query.dtype
+    if out.dtype is not dt or k_cache.dtype is not dt or v_cache.dtype is not dt:
+        raise TypeError("dtype mismatch")
     NB, Hkv, bs, D = shape = k_cache.shape
     qshape = query.shape
     B, Hq, Dq = qshape
@@ -670,10 +673,13 @@ def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, new_block_ta
     dev = _index(k_cache)
     _checked(dev, k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_context_lens,
              new_weights, kept, workspace, d_err)
-    _typed(torch.int32, "tables, lengths and kept must be int32", block_tables, context_lens, new_block_tables,
-           new_context_lens, kept)
-    _typed(torch.float32, "weights must be float32", weights, new_weights)
-    _typed(k_cache.dtype, "dtype mismatch", v_cache)
+    if block_tables.dtype is not _I32 or context_lens.dtype is not _I32 or new_block_tables.dtype is not _I32 or \
+            new_context_lens.dtype is not _I32 or kept.dtype is not _I32:
+        raise TypeError("tables, lengths and kept must be int32")
+    if weights.dtype is not _F32 or new_weights.dtype is not _F32:
+        raise TypeError("weights must be float32")
+    if v_cache.dtype is not k_cache.dtype:
+        raise TypeError("dtype mismatch")
     NB, Hkv, bs, D = shape = k_cache.shape
     B = context_lens.numel()
     wshape = weights.shape
@@ -715,8 +721,11 @@ def pa_decode_common_prefix(out, query, k_cache, v_cache, block_tables, context_
     sequences (any size) share their first ``prefix_blocks`` physical blocks."""
     dev = _index(query)
     _checked(dev, query, out, k_cache, v_cache, block_tables, context_lens, workspace, d_err)
-    _typed(torch.int32, "block_tables and context_lens must be int32", block_tables, context_lens)
-    _typed(query.dtype, "dtype mismatch", out, k_cache, v_cache)
+    if block_tables.dtype is not _I32 or context_lens.dtype is not _I32:
+        raise TypeError("block_tables and context_lens must be int32")
+    dt = query.dtype
+    if out.dtype is not dt or k_cache.dtype is not dt or v_cache.dtype is not dt:
+        raise TypeError("dtype mismatch")
     NB, Hkv, bs, D = shape = k_cache.shape
     qshape = query.shape
     B, Hq, Dq = qshape

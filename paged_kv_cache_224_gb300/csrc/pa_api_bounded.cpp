@@ -84,6 +84,7 @@ struct WeightsWs {
 constexpr size_t kQueueBytes = 256;
 struct PrefixWs {
     int pt, pieces, slots;
+    pa::PrefixSchedules sched;
     size_t acc, ml;
     bool ok;
     PrefixWs(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
@@ -95,8 +96,10 @@ struct PrefixWs {
         pt = partition_tokens ? partition_tokens
                               : pa::prefix_partition_tokens(num_seqs, num_kv_heads, block_size, longest);
         const int partitions = std::max(1, (int)(((long long)longest + pt - 1) / pt));
-        pieces = pa::prefix_pieces(num_seqs / group_size, group_size, prefix, num_heads / num_kv_heads, num_kv_heads,
-                                   longest, partitions, num_seqs);
+        const int groups = num_seqs / group_size;
+        sched = pa::prefix_schedules(groups, group_size, prefix, num_heads / num_kv_heads, num_kv_heads, longest,
+                                     partitions, num_seqs);
+        pieces = pa::prefix_pieces(groups, sched);
         slots = pieces + partitions;
         const PartialWs w(num_seqs, num_heads, head_dim, slots);
         acc = w.acc;
@@ -350,6 +353,7 @@ int pa_decode_common_prefix(void *out, const void *query, const void *k_cache, c
     pp.groups = num_seqs / group_size;
     pp.group_size = group_size;
     pp.prefix_tokens = prefix_blocks * block_size;
+    pp.sched = w.sched;
     pp.d = decode_params(out, query, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
                          num_heads, num_kv_heads, block_size, num_blocks, max_context_len, scale, w.pt, d_err);
     pa::DecodeParams &d = pp.d;

@@ -28,6 +28,10 @@
 // slower (106 and 78 us: a CTA or cluster per row shares the rows out worse
 // than a CTA per 256 of them).
 //
+// Few blocks (kOneCheck): the CTA that checks marks them too, all of them by
+// itself, and the first launch falls away (3 sequences of 40..200 tokens to 48:
+// 6.6 us and 14.5 us of host time with it, 6.2 and 12.2 without).
+//
 // owner[] needs no clearing: an entry e counts for block b only if the new
 // table's entry e names b, so a stale value proves nothing by itself.
 #include <cooperative_groups.h>
@@ -55,10 +59,8 @@ __device__ __forceinline__ int evict_len(const EvictParams &p, int s, bool *bad)
 
 __device__ __forceinline__ int blocks_of(int tokens, int bs) { return (tokens + bs - 1) / bs; }
 
-__global__ void __launch_bounds__(128) evict_mark_kernel(const __grid_constant__ EvictParams p) {
-    pdl_wait();
-    pdl_trigger();  // after the wait: the selecting CTAs rely on it
-    const int s = blockIdx.x;
+// The sequence's new blocks, by one CTA.
+__device__ __forceinline__ void mark_blocks(const EvictParams &p, int s) {
     bool bad;
     const int n = min(evict_len(p, s, &bad), p.keep);
     const int nb = blocks_of(n, p.block_size);
@@ -67,6 +69,12 @@ __global__ void __launch_bounds__(128) evict_mark_kernel(const __grid_constant__
         if (b >= 0 && b < p.num_blocks) p.owner[b] = s * p.new_max_blocks + j;
         else flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
     }
+}
+
+__global__ void __launch_bounds__(128) evict_mark_kernel(const __grid_constant__ EvictParams p) {
+    pdl_wait();
+    pdl_trigger();  // after the wait: the selecting CTAs rely on it
+    mark_blocks(p, blockIdx.x);
 }
 
 // One CTA per sequence, beside the selecting ones: its new length, and the new
@@ -136,14 +144,22 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     };
     for (int i = tid; i < 4 * 256; i += kSelThreads) (&s_hist[0][0])[i] = 0u;
     __syncthreads();
-    // This grid starts once every CTA of the marking one has got past its own
-    // wait, so whatever came before that one on the stream is complete: only
-    // the CTAs that read the marks wait for them.
+    // After a marking launch this grid starts once every CTA of that one has got
+    // past its own wait, so whatever came before it on the stream is complete:
+    // only the CTAs that read the marks wait for them.
+    if (p.one_check) pdl_wait();
     pdl_trigger();
     if (row >= p.num_seqs * p.num_kv_heads) {  // clusters that do not select (and so never sync)
-        pdl_wait();
         const int seq = blockIdx.x - p.num_seqs * p.num_kv_heads * CL;
-        if (seq < p.num_seqs) check_blocks(p, seq);
+        if (p.one_check) {
+            if (seq > 0) return;
+            for (int i = 0; i < p.num_seqs; ++i) mark_blocks(p, i);
+            __syncthreads();
+            for (int i = 0; i < p.num_seqs; ++i) check_blocks(p, i);
+        } else {
+            pdl_wait();
+            if (seq < p.num_seqs) check_blocks(p, seq);
+        }
         return;
     }
     bool bad;
@@ -390,14 +406,19 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
     }
 }
 
+// Most table entries, and sequences, that one CTA marks and checks by itself
+// (a sequence takes it some 2 us of dependent loads, beside the selection's 6).
+constexpr int kOneCheckBlocks = 1024, kOneCheckSeqs = 4;
+
 constexpr int kNarrow = 256, kNarrowItems = 16;
 constexpr int kWide = 512, kWideItems = 16;
 
 template <int CL, int kThreads, int kItems>
 int launch_select(const EvictParams &p, long long rows, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    // a CTA per sequence beside them, in whole clusters
-    cfg.gridDim = dim3((unsigned)(rows * CL + (p.num_seqs + CL - 1) / CL * CL));
+    // the checking CTAs beside them, in whole clusters
+    const int checks = p.one_check ? 1 : p.num_seqs;
+    cfg.gridDim = dim3((unsigned)(rows * CL + (checks + CL - 1) / CL * CL));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -414,8 +435,13 @@ int launch_select(const EvictParams &p, long long rows, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_evict(const EvictParams &p, cudaStream_t stream) {
-    if (launch_pdl(evict_mark_kernel, dim3(p.num_seqs), dim3(128), 0, stream, p) != cudaSuccess) return PA_ERR_CUDA;
+int launch_evict(const EvictParams &p_in, cudaStream_t stream) {
+    EvictParams p = p_in;
+    p.one_check = p.num_seqs <= kOneCheckSeqs &&
+                  (long long)p.num_seqs * (p.max_blocks + p.new_max_blocks) <= kOneCheckBlocks;
+    if (!p.one_check &&
+        launch_pdl(evict_mark_kernel, dim3(p.num_seqs), dim3(128), 0, stream, p) != cudaSuccess)
+        return PA_ERR_CUDA;
     const long long rows = (long long)p.num_seqs * p.num_kv_heads;
     const int most = std::min(p.keep, std::min(p.max_context_len, p.width));
     const int chunks = std::max(1, (most + kCopyRows - 1) / kCopyRows);

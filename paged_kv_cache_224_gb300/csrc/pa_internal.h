@@ -165,6 +165,7 @@ struct EvictParams {
     int *d_err;
     int num_seqs, num_kv_heads, head_dim, block_size, num_blocks, max_blocks, new_max_blocks;
     int width, max_context_len, keep, sink, recent;
+    int one_check;               // one CTA beside the selecting ones marks and checks all blocks
 };
 
 // Split-K partition length for the automatic setting.
@@ -232,9 +233,23 @@ int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const P
 // its own tokens.  A unit's key tiles are shared out over the CTAs as in the
 // stream-K prefill, and each piece of a unit leaves an unnormalised partial in
 // its own slot; prefix_pieces is the most pieces a unit can be cut into.
+// The schedule of one launch, of up to kPrefillMaxSeqs groups.
+struct PrefixSchedule {
+    long long tiles;  // key tiles of all units
+    int row_tiles;    // units per (group, kv head)
+    int n;            // key tiles per unit
+    int ctas;         // CTAs that the tiles are shared out to
+};
+// The launches of a call: full ones, whose CTAs have nothing to decode (none, if
+// the groups fit one launch), and the last, with the own tokens of all sequences.
+struct PrefixSchedules {
+    PrefixSchedule full, last;
+    int last_groups;
+};
 struct PrefixParams {
     DecodeParams d;              // of the own tokens: d.slots, d.part_base (= pieces), d.len_offset
     int groups, group_size, prefix_tokens;
+    PrefixSchedules sched;
     unsigned *queue;             // the decode instances' shared unit queue, one counter
 };
 // One launch: the prefixes of up to kPrefillMaxSeqs groups; the last one also
@@ -245,8 +260,9 @@ struct PrefixLaunch {
     int prefix_ctas, decode_units;
     unsigned *decode_next;
 };
-int prefix_pieces(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads, int longest_own,
-                  int partitions, int num_seqs);
+PrefixSchedules prefix_schedules(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads,
+                                 int longest_own, int partitions, int num_seqs);
+int prefix_pieces(int groups, const PrefixSchedules &x);
 // Partition length of the own tokens when the caller leaves it open: the
 // decode instances take units from a queue, so a sequence is split only as far
 // as it takes to give each about four.

@@ -51,13 +51,6 @@ int split_ctas(long long tiles, int unit_tiles, double units, double unit_bytes)
     return best;
 }
 
-// Schedule of one launch of `groups` groups (at most kPrefillMaxSeqs).
-struct PrefixSchedule {
-    long long tiles;  // key tiles of all units
-    int row_tiles;    // units per (group, kv head)
-    int n;            // key tiles per unit
-    int ctas;
-};
 PrefixSchedule prefix_schedule(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads,
                                double units, double unit_bytes) {
     PrefixSchedule s;
@@ -66,29 +59,6 @@ PrefixSchedule prefix_schedule(int groups, int group_size, int prefix_tokens, in
     s.tiles = (long long)groups * num_kv_heads * s.row_tiles * s.n;
     s.ctas = (int)std::min<long long>(split_ctas(s.tiles, s.n, units, unit_bytes), s.tiles);
     return s;
-}
-
-// The launches of a call: full ones, whose CTAs have nothing to decode, and the
-// last, with the own tokens of all sequences.
-struct Schedules {
-    PrefixSchedule full, last;
-    int last_groups;
-};
-Schedules schedules(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads, int longest_own,
-                    int partitions, int num_seqs) {
-    Schedules x;
-    x.last_groups = (groups - 1) % kPrefillMaxSeqs + 1;
-    x.full = prefix_schedule(kPrefillMaxSeqs, group_size, prefix_tokens, group, num_kv_heads, 0.0, 0.0);
-    // the own tokens' lengths are on the device: half of the longest each
-    const double bytes = 0.5 * longest_own * (2 * kD * 2) * num_kv_heads * num_seqs;
-    const double units = longest_own > 0 ? (double)num_seqs * num_kv_heads * std::max(1.0, 0.5 * partitions) : 0.0;
-    x.last = prefix_schedule(x.last_groups, group_size, prefix_tokens, group, num_kv_heads, units,
-                             units > 0 ? bytes / units : 0.0);
-    return x;
-}
-Schedules schedules(const PrefixParams &pp, int group) {
-    return schedules(pp.groups, pp.group_size, pp.prefix_tokens, group, pp.d.num_kv_heads,
-                     pp.d.max_context_len - pp.prefix_tokens, pp.d.max_partitions, pp.d.num_seqs);
 }
 
 // Where the merge finds a row's prefix partials.
@@ -189,10 +159,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 
 }  // namespace
 
-int prefix_pieces(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads, int longest_own,
-                  int partitions, int num_seqs) {
-    const Schedules x =
-        schedules(groups, group_size, prefix_tokens, group, num_kv_heads, longest_own, partitions, num_seqs);
+PrefixSchedules prefix_schedules(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads,
+                                 int longest_own, int partitions, int num_seqs) {
+    PrefixSchedules x{};
+    x.last_groups = (groups - 1) % kPrefillMaxSeqs + 1;
+    if (groups > kPrefillMaxSeqs)
+        x.full = prefix_schedule(kPrefillMaxSeqs, group_size, prefix_tokens, group, num_kv_heads, 0.0, 0.0);
+    // the own tokens' lengths are on the device: half of the longest each
+    const double bytes = 0.5 * longest_own * (2 * kD * 2) * num_kv_heads * num_seqs;
+    const double units = longest_own > 0 ? (double)num_seqs * num_kv_heads * std::max(1.0, 0.5 * partitions) : 0.0;
+    x.last = prefix_schedule(x.last_groups, group_size, prefix_tokens, group, num_kv_heads, units,
+                             units > 0 ? bytes / units : 0.0);
+    return x;
+}
+
+int prefix_pieces(int groups, const PrefixSchedules &x) {
     // a unit's first and last pieces, and whole ranges of at least q tiles between them
     auto most = [](const PrefixSchedule &s) {
         const long long q = s.tiles / s.ctas;
@@ -215,7 +196,7 @@ int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp
     const bool any_own = d.max_context_len > pp.prefix_tokens;
     const long long units = any_own ? (long long)d.max_partitions * d.num_seqs * d.num_kv_heads : 0;
     if (units > 0x3fffffffLL) return PA_ERR_UNSUPPORTED;
-    const Schedules x = schedules(pp, group);
+    const PrefixSchedules &x = pp.sched;
     PrefixLaunch pl{};
     PrefillParams &p = pl.pp;
     p.query = d.query;
@@ -257,7 +238,7 @@ int launch_prefix(pa_dtype dt, int block_size, int group, const PrefixParams &pp
 
 int launch_prefix_merge(pa_dtype dt, int group, const PrefixParams &pp, cudaStream_t stream) {
     const DecodeParams &d = pp.d;
-    const Schedules x = schedules(pp, group);
+    const PrefixSchedules &x = pp.sched;
     MergeParams mp{};
     mp.group_size = pp.group_size;
     mp.head_group = group;

@@ -77,6 +77,7 @@ def check(c, skip=()):
 
 
 CASES = [
+    ([90, 17, 64, 200, 33, 5, 0, 120], 40, 2, 9, 2, 64, 16, "bf16", "random"),
     # (lens, keep, sink, recent, Hkv, D, bs, dtype, values)
     ([40, 200, 48, 49, 0, 1], 48, 4, 16, 4, 64, 16, "f16", "ties"),
     ([1], 1, 0, 0, 1, 128, 16, "bf16", "ties"),
@@ -128,6 +129,15 @@ def test_a_new_block_named_twice_is_written_by_nobody():
     # the third sequence's blocks are the first's, all four of them
     c["new"][2] = c["new"][0]
     assert check(c, skip=(0, 2)) == pa.capi.DEVERR["copy_pair"]
+
+
+def test_conflicts_among_many_sequences():
+    # more than one CTA marks and checks: a block named twice, one still read, one of its own
+    c = setup([100 + i for i in range(9)], 64, 4, 8, 2, 64, 16, "bf16", seed=16)
+    c["new"][7] = c["new"][3]
+    c["new"][5] = c["old"][8, :4]
+    c["new"][0] = c["old"][0, 2:6]
+    assert check(c, skip=(0, 3, 5, 7)) == pa.capi.DEVERR["copy_pair"]
 
 
 def test_a_new_block_that_is_still_read_is_not_written():
