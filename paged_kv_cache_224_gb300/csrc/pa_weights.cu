@@ -16,8 +16,8 @@
 // Where every sequence is a single unit the decode kernel adds the weights up
 // itself, from scores it has just written (one launch less: 2 us of a short
 // batch's 12).  Otherwise one kernel, two kinds of CTA:
-//   merge    the log-sum-exp merge of a split sequence's partials, one warp per
-//            (sequence, head): out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p;
+//   merge    the log-sum-exp merge of a split sequence's partials, a warp (a CTA,
+//            with many partials) per (sequence, head): out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p;
 //   totals   one CTA per (row of totals, kv head, chunk of tokens): each
 //            token's weight is sum_h 2^(score_h - M_h) / l_h over the group's
 //            heads, added up over the row's sequences in their order (so the
@@ -39,8 +39,15 @@ __device__ __forceinline__ int clamped_len(const DecodeParams &p, int s) {
     return max(0, min(p.context_lens[s], cap));
 }
 
-template <typename T, int D>
-__device__ __forceinline__ void merge_row(const DecodeParams &p, int pair, int lane) {
+// Partials from which a row is merged by a whole CTA: a warp takes some 0.15 us a
+// partial (246 of them, three sequences of 65536 tokens: 43 us by a warp each,
+// 19 by a CTA).
+constexpr int kWideMerge = 17;
+
+// One (sequence, head) by one warp (kParts 1), or by a CTA of kParts warps, each
+// with every kParts-th partial, their sums added in the warps' order.
+template <typename T, int D, int kParts>
+__device__ __forceinline__ void merge_row(const DecodeParams &p, int pair, int lane, int part) {
     constexpr int VPL = D / 32;  // values per lane
     const int s = pair / p.num_heads;
     const int L = clamped_len(p, s);
@@ -56,7 +63,7 @@ __device__ __forceinline__ void merge_row(const DecodeParams &p, int pair, int l
     for (int d = 0; d < VPL; ++d) o[d] = 0.f;
     if (M != -INFINITY) {  // else every key was left out: zeros
 #pragma unroll 4
-        for (int i = 0; i < nparts; ++i) {
+        for (int i = part; i < nparts; i += kParts) {
             const float2 ml = p.ws_ml[base + i];
             const float w = fast_exp2(ml.x - M);
             lsum = fmaf(w, ml.y, lsum);
@@ -71,6 +78,21 @@ __device__ __forceinline__ void merge_row(const DecodeParams &p, int pair, int l
             }
         }
     }
+    if constexpr (kParts > 1) {
+        __shared__ float s_o[kParts][D];
+        __shared__ float s_l[kParts];
+#pragma unroll
+        for (int d = 0; d < VPL; ++d) s_o[part][lane * VPL + d] = o[d];
+        if (lane == 0) s_l[part] = lsum;
+        __syncthreads();
+        if (part) return;
+#pragma unroll
+        for (int q = 1; q < kParts; ++q) {
+#pragma unroll
+            for (int d = 0; d < VPL; ++d) o[d] += s_o[q][lane * VPL + d];
+            lsum += s_l[q];
+        }
+    }
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
     T *orow = static_cast<T *>(p.out) + (size_t)pair * D + lane * VPL;
     if constexpr (VPL == 4) {
@@ -83,8 +105,8 @@ __device__ __forceinline__ void merge_row(const DecodeParams &p, int pair, int l
     }
 }
 
-// kItems tokens per thread: 4 (2 at eight heads, for registers), or 1 when the
-// rows are too few to fill the GPU.
+// kItems tokens per thread: 2 (8 or 4 at a time measured 33 against 23 us over 256
+// sequences of up to 4096 tokens), or 1 when the rows are too few to fill the GPU.
 // kMany: several sequences add to a row.
 template <typename T, int D, int G, int kItems, bool kMany>
 __global__ void __launch_bounds__(kThreads)
@@ -96,8 +118,12 @@ __global__ void __launch_bounds__(kThreads)
     pdl_wait();  // the decode kernel's scores and partials are complete and visible
     pdl_trigger();
     if ((int)blockIdx.x < merge_ctas) {
-        const int pair = blockIdx.x * (kThreads / 32) + warp;
-        if (pair < p.num_seqs * p.num_heads) merge_row<T, D>(p, pair, lane);
+        if (p.slots >= kWideMerge) {
+            merge_row<T, D, kThreads / 32>(p, blockIdx.x, lane, warp);
+        } else {
+            const int pair = blockIdx.x * (kThreads / 32) + warp;
+            if (pair < p.num_seqs * p.num_heads) merge_row<T, D, 1>(p, pair, lane, 0);
+        }
         return;
     }
     const int u = blockIdx.x - merge_ctas;
@@ -234,16 +260,19 @@ template <typename T, int D, int G>
 int launch_merge_t(const DecodeParams &p, const float *weights, float *weights_out, int width, int queries_per_row,
                    cudaStream_t stream) {
     const long long rows = (long long)(p.num_seqs / queries_per_row) * p.num_kv_heads;
-    constexpr int kMost = G == 8 ? 2 : 4;
+    constexpr int kMost = 2;
     const bool few = rows * ((p.max_context_len + kMost * kThreads - 1) / (kMost * kThreads)) < 2 * sm_count();
     const int chunk = few ? kThreads : kMost * kThreads;
     int chunks = std::max(1, (p.max_context_len + chunk - 1) / chunk);
     // with many chunks a CTA takes several of a row's, the next one's loads ahead
-    const int loops =
-        queries_per_row > 1 ? 1 : (int)std::min<long long>(std::min(chunks, 8), std::max(1LL, rows * chunks / (8 * sm_count())));
+    // (8 or 12 CTAs an SM measured best at 8 and at 4 heads)
+    constexpr int kPerSm = G == 8 ? 8 : 12;
+    const long long share = std::max(1LL, rows * chunks / (kPerSm * sm_count()));
+    const int loops = queries_per_row > 1 ? 1 : (int)std::min<long long>(share, std::min(chunks, G == 8 ? 8 : 16));
     chunks = (chunks + loops - 1) / loops;
     const long long pairs = (long long)p.num_seqs * p.num_heads;
-    const long long merge = p.max_partitions > 1 ? (pairs + kThreads / 32 - 1) / (kThreads / 32) : 0;
+    const int per_cta = p.slots >= kWideMerge ? 1 : kThreads / 32;
+    const long long merge = p.max_partitions > 1 ? (pairs + per_cta - 1) / per_cta : 0;
     const long long total = merge + rows * chunks;
     if (total > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
     auto kern = queries_per_row > 1
