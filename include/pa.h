@@ -363,8 +363,7 @@ PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const 
  *   weights_out[r][kvh][j] = weights[r][kvh][j] + sum softmax_j(...)
  * over row r's queries and the query heads of kv head kvh, for every j below
  * the longest of the row's contexts; entries from there on are left as they
- * are.  out as from pa_decode (the same kernels and partitions; equal to it up
- * to rounding).
+ * are.  out as from pa_decode (the same kernels; equal to it up to rounding).
  *   weights, weights_out  float [num_seqs / queries_per_row][num_kv_heads]
  *                  [weights_len]; weights_out may be weights itself, else the
  *                  two must not overlap

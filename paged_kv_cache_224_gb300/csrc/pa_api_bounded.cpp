@@ -29,13 +29,6 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Partition length for contexts of at most `longest` tokens, or -1.
-int partition_for(int num_seqs, int num_heads, int num_kv_heads, int block_size, int longest, int partition_tokens) {
-    if (partition_tokens < 0 || partition_tokens % block_size) return -1;
-    if (partition_tokens) return partition_tokens;
-    return pa::auto_partition_tokens(num_seqs, num_heads, num_kv_heads, block_size, longest);
-}
-
 // Partials: fp32 accumulators, then (max, sum) pairs, `slots` per (sequence, head).
 struct PartialWs {
     size_t acc, ml;
@@ -57,15 +50,15 @@ struct WeightsWs {
               int queries_per_row, int partition_tokens) {
         const int group = num_heads / num_kv_heads;
         window = pa::window_supported(head_dim, block_size, group, queries_per_row);
+        ok = partition_tokens >= 0 && partition_tokens % block_size == 0;
+        if (!ok) return;
         if (window) {
-            ok = partition_tokens >= 0 && partition_tokens % block_size == 0;
-            if (!ok) return;
             slots = pa::window_pieces(num_seqs / queries_per_row, queries_per_row, group, num_kv_heads, max_context_len);
             stride = pa::window_score_stride(max_context_len);
         } else {
-            pt = partition_for(num_seqs, num_heads, num_kv_heads, block_size, max_context_len, partition_tokens);
-            ok = pt > 0;
-            if (!ok) return;
+            pt = partition_tokens ? partition_tokens
+                                  : pa::weights_partition_tokens(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                                 max_context_len);
             slots = std::max(1, (int)(((long long)max_context_len + pt - 1) / pt));
             stride = ((long long)max_context_len + 3) / 4 * 4;
         }

@@ -193,6 +193,9 @@ int launch_decode_scores_bf16(int head_dim, int block_size, int group, const Dec
 int launch_decode_scores_f16(int head_dim, int block_size, int group, const DecodeParams &p, cudaStream_t stream);
 int launch_decode_tc_scores(pa_dtype dt, int head_dim, int block_size, int group, const DecodeParams &p,
                             cudaStream_t stream);
+// Partition length when the caller leaves it open.
+int weights_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                             int max_context_len);
 // After launch_decode_scores: merges split sequences' partials into p.out and
 // adds every token's weights to its row's total, queries_per_row sequences to
 // a row of `width` totals.

@@ -8,10 +8,12 @@
 // against 4 D bytes of K and V per (token, kv head): 1.6% of it at one query
 // head per kv head and head_dim 128, 12.5% at eight.
 //
-// Measured: 256 sequences of up to 4096 tokens, 32/8 heads, bf16, 361 us, 6.05 TB/s
-// of what the call cannot do without (90% of the copy rate), 326 of them the
-// decode kernel with its score stores, 25 this one; 8 of 16384 to 65536, 64/8
-// heads, 286 us (88%), 256 and 27.
+// Measured: 256 sequences of up to 4096 tokens, 32/8 heads, bf16, 358 us, 6.1 TB/s
+// of what the call cannot do without (91% of the copy rate), 326 of them the
+// decode kernel with its score stores, 23 this one; 8 of 16384 to 65536, 64/8
+// heads, 285 us (88%), 256 and 27.  Finishing a sequence in the decode kernel, by
+// its last unit to arrive, took as long: the units that do it are missing from
+// the K/V stream.
 //
 // Where every sequence is a single unit the decode kernel adds the weights up
 // itself, from scores it has just written (one launch less: 2 us of a short
@@ -23,6 +25,7 @@
 //            heads, added up over the row's sequences in their order (so the
 //            result does not depend on scheduling) and then to its total.
 #include <algorithm>
+#include <cmath>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -304,6 +307,26 @@ int launch_decode_scores(pa_dtype dt, int head_dim, int block_size, int group, c
     if (rc != PA_ERR_UNSUPPORTED) return rc;
     return dt == PA_BF16 ? launch_decode_scores_bf16(head_dim, block_size, group, p, stream)
                          : launch_decode_scores_f16(head_dim, block_size, group, p, stream);
+}
+
+// Groups of 8 (the tensor-core decode): a unit costs some 5 us apart from its
+// tokens (its set-up, its partial and that one's merge), a token 24 ns of a CTA's
+// share of HBM, and on average half a unit per CTA slot is lost to the last
+// round; with N tokens a slot the sum N / pt * 5 us + pt / 2 * 24 ns is least at
+// pt = sqrt(417 N).  Lengths are on the device: three quarters of the longest
+// each.  One sequence of 62000 tokens, 64/8 heads: 54 us at 512 (48 at 1024) against
+// 60 at pa_decode's 256; three of 16384 to 65536 116 (1024) against 134; eight 285
+// (2048) against 288 (1024).  Smaller groups keep pa_decode's choice (within 10% of the
+// best everywhere it was tried).
+int weights_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                             int max_context_len) {
+    if (head_dim != 128 || !decode_tc_group(num_heads / num_kv_heads))
+        return auto_partition_tokens(num_seqs, num_heads, num_kv_heads, block_size, max_context_len);
+    const double per_slot = 0.75 * num_seqs * max_context_len * num_kv_heads / (2.0 * sm_count());
+    const double best = std::sqrt(417.0 * per_slot);
+    int pt = 256;  // a multiple of every block size
+    while (pt < 4096 && best > pt * 1.41421356) pt *= 2;
+    return pt;
 }
 
 int launch_weights_merge(pa_dtype dt, int head_dim, int group, const DecodeParams &p, const float *weights,
