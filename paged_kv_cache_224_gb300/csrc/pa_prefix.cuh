@@ -10,7 +10,11 @@
 // CTA then runs two decode instances (pa_decode_tc.cuh) over the sequences' own
 // tokens, units drawn from a queue the grid shares.  The two halves bind on
 // different things, the tensor pipe and HBM, and so run side by side; both
-// leave unnormalised partials for the merge (pa_prefix.cu).
+// leave unnormalised partials for the merge (pa_prefix.cu).  Scores, maxima,
+// sums, accumulators and partials are fp32; the prefix's softmax weights are
+// rounded once to the element type for their product with V, the prefill's
+// choice (an MMA operand is 16 bits; a second product for the residual would
+// take up to a third more tensor time), the own tokens' as two values.
 //
 // 256 sequences after 8192 shared tokens, own tokens up to 512, 64/8 heads,
 // bf16: 121 us, 587 TFLOP/s and 2.7 TB/s at once (two launches, prefix and own

@@ -5,7 +5,9 @@
 // The CTA's code is the chunked prefill's (pa_prefill.cuh, kPrefix and kWindow):
 // the rows of a unit are the query positions times the G heads of one kv head,
 // up to 256 of them against every K/V tile, where the decode kernels would read
-// the whole cache once per position.  16 positions of 4 heads over 8191 tokens,
+// the whole cache once per position.  Softmax weights are rounded once to the
+// element type for their product with V, as in the prefill; the totals take
+// them in fp32 from the kept scores.  16 positions of 4 heads over 8191 tokens,
 // 8 kv heads, f16: 25 us (98 position by position), of which a CTA's 3 to 4 key
 // tiles take 1.7 us each and its first copies, its partial and the totals the
 // rest: bound by latency at this size.

@@ -14,7 +14,7 @@ import torch
 
 import paged_kv_cache_224_gb300 as pa
 from tests.helpers import check_attention, to_f64
-from tests.ref64 import DTYPES, attend, evict_choice, gather, half_step, rotate
+from tests.ref64 import DTYPES, attend, evict_choice, gather, half_step, make_pool, rotate
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0") if torch.cuda.is_available() else None
@@ -196,3 +196,78 @@ def test_a_batch_behind_a_system_prompt_step_by_step():
             check_attention(to_f64(out), torch.stack(ref).numpy(), "bf16", f"step {step}")
     torch.cuda.synchronize()
     assert int(e.err.item()) == 0
+
+
+def test_pools_of_more_than_two_to_the_32_elements():
+    """Blocks past element 2^32 of a pool (8.6 GB a cache) against the same blocks
+    in a small one: every call gives the same bits."""
+    Hkv, Hq, bs, D, n = 8, 32, 16, 128, 40
+    far = (1 << 32) // (Hkv * bs * D)
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of free device memory")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    small = [torch.randn((n, Hkv, bs, D), device=DEV, generator=g).half() for _ in range(2)]
+    big = [torch.empty((far + n, Hkv, bs, D), dtype=torch.float16, device=DEV) for _ in range(2)]
+    for b, c in zip(big, small):
+        b[far:] = c
+    q = torch.randn((2, Hq, D), device=DEV, generator=g).half()
+    k, v = (torch.randn((2, Hkv, D), device=DEV, generator=g).half() for _ in range(2))
+    tot = torch.rand((2, Hkv, 200), device=DEV, generator=g)
+    lens = torch.tensor([160, 131], dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def run(kc, vc, off):
+        old = torch.arange(20, dtype=torch.int32, device=DEV).view(2, 10) + off
+        new = torch.arange(20, 28, dtype=torch.int32, device=DEV).view(2, 4) + off
+        slots = torch.tensor([9 * bs + 15, 18 * bs + 2], device=DEV) + off * bs
+        qr = torch.empty_like(q)
+        pa.pa_rotary_and_cache(qr, q, k, v, kc, vc, torch.tensor([7, 99], dtype=torch.int32, device=DEV), slots,
+                               torch.ones(64, device=DEV), d_err=err)
+        out, t = torch.empty_like(q), tot.clone()
+        pa.pa_decode_weights(out, qr, kc, vc, old, lens, 0.09, 160, t, d_err=err)
+        four = [x.repeat_interleave(4, 0).contiguous() for x in (qr, old, lens)]   # attended together
+        wout, wt = torch.empty_like(four[0]), tot.clone()
+        pa.pa_decode_weights(wout, four[0], kc, vc, four[1], four[2], 0.09, 160, wt, queries_per_row=4, d_err=err)
+        kept = torch.empty((2, Hkv, 64), dtype=torch.int32, device=DEV)
+        nl, nt = torch.empty_like(lens), torch.empty_like(tot)
+        pa.pa_evict(kc, vc, t, old, lens, new, nl, nt, kept, 64, 4, 8, 160, d_err=err)
+        shared = torch.cat((old[:1, :4].repeat(2, 1), old[:, 4:]), 1).contiguous()
+        pout = torch.empty_like(q)
+        pa.pa_decode_common_prefix(pout, qr, kc, vc, shared, lens, 0.09, 160, 2, 4, d_err=err)
+        torch.cuda.synchronize()
+        return qr, out, t, wout, wt, kept, nl, nt, pout, kc[off:off + n], vc[off:off + n]
+    for i, (x, y) in enumerate(zip(run(*small, 0), run(*big, far))):
+        assert torch.equal(x, y), i
+    assert int(err.item()) == 0
+
+
+def test_two_streams_at_once():
+    """The same calls from two streams, with workspaces of their own, side by side."""
+    jobs = []
+    for i, lens in enumerate(([900, 300, 77], [1200, 64, 500])):
+        kc, vc, old, new = make_pool(lens, 2, 128, 16, "bf16", DEV, 50 + i, extra=[64] * 3)
+        g = torch.Generator().manual_seed(i)
+        q, tot = torch.randn((3, 16, 128), generator=g).bfloat16().to(DEV), torch.rand((3, 2, 1200), generator=g).to(DEV)
+        n, ml = torch.tensor(lens, dtype=torch.int32, device=DEV), max(lens)
+        one = old[:1].repeat(3, 1).contiguous()       # three samples of the first sequence
+        same = torch.full_like(n, lens[0])
+        res = dict(out=torch.empty_like(q), t=torch.zeros_like(tot), kept=torch.empty((3, 2, 64), dtype=torch.int32, device=DEV),
+                   nl=torch.empty_like(n), nt=torch.empty_like(tot), pout=torch.empty_like(q))
+        ws = (pa.decode_weights_workspace(q, 2, 16, ml), pa.evict_workspace(kc),
+              pa.decode_common_prefix_workspace(q, 2, 16, ml, 3, 20))
+
+        def job(stream, kc=kc, vc=vc, old=old, new=new, q=q, tot=tot, n=n, ml=ml, one=one, same=same, r=res, ws=ws):
+            pa.pa_decode_weights(r["out"], q, kc, vc, old, n, 0.09, ml, tot, r["t"], workspace=ws[0], stream=stream)
+            pa.pa_evict(kc, vc, r["t"], old, n, new, r["nl"], r["nt"], r["kept"], 64, 4, 16, ml, workspace=ws[1], stream=stream)
+            pa.pa_decode_common_prefix(r["pout"], q, kc, vc, one, same, 0.09, ml, 3, 20, workspace=ws[2], stream=stream)
+        job(None)
+        torch.cuda.synchronize()
+        jobs.append((job, res, {k: x.clone() for k, x in res.items()}))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(8):
+        for (job, _, _), s in zip(jobs, streams):
+            job(s)
+    torch.cuda.synchronize()
+    for _, res, want in jobs:
+        for name, x in want.items():
+            assert torch.equal(res[name], x), name
