@@ -71,9 +71,12 @@ typedef enum {
 #define PA_DEVERR_SLOT_RANGE 0x1    /* slot_mapping entry >= num_blocks*block_size */
 #define PA_DEVERR_BLOCK_RANGE 0x2   /* block-table entry outside [0, num_blocks) */
 #define PA_DEVERR_CONTEXT_RANGE 0x4 /* context length < 0, > max_context_len or > table */
-#define PA_DEVERR_COPY_PAIR 0x8     /* copy pair out of pool, src==dst, or dst conflict */
+#define PA_DEVERR_COPY_PAIR 0x8     /* copy pair out of pool, src==dst, or dst conflict; pa_evict: a new
+                                       block named twice or still read */
 #define PA_DEVERR_TIMEOUT 0x10      /* a bounded pipeline wait gave up */
-#define PA_DEVERR_PREFIX 0x20       /* pa_decode_shared_prefix: a group's prefix table rows differ */
+#define PA_DEVERR_PREFIX 0x20       /* table rows that must be the same differ: a group's prefix
+                                       (pa_decode_shared_prefix, pa_decode_common_prefix), a row of
+                                       totals' positions (pa_decode_weights) */
 
 /* Human-readable name of a pa_status value. */
 PA_API const char *pa_status_string(int status);
