@@ -29,6 +29,13 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// A caller's partition_tokens, at most what holds the longest length: the kernels
+// add a length to it in 32 bits.
+int clamp_partition(int partition_tokens, int longest, int block_size) {
+    const long long whole = ((long long)std::max(longest, 1) + block_size - 1) / block_size * block_size;
+    return (int)std::min<long long>(partition_tokens, whole);
+}
+
 // Partials: fp32 accumulators, then (max, sum) pairs, `slots` per (sequence, head).
 struct PartialWs {
     size_t acc, ml;
@@ -56,7 +63,7 @@ struct WeightsWs {
             slots = pa::window_pieces(num_seqs / queries_per_row, queries_per_row, group, num_kv_heads, max_context_len);
             stride = pa::window_score_stride(max_context_len);
         } else {
-            pt = partition_tokens ? partition_tokens
+            pt = partition_tokens ? clamp_partition(partition_tokens, max_context_len, block_size)
                                   : pa::weights_partition_tokens(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
                                                                  max_context_len);
             slots = std::max(1, (int)(((long long)max_context_len + pt - 1) / pt));
@@ -86,7 +93,7 @@ struct PrefixWs {
         const int longest = max_context_len - prefix;
         ok = partition_tokens >= 0 && partition_tokens % block_size == 0;
         if (!ok) return;
-        pt = partition_tokens ? partition_tokens
+        pt = partition_tokens ? clamp_partition(partition_tokens, longest, block_size)
                               : pa::prefix_partition_tokens(num_seqs, num_kv_heads, block_size, longest);
         const int partitions = std::max(1, (int)(((long long)longest + pt - 1) / pt));
         const int groups = num_seqs / group_size;

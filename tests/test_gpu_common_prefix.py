@@ -91,6 +91,11 @@ def test_partitions_of_the_own_tokens(pt):
     check(c, partition_tokens=pt)
 
 
+def test_a_partition_longer_than_any_context():
+    c = setup(1, 10, 20, [0, 1, 15, 16, 17, 64, 65, 200, 333, 500], 8, 2, 16, "bf16", seed=31)
+    check(c, partition_tokens=2 ** 31 - 16)
+
+
 def test_garbage_outside_the_contexts_stays_outside():
     check(setup(2, 10, 9, [3, 0, 17, 40, 5, 1, 2, 16, 31, 100] * 2, 8, 2, 16, "f16", seed=21, nan=True))
 

@@ -99,6 +99,11 @@ def test_partitions(G, D, pt):
     check(setup([1, 16, 17, 300, 1025], 1, G, 1, D, 16, "bf16", seed=pt + G), partition_tokens=pt)
 
 
+@pytest.mark.parametrize("G,D,w", [(4, 128, 1), (1, 64, 1), (2, 128, 3)])
+def test_a_partition_longer_than_any_context(G, D, w):
+    check(setup([1, 16, 17, 300, 1025], w, G, 1, D, 16, "bf16", seed=D + G), partition_tokens=2 ** 31 - 16)
+
+
 @pytest.mark.parametrize("w", [2, 5, 16])
 @pytest.mark.parametrize("G", [4, 8])
 def test_several_queries_add_to_one_row_in_place(w, G):
