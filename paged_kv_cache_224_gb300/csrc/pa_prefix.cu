@@ -69,8 +69,9 @@ struct MergeParams {
     int prefix_blocks;
 };
 
-// CTAs 0 .. merge_ctas-1: one warp per (sequence, head).  The others compare
-// a sequence's prefix table entries with its group's first sequence's.
+// CTAs 0 .. merge_ctas-1: one warp per (sequence, head).  The others check a
+// sequence each: its prefix table entries against its group's first sequence's,
+// and its length, which nothing else looks at where no own tokens are allowed.
 template <typename T>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     prefix_merge_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ MergeParams mp, int merge_ctas) {
@@ -85,6 +86,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         bool same = true;
         for (int j = threadIdx.x; j < mp.prefix_blocks; j += blockDim.x) same = same && row[j] == lead[j];
         if (!same) flag_error(p.d_err, PA_DEVERR_PREFIX);
+        if (threadIdx.x == 0) {
+            const int L = p.context_lens[s];
+            const long long room = (long long)p.max_blocks_per_seq * p.block_size;
+            if (L < p.len_offset || L > min((long long)p.max_context_len, room)) flag_error(p.d_err, PA_DEVERR_CONTEXT_RANGE);
+        }
         return;
     }
     const int pair = blockIdx.x * kMergeWarps + warp;

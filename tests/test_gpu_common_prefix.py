@@ -151,6 +151,17 @@ def test_broken_promises_are_flagged():
     assert torch.equal(out[10:], good[10:])
 
 
+@pytest.mark.parametrize("length", [0, 63, 65, 200])
+def test_wrong_lengths_are_flagged_where_the_prefix_is_the_whole_context(length):
+    c = setup(2, 3, 4, [0] * 6, 4, 2, 16, "bf16", seed=32)
+    good = check(c)
+    lens = list(c["lens"])
+    lens[4] = length
+    out, err = call(c, lens=lens)
+    assert err == pa.capi.DEVERR["context_range"]
+    assert torch.equal(out[:4], good[:4]) and torch.equal(out[5:], good[5:])
+
+
 def test_results_repeat_bit_for_bit_whatever_the_workspace_holds_captured_and_on_another_stream():
     c = setup(1, 24, 70, list(range(24)), 8, 2, 16, "bf16", seed=26)
     ref, _ = call(c)
