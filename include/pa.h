@@ -418,7 +418,7 @@ PA_API int pa_decode_weights(void *out, const void *query, const void *k_cache, 
  *   new_weights[s][h][i] = weights[s][h][kept[s][h][i]], 0 from n to weights_len
  *   new_context_lens[s] = n
  * The old blocks are only read (other sequences may share them); the caller
- * drops them afterwards (pa_bm_evict_sequence).  Tokens keep the positions they
+ * drops them afterwards (pa_bm_evict_sequences).  Tokens keep the positions they
  * were rotated with, so a later token's position is no longer its index.
  *   weights, new_weights  float [num_seqs][num_kv_heads][weights_len], not
  *                  overlapping; weights_len >= max_context_len
@@ -626,14 +626,23 @@ PA_API size_t pa_prefill_workspace_bytes(int num_seqs, int total_chunk_len, int 
  *       tree stay cached (reusable) until evicted; the others are free.
  *       Allocation evicts the least recently released cached leaf block when
  *       no free block is left.
+ *   pa_bm_evict_sequences(m, seq_ids, num_seqs, keep)
+ *       each sequence keeps min(its length, keep) tokens in fresh private
+ *       blocks, for one pa_evict over the batch: read the old tables first, call
+ *       this, then read the new ones.  Every new block is taken before any old
+ *       one is given up, so no new table names a block that an old one of the
+ *       batch does.  The references to the old blocks are dropped; their
+ *       contents stay valid until work enqueued after the copy writes them.  The
+ *       kept blocks no longer spell a prefix, so none of them joins the prefix
+ *       tree.  All or nothing: PA_ERR_INVALID_ARG for an unknown seq_id or one
+ *       named twice, PA_ERR_OUT_OF_RANGE for keep < 0, PA_ERR_NO_BLOCKS (every
+ *       sequence unchanged) when the pool cannot hold the old and the new blocks.
  *   pa_bm_evict_sequence(m, seq_id, new_len)
- *       the sequence keeps new_len tokens in fresh private blocks (for
- *       pa_evict: read the old table first, then call this, then read the new
- *       one) and drops its references to the old ones, whose contents stay
- *       valid until work enqueued after the copy writes them.  Its blocks no
- *       longer spell a prefix, so none of them joins the prefix tree.
- *       PA_ERR_OUT_OF_RANGE unless 0 <= new_len <= the length; PA_ERR_NO_BLOCKS
- *       (the sequence unchanged) when the pool runs out.
+ *       the same for one sequence and a pa_evict over it alone: what the next
+ *       call of this or of any allocating function hands out may be this
+ *       sequence's old blocks, so sequences that one pa_evict cuts down go
+ *       through pa_bm_evict_sequences together.  PA_ERR_OUT_OF_RANGE unless
+ *       0 <= new_len <= the length; PA_ERR_NO_BLOCKS (the sequence unchanged).
  *   pa_bm_block_table(m, seq_id, out, max_blocks) -> number of blocks, or
  *       PA_ERR_OUT_OF_RANGE if max_blocks is too small.
  *   pa_bm_seq_len, pa_bm_block_refcount, pa_bm_stats: introspection.  The
@@ -653,6 +662,7 @@ PA_API int pa_bm_append_token(pa_block_manager *m, int64_t seq_id, int32_t token
                               int64_t *copy_src, int64_t *copy_dst);
 PA_API int pa_bm_free_sequence(pa_block_manager *m, int64_t seq_id);
 PA_API int pa_bm_evict_sequence(pa_block_manager *m, int64_t seq_id, int new_len);
+PA_API int pa_bm_evict_sequences(pa_block_manager *m, const int64_t *seq_ids, int num_seqs, int keep);
 PA_API int pa_bm_block_table(const pa_block_manager *m, int64_t seq_id, int32_t *out, int max_blocks);
 PA_API int64_t pa_bm_seq_len(const pa_block_manager *m, int64_t seq_id);
 PA_API int pa_bm_block_refcount(const pa_block_manager *m, int block);

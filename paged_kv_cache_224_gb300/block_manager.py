@@ -71,9 +71,21 @@ class BlockManager:
     def free_sequence(self, seq_id: int) -> None:
         self._check("pa_bm_free_sequence", self._L.pa_bm_free_sequence(self._h, int(seq_id)))
 
+    def evict_sequences(self, seq_ids, keep: int) -> None:
+        """Each sequence keeps min(its length, ``keep``) tokens in fresh private
+        blocks, none of them an old block of these sequences (for one ``pa_evict``
+        over them: read the old tables first, call this, then read the new ones).
+        Nothing changes when the pool runs out."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        if ids.ndim != 1:
+            raise ValueError("seq_ids must be one-dimensional")
+        self._check("pa_bm_evict_sequences",
+                    self._L.pa_bm_evict_sequences(self._h, ids.ctypes.data, ids.size, int(keep)))
+
     def evict_sequence(self, seq_id: int, new_len: int) -> None:
-        """Keep ``new_len`` tokens in fresh private blocks (for ``pa_evict``: read
-        the old table first, call this, then read the new one)."""
+        """Keep ``new_len`` tokens in fresh private blocks, for a ``pa_evict`` over
+        this sequence alone (several: ``evict_sequences``): read the old table
+        first, call this, then read the new one."""
         self._check("pa_bm_evict_sequence", self._L.pa_bm_evict_sequence(self._h, int(seq_id), int(new_len)))
 
     def block_table(self, seq_id: int) -> np.ndarray:

@@ -34,7 +34,7 @@ EXPORTED = ("pa_status_string", "pa_reshape_and_cache", "pa_decode_partition_tok
             "pa_mixed_step", "pa_mixed_step_workspace_bytes", "pa_bounded_wait_polls", "pa_selftest_bounded_wait",
             "pa_rotary_and_cache", "pa_decode_weights_workspace_bytes", "pa_decode_weights",
             "pa_evict_workspace_bytes", "pa_evict", "pa_decode_common_prefix_workspace_bytes",
-            "pa_decode_common_prefix", "pa_bm_evict_sequence")
+            "pa_decode_common_prefix", "pa_bm_evict_sequence", "pa_bm_evict_sequences")
 PA_ERR_NO_BLOCKS = -8
 PA_ERR_SCRATCH_LIMIT = -7
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -135,6 +135,8 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_common_prefix.restype = i
         L.pa_bm_evict_sequence.argtypes = [p, i64, i]
         L.pa_bm_evict_sequence.restype = i
+        L.pa_bm_evict_sequences.argtypes = [p, p, i, i]
+        L.pa_bm_evict_sequences.restype = i
         L.pa_bounded_wait_polls.argtypes = []
         L.pa_bounded_wait_polls.restype = i
         L.pa_selftest_bounded_wait.argtypes = [i, p, p, p]

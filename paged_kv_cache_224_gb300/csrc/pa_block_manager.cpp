@@ -26,12 +26,14 @@
 // pa_reshape_and_cache for the returned slots) before the next kernel reads
 // the blocks.
 
+#include <algorithm>
 #include <cstdint>
 #include <list>
 #include <map>
 #include <memory>
 #include <new>
 #include <unordered_map>
+#include <unordered_set>
 #include <vector>
 
 #include "../../include/pa.h"
@@ -129,6 +131,39 @@ struct pa_block_manager {
         parent->children.emplace(s.tail, std::move(n));
         node_of[b] = raw;
         s.node = raw;
+    }
+
+    // Each sequence keeps min(its length, keep) tokens, in fresh private blocks.
+    // All of them are taken before any old one is given up: a copy of the kept
+    // rows reads every old block of the batch, so none may be a new one of it.
+    // Running out leaves every sequence as it was.
+    int evict(const std::vector<Seq *> &batch, int64_t keep) {
+        auto blocks_of = [&](const Seq *s) { return (std::min(s->len, keep) + block_size - 1) / block_size; };
+        // the room for the new tables comes before anything changes
+        std::vector<std::vector<int32_t>> fresh(batch.size());
+        for (size_t i = 0; i < batch.size(); ++i) fresh[i].reserve((size_t)std::min<int64_t>(blocks_of(batch[i]), num_blocks));
+        for (size_t i = 0; i < batch.size(); ++i) {
+            for (int64_t k = blocks_of(batch[i]); k > 0; --k) {
+                const int32_t b = alloc();
+                if (b < 0) {
+                    for (size_t j = i + 1; j-- > 0;)
+                        for (auto f = fresh[j].rbegin(); f != fresh[j].rend(); ++f) release(*f);
+                    return PA_ERR_NO_BLOCKS;
+                }
+                fresh[i].push_back(b);
+            }
+        }
+        for (size_t i = 0; i < batch.size(); ++i) {
+            Seq &s = *batch[i];
+            for (auto b = s.blocks.rbegin(); b != s.blocks.rend(); ++b) release(*b);
+            s.blocks = std::move(fresh[i]);
+            s.len = std::min(s.len, keep);
+            // the kept tokens are not consecutive: no block of this sequence is a prefix's from here on
+            s.tail.clear();
+            s.node = nullptr;
+            s.chained = false;
+        }
+        return PA_OK;
     }
 };
 
@@ -264,31 +299,29 @@ int pa_bm_evict_sequence(pa_block_manager *m, int64_t seq_id, int new_len) {
     if (!m) return PA_ERR_INVALID_ARG;
     auto it = m->seqs.find(seq_id);
     if (it == m->seqs.end()) return PA_ERR_INVALID_ARG;
-    Seq &s = it->second;
-    if (new_len < 0 || new_len > s.len) return PA_ERR_OUT_OF_RANGE;
-    const int need = (int)(((int64_t)new_len + m->block_size - 1) / m->block_size);
-    std::vector<int32_t> fresh;
+    if (new_len < 0 || new_len > it->second.len) return PA_ERR_OUT_OF_RANGE;
     try {
-        fresh.reserve(need);  // so that nothing below can throw half way
+        return m->evict({&it->second}, new_len);
     } catch (const std::bad_alloc &) {
         return PA_ERR_NO_BLOCKS;
     }
-    for (int k = 0; k < need; ++k) {
-        const int32_t b = m->alloc();
-        if (b < 0) {
-            for (int32_t f : fresh) m->release(f);
-            return PA_ERR_NO_BLOCKS;
+}
+
+int pa_bm_evict_sequences(pa_block_manager *m, const int64_t *seq_ids, int num_seqs, int keep) {
+    if (!m || num_seqs < 0 || (num_seqs > 0 && !seq_ids)) return PA_ERR_INVALID_ARG;
+    if (keep < 0) return PA_ERR_OUT_OF_RANGE;
+    try {
+        std::vector<Seq *> batch;
+        std::unordered_set<int64_t> named;
+        for (int i = 0; i < num_seqs; ++i) {
+            auto it = m->seqs.find(seq_ids[i]);
+            if (it == m->seqs.end() || !named.insert(seq_ids[i]).second) return PA_ERR_INVALID_ARG;
+            batch.push_back(&it->second);
         }
-        fresh.push_back(b);
+        return m->evict(batch, keep);
+    } catch (const std::bad_alloc &) {
+        return PA_ERR_NO_BLOCKS;
     }
-    for (auto b = s.blocks.rbegin(); b != s.blocks.rend(); ++b) m->release(*b);
-    s.blocks = std::move(fresh);
-    s.len = new_len;
-    // the kept tokens are not consecutive: no block of this sequence is a prefix's from here on
-    s.tail.clear();
-    s.node = nullptr;
-    s.chained = false;
-    return PA_OK;
 }
 
 int pa_bm_block_table(const pa_block_manager *m, int64_t seq_id, int32_t *out, int max_blocks) {
