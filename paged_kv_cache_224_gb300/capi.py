@@ -540,13 +540,12 @@ def _opt(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(device, nbytes, stream):
-    """A uint8 workspace; one made for a call on a given stream stays reserved
-    until that stream is done with it."""
-    w = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
-    if stream is not None:
-        w.record_stream(stream)
-    return w
+def _scratch(device, nbytes, stream, make=torch.empty):
+    """A uint8 workspace for work on ``stream`` (None: the current one), allocated
+    on that stream: memory freed on another may still be in use by what is queued
+    there."""
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        return make(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
 def _token_rows(index, dtype, t, shape, row) -> int:
@@ -616,7 +615,8 @@ def pa_decode_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_di
 
 def decode_weights_workspace(query, num_kv_heads, block_size, max_context_len, partition_tokens=0, queries_per_row=1,
                              stream=None):
-    """Allocate (with torch) a workspace big enough for ``pa_decode_weights``."""
+    """Allocate (with torch) a workspace big enough for ``pa_decode_weights`` on
+    ``stream`` (None: the current one)."""
     B, Hq, D = query.shape
     with torch.cuda.device(query.device):
         n = pa_decode_weights_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, queries_per_row,
@@ -661,8 +661,8 @@ def pa_decode_weights(out, query, k_cache, v_cache, block_tables, context_lens, 
 
 
 def evict_workspace(k_cache, num_seqs=0, keep=0, stream=None):
-    """Allocate (with torch) a workspace for ``pa_evict`` on this pool (its size
-    depends on the pool alone)."""
+    """Allocate (with torch) a workspace for ``pa_evict`` on this pool and ``stream``
+    (its size depends on the pool alone)."""
     return _scratch(k_cache.device, lib().pa_evict_workspace_bytes(k_cache.shape[0]), stream)
 
 
@@ -713,8 +713,7 @@ def decode_common_prefix_workspace(query, num_kv_heads, block_size, max_context_
     with torch.cuda.device(query.device):
         n = pa_decode_common_prefix_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, group_size,
                                                     prefix_blocks, partition_tokens)
-    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-        return torch.zeros(max(n, 1), dtype=torch.uint8, device=query.device)
+    return _scratch(query.device, n, stream, torch.zeros)
 
 
 def pa_decode_common_prefix(out, query, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
