@@ -180,6 +180,14 @@ def _check(fn, rc):
         raise PAError(fn, rc)
 
 
+def _scratch(device, nbytes, stream, make=torch.empty):
+    """A uint8 workspace for work on ``stream`` (None: the current one), allocated
+    on that stream: memory freed on another may still be in use by what is queued
+    there."""
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        return make(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+
+
 def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, d_err=None, stream=None):
     """key/value [T][Hkv][D]; caches [NB][Hkv][bs][D]; slot_mapping int64 [T]."""
     _dev(key, value, k_cache, v_cache, slot_mapping, d_err)
@@ -209,11 +217,12 @@ def pa_decode_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block
                                            max_context_len, partition_tokens)
 
 
-def decode_workspace(query, num_kv_heads, block_size, max_context_len, partition_tokens=0):
-    """Allocate (with torch) a workspace big enough for ``pa_decode``."""
+def decode_workspace(query, num_kv_heads, block_size, max_context_len, partition_tokens=0, stream=None):
+    """Allocate (with torch) a workspace big enough for ``pa_decode`` on ``stream``
+    (None: the current one)."""
     B, Hq, D = query.shape
     n = pa_decode_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, partition_tokens)
-    return torch.empty(max(n, 1), dtype=torch.uint8, device=query.device)
+    return _scratch(query.device, n, stream)
 
 
 def pa_decode(out, query, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
@@ -230,7 +239,7 @@ def pa_decode(out, query, k_cache, v_cache, block_tables, context_lens, scale, m
     if not (out.dtype == query.dtype == k_cache.dtype == v_cache.dtype):
         raise TypeError("dtype mismatch")
     if workspace is None:
-        workspace = decode_workspace(query, Hkv, bs, max_context_len, partition_tokens)
+        workspace = decode_workspace(query, Hkv, bs, max_context_len, partition_tokens, stream)
     rc = lib().pa_decode(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                          block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, bs, NB,
                          int(max_context_len), float(scale), int(partition_tokens), _dt(query),
@@ -262,7 +271,7 @@ def pa_decode_shared_prefix(out, query, k_cache, v_cache, block_tables, context_
     if workspace is None:
         n = pa_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, D, bs, max_context_len, prefix_blocks,
                                                     partition_tokens)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=query.device)
+        workspace = _scratch(query.device, n, stream)
     rc = lib().pa_decode_shared_prefix(
         _ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
         _ptr(context_lens), B, int(group_size), int(prefix_blocks), Hq, Hkv, D, bs, NB,
@@ -336,7 +345,7 @@ def pa_decode_step_host(out, query, new_key, new_value, slot_mapping, block_tabl
     if staging is None:
         need = pa_decode_step_host_staging_bytes(B, Hq, Hkv, D, bs, MB, max_context_len, T, n, group_size,
                                                  prefix_blocks, partition_tokens)
-        staging = torch.empty(max(need, 1), dtype=torch.uint8, device=k_cache.device)
+        staging = _scratch(k_cache.device, need, stream)
     rc = lib().pa_decode_step_host(
         _ptr(out), _ptr(query), _ptr(new_key), _ptr(new_value), _ptr(slot_mapping), T, _ptr(pairs), n,
         _ptr(block_tables), MB, _ptr(context_lens), B, int(group_size), int(prefix_blocks), Hq, Hkv, D, bs, NB,
@@ -373,7 +382,7 @@ def pa_mixed_step(prefill_out, prefill_query, prefill_block_tables, prefix_lens,
             v_cache.dtype):
         raise TypeError("dtype mismatch")
     if workspace is None:
-        workspace = mixed_workspace(prefill_query, decode_query, Hkv, bs, n, max_context_len, partition_tokens)
+        workspace = mixed_workspace(prefill_query, decode_query, Hkv, bs, n, max_context_len, partition_tokens, stream)
     rc = lib().pa_mixed_step(
         _ptr(prefill_out), _ptr(prefill_query), _ptr(prefill_block_tables), prefill_block_tables.shape[1],
         P.ctypes.data_as(ctypes.c_void_p), C.ctypes.data_as(ctypes.c_void_p), n, _ptr(decode_out),
@@ -385,14 +394,14 @@ def pa_mixed_step(prefill_out, prefill_query, prefill_block_tables, prefix_lens,
 
 
 def mixed_workspace(prefill_query, decode_query, num_kv_heads, block_size, num_prefill, max_context_len,
-                    partition_tokens=0):
+                    partition_tokens=0, stream=None):
     """A zero-filled uint8 CUDA workspace for ``pa_mixed_step`` (zero-filled
-    once; the calls keep it usable)."""
+    once, on ``stream`` or the current one; the calls keep it usable)."""
     R, Hq, D = prefill_query.shape
     B = decode_query.shape[0]
     n = int(lib().pa_mixed_step_workspace_bytes(int(num_prefill), R, B, Hq, int(num_kv_heads), D, int(block_size),
                                                 int(max_context_len), int(partition_tokens)))
-    return torch.zeros(max(n, 1), dtype=torch.uint8, device=decode_query.device)
+    return _scratch(decode_query.device, n, stream, torch.zeros)
 
 
 def pa_selftest_bounded_wait(max_polls, d_err, d_cycles=None, stream=None):
@@ -417,8 +426,7 @@ def pa_copy_blocks(k_cache, v_cache, pairs, d_err=None, stream=None, workspace=N
     NB, Hkv, bs, D = k_cache.shape
     n = pairs.shape[0] if pairs.numel() else 0
     if workspace is None:
-        workspace = torch.empty(max(1, pa_copy_blocks_workspace_bytes(n)), dtype=torch.uint8,
-                                device=k_cache.device)
+        workspace = _scratch(k_cache.device, pa_copy_blocks_workspace_bytes(n), stream)
     rc = lib().pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(pairs), n, Hkv, D, bs, NB,
                               _dt(k_cache), _ptr(workspace), workspace.numel() * workspace.element_size(),
                               _ptr(d_err), _stream(k_cache, stream))
@@ -430,12 +438,13 @@ def pa_prefill_workspace_bytes(num_seqs, total_chunk_len, num_heads, num_kv_head
                                                 int(num_kv_heads), int(head_dim)))
 
 
-def prefill_workspace(query, num_kv_heads, num_seqs=1):
+def prefill_workspace(query, num_kv_heads, num_seqs=1, stream=None):
     """A zero-filled uint8 CUDA workspace big enough for prefill of ``query``'s
-    rows in ``num_seqs`` chunks (zero-filled once; the calls keep it usable)."""
+    rows in ``num_seqs`` chunks (zero-filled once, on ``stream`` or the current
+    one; the calls keep it usable)."""
     R, Hq, D = query.shape
     n = pa_prefill_workspace_bytes(num_seqs, R, Hq, num_kv_heads, D)
-    return torch.zeros(max(n, 1), dtype=torch.uint8, device=query.device)
+    return _scratch(query.device, n, stream, torch.zeros)
 
 
 def _ws(workspace):
@@ -538,14 +547,6 @@ def _raw_stream(index, stream):
 
 def _opt(t):
     return None if t is None else t.data_ptr()
-
-
-def _scratch(device, nbytes, stream, make=torch.empty):
-    """A uint8 workspace for work on ``stream`` (None: the current one), allocated
-    on that stream: memory freed on another may still be in use by what is queued
-    there."""
-    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-        return make(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
 def _token_rows(index, dtype, t, shape, row) -> int:
