@@ -380,9 +380,7 @@ PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const 
  *                  on, at head_dim 128 and block_size >= 16, they are attended
  *                  together on the tensor cores: the row of the first position is the one
  *                  that is read (another that differs in a position's context
- *                  sets PA_DEVERR_PREFIX, outputs and totals undefined), the
- *                  softmax weights are rounded to dtype for their product with
- *                  V as in pa_prefill_chunk (the totals take them in fp32),
+ *                  sets PA_DEVERR_PREFIX, outputs and totals undefined),
  *                  partition_tokens has no effect, and a V row that holds a NaN
  *                  or infinity within the longest of the contexts reaches the
  *                  outputs of the others
@@ -465,8 +463,10 @@ PA_API int pa_evict(void *k_cache, void *v_cache, const float *weights, float *n
  *                  PA_DEVERR_TIMEOUT, zero-fill it again).  It must not be shared
  *                  with work that overlaps the call on the device
  * Supported: head_dim 128, block_size in {16, 32, 64, 128}, num_heads /
- * num_kv_heads in {1, 2, 4, 8}.  The softmax weights of prefix keys are rounded
- * to dtype for their product with V, as in pa_prefill_chunk.
+ * num_kv_heads in {1, 2, 4, 8}.  Groups of more than 128 query rows (group_size
+ * times heads per kv head) round the softmax weights of prefix keys to dtype, once,
+ * for their product with V, as pa_prefill_chunk does; smaller ones, like pa_decode,
+ * give them about twice dtype's bits.
  */
 PA_API size_t pa_decode_common_prefix_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                                       int block_size, int max_context_len, int group_size,

@@ -72,6 +72,14 @@
 // later merge with the sequences' own tokens.  kWindow instances on top of that
 // serve several query positions over one cache (pa_window.cuh): each position
 // has its own context length, on the device, and every score is kept.
+//
+// kTwoP instances send each softmax weight to its product with V as two 16-bit
+// values, the rounded one and what the rounding left over (a second set of MMAs
+// on the same columns of O), where the others round it once.  A Q tile 1 without
+// rows gets no MMAs and no softmax there, so a unit of up to 128 rows has less
+// for the tensor pipe than two whole Q tiles.  (Handing that tile the second
+// values instead, its rows a copy of tile 0's, took as long or longer: 32 to 35 us
+// against 32 where one value takes 28, 16 positions of 4 heads over 8191 tokens.)
 #pragma once
 
 #include <cuda.h>
@@ -176,6 +184,12 @@ __device__ __forceinline__ Seg seg_at(const PrefillParams &p, int x, int x_end) 
         s.t1 = max(s.t0, min(s.t1, (s.longest + kNK - 1) / kNK));
     }
     return s;
+}
+
+// Whether the unit of a segment has rows in Q tile 1.
+template <int G>
+__device__ __forceinline__ bool second_tile(const PrefillParams &p, const Seg &sg) {
+    return p.seqs[sg.si].chunk_len * G > sg.r * kUnitRows + kM;
 }
 
 // Global tile range of unit u (the schedule without a workspace).
@@ -353,7 +367,8 @@ static __device__ __noinline__ void store_partial(float *part_o, float2 *part_ml
 // share of the key tiles; without, unit `cta` (all of the CTA's threads call this).
 // Returns the CTA's TMEM base; with kKeepTmem (the one-launch step, whose
 // prefill CTAs go on to decode) the allocation is left for the caller to free.
-template <typename T, int BS, int G, bool kKeepTmem = false, bool kPrefix = false, bool kWindow = false>
+template <typename T, int BS, int G, bool kKeepTmem = false, bool kPrefix = false, bool kWindow = false,
+          bool kTwoP = false>
 __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CUtensorMap &tmk,
                                                 const CUtensorMap &tmv, const CUtensorMap &tmq, int cta, int ncta) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -361,6 +376,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
     static_assert(kNK % BS == 0 && BS % 8 == 0 && 32 % kBlocksPerTile == 0, "block_size");
     static_assert(kM % G == 0, "group");
     static_assert(kPrefix || !kWindow, "a window leaves partials");
+    static_assert(kPrefix || !kTwoP, "Q tile 1 may be left out of partials only");
 
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -525,6 +541,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     --sc;
                     continue;
                 }
+                const bool both = !kTwoP || second_tile<G>(p, sg);  // else nothing is issued for Q tile 1
                 if (lane == 0) wait_or_flag(q_full, (uint32_t)sc & 1u, p.d_err);
                 for (int k = 0; k <= nt; ++k) {
                     const int gt = tc + k;  // this CTA's tile count
@@ -547,10 +564,13 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                             if (lane == 0) {
                                 tc_fence_after();
                                 const uint32_t v_lo = v_lo0 + sl_v * (kKVTile >> 4);
+                                if (g == 0 || both) {
 #pragma unroll
-                                for (int kk = 0; kk < kNK / 16; ++kk)
-                                    mma_f16_ts(tmem + kColO + g * kD, tS + kk * 8,
-                                               desc_of(v_lo + kk * (4096 >> 4), hi_kv), idesc_pv, k > 1 || kk > 0);
+                                    for (int kk = 0; kk < (kTwoP ? 2 : 1) * kNK / 16; ++kk)
+                                        mma_f16_ts(tmem + kColO + g * kD, tS + kk * 8,
+                                                   desc_of(v_lo + kk % (kNK / 16) * (4096 >> 4), hi_kv), idesc_pv,
+                                                   k > 1 || kk > 0);
+                                }
                                 if (k == nt) mma_commit(&o_done[g]);
                             }
                         }
@@ -558,11 +578,13 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                             // S_g = Q_g K(k)^T
                             const uint32_t q_lo = q_lo0 + g * (kQTile >> 4);
                             const uint32_t k_lo = k_lo0 + sl_k * (kKVTile >> 4);
+                            if (g == 0 || both) {
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const uint32_t qo = ((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4;
-                                const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-                                mma_f16(tS, desc_of(q_lo + qo, hi_q), desc_of(k_lo + ko, hi_kv), idesc_qk, kk > 0);
+                                for (int kk = 0; kk < 8; ++kk) {
+                                    const uint32_t qo = ((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4;
+                                    const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+                                    mma_f16(tS, desc_of(q_lo + qo, hi_q), desc_of(k_lo + ko, hi_kv), idesc_qk, kk > 0);
+                                }
                             }
                             mma_commit(&s_full[g]);
                         }
@@ -677,6 +699,8 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     kend = sg.longest - 1;
                     jn = kend / kNK;
                 }
+                // no last tile (and no register for it): this Q tile has no rows
+                if (kTwoP && g == kQT - 1 && !second_tile<G>(p, sg)) jn = -1;
             }
             if constexpr (kWindow) {
                 if (nt == 0) {
@@ -716,6 +740,12 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     if (gt >= 1 && 2 * gt - 1 + kSlots < nitems) mbar_arrive1(&empty[(2 * gt - 1) % kSlots]);
                     // and on the segment's last tile, both QKs of it have read Q
                     if (k == nt - 1) mbar_arrive1(q_empty);
+                }
+                if constexpr (kTwoP) {
+                    if (jn < 0) {
+                        named_bar_arrive(kBarP + g, 160);
+                        continue;
+                    }
                 }
                 // causal mask only on tiles that reach past some row's limit
                 const int kb = j * kNK;
@@ -787,6 +817,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
 #pragma unroll
                 for (int h = 0; h < kNK / 16; ++h) {
                     uint32_t pk[8];
+                    [[maybe_unused]] uint32_t pl[8];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const int kk = h * 16 + 2 * c;
@@ -794,8 +825,16 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                         const float2 e2 = make_float2(fast_exp2(a.x), fast_exp2(a.y));
                         l2[c & 3] = __fadd2_rn(l2[c & 3], e2);
                         pk[c] = Elem<T>::pack2(e2.x, e2.y);
+                        if constexpr (kTwoP) {
+                            // what the rounding left, rounded itself, goes over S's other
+                            // 64 columns: together about twice the type's bits
+                            float r0, r1;
+                            Elem<T>::unpack2(pk[c], r0, r1);
+                            pl[c] = Elem<T>::pack2(e2.x - r0, e2.y - r1);
+                        }
                     }
                     tmem_st8u(tS + h * 8, pk);
+                    if constexpr (kTwoP) tmem_st8u(tS + kNK / 2 + h * 8, pl);
                 }
                 if (any_up && k >= 1) {
                     // S complete means O holds every PV before it: rescale in
@@ -849,8 +888,9 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 const size_t out_row = (size_t)(q.row_start + rw.ipos) * p.num_heads + sg.h * G + rw.head;
                 T *orow = static_cast<T *>(p.out) + out_row * kD;
                 if constexpr (kPrefix) {
-                    store_partial(p.part_o, p.part_ml, out_row * p.part_slots, rw.valid, tO, cta, sg.x_unit,
-                                  p.total_tiles, ncta, m_run, l_run);
+                    if (!kTwoP || jn >= 0)
+                        store_partial(p.part_o, p.part_ml, out_row * p.part_slots, rw.valid, tO, cta, sg.x_unit,
+                                      p.total_tiles, ncta, m_run, l_run);
                 } else if (sg.t0 == 0 && sg.t1 == sg.n) {
                     // the whole unit: normalise, round once, store
                     store_out(orow, l_run > 0.f ? 1.f / l_run : 0.f, rw.valid);

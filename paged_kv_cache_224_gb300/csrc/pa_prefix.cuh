@@ -11,13 +11,16 @@
 // tokens, units drawn from a queue the grid shares.  The two halves bind on
 // different things, the tensor pipe and HBM, and so run side by side; both
 // leave unnormalised partials for the merge (pa_prefix.cu).  Scores, maxima,
-// sums, accumulators and partials are fp32; the prefix's softmax weights are
-// rounded once to the element type for their product with V, the prefill's
-// choice (an MMA operand is 16 bits; a second product for the residual would
-// take up to a third more tensor time), the own tokens' as two values.
+// sums, accumulators and partials are fp32.  The softmax weights are MMA operands
+// of 16 bits: the own tokens' go in as two values, and so do the prefix's for
+// groups of up to 128 rows (kTwoP; 2 x 12 sequences after 992 tokens, 16 heads:
+// 22.7 us against 21.8 rounded once).  Larger groups round the prefix's once, the
+// prefill's choice: two values took the case below from 127 to 171 us, and over a
+// prefix's keys, 16 at least, one rounding each averages out (bf16, 8192 keys:
+// at most 2.3e-3 off where two values are 1.7e-3 off, the result's own rounding).
 //
 // 256 sequences after 8192 shared tokens, own tokens up to 512, 64/8 heads,
-// bf16: 121 us, 587 TFLOP/s and 2.7 TB/s at once (two launches, prefix and own
+// bf16: 127 us, 557 TFLOP/s and 2.5 TB/s at once (two launches, prefix and own
 // tokens one after the other: 153).  Of a decode instance's 5 to 8 us per
 // sequence and kv head 1.2 us per 128-key tile are work; the rest is the chain
 // of its length, queries, last product and partial.
@@ -45,7 +48,7 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-template <typename T, int BS, int G>
+template <typename T, int BS, int G, bool kTwoP>
 __global__ void __launch_bounds__(kStepThreads, 1)
     prefix_tc_kernel(const __grid_constant__ PrefixLaunch pl, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
@@ -62,7 +65,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
     }
     uint32_t tmem = 0;
     if (prefix)  // ends with a CTA barrier: every warp is past the pass's use of shared memory and TMEM
-        tmem = prefill_cta<T, BS, G, true, true>(pl.pp, tmk, tmv, tmq, (int)blockIdx.x, pl.prefix_ctas);
+        tmem = prefill_cta<T, BS, G, true, true, false, kTwoP>(pl.pp, tmk, tmv, tmq, (int)blockIdx.x, pl.prefix_ctas);
     tcd::TcRun r;
     tcd::tc_init<kDecodeSlots>(r, inst * kDecodeInst1, inst * 6, kBarL + 1 + inst);
     if (!prefix && warp == 1) tcd::tc_alloc(holder, 2 * tcd::kTmemCols);
@@ -79,9 +82,9 @@ __global__ void __launch_bounds__(kStepThreads, 1)
     if (warp == 1) tcd::tc_dealloc(tmem, prefix ? (uint32_t)kTmemCols : 2 * tcd::kTmemCols);
 }
 
-template <typename T, int BS, int G>
+template <typename T, int BS, int G, bool kTwoP>
 int launch_prefix_t(const PrefixLaunch &pl, unsigned grid, cudaStream_t stream) {
-    auto kern = prefix_tc_kernel<T, BS, G>;
+    auto kern = prefix_tc_kernel<T, BS, G, kTwoP>;
     static std::atomic<uint64_t> attr_done{0};
     if (ensure_smem_attr(kern, kSmemAlloc, attr_done) != PA_OK) return PA_ERR_CUDA;
     const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -100,7 +103,9 @@ int launch_prefix_t(const PrefixLaunch &pl, unsigned grid, cudaStream_t stream) 
 template <typename T>
 int launch_prefix_dtype(int block_size, int group, const PrefixLaunch &pl, unsigned grid, cudaStream_t stream) {
 #define PA_PFX_CASE(BB, GG) \
-    if (block_size == BB && group == GG) return launch_prefix_t<T, BB, GG>(pl, grid, stream);
+    if (block_size == BB && group == GG)                                             \
+        return pl.pp.seqs[0].chunk_len * GG <= kM ? launch_prefix_t<T, BB, GG, true>(pl, grid, stream) \
+                                                  : launch_prefix_t<T, BB, GG, false>(pl, grid, stream);
 #define PA_PFX_GROUPS(BB) PA_PFX_CASE(BB, 1) PA_PFX_CASE(BB, 2) PA_PFX_CASE(BB, 4) PA_PFX_CASE(BB, 8)
     PA_PFX_GROUPS(16)
     PA_PFX_GROUPS(32)

@@ -5,12 +5,13 @@
 // The CTA's code is the chunked prefill's (pa_prefill.cuh, kPrefix and kWindow):
 // the rows of a unit are the query positions times the G heads of one kv head,
 // up to 256 of them against every K/V tile, where the decode kernels would read
-// the whole cache once per position.  Softmax weights are rounded once to the
-// element type for their product with V, as in the prefill; the totals take
-// them in fp32 from the kept scores.  16 positions of 4 heads over 8191 tokens,
-// 8 kv heads, f16: 25 us (98 position by position), of which a CTA's 3 to 4 key
-// tiles take 1.7 us each and its first copies, its partial and the totals the
-// rest: bound by latency at this size.
+// the whole cache once per position.  Softmax weights go to their product with V
+// as two 16-bit values (kTwoP): rounded once, over two to four keys, they would
+// put outputs past what a position alone keeps to.  The totals take them in fp32
+// from the kept scores.  16 positions of 4 heads over 8191 tokens, 8 kv heads,
+// f16: 32 us (28 with weights rounded once, 98 position by position), of which a
+// CTA's 3 to 4 key tiles take some 2.5 us each and its first copies, its partial
+// and the totals the rest: bound by latency at this size.
 #pragma once
 
 #include "pa_prefill.cuh"
@@ -24,7 +25,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     window_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
     pdl_wait();  // the kernel before this one on the stream (e.g. the cache write) has finished
-    prefill_cta<T, BS, G, false, true, true>(p, tmk, tmv, tmq, (int)blockIdx.x, (int)gridDim.x);
+    prefill_cta<T, BS, G, false, true, true, true>(p, tmk, tmv, tmq, (int)blockIdx.x, (int)gridDim.x);
 }
 
 template <typename T, int BS, int G>
