@@ -381,9 +381,11 @@ PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const 
  *                  together on the tensor cores: the row of the first position is the one
  *                  that is read (another that differs in a position's context
  *                  sets PA_DEVERR_PREFIX, outputs and totals undefined),
- *                  partition_tokens has no effect, and a V row that holds a NaN
- *                  or infinity within the longest of the contexts reaches the
- *                  outputs of the others
+ *                  and partition_tokens has no effect.  (Where V holds a NaN or
+ *                  infinity within the longest of the contexts, the outputs of
+ *                  the row are computed again key by key, so that it reaches
+ *                  those alone that see it: 16 positions over 8191 tokens take
+ *                  2.4 ms then.)
  *   workspace      >= pa_decode_weights_workspace_bytes(...) bytes, 256-byte
  *                  aligned, scratch: the partials, and every score in fp32
  *                  (num_seqs * num_heads * max_context_len * 4 bytes; rows that are

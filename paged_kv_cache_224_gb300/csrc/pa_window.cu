@@ -2,7 +2,8 @@
 // the tensor-core pass (pa_window.cuh), and what follows it.
 //
 // One kernel follows, with three kinds of CTA:
-//   merge    one warp per (sequence, head): the log-sum-exp merge of its pieces;
+//   merge    one warp per (sequence, head): the log-sum-exp merge of its pieces,
+//            and rows that a NaN or infinity behind their mask reached anew;
 //   totals   one CTA per (row of totals, kv head, 128 tokens): a token's weight
 //            is sum_r 2^(score_r - M_r) / l_r over the row's query rows
 //            (positions x heads) that see it.  A warp takes 32 tokens, a lane
@@ -169,6 +170,31 @@ __global__ void __launch_bounds__(kTotThreads)
         const float4 x = *reinterpret_cast<const float4 *>(p.ws_acc + (base + k) * kD + lane * VPL);
         o[0] = fmaf(e, x.x, o[0]); o[1] = fmaf(e, x.y, o[1]);
         o[2] = fmaf(e, x.z, o[2]); o[3] = fmaf(e, x.w, o[3]);
+    }
+    // In the MMAs every row meets every key, with weight 0 where it does not see
+    // it, and 0 * NaN or infinity is NaN: a row that is not finite is added up
+    // again from its kept scores, over its own keys alone.
+    if (M != -INFINITY && __any_sync(kFull, !(isfinite(o[0]) && isfinite(o[1]) && isfinite(o[2]) && isfinite(o[3])))) {
+#pragma unroll
+        for (int d = 0; d < VPL; ++d) o[d] = 0.f;
+        const int kvh = hq / G, gr = s % w * G + hq % G, bs = p.block_size;
+        const int L = clamped_len(p, s);
+        const int32_t *table = p.block_tables + (size_t)(s - s % w) * p.max_blocks_per_seq;
+        const float *sc = p.scores + (((size_t)(s / w * p.num_kv_heads + kvh) * ((w * G + 31) / 32) + gr / 32) * p.score_stride) * 32 +
+                          gr % 32;
+#pragma unroll 8
+        for (int j = 0; j < L; ++j) {
+            const int b = table[j / bs];
+            if (b < 0 || b >= p.num_blocks) continue;
+            const float e = fast_exp2(fmaf(sc[(size_t)j * 32], p.scale_log2, -M));
+            float v[VPL];
+            const uint2 raw = *reinterpret_cast<const uint2 *>(
+                static_cast<const T *>(p.v_cache) + (((size_t)b * p.num_kv_heads + kvh) * bs + j % bs) * kD + lane * VPL);
+            Elem<T>::unpack2(raw.x, v[0], v[1]);
+            Elem<T>::unpack2(raw.y, v[2], v[3]);
+#pragma unroll
+            for (int d = 0; d < VPL; ++d) o[d] = fmaf(e, v[d], o[d]);
+        }
     }
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
     uint2 u;
