@@ -391,7 +391,6 @@ __device__ __forceinline__ void tc_unit(const DecodeParams &p, const CUtensorMap
             tc_fence_after();
             float sc[kTG];
             tmem_ld8(tmem + lane_off + kColS + b * kTN, sc);
-            tmem_wait_ld();
             const bool valid = key < ntok && ent >= 0 && ent < p.num_blocks;
 #pragma unroll
             for (int h = 0; h < kTG; ++h) sc[h] = valid ? sc[h] * csc : -INFINITY;
@@ -435,7 +434,6 @@ __device__ __forceinline__ void tc_unit(const DecodeParams &p, const CUtensorMap
                 tc_fence_after();
                 float o[2 * kTG];  // the P_hi and P_lo columns of each head
                 tmem_ld16(tmem + lane_off + kColO, o);
-                tmem_wait_ld();
 #pragma unroll
                 for (int h = 0; h < kTG; ++h) {
                     o[h] *= alpha[h];
@@ -510,7 +508,6 @@ __device__ __forceinline__ void tc_unit(const DecodeParams &p, const CUtensorMap
         {
             float o2[2 * kTG];
             tmem_ld16(tmem + lane_off + kColO, o2);
-            tmem_wait_ld();
 #pragma unroll
             for (int h = 0; h < kTG; ++h) o[h] = o2[h] + o2[kTG + h];  // V.P_hi + V.P_lo
         }

@@ -256,7 +256,6 @@ __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, uns
         for (int c = 0; c < 4; ++c) {
             float v[32];
             tmem_ld32(tO + c * 32, v);
-            tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 8; ++e) __stcg(po(slot, c * 8 + e), make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
         }
@@ -289,7 +288,6 @@ __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, uns
                 for (int c2 = 0; c2 < 2; ++c2) {
                     float v[32];
                     tmem_ld32(tO + (hh * 2 + c2) * 32, v);
-                    tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) ld[c2 * 8 + e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 }
@@ -306,7 +304,6 @@ __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, uns
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;
                 } else {
                     tmem_ld32(col, v);
-                    tmem_wait_ld();
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -326,7 +323,6 @@ __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, uns
     for (int c = 0; c < 4; ++c) {
         float v[32];
         tmem_ld32(tA + c * 32, v);
-        tmem_wait_ld();
         if (valid) {
 #pragma unroll
             for (int q8 = 0; q8 < 4; ++q8) {
@@ -352,7 +348,7 @@ static __device__ __noinline__ void store_partial(float *part_o, float2 *part_ml
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float v[32];
-        tmem_ld32_wait(tO + c * 32, v);
+        tmem_ld32(tO + c * 32, v);
         if (valid) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
@@ -653,7 +649,6 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             for (int c = 0; c < 4; ++c) {
                 float v[32];
                 tmem_ld32(tO + c * 32, v);
-                tmem_wait_ld();
                 if (valid) {
 #pragma unroll
                     for (int q8 = 0; q8 < 4; ++q8) {
@@ -752,12 +747,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 const bool need_mask = kb + kNK - 1 > plim_min;
                 // the whole S row in registers: four loads, one wait
                 float s[kNK];
-                tmem_ld32p(tS + 0, s + 0);
-                tmem_ld32p(tS + 32, s + 32);
-                tmem_ld32p(tS + 64, s + 64);
-                tmem_ld32p(tS + 96, s + 96);
-                tmem_wait_ld();
-                if constexpr (kWindow) tie(s);  // the scores go straight to stores
+                tmem_ld128(tS, s);
                 if (need_mask) {
 #pragma unroll
                     for (int c = 0; c < kNK; ++c) s[c] = (kb + c <= plim) ? s[c] : -INFINITY;
@@ -844,7 +834,6 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     for (int c = 0; c < 4; ++c) {
                         float v[32];
                         tmem_ld32(tO + c * 32, v);
-                        tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] *= alpha;
                         tmem_st32(tO + c * 32, v);
