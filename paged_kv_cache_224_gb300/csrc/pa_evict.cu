@@ -20,9 +20,9 @@
 //           or still read, and strikes them from owner[];
 //   copy    HBM-bound: 16-byte vectors of the kept rows, K and V, to the new
 //           blocks that owner[] still grants.
-// 64 sequences of 8 kv heads, 1025..4096 tokens to 1024, head_dim 128: 102 us,
-// 5.4 TB/s (81% of the copy rate), 79 of them the copy (6.8 TB/s); 2 of 65536
-// to 16384: 67 us, 39 of them the copy.  The selection is bound by instruction
+// 64 sequences of 8 kv heads, 1025..4096 tokens to 1024, head_dim 128: 104 us,
+// 5.3 TB/s (80% of the copy rate), 79 of them the copy (6.8 TB/s); 2 of 65536
+// to 16384: 71 us, 39 of them the copy.  The selection is bound by instruction
 // issue with many rows and by its barriers with few.  Selecting and copying in
 // one kernel, so that a row's copy runs under other rows' selections, was
 // slower (106 and 78 us: a CTA or cluster per row shares the rows out worse
@@ -73,7 +73,7 @@ __device__ __forceinline__ void mark_blocks(const EvictParams &p, int s) {
 
 __global__ void __launch_bounds__(128) evict_mark_kernel(const __grid_constant__ EvictParams p) {
     pdl_wait();
-    pdl_trigger();  // after the wait: the selecting CTAs rely on it
+    pdl_trigger();
     mark_blocks(p, blockIdx.x);
 }
 
@@ -144,10 +144,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     };
     for (int i = tid; i < 4 * 256; i += kSelThreads) (&s_hist[0][0])[i] = 0u;
     __syncthreads();
-    // After a marking launch this grid starts once every CTA of that one has got
-    // past its own wait, so whatever came before it on the stream is complete:
-    // only the CTAs that read the marks wait for them.
-    if (p.one_check) pdl_wait();
+    pdl_wait();  // the totals and lengths (and the marks) are complete and visible
     pdl_trigger();
     if (row >= p.num_seqs * p.num_kv_heads) {  // clusters that do not select (and so never sync)
         const int seq = blockIdx.x - p.num_seqs * p.num_kv_heads * CL;
@@ -156,9 +153,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
             for (int i = 0; i < p.num_seqs; ++i) mark_blocks(p, i);
             __syncthreads();
             for (int i = 0; i < p.num_seqs; ++i) check_blocks(p, i);
-        } else {
-            pdl_wait();
-            if (seq < p.num_seqs) check_blocks(p, seq);
+        } else if (seq < p.num_seqs) {
+            check_blocks(p, seq);
         }
         return;
     }
