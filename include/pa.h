@@ -333,8 +333,9 @@ PA_API int pa_mixed_step(void *prefill_out, const void *prefill_query, const int
  *   (a, b) -> (a cos - b sin, b cos + a sin)
  * where pair i of a head is its dimensions (i, rot_dim/2 + i), or (2i, 2i + 1)
  * when `interleaved` is non-zero; dimensions from rot_dim on pass unchanged.
- * The angle is reduced to one turn in 64-bit fixed point (no digits are lost
- * to a far position), the rotation is fp32, each result is rounded once.
+ * The angle is reduced to one turn in 64-bit fixed point, so that no digits are
+ * lost to a far position or a high frequency (it is off by up to |position| *
+ * 2^-64 turns), the rotation is fp32, each result is rounded once.
  *
  *   query, query_out  [num_tokens][num_heads][head_dim] dtype; query_out may be
  *                     query itself (same pointer and stride) but must not

@@ -8,11 +8,14 @@
 //
 // Angles.  fp32 has no digits left for the fraction of a turn once a position
 // passes a few thousand, so the turn count is kept in fixed point: inv_freq /
-// 2 pi, reduced to [-1/2, 1/2] in fp64, becomes a 64-bit fraction of a turn,
-// and position * fraction modulo 2^64 -- one wrapping integer product -- is
-// the angle modulo a whole turn, with nothing lost to the position's size.
-// Its top 32 bits go to sincospi: the angle is within 2^-25 turns' worth of
-// fp32 rounding plus |position| * 2^-55 turns of the exact product.
+// 2 pi modulo 1 becomes a 64-bit fraction of a turn, and position * fraction
+// modulo 2^64 -- one wrapping integer product -- is the angle modulo a whole
+// turn, with nothing lost to the position's size.  Its top 32 bits go to
+// sincospi: the angle is within 2^-25 turns' worth of fp32 rounding plus
+// |position| * 2^-64 turns of the exact product, whatever inv_freq is.  (An fp64
+// product for the fraction is off by up to 2^-54 of the turns a position makes,
+// too much far out for frequencies above 1, and slower: 8192 tokens take 57 us by
+// one, 59.6 by two that add up, 55.5 by the integers.)
 //
 // HBM-bound: every row is read and written once.  A CTA walks tokens
 // blockIdx.x, + gridDim.x, ...; a token's cosines and sines are computed once,
@@ -22,9 +25,9 @@
 // pairs); its place in the head is the same for every head it takes, so it
 // reads its 8 cosines and sines once per token, and pair i's turns per
 // position stay in one thread's register throughout.  8192 tokens of 64/8 heads
-// of 128, bf16: 57 us, 5.9 TB/s (88% of the copy rate); one CTA per token, which
-// does the fp64 and the first loads of every token anew, took 147 us, blocks of
-// 640 threads, two to an SM, 64 us.
+// of 128, bf16: 55.5 us, 6.0 TB/s (90% of the copy rate).  With the fp64 product,
+// one CTA per token, which does that and the first loads of every token anew, took
+// 147 us, blocks of 640 threads, two to an SM, 64.
 #include <algorithm>
 #include <type_traits>
 
@@ -52,6 +55,26 @@ __device__ __forceinline__ long long cache_row(const RotaryParams &p, long long 
     // most pools have fewer than 2^32 slots, and a 32-bit division costs a third
     const long long blk = (slot >> 32) ? slot / p.block_size : (long long)((unsigned)slot / (unsigned)p.block_size);
     return (blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size)) * p.head_dim;
+}
+
+// f / (2 pi) modulo 1, in 2^-64, to half a unit, for finite f.  With f = m 2^e
+// (m of 24 bits) only the bits of 1 / (2 pi) from e places after the binary point
+// on count modulo 1, and 96 of them are enough (Payne and Hanek's reduction,
+// 1983): three 32-bit products, no fp64.
+__device__ __forceinline__ long long turn_fraction(float f) {
+    // 160 zeros, for e < 0, and 1 / (2 pi) to 224 bits
+    static constexpr unsigned kBits[12] = {0u, 0u, 0u, 0u, 0u, 0x28be60dbu, 0x9391054au, 0x7f09d5f4u, 0x7d4d3770u,
+                                           0x36d8a566u, 0x4f10e410u, 0x7f9458eau};
+    const unsigned u = __float_as_uint(f), ex = u >> 23 & 255u;
+    const unsigned m = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
+    const int at = (int)min(max(ex, 1u), 254u) - 150 + 160;  // the first bit that counts, 11 .. 264
+    const int k = at >> 5, s = at & 31;
+    const unsigned w0 = kBits[k], w1 = kBits[k + 1], w2 = kBits[k + 2], w3 = kBits[k + 3];
+    const unsigned hi = __funnelshift_l(w1, w0, s), mid = __funnelshift_l(w2, w1, s), lo = __funnelshift_l(w3, w2, s);
+    const unsigned long long low = (unsigned long long)m * lo;
+    const unsigned long long frac = ((unsigned long long)(m * hi) << 32) + (unsigned long long)m * mid + (low >> 32) +
+                                    (low >> 31 & 1u);
+    return (long long)((u >> 31) ? 0ull - frac : frac);
 }
 
 constexpr int kMaxThreads = 320;
@@ -85,9 +108,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_con
     auto turns_of = [&](int i, bool &ok) {
         const float f = p.inv_freq[i];
         ok = isfinite(f);
-        double turns = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-        turns -= rint(turns);
-        return __double2ll_rn(turns * 18446744073709551616.0);
+        return turn_fraction(f);
     };
     if (mine < half) frac = turns_of(mine, finite);
     if (mine + (int)blockDim.x < half) frac2 = turns_of(mine + blockDim.x, finite2);
