@@ -378,19 +378,21 @@ PA_API int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, const 
  *                  new tokens at once) repeat the sequence's block-table row,
  *                  each with its own context length, and need scale > 0.  From 4
  *                  positions and 16 query rows (positions times heads per kv head)
- *                  on, at head_dim 128 and block_size >= 16, they are attended
- *                  together on the tensor cores: the row of the first position is the one
- *                  that is read (another that differs in a position's context
- *                  sets PA_DEVERR_PREFIX, outputs and totals undefined),
- *                  and partition_tokens has no effect.  (Where V holds a NaN or
+ *                  on, at head_dim 128 and block_size >= 16, they may be attended
+ *                  together on the tensor cores (by a rule on these numbers and
+ *                  max_context_len): the row of the first position is the one
+ *                  that counts (another that differs in a position's context
+ *                  sets PA_DEVERR_PREFIX, outputs and totals undefined), and
+ *                  partition_tokens then has no effect.  (Where V holds a NaN or
  *                  infinity within the longest of the contexts, the outputs of
  *                  the row are computed again key by key, so that it reaches
  *                  those alone that see it: 16 positions over 8191 tokens take
  *                  2.4 ms then.)
  *   workspace      >= pa_decode_weights_workspace_bytes(...) bytes, 256-byte
  *                  aligned, scratch: the partials, and every score in fp32
- *                  (num_seqs * num_heads * max_context_len * 4 bytes; rows that are
- *                  attended together take whole sets of 32 query rows)
+ *                  (num_seqs * num_heads * max_context_len * 4 bytes; rows that may
+ *                  be attended together take whole sets of 32 query rows): pass
+ *                  the batch's own longest length, not the model's
  * The weights are fp32 from fp32 scores; sums run in a fixed order.  Keys that
  * an invalid table entry leaves out of the softmax weigh 0.  Shapes,
  * partition_tokens, data errors as for pa_decode.

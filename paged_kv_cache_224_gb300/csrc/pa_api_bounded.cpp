@@ -47,37 +47,44 @@ struct PartialWs {
 };
 
 // Decode with kept scores: the partials, then the scores.  `window`: the rows of
-// several queries are attended together.
+// several queries are attended together; where a shape allows that, the workspace
+// holds either form.
 struct WeightsWs {
     int pt = 1, slots;
     long long stride;  // tokens of a row's scores
-    size_t acc, ml, scores;
-    bool window, ok;
+    size_t acc, ml, scores, bytes;
+    bool one_table, window, ok;  // one_table: the queries of a row are to have the same table row
     WeightsWs(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
               int queries_per_row, int partition_tokens) {
         const int group = num_heads / num_kv_heads;
-        window = pa::window_supported(head_dim, block_size, group, queries_per_row);
+        one_table = pa::window_supported(head_dim, block_size, group, queries_per_row);
+        window = one_table && pa::window_preferred(group, queries_per_row, max_context_len);
         ok = partition_tokens >= 0 && partition_tokens % block_size == 0;
         if (!ok) return;
-        if (window) {
-            slots = pa::window_pieces(num_seqs / queries_per_row, queries_per_row, group, num_kv_heads, max_context_len);
-            stride = pa::window_score_stride(max_context_len);
-        } else {
-            pt = partition_tokens ? clamp_partition(partition_tokens, max_context_len, block_size)
-                                  : pa::weights_partition_tokens(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
-                                                                 max_context_len);
-            slots = std::max(1, (int)(((long long)max_context_len + pt - 1) / pt));
-            stride = ((long long)max_context_len + 3) / 4 * 4;
+        const int rows = num_seqs / queries_per_row;
+        bytes = 0;
+        for (const bool together : {!window, window}) {  // the form that is not taken, then the one that is
+            if (together && !one_table) continue;
+            if (together) {
+                slots = pa::window_pieces(rows, queries_per_row, group, num_kv_heads, max_context_len);
+                stride = pa::window_score_stride(max_context_len);
+            } else {
+                pt = partition_tokens ? clamp_partition(partition_tokens, max_context_len, block_size)
+                                      : pa::weights_partition_tokens(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                                     block_size, max_context_len);
+                slots = std::max(1, (int)(((long long)max_context_len + pt - 1) / pt));
+                stride = ((long long)max_context_len + 3) / 4 * 4;
+            }
+            const PartialWs w(num_seqs, num_heads, head_dim, slots);
+            acc = slots > 1 || together ? w.acc : 0;
+            ml = w.ml;
+            scores = round256((together ? pa::window_score_floats(rows, num_kv_heads, queries_per_row * group, max_context_len)
+                                        : (size_t)num_seqs * num_heads * stride) *
+                              sizeof(float));
+            bytes = std::max(bytes, acc + ml + scores);
         }
-        const PartialWs w(num_seqs, num_heads, head_dim, slots);
-        acc = slots > 1 || window ? w.acc : 0;
-        ml = w.ml;
-        scores = round256((window ? pa::window_score_floats(num_seqs / queries_per_row, num_kv_heads, queries_per_row * group,
-                                                            max_context_len)
-                                  : (size_t)num_seqs * num_heads * stride) *
-                          sizeof(float));
     }
-    size_t total() const { return acc + ml + scores; }
+    size_t total() const { return bytes; }
 };
 
 // The shared-prefix step: the decode instances' queue counter, then the partials.
@@ -257,7 +264,8 @@ int pa_decode_weights(void *out, const void *query, const void *k_cache, const v
     }
     const int rc = pa::launch_decode_scores(dtype, head_dim, block_size, group, p, st);
     if (rc != PA_OK || whole) return rc;
-    return pa::launch_weights_merge(dtype, head_dim, group, p, weights, weights_out, weights_len, queries_per_row, st);
+    return pa::launch_weights_merge(dtype, head_dim, group, p, weights, weights_out, weights_len, queries_per_row,
+                                    w.one_table, st);
 }
 
 size_t pa_evict_workspace_bytes(int num_blocks) {

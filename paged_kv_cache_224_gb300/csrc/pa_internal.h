@@ -198,9 +198,9 @@ int weights_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int 
                              int max_context_len);
 // After launch_decode_scores: merges split sequences' partials into p.out and
 // adds every token's weights to its row's total, queries_per_row sequences to
-// a row of `width` totals.
+// a row of `width` totals.  one_table: flags sequences of a row whose table rows differ.
 int launch_weights_merge(pa_dtype dt, int head_dim, int group, const DecodeParams &p, const float *weights,
-                         float *weights_out, int width, int queries_per_row, cudaStream_t stream);
+                         float *weights_out, int width, int queries_per_row, bool one_table, cudaStream_t stream);
 // Log-sum-exp merge of the partials in p's workspace into p.out.
 int launch_decode_reduce(pa_dtype dt, int head_dim, const DecodeParams &p, cudaStream_t stream);
 int launch_reshape_and_cache(const void *key, const void *value, void *k_cache, void *v_cache,
@@ -279,6 +279,7 @@ int launch_prefix_f16(int block_size, int group, const PrefixLaunch &pl, unsigne
 // consecutive sequences is attended together on the tensor cores, its scores
 // kept (window_score_floats in all), and then merged and added up.  window_pieces: the most pieces (partials) of a unit.
 bool window_supported(int head_dim, int block_size, int group, int queries_per_row);
+bool window_preferred(int group, int queries_per_row, int max_context_len);
 int window_pieces(int rows, int queries_per_row, int group, int num_kv_heads, int max_context_len);
 inline long long window_score_stride(int max_context_len) { return ((long long)max_context_len + 127) / 128 * 128; }
 inline size_t window_score_floats(int rows, int num_kv_heads, int query_rows, int max_context_len) {

@@ -17,7 +17,8 @@
 //
 // Where every sequence is a single unit the decode kernel adds the weights up
 // itself, from scores it has just written (one launch less: 2 us of a short
-// batch's 12).  Otherwise one kernel, two kinds of CTA:
+// batch's 12).  Otherwise one kernel, two kinds of CTA (and, for positions that
+// might be attended together (pa_window.cu), one that looks at their table rows):
 //   merge    the log-sum-exp merge of a split sequence's partials, a warp (a CTA,
 //            with many partials) per (sequence, head): out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p;
 //   totals   one CTA per (row of totals, kv head, chunk of tokens): each
@@ -114,7 +115,7 @@ __device__ __forceinline__ void merge_row(const DecodeParams &p, int pair, int l
 template <typename T, int D, int G, int kItems, bool kMany>
 __global__ void __launch_bounds__(kThreads)
     weights_merge_kernel(const __grid_constant__ DecodeParams p, const float *weights, float *weights_out, int width,
-                         int queries_per_row, int loops, int chunks, int merge_ctas) {
+                         int queries_per_row, int loops, int chunks, int merge_ctas, int total_ctas) {
     __shared__ float2 s_ml[(kMany ? kMembers : 1) * G];  // (maximum, 1 / sum) per sequence and head
     __shared__ int s_len[kMany ? kMembers : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -130,6 +131,15 @@ __global__ void __launch_bounds__(kThreads)
         return;
     }
     const int u = blockIdx.x - merge_ctas;
+    if (kMany && u >= total_ctas) {  // a sequence's table row against its row's first one's
+        const int s = u - total_ctas;
+        const int32_t *row = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+        const int32_t *lead = p.block_tables + (size_t)(s - s % queries_per_row) * p.max_blocks_per_seq;
+        bool same = true;
+        for (int j = tid; j < (clamped_len(p, s) + p.block_size - 1) / p.block_size; j += kThreads) same = same && row[j] == lead[j];
+        if (!same) flag_error(p.d_err, PA_DEVERR_PREFIX);
+        return;
+    }
     const int chunk = u % chunks, rh = u / chunks;
     const int r = rh / p.num_kv_heads, kvh = rh - r * p.num_kv_heads;
     const int j0 = chunk * loops * kThreads * kItems + tid;  // this thread's first tokens: j0 + i * kThreads
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, int D, int G>
 int launch_merge_t(const DecodeParams &p, const float *weights, float *weights_out, int width, int queries_per_row,
-                   cudaStream_t stream) {
+                   bool one_table, cudaStream_t stream) {
     const long long rows = (long long)(p.num_seqs / queries_per_row) * p.num_kv_heads;
     constexpr int kMost = 2;
     const bool few = rows * ((p.max_context_len + kMost * kThreads - 1) / (kMost * kThreads)) < 2 * sm_count();
@@ -276,23 +286,23 @@ int launch_merge_t(const DecodeParams &p, const float *weights, float *weights_o
     const long long pairs = (long long)p.num_seqs * p.num_heads;
     const int per_cta = p.slots >= kWideMerge ? 1 : kThreads / 32;
     const long long merge = p.max_partitions > 1 ? (pairs + per_cta - 1) / per_cta : 0;
-    const long long total = merge + rows * chunks;
+    const long long total = merge + rows * chunks + (one_table ? p.num_seqs : 0);
     if (total > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
     auto kern = queries_per_row > 1
                     ? (few ? weights_merge_kernel<T, D, G, 1, true> : weights_merge_kernel<T, D, G, kMost, true>)
                     : (few ? weights_merge_kernel<T, D, G, 1, false> : weights_merge_kernel<T, D, G, kMost, false>);
     return launch_pdl(kern, dim3((unsigned)total), dim3(kThreads), 0, stream, p, weights,
-                      weights_out, width, queries_per_row, loops, chunks, (int)merge) == cudaSuccess
+                      weights_out, width, queries_per_row, loops, chunks, (int)merge, (int)(rows * chunks)) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }
 
 template <typename T>
 int launch_merge_dtype(int head_dim, int group, const DecodeParams &p, const float *weights, float *weights_out,
-                       int width, int queries_per_row, cudaStream_t stream) {
+                       int width, int queries_per_row, bool one_table, cudaStream_t stream) {
 #define PA_MERGE_CASE(DD, GG)                \
     if (head_dim == DD && group == GG)       \
-        return launch_merge_t<T, DD, GG>(p, weights, weights_out, width, queries_per_row, stream);
+        return launch_merge_t<T, DD, GG>(p, weights, weights_out, width, queries_per_row, one_table, stream);
     PA_MERGE_CASE(64, 1) PA_MERGE_CASE(64, 2) PA_MERGE_CASE(64, 4) PA_MERGE_CASE(64, 8)
     PA_MERGE_CASE(128, 1) PA_MERGE_CASE(128, 2) PA_MERGE_CASE(128, 4) PA_MERGE_CASE(128, 8)
 #undef PA_MERGE_CASE
@@ -330,10 +340,11 @@ int weights_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int 
 }
 
 int launch_weights_merge(pa_dtype dt, int head_dim, int group, const DecodeParams &p, const float *weights,
-                         float *weights_out, int width, int queries_per_row, cudaStream_t stream) {
-    return dt == PA_BF16
-               ? launch_merge_dtype<__nv_bfloat16>(head_dim, group, p, weights, weights_out, width, queries_per_row, stream)
-               : launch_merge_dtype<__half>(head_dim, group, p, weights, weights_out, width, queries_per_row, stream);
+                         float *weights_out, int width, int queries_per_row, bool one_table, cudaStream_t stream) {
+    return dt == PA_BF16 ? launch_merge_dtype<__nv_bfloat16>(head_dim, group, p, weights, weights_out, width,
+                                                             queries_per_row, one_table, stream)
+                         : launch_merge_dtype<__half>(head_dim, group, p, weights, weights_out, width, queries_per_row,
+                                                      one_table, stream);
 }
 
 }  // namespace pa

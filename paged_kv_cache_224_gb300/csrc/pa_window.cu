@@ -205,14 +205,29 @@ __global__ void __launch_bounds__(kTotThreads)
 
 }  // namespace
 
-// Measured on a GB300, 8 kv heads, together against one position after the
-// other (us): 4 positions of 4 heads over 8191 tokens 24 / 33, over 32 caches of
-// up to 4096 tokens 153 / 205, over 64 of up to 512 85 / 68; 8 positions 29 / 51
-// and 184 / 375; 16 positions of one head over 16 caches 85 / 199; but 2
-// positions of 8 heads 24 / 18 and 153 / 97 (the second position finds K and V
-// in L2).
 bool window_supported(int head_dim, int block_size, int group, int queries_per_row) {
     return head_dim == kD && block_size >= 16 && queries_per_row >= 4 && (long long)queries_per_row * group >= 16;
+}
+
+// Whether a supported window is attended together.  One position after the other
+// reads the cache once each (from L2, mostly, after the first); together a unit has
+// the set-up and the tiles of 128 keys of the prefill's CTA.  Measured on a GB300, 8
+// kv heads, bf16, caches of half to all of L tokens, together / apart in us, by the
+// number of caches (1, 16, 256):
+//   8 heads a kv head, tensor-core decode:
+//     4 positions  L 256: 13/12  24/24  339/229    8192: 26/25  203/163  2987/2388
+//     8 positions  L 256: 14/17  28/41  414/455    8192: 27/39  235/287  (64: 890/1137)
+//   4 heads:
+//     4 positions  L 512: 12/11  31/25  452/244    2048: 15/15  72/76  987/859    8192: 25/30  201/237  2946/3231
+//     8 positions  L 64: 13/10  17/19  220/161     512: 13/14  33/45  488/486     8192: 26/52  204/437  3002/6335
+//     16 positions L 64: 14/15  20/33  284/330     8192: 28/94  237/836
+//   2 heads:
+//     8 positions  L 512: 12/11  31/35  452/353    1024: 14/13  45/64  636/646    8192: 25/40  200/313  2935/4607
+//   1 head:
+//     16 positions L 64: 13/11  16/22  198/219     8192: 25/59  200/477  2931/7377
+bool window_preferred(int group, int queries_per_row, int max_context_len) {
+    if (group == 8) return queries_per_row >= 8;
+    return queries_per_row >= 16 || max_context_len >= (queries_per_row >= 8 ? 2048 / group : 4096);
 }
 
 int window_pieces(int rows, int queries_per_row, int group, int num_kv_heads, int max_context_len) {
