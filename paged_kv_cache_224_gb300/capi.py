@@ -630,7 +630,9 @@ def pa_decode_weights(out, query, k_cache, v_cache, block_tables, context_lens, 
                       stream=None):
     """``pa_decode`` that adds each cached token's attention weight to a total:
     weights float32 [B / queries_per_row][Hkv][W], W >= max_context_len, updated
-    in place unless ``weights_out`` (of the same shape) is given."""
+    in place unless ``weights_out`` (of the same shape) is given.  ``workspace``
+    (``decode_weights_workspace``) grows with max_context_len; one that is made
+    here, with the tables' width where that is less."""
     if weights_out is None:
         weights_out = weights
     dev = _index(query)
@@ -653,6 +655,10 @@ def pa_decode_weights(out, query, k_cache, v_cache, block_tables, context_lens, 
             wshape[0] != B // queries_per_row or wshape[1] != Hkv or weights_out.shape != wshape:
         raise ValueError("shape mismatch")
     if workspace is None:
+        # it holds a score for every token that the bound allows: no more than the
+        # tables hold (longer contexts are clamped and flagged by either)
+        if block_tables.shape[1] * bs < max_context_len <= wshape[2]:
+            max_context_len = block_tables.shape[1] * bs
         workspace = decode_weights_workspace(query, Hkv, bs, max_context_len, partition_tokens, queries_per_row, stream)
     _call("pa_decode_weights", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB,
