@@ -263,6 +263,9 @@ struct PrefixLaunch {
     int prefix_ctas, decode_units;
     unsigned *decode_next;
 };
+// Whether a group's softmax weights over its prefix go to their product with V as
+// two values (pa_prefill.cuh): its rows fit one of a unit's two Q tiles.
+inline bool prefix_two_values(int group_size, int group) { return (long long)group_size * group <= 128; }
 PrefixSchedules prefix_schedules(int groups, int group_size, int prefix_tokens, int group, int num_kv_heads,
                                  int longest_own, int partitions, int num_seqs);
 int prefix_pieces(int groups, const PrefixSchedules &x);

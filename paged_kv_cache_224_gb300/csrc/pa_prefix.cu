@@ -16,20 +16,31 @@ using namespace pfx;
 
 constexpr int kMergeWarps = 4;
 
-// Prefix CTAs of a launch, the rest decoding from the start, by a time model
-// (figures measured on a GB300).  A prefix CTA takes about 5 us to its first
-// tile, 1.8 us for a 128-key tile of 256 rows, and 3 us for the end of each
-// segment, so counts that cut units evenly are better than those that leave
-// every CTA pieces of two.  A decode instance, two to a CTA, takes about 3.2 us
-// for a unit's chain of loads (its number, length, table entries, keys) and
-// then 40 GB/s, all together at most 6.4 TB/s.  A CTA whose prefix tiles are
-// done decodes, some 4 us later.  The count is even (a prefix CTA that shares
-// its SM pair with a decoding one runs a third longer).  Measured on 256
-// sequences after 8192 tokens, own tokens up to 512, 64/8 heads: 123 us at 64
-// prefix CTAs (one unit each), 129 at 96, 136 at 152, 223 at 32.
-int split_ctas(long long tiles, int unit_tiles, double units, double unit_bytes) {
+// Prefix CTAs of a launch, the rest decoding from the start, by a time model.
+// A prefix CTA takes about 5 us to its first tile, 1.8 us for a 128-key tile of
+// 256 rows (2.4 with the weights in two values), and 4 us for the end of each
+// segment, so counts that divide the units or that the units divide, where no CTA
+// has pieces of two, are better than others.  A decode instance, two to a CTA,
+// takes about 6 us for a unit beside its keys (the chain of its number, length,
+// table entries and first keys, its last product and partial) and then 60 GB/s,
+// all together at most 6.4 TB/s.  A CTA whose prefix tiles are
+// done decodes.  The count is even (a prefix CTA that shares its SM pair with a
+// decoding one runs a third longer).  The constants are fitted to sweeps of 8 to
+// 152 CTAs over 19 shapes on a GB300: the choice is within 2.5% of a sweep's best,
+// 7% in one.  It, that best, and all 152, CTAs: us:
+//   groups x size after prefix, own tokens up to, heads    choice      best       152
+//   1 x 256 after 8192,  512, 64/8                          84: 122     96: 122   131
+//   1 x 256 after 1024, 4096, 64/8                           6: 321     32: 318   338
+//   1 x 128 after 4096, 1024, 64/8                          48: 70      40: 69     82
+//   1 x 64 after 4096,   256, 32/8                          48: 27      40: 25     37
+//   32 x 8 after 1008,   512, 32/32                        128: 337    128: 337   387
+//   64 x 4 after 512,    512, 32/8                         128: 115    128: 116   135
+//   2 x 12 after 992,    200, 16/16                         64: 21      64: 21     28
+//   1 x 8 after 8192,    256, 8/8                          128: 22     128: 22     27
+int split_ctas(long long tiles, int unit_tiles, bool two_values, double units, double unit_bytes) {
     const int sms = sm_count();
-    const double t_unit = 3.2e-6 + unit_bytes / 40e9;
+    const double t_tile = two_values ? 2.4e-6 : 1.8e-6, t_unit = 6e-6 + unit_bytes / 60e9;
+    const long long prefix_units = tiles / unit_tiles;
     auto rate = [&](int ctas) {  // units per second
         const double r = 2.0 * ctas / t_unit;
         return unit_bytes > 0 ? std::min(r, 6.4e12 / unit_bytes) : r;
@@ -38,11 +49,11 @@ int split_ctas(long long tiles, int unit_tiles, double units, double unit_bytes)
     double best_t = 1e30;
     for (int n = 2; n <= sms; n += 2) {
         const long long q = (tiles + n - 1) / n;
-        const bool even = tiles % n == 0 && (q % unit_tiles == 0 || unit_tiles % q == 0);
+        const bool even = prefix_units % n == 0 || n % prefix_units == 0;
         const double segments = (double)((q + unit_tiles - 1) / unit_tiles) + (even ? 0.0 : 1.0);
-        const double tp = 5e-6 + q * 1.8e-6 + segments * 3e-6;
+        const double tp = 5e-6 + q * t_tile + segments * 4e-6;
         const double done = rate(sms - n) * tp;
-        const double t = units <= done ? tp : tp + 4e-6 + std::max(t_unit, (units - done) / rate(sms));
+        const double t = units <= done ? tp : tp + std::max(t_unit, (units - done) / rate(sms));
         if (t < best_t) {
             best_t = t;
             best = n;
@@ -57,7 +68,7 @@ PrefixSchedule prefix_schedule(int groups, int group_size, int prefix_tokens, in
     s.row_tiles = (int)(((long long)group_size * group + kUnitRows - 1) / kUnitRows);
     s.n = (prefix_tokens + kNK - 1) / kNK;
     s.tiles = (long long)groups * num_kv_heads * s.row_tiles * s.n;
-    s.ctas = (int)std::min<long long>(split_ctas(s.tiles, s.n, units, unit_bytes), s.tiles);
+    s.ctas = (int)std::min<long long>(split_ctas(s.tiles, s.n, prefix_two_values(group_size, group), units, unit_bytes), s.tiles);
     return s;
 }
 

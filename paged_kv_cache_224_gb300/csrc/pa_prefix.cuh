@@ -104,8 +104,9 @@ template <typename T>
 int launch_prefix_dtype(int block_size, int group, const PrefixLaunch &pl, unsigned grid, cudaStream_t stream) {
 #define PA_PFX_CASE(BB, GG) \
     if (block_size == BB && group == GG)                                             \
-        return pl.pp.seqs[0].chunk_len * GG <= kM ? launch_prefix_t<T, BB, GG, true>(pl, grid, stream) \
-                                                  : launch_prefix_t<T, BB, GG, false>(pl, grid, stream);
+        return prefix_two_values(pl.pp.seqs[0].chunk_len, GG)                        \
+                   ? launch_prefix_t<T, BB, GG, true>(pl, grid, stream)              \
+                   : launch_prefix_t<T, BB, GG, false>(pl, grid, stream);
 #define PA_PFX_GROUPS(BB) PA_PFX_CASE(BB, 1) PA_PFX_CASE(BB, 2) PA_PFX_CASE(BB, 4) PA_PFX_CASE(BB, 8)
     PA_PFX_GROUPS(16)
     PA_PFX_GROUPS(32)
