@@ -78,11 +78,13 @@ int resolve_partition(int num_seqs, int num_heads, int num_kv_heads, int block_s
     if (partition_tokens == 0)
         return pa::auto_partition_tokens(num_seqs, num_heads, num_kv_heads, block_size, max_context_len);
     if (partition_tokens % block_size) return -1;
-    return partition_tokens;
+    // at most what holds the longest length: the kernels add a length to it in 32 bits
+    const long long whole = ((long long)std::max(max_context_len, 1) + block_size - 1) / block_size * block_size;
+    return (int)std::min<long long>(partition_tokens, whole);
 }
 
 int max_parts(int max_context_len, int pt) {
-    return max_context_len > 0 ? (max_context_len + pt - 1) / pt : 1;
+    return max_context_len > 0 ? (int)(((long long)max_context_len + pt - 1) / pt) : 1;
 }
 
 }  // namespace
@@ -129,7 +131,7 @@ int pa_decode_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, in
         return 0;
     const int pt = resolve_partition(num_seqs, num_heads, num_kv_heads, block_size, max_context_len,
                                      partition_tokens);
-    return pt > 0 ? pt : 0;
+    return pt <= 0 ? 0 : partition_tokens > 0 ? partition_tokens : pt;
 }
 
 size_t pa_decode_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
