@@ -13,9 +13,11 @@
 //           threshold total by radix selection (four histograms of 8 bits over
 //           an order-preserving integer image of the fp32 totals), then one
 //           pass in index order that emits the kept indices and their totals.
-//           The totals are read once, into registers (up to 4096 or 8192 a CTA;
-//           rows of more than 65536 read them again in every pass); a cluster's CTAs read each
-//           other's histograms and counts through distributed shared memory.
+//           The totals' images stay in registers (up to 4096 or 8192 a CTA), so
+//           that the totals are read twice, to rank them and, from L2, to emit
+//           them; rows of more than 65536 read them again in every pass.  A
+//           cluster's CTAs read each other's histograms and counts through
+//           distributed shared memory.
 //           Beside them one CTA per sequence looks for new blocks named twice
 //           or still read, and strikes them from owner[];
 //   copy    HBM-bound: 16-byte vectors of the kept rows, K and V, to the new
