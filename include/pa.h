@@ -470,8 +470,9 @@ PA_API int pa_evict(void *k_cache, void *v_cache, const float *weights, float *n
  * Supported: head_dim 128, block_size in {16, 32, 64, 128}, num_heads /
  * num_kv_heads in {1, 2, 4, 8}.  Groups of more than 128 query rows (group_size
  * times heads per kv head) round the softmax weights of prefix keys to dtype, once,
- * for their product with V, as pa_prefill_chunk does; smaller ones, like pa_decode,
- * give them about twice dtype's bits.
+ * for their product with V, as pa_prefill_chunk does; smaller ones, like pa_decode
+ * with 8 heads per kv head, send them as two values of dtype, about twice its bits
+ * (so that an infinity in V comes out as NaN).
  * Groups of 1, 2, 4 or 8 rows can take either call: pa_decode_shared_prefix reads
  * their prefixes at the memory's rate and is the faster one, but for a single group
  * of few kv heads.  This call / that one / pa_decode in us, own tokens up to 256:

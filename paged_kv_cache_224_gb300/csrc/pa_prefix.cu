@@ -23,11 +23,11 @@ constexpr int kMergeWarps = 4;
 // has pieces of two, are better than others.  A decode instance, two to a CTA,
 // takes about 6 us for a unit beside its keys (the chain of its number, length,
 // table entries and first keys, its last product and partial) and then 60 GB/s,
-// all together at most 6.4 TB/s.  A CTA whose prefix tiles are
-// done decodes.  The count is even (a prefix CTA that shares its SM pair with a
-// decoding one runs a third longer).  The constants are fitted to sweeps of 8 to
-// 152 CTAs over 19 shapes on a GB300: the choice is within 2.5% of a sweep's best,
-// 7% in one.  It, that best, and all 152, CTAs: us:
+// all together at most 6.4 TB/s.  A CTA whose prefix tiles are done decodes.  The
+// count is even (a prefix CTA that shares its SM pair with a decoding one runs a
+// third longer).  The constants are fitted to sweeps of 8 to 152 CTAs over 19
+// shapes on a GB300: the choice is within 2.5% of a sweep's best, 7% in one.  CTAs
+// and us, of the choice, of that best and of all 152:
 //   groups x size after prefix, own tokens up to, heads    choice      best       152
 //   1 x 256 after 8192,  512, 64/8                          84: 122     96: 122   131
 //   1 x 256 after 1024, 4096, 64/8                           6: 321     32: 318   338
