@@ -491,6 +491,119 @@ PA_API int pa_decode_common_prefix(void *out, const void *query, const void *k_c
                                    int *d_err, void *stream);
 
 /*
+ * pa_norm_rotary_and_cache -- pa_rotary_and_cache for models that normalise their
+ * queries and keys head by head: before the rotation each head of query and key
+ * becomes
+ *   x[d] / sqrt(mean(x^2) + eps) * norm[d],   d < head_dim
+ * in fp32 like the rotation, so that each result is rounded once.  Values pass
+ * unchanged.
+ *   query_norm, key_norm  [head_dim] dtype (device), both required
+ *   eps            finite, >= 0
+ * Everything else as for pa_rotary_and_cache.
+ */
+PA_API int pa_norm_rotary_and_cache(void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
+                                    const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+                                    void *k_cache, void *v_cache, const int32_t *positions, const int64_t *slot_mapping,
+                                    const float *inv_freq, const int *pair_axis, int num_axes, int rot_dim,
+                                    int interleaved, const void *query_norm, const void *key_norm, float eps,
+                                    int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int num_blocks, pa_dtype dtype, int *d_err, void *stream);
+
+/*
+ * Caches of 8 bits.  k_cache and v_cache hold e4m3 codes (1 sign, 4 exponent, 3
+ * mantissa bits, no infinities), [num_blocks][num_kv_heads][block_size][head_dim];
+ * k_scales and v_scales, uint8 [num_blocks][num_kv_heads], hold one power of two for
+ * each block and kv head, 2^(byte - 127) (e8m0; 255 is NaN).  A row's values are its
+ * codes times its block's scale.  Everything outside the cache stays dtype (fp16 or
+ * bf16): queries, outputs, new keys and values.
+ *
+ * Writing (pa_reshape_and_cache_fp8, pa_rotary_and_cache_fp8).  A call decides the
+ * scale of each block that it writes to, per kv head and for K and V apart:
+ *   need = the smallest power of two, from 2^-64 on, with |x| <= 448 need for every
+ *          element x of the rows that the call writes to the block
+ *   the new scale is need when the block's first row is among them (the block starts
+ *   afresh: what it held counts for nothing), else the larger of the old scale and need.
+ * So a sequence fills a block from its first row on, in as many calls as it likes.  Rows
+ * that the call does not write are moved to a scale that grew (rounded to nearest even
+ * where their codes become subnormal, exact otherwise); in a block that starts afresh,
+ * and under a scale that stays, they are left as they are.  Each new element is rounded
+ * once, from fp32, to nearest even: within 2^-4 of itself, or 2^-10 need.  An infinity
+ * or NaN becomes NaN and does not count towards the scale; with dtype fp16, magnitudes
+ * above 61440 (the largest code times a power of two that fp16 holds) become 61440.
+ * The result does not depend on the order in which the device works: where two tokens
+ * name the same slot, the later one (the larger token index) is written.
+ *
+ *   arguments      as for pa_reshape_and_cache and pa_rotary_and_cache; k_scales and
+ *                  v_scales are read and written; query_norm, key_norm and eps as for
+ *                  pa_norm_rotary_and_cache, or both norms NULL for none
+ * Supported: head_dim a multiple of 16 up to 256, block_size in {8, 16, 32, 64, 128}.
+ * num_tokens == 0 is a no-op.
+ */
+PA_API int pa_reshape_and_cache_fp8(const void *key, const void *value, uint8_t *k_cache, uint8_t *v_cache,
+                                    uint8_t *k_scales, uint8_t *v_scales, const int64_t *slot_mapping, int num_tokens,
+                                    int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_dtype dtype,
+                                    int *d_err, void *stream);
+PA_API int pa_rotary_and_cache_fp8(void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
+                                   const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+                                   uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_scales, uint8_t *v_scales,
+                                   const int32_t *positions, const int64_t *slot_mapping, const float *inv_freq,
+                                   const int *pair_axis, int num_axes, int rot_dim, int interleaved,
+                                   const void *query_norm, const void *key_norm, float eps, int num_tokens,
+                                   int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                   pa_dtype dtype, int *d_err, void *stream);
+
+/*
+ * pa_decode_fp8 -- pa_decode over an 8-bit cache: softmax(scale * q . k) v with the
+ * cached values as above, sums in fp32, the output rounded once to dtype.
+ * Arguments, shapes, partition_tokens and data errors as for pa_decode (invalid table
+ * entries are flagged and the keys they would supply are left out).
+ *   workspace      >= pa_decode_fp8_workspace_bytes(...) bytes, 256-byte aligned,
+ *                  scratch (may be NULL when that is 0)
+ * max_blocks_per_seq * block_size must stay below 2^31 - 256.
+ */
+PA_API size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                            int block_size, int max_context_len, int partition_tokens);
+PA_API int pa_decode_fp8(void *out, const void *query, const uint8_t *k_cache, const uint8_t *v_cache,
+                         const uint8_t *k_scales, const uint8_t *v_scales, const int32_t *block_tables,
+                         int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
+                         int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_context_len,
+                         float scale, int partition_tokens, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                         int *d_err, void *stream);
+
+/*
+ * pa_prefill_batch_fp8 -- pa_prefill_batch over an 8-bit cache: causal attention of
+ * prompt chunks whose own keys and values are in the cache already.  The sequences'
+ * cached values are laid out once in dtype (exact: every code times its scale is a
+ * bf16 value, and an fp16 one as far as fp16 reaches) and attended as pa_prefill_batch
+ * does, with its numerics.
+ *   prefix_lens, chunk_lens  int [num_seqs], HOST memory
+ *   workspace      >= pa_prefill_batch_fp8_workspace_bytes(...) bytes, 256-byte
+ *                  aligned, required; its content on entry is ignored; not to be shared
+ *                  with work that overlaps the call on the device.  It holds the
+ *                  sequences' cached values in 16 bits: 4 * head_dim * num_kv_heads
+ *                  bytes a token of prefix and chunk, rounded up to whole blocks (of
+ *                  the 64 sequences that have most, where the batch has more)
+ * Shapes, arguments and errors as for pa_prefill_batch (an invalid table entry is
+ * flagged and that sequence's outputs are undefined).
+ */
+PA_API size_t pa_prefill_batch_fp8_workspace_bytes(const int *prefix_lens, const int *chunk_lens, int num_seqs,
+                                                   int num_heads, int num_kv_heads, int head_dim, int block_size);
+PA_API int pa_prefill_batch_fp8(void *out, const void *query, const uint8_t *k_cache, const uint8_t *v_cache,
+                                const uint8_t *k_scales, const uint8_t *v_scales, const int32_t *block_tables,
+                                int max_blocks_per_seq, const int *prefix_lens, const int *chunk_lens, int num_seqs,
+                                int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes, int *d_err,
+                                void *stream);
+
+/*
+ * pa_copy_blocks_fp8 -- pa_copy_blocks for an 8-bit cache: codes and scales of each
+ * pair's blocks, with the same rules and workspace (pa_copy_blocks_workspace_bytes).
+ */
+PA_API int pa_copy_blocks_fp8(uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_scales, uint8_t *v_scales,
+                              const int64_t *pairs, int num_pairs, int num_kv_heads, int head_dim, int block_size,
+                              int num_blocks, void *workspace, size_t workspace_bytes, int *d_err, void *stream);
+
+/*
  * Failure detection.  Every wait inside the kernels (on TMA copies, MMA
  * completions, other warps) is bounded: after pa_bounded_wait_polls() polls
  * it gives up, ORs PA_DEVERR_TIMEOUT into *d_err and lets the kernel finish,

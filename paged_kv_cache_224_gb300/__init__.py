@@ -13,5 +13,8 @@ from .capi import (PAError, lib, pa_copy_blocks, pa_copy_blocks_workspace_bytes,
                    pa_status_string, decode_workspace,
                    pa_rotary_and_cache, pa_decode_weights, pa_decode_weights_workspace_bytes,
                    decode_weights_workspace, pa_evict, evict_workspace, pa_decode_common_prefix,
-                   pa_decode_common_prefix_workspace_bytes, decode_common_prefix_workspace)
+                   pa_decode_common_prefix_workspace_bytes, decode_common_prefix_workspace,
+                   pa_norm_rotary_and_cache, pa_reshape_and_cache_fp8, pa_rotary_and_cache_fp8, pa_decode_fp8,
+                   pa_decode_fp8_workspace_bytes, decode_fp8_workspace, pa_prefill_batch_fp8, prefill_fp8_workspace,
+                   pa_copy_blocks_fp8)
 from .block_manager import BlockManager  # noqa: F401,E402

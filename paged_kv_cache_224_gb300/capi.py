@@ -34,7 +34,10 @@ EXPORTED = ("pa_status_string", "pa_reshape_and_cache", "pa_decode_partition_tok
             "pa_mixed_step", "pa_mixed_step_workspace_bytes", "pa_bounded_wait_polls", "pa_selftest_bounded_wait",
             "pa_rotary_and_cache", "pa_decode_weights_workspace_bytes", "pa_decode_weights",
             "pa_evict_workspace_bytes", "pa_evict", "pa_decode_common_prefix_workspace_bytes",
-            "pa_decode_common_prefix", "pa_bm_evict_sequence", "pa_bm_evict_sequences")
+            "pa_decode_common_prefix", "pa_bm_evict_sequence", "pa_bm_evict_sequences",
+            "pa_norm_rotary_and_cache", "pa_reshape_and_cache_fp8", "pa_rotary_and_cache_fp8",
+            "pa_decode_fp8_workspace_bytes", "pa_decode_fp8", "pa_prefill_batch_fp8_workspace_bytes",
+            "pa_prefill_batch_fp8", "pa_copy_blocks_fp8")
 PA_ERR_NO_BLOCKS = -8
 PA_ERR_SCRATCH_LIMIT = -7
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -137,6 +140,22 @@ def lib() -> ctypes.CDLL:
         L.pa_bm_evict_sequence.restype = i
         L.pa_bm_evict_sequences.argtypes = [p, p, i, i]
         L.pa_bm_evict_sequences.restype = i
+        L.pa_norm_rotary_and_cache.argtypes = [p, i64, p, i64, p, i64, p, i64] + [p] * 6 + [i, i, i, p, p, f] + [i] * 7 + [p, p]
+        L.pa_norm_rotary_and_cache.restype = i
+        L.pa_reshape_and_cache_fp8.argtypes = [p] * 7 + [i] * 6 + [p, p]
+        L.pa_reshape_and_cache_fp8.restype = i
+        L.pa_rotary_and_cache_fp8.argtypes = [p, i64, p, i64, p, i64, p, i64] + [p] * 8 + [i, i, i, p, p, f] + [i] * 7 + [p, p]
+        L.pa_rotary_and_cache_fp8.restype = i
+        L.pa_decode_fp8_workspace_bytes.argtypes = [i] * 7
+        L.pa_decode_fp8_workspace_bytes.restype = sz
+        L.pa_decode_fp8.argtypes = [p] * 7 + [i, p] + [i] * 7 + [f, i, i, p, sz, p, p]
+        L.pa_decode_fp8.restype = i
+        L.pa_prefill_batch_fp8_workspace_bytes.argtypes = [p, p] + [i] * 5
+        L.pa_prefill_batch_fp8_workspace_bytes.restype = sz
+        L.pa_prefill_batch_fp8.argtypes = [p] * 7 + [i, p, p] + [i] * 6 + [f, i, p, sz, p, p]
+        L.pa_prefill_batch_fp8.restype = i
+        L.pa_copy_blocks_fp8.argtypes = [p] * 5 + [i] * 5 + [p, sz, p, p]
+        L.pa_copy_blocks_fp8.restype = i
         L.pa_bounded_wait_polls.argtypes = []
         L.pa_bounded_wait_polls.restype = i
         L.pa_selftest_bounded_wait.argtypes = [i, p, p, p]
@@ -747,3 +766,232 @@ def pa_decode_common_prefix(out, query, k_cache, v_cache, block_tables, context_
           block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, int(group_size),
           int(prefix_blocks), Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), int(partition_tokens), _dt(query),
           workspace.data_ptr(), workspace.numel() * workspace.element_size(), _opt(d_err), _raw_stream(dev, stream))
+
+
+# ---- head norms, and caches of 8 bits ---------------------------------------------
+
+
+def _dt_int(dtype) -> int:
+    if dtype is torch.bfloat16:
+        return PA_BF16
+    if dtype is torch.float16:
+        return PA_F16
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq, query_norm,
+                 key_norm, eps, pair_axis, interleaved):
+    """The arguments up to value_stride, and from positions to eps, of a rotary call."""
+    if slot_mapping.dtype is not _I64:
+        raise TypeError("slot_mapping must be int64")
+    if query.dim() != 3:
+        raise ValueError("shape mismatch")
+    qshape = query.shape
+    T, Hq, _ = qshape
+    if slot_mapping.shape != (T,) or qshape[2] != D:
+        raise ValueError("shape mismatch")
+    half, axes, ax = 0, 1, None
+    if inv_freq is not None:
+        if inv_freq.dtype is not _F32:
+            raise TypeError("inv_freq must be float32")
+        if positions is None:
+            raise ValueError("inv_freq needs positions")
+        if positions.dtype is not _I32:
+            raise TypeError("positions must be int32")
+        pshape = positions.shape
+        if inv_freq.dim() != 1 or len(pshape) not in (1, 2) or pshape[-1] != T:
+            raise ValueError("shape mismatch")
+        axes = pshape[0] if len(pshape) == 2 else 1
+        half = inv_freq.shape[0]
+    if pair_axis is not None:
+        ax = np.asarray(pair_axis, dtype=np.int32)
+        if ax.shape != (half,):
+            raise ValueError("pair_axis must name an axis for every pair")
+        ax = ax.tobytes()
+    if (query_norm is None) != (key_norm is None):
+        raise ValueError("query_norm and key_norm go together")
+    if query_norm is not None:
+        if query_norm.dtype is not dt or key_norm.dtype is not dt:
+            raise TypeError("dtype mismatch")
+        if query_norm.shape != (D,) or key_norm.shape != (D,):
+            raise ValueError("shape mismatch")
+    qrow, krow, kshape = Hq * D, Hkv * D, (T, Hkv, D)
+    rows = (query_out.data_ptr(), _token_rows(dev, dt, query_out, qshape, qrow), query.data_ptr(),
+            _token_rows(dev, dt, query, qshape, qrow), key.data_ptr(), _token_rows(dev, dt, key, kshape, krow),
+            value.data_ptr(), _token_rows(dev, dt, value, kshape, krow))
+    rest = (_opt(positions), slot_mapping.data_ptr(), _opt(inv_freq), ax, axes, 2 * half, 1 if interleaved else 0,
+            _opt(query_norm), _opt(key_norm), float(eps), T, Hq, Hkv, D, bs, NB, _dt_int(dt))
+    return rows, rest
+
+
+def pa_norm_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, query_norm,
+                             key_norm, eps, pair_axis=None, interleaved=False, d_err=None, stream=None):
+    """``pa_rotary_and_cache`` with an RMS norm of every query and key head before
+    the rotation: query_norm, key_norm [D] weights of the cache's dtype.  inv_freq
+    and positions may be None (norms alone)."""
+    dev = _index(k_cache)
+    _checked(dev, k_cache, v_cache, positions, slot_mapping, inv_freq, query_norm, key_norm, d_err)
+    dt = k_cache.dtype
+    if v_cache.dtype is not dt:
+        raise TypeError("dtype mismatch")
+    NB, Hkv, bs, D = shape = k_cache.shape
+    if v_cache.shape != shape or query_norm is None or key_norm is None:
+        raise ValueError("two caches of one shape and both norms are needed")
+    rows, rest = _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq,
+                              query_norm, key_norm, eps, pair_axis, interleaved)
+    _call("pa_norm_rotary_and_cache", dev, *rows, k_cache.data_ptr(), v_cache.data_ptr(), *rest, _opt(d_err),
+          _raw_stream(dev, stream))
+
+
+_E4M3, _SCALES = torch.float8_e4m3fn, (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _cache8(k_cache, v_cache, k_scales, v_scales):
+    """The shape of an 8-bit cache: codes float8_e4m3fn [NB][Hkv][bs][D], scales
+    float8_e8m0fnu (or uint8, its bytes) [NB][Hkv]."""
+    if k_cache.dtype is not _E4M3 or v_cache.dtype is not _E4M3:
+        raise TypeError("caches must be float8_e4m3fn")
+    if k_scales.dtype not in _SCALES or v_scales.dtype not in _SCALES:
+        raise TypeError("scales must be float8_e8m0fnu or uint8")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+        raise ValueError("shape mismatch")
+    return shape
+
+
+def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping, d_err=None, stream=None):
+    """``pa_reshape_and_cache`` into an 8-bit cache: key/value [T][Hkv][D]; caches
+    float8_e4m3fn [NB][Hkv][bs][D] with scales float8_e8m0fnu (or uint8) [NB][Hkv];
+    slot_mapping int64 [T]."""
+    dev = _index(k_cache)
+    _checked(dev, key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping, d_err)
+    NB, Hkv, bs, D = _cache8(k_cache, v_cache, k_scales, v_scales)
+    if slot_mapping.dtype is not _I64:
+        raise TypeError("slot_mapping must be int64")
+    if value.dtype is not key.dtype:
+        raise TypeError("dtype mismatch")
+    T = key.shape[0]
+    if key.shape != (T, Hkv, D) or value.shape != key.shape or slot_mapping.shape != (T,):
+        raise ValueError("shape mismatch")
+    _call("pa_reshape_and_cache_fp8", dev, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, bs, NB, _dt_int(key.dtype),
+          _opt(d_err), _raw_stream(dev, stream))
+
+
+def pa_rotary_and_cache_fp8(query_out, query, key, value, k_cache, v_cache, k_scales, v_scales, positions, slot_mapping,
+                            inv_freq, query_norm=None, key_norm=None, eps=0.0, pair_axis=None, interleaved=False,
+                            d_err=None, stream=None):
+    """``pa_rotary_and_cache`` into an 8-bit cache (as ``pa_reshape_and_cache_fp8``),
+    with ``pa_norm_rotary_and_cache``'s norms where query_norm and key_norm are given.
+    inv_freq and positions may be None (no rotation)."""
+    dev = _index(k_cache)
+    _checked(dev, k_cache, v_cache, k_scales, v_scales, positions, slot_mapping, inv_freq, query_norm, key_norm, d_err)
+    NB, Hkv, bs, D = _cache8(k_cache, v_cache, k_scales, v_scales)
+    rows, rest = _rotary_args(dev, query.dtype, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping,
+                              inv_freq, query_norm, key_norm, eps, pair_axis, interleaved)
+    _call("pa_rotary_and_cache_fp8", dev, *rows, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+          v_scales.data_ptr(), *rest, _opt(d_err), _raw_stream(dev, stream))
+
+
+def pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                  partition_tokens=0) -> int:
+    return lib().pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                               partition_tokens)
+
+
+def decode_fp8_workspace(query, num_kv_heads, block_size, max_context_len, partition_tokens=0, stream=None):
+    """Allocate (with torch) a workspace big enough for ``pa_decode_fp8`` on ``stream``
+    (None: the current one)."""
+    B, Hq, D = query.shape
+    with torch.cuda.device(query.device):
+        n = pa_decode_fp8_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, partition_tokens)
+    return _scratch(query.device, n, stream)
+
+
+def pa_decode_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, max_context_len,
+                  partition_tokens=0, workspace=None, d_err=None, stream=None):
+    """``pa_decode`` over an 8-bit cache: out/query [B][Hq][D]; caches float8_e4m3fn
+    [NB][Hkv][bs][D] with scales float8_e8m0fnu (or uint8) [NB][Hkv]; block_tables
+    int32 [B][MB]; context_lens int32 [B].  ``workspace`` defaults to a fresh one."""
+    dev = _index(query)
+    _checked(dev, query, out, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, workspace, d_err)
+    if block_tables.dtype is not _I32 or context_lens.dtype is not _I32:
+        raise TypeError("block_tables and context_lens must be int32")
+    NB, Hkv, bs, D = _cache8(k_cache, v_cache, k_scales, v_scales)
+    dt, qshape = query.dtype, query.shape
+    if out.dtype is not dt:
+        raise TypeError("dtype mismatch")
+    B, Hq, Dq = qshape
+    if Dq != D or out.shape != qshape or block_tables.dim() != 2 or block_tables.shape[0] != B or \
+            context_lens.shape != (B,):
+        raise ValueError("shape mismatch")
+    if workspace is None:
+        workspace = decode_fp8_workspace(query, Hkv, bs, max_context_len, partition_tokens, stream)
+    _call("pa_decode_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+          context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), int(partition_tokens),
+          _dt_int(dt), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _opt(d_err),
+          _raw_stream(dev, stream))
+
+
+def _lens32(prefix_lens, chunk_lens):
+    pl = np.ascontiguousarray(prefix_lens, dtype=np.int32)
+    cl = np.ascontiguousarray(chunk_lens, dtype=np.int32)
+    if pl.ndim != 1 or pl.shape != cl.shape:
+        raise ValueError("prefix_lens and chunk_lens must name the same sequences")
+    return pl, cl
+
+
+def prefill_fp8_workspace(query, k_cache, prefix_lens, chunk_lens, stream=None):
+    """A workspace big enough for ``pa_prefill_batch_fp8`` of these chunks."""
+    pl, cl = _lens32(prefix_lens, chunk_lens)
+    _, Hq, D = query.shape
+    with torch.cuda.device(query.device):
+        n = lib().pa_prefill_batch_fp8_workspace_bytes(pl.ctypes.data, cl.ctypes.data, pl.size, Hq, k_cache.shape[1], D,
+                                                       k_cache.shape[2])
+    return _scratch(query.device, n, stream)
+
+
+def pa_prefill_batch_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, prefix_lens, chunk_lens, scale,
+                         workspace=None, d_err=None, stream=None):
+    """``pa_prefill_batch`` over an 8-bit cache (as ``pa_decode_fp8``): out/query
+    [sum(chunk_lens)][Hq][D]; block_tables int32 [n][MB] on the device; prefix_lens,
+    chunk_lens: n host ints.  ``workspace`` (``prefill_fp8_workspace``) defaults to a
+    fresh one; it grows with the chunks' whole contexts."""
+    dev = _index(query)
+    _checked(dev, query, out, k_cache, v_cache, k_scales, v_scales, block_tables, workspace, d_err)
+    if block_tables.dtype is not _I32:
+        raise TypeError("block_tables must be int32")
+    NB, Hkv, bs, D = _cache8(k_cache, v_cache, k_scales, v_scales)
+    pl, cl = _lens32(prefix_lens, chunk_lens)
+    dt, n = query.dtype, pl.size
+    if out.dtype is not dt:
+        raise TypeError("dtype mismatch")
+    R, Hq, Dq = query.shape
+    if Dq != D or out.shape != query.shape or block_tables.dim() != 2 or block_tables.shape[0] != n or \
+            int(cl.sum()) != R:
+        raise ValueError("shape mismatch")
+    if workspace is None:
+        workspace = prefill_fp8_workspace(query, k_cache, pl, cl, stream)
+    _call("pa_prefill_batch_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], pl.ctypes.data,
+          cl.ctypes.data, n, Hq, Hkv, D, bs, NB, float(scale), _dt_int(dt), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _opt(d_err), _raw_stream(dev, stream))
+
+
+def pa_copy_blocks_fp8(k_cache, v_cache, k_scales, v_scales, pairs, workspace=None, d_err=None, stream=None):
+    """``pa_copy_blocks`` for an 8-bit cache: pairs int64 [n][2] of (src, dst) block
+    ids; ``workspace`` as there."""
+    dev = _index(k_cache)
+    _checked(dev, k_cache, v_cache, k_scales, v_scales, pairs, workspace, d_err)
+    if pairs.dtype is not _I64:
+        raise TypeError("pairs must be int64")
+    NB, Hkv, bs, D = _cache8(k_cache, v_cache, k_scales, v_scales)
+    if pairs.numel() and (pairs.dim() != 2 or pairs.shape[1] != 2):
+        raise ValueError("pairs must be [n][2]")
+    n = pairs.shape[0] if pairs.numel() else 0
+    if workspace is None:
+        workspace = _scratch(k_cache.device, pa_copy_blocks_workspace_bytes(n), stream)
+    _call("pa_copy_blocks_fp8", dev, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+          pairs.data_ptr(), n, Hkv, D, bs, NB, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _opt(d_err), _raw_stream(dev, stream))

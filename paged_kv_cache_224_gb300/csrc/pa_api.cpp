@@ -327,8 +327,8 @@ int pa_copy_blocks(void *k_cache, void *v_cache, const int64_t *pairs, int num_p
     if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGNMENT;
     if (!workspace || workspace_bytes < pa::copy_blocks_workspace_bytes(num_pairs)) return PA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PA_ERR_ALIGNMENT;
-    return pa::launch_copy_blocks(k_cache, v_cache, pairs, num_pairs, num_kv_heads, head_dim,
-                                  block_size, num_blocks, workspace, d_err, static_cast<cudaStream_t>(stream));
+    return pa::launch_copy_blocks(k_cache, v_cache, pairs, num_pairs, 2LL * num_kv_heads * block_size * head_dim, nullptr,
+                                  nullptr, num_kv_heads, num_blocks, workspace, d_err, static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_prefill_workspace_bytes(int num_seqs, int total_chunk_len, int num_heads, int num_kv_heads,

@@ -125,7 +125,8 @@ cow_count_kernel(CowEntry *table, unsigned int mask, const int64_t *__restrict__
 __global__ void __launch_bounds__(256)
 copy_blocks_kernel(uint4 *__restrict__ k_cache, uint4 *__restrict__ v_cache,
                    const int64_t *__restrict__ pairs, const CowEntry *__restrict__ table, unsigned int mask,
-                   long long chunks_per_block, long long chunks_per_piece, int num_blocks, int *d_err) {
+                   long long chunks_per_block, long long chunks_per_piece, int num_blocks, uint8_t *k_scales,
+                   uint8_t *v_scales, int num_kv_heads, int *d_err) {
     __shared__ int s_ok;
     const int i = blockIdx.x;
     const int64_t src = pairs[2 * i];
@@ -155,6 +156,12 @@ copy_blocks_kernel(uint4 *__restrict__ k_cache, uint4 *__restrict__ v_cache,
     const long long end = min(begin + chunks_per_piece, chunks_per_block);
     const uint4 *ks = k_cache + src * chunks_per_block;
     const uint4 *vs = v_cache + src * chunks_per_block;
+    if (k_scales && blockIdx.y == 0) {
+        for (int h = threadIdx.x; h < num_kv_heads; h += blockDim.x) {
+            k_scales[dst * num_kv_heads + h] = k_scales[src * num_kv_heads + h];
+            v_scales[dst * num_kv_heads + h] = v_scales[src * num_kv_heads + h];
+        }
+    }
     uint4 *kd = k_cache + dst * chunks_per_block;
     uint4 *vd = v_cache + dst * chunks_per_block;
     for (long long c = begin + threadIdx.x; c < end; c += blockDim.x) {
@@ -178,8 +185,8 @@ size_t copy_blocks_workspace_bytes(int num_pairs) {
     return (size_t)cow_capacity(num_pairs) * sizeof(CowEntry);
 }
 
-int launch_copy_blocks(void *k_cache, void *v_cache, const int64_t *pairs, int num_pairs,
-                       int num_kv_heads, int head_dim, int block_size, int num_blocks, void *workspace,
+int launch_copy_blocks(void *k_cache, void *v_cache, const int64_t *pairs, int num_pairs, long long block_bytes,
+                       uint8_t *k_scales, uint8_t *v_scales, int num_kv_heads, int num_blocks, void *workspace,
                        int *d_err, cudaStream_t stream) {
     if (num_pairs == 0) return PA_OK;
     const unsigned long long cap = cow_capacity(num_pairs);
@@ -189,7 +196,7 @@ int launch_copy_blocks(void *k_cache, void *v_cache, const int64_t *pairs, int n
     cow_clear_kernel<<<clear_blocks, 256, 0, stream>>>(table, (unsigned int)cap);
     const unsigned count_blocks = (unsigned)std::min<long long>(((long long)num_pairs + 255) / 256, (long long)sms * 8);
     cow_count_kernel<<<count_blocks, 256, 0, stream>>>(table, (unsigned int)(cap - 1), pairs, num_pairs, num_blocks);
-    const long long cpb = (long long)num_kv_heads * block_size * head_dim / 8;
+    const long long cpb = block_bytes / 16;
     const long long per_piece = 256 * 4;  // 4 vectors per thread per cache
     long long pieces = (cpb + per_piece - 1) / per_piece;
     if (pieces > 65535) pieces = 65535;
@@ -197,7 +204,7 @@ int launch_copy_blocks(void *k_cache, void *v_cache, const int64_t *pairs, int n
     dim3 grid((unsigned)num_pairs, (unsigned)pieces);
     copy_blocks_kernel<<<grid, 256, 0, stream>>>(static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache),
                                                  pairs, table, (unsigned int)(cap - 1), cpb, chunks_per_piece,
-                                                 num_blocks, d_err);
+                                                 num_blocks, k_scales, v_scales, num_kv_heads, d_err);
     return cudaPeekAtLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

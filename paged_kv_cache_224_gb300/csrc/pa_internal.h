@@ -148,6 +148,13 @@ struct RotaryParams {
     int num_tokens, num_heads, num_kv_heads, head_dim, rot_dim, interleaved;
     int block_size, num_blocks;
     uint8_t pair_axis[kRotaryMaxDim / 2];
+    // RMS norms of the heads before they are rotated, or null
+    const void *query_norm;      // [head_dim] dtype
+    const void *key_norm;
+    float eps;
+    // 8-bit cache: k_cache and v_cache hold codes, these their scales [NB][Hkv]
+    uint8_t *k_scales;
+    uint8_t *v_scales;
 };
 
 // One eviction (see pa_evict): the kernels mark, select and copy.
@@ -201,12 +208,41 @@ int weights_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int 
 // a row of `width` totals.  one_table: flags sequences of a row whose table rows differ.
 int launch_weights_merge(pa_dtype dt, int head_dim, int group, const DecodeParams &p, const float *weights,
                          float *weights_out, int width, int queries_per_row, bool one_table, cudaStream_t stream);
+// Decode over an 8-bit cache, with the merge of the partials.
+struct Fp8DecodeParams {
+    DecodeParams d;
+    const uint8_t *k_scales;     // [NB][Hkv]
+    const uint8_t *v_scales;
+};
+int launch_decode_fp8(pa_dtype dt, int head_dim, int block_size, int group, const Fp8DecodeParams &p,
+                      cudaStream_t stream);
+int fp8_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                         int max_context_len);
+// The codes of the sequences' first blocks as values of dt, laid end to end: block
+// j of sequence i becomes block first[i] + j of k_out and v_out, whose own table is
+// `table` (the number itself, or -1 where the sequence's entry is outside the pool,
+// which is flagged).  Also clears num_zero words at zero.
+struct Fp8ExpandParams {
+    const uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
+    void *k_out, *v_out;
+    int32_t *table;
+    unsigned *zero;
+    int *d_err;
+    int num_zero, num_seqs, num_kv_heads, head_dim, block_size, num_blocks;
+    const int32_t *tables[kPrefillMaxSeqs];
+    int first[kPrefillMaxSeqs + 1];
+};
+int launch_expand_fp8(pa_dtype dt, const Fp8ExpandParams &p, cudaStream_t stream);
 // Log-sum-exp merge of the partials in p's workspace into p.out.
 int launch_decode_reduce(pa_dtype dt, int head_dim, const DecodeParams &p, cudaStream_t stream);
 int launch_reshape_and_cache(const void *key, const void *value, void *k_cache, void *v_cache,
                              const int64_t *slots, int num_tokens, int num_kv_heads, int head_dim,
                              int block_size, int num_blocks, int *d_err, cudaStream_t stream);
 int launch_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream);
+// Keys (normed and rotated as p says) and values into an 8-bit cache, then the
+// queries as launch_rotary does; block_size up to kStoreMaxBlock.
+constexpr int kStoreMaxBlock = 128;
+int launch_store_fp8(pa_dtype dt, const RotaryParams &p, cudaStream_t stream);
 int launch_evict(const EvictParams &p, cudaStream_t stream);
 // Copies of up to kGatherMax buffers in one launch, each from memory the
 // device can address (pinned host memory through its device view included)
@@ -221,12 +257,16 @@ struct GatherList {
 };
 int launch_gather(const GatherList &list, cudaStream_t stream);
 size_t copy_blocks_workspace_bytes(int num_pairs);
-int launch_copy_blocks(void *k_cache, void *v_cache, const int64_t *pairs, int num_pairs,
-                       int num_kv_heads, int head_dim, int block_size, int num_blocks, void *workspace,
+// Copies of whole blocks of block_bytes (a multiple of 16) in either cache; with
+// k_scales and v_scales, also of num_kv_heads scale bytes in either.
+int launch_copy_blocks(void *k_cache, void *v_cache, const int64_t *pairs, int num_pairs, long long block_bytes,
+                       uint8_t *k_scales, uint8_t *v_scales, int num_kv_heads, int num_blocks, void *workspace,
                        int *d_err, cudaStream_t stream);
 // Workspace for the stream-K prefill schedule (an upper bound for any batch of
 // num_seqs chunks totalling total_chunk_len rows).
 size_t prefill_workspace_bytes(int num_seqs, long long total_chunk_len, int group, int num_kv_heads);
+// Where its counters begin (the same on every call); they reach to its end.
+size_t prefill_counters_offset();
 // workspace may be NULL (or too small): each CTA then computes one whole unit.
 int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const PrefillParams &p,
                    void *workspace, size_t workspace_bytes, cudaStream_t stream);

@@ -60,6 +60,8 @@ size_t prefill_workspace_bytes(int num_seqs, long long total_chunk_len, int grou
     return prefill_ws(sm_count(), units).total();
 }
 
+size_t prefill_counters_offset() { return prefill_ws(sm_count(), 1).cnt_off(); }
+
 int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const PrefillParams &p_in,
                    void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (head_dim != kD) return PA_ERR_UNSUPPORTED;

@@ -33,17 +33,10 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_rotary.cuh"
 
 namespace pa {
 namespace {
-
-__device__ __forceinline__ uint4 ldg_stream(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 
 // A token's kv head 0 row: element offset in the caches, or -1 for none.
 __device__ __forceinline__ long long cache_row(const RotaryParams &p, long long slot) {
@@ -57,30 +50,14 @@ __device__ __forceinline__ long long cache_row(const RotaryParams &p, long long 
     return (blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size)) * p.head_dim;
 }
 
-// f / (2 pi) modulo 1, in 2^-64, to half a unit, for finite f.  With f = m 2^e
-// (m of 24 bits) only the bits of 1 / (2 pi) from e places after the binary point
-// on count modulo 1, and 96 of them are enough (Payne and Hanek's reduction,
-// 1983): three 32-bit products, no fp64.
-__device__ __forceinline__ long long turn_fraction(float f) {
-    // 160 zeros, for e < 0, and 1 / (2 pi) to 224 bits
-    static constexpr unsigned kBits[12] = {0u, 0u, 0u, 0u, 0u, 0x28be60dbu, 0x9391054au, 0x7f09d5f4u, 0x7d4d3770u,
-                                           0x36d8a566u, 0x4f10e410u, 0x7f9458eau};
-    const unsigned u = __float_as_uint(f), ex = u >> 23 & 255u;
-    const unsigned m = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
-    const int at = (int)min(max(ex, 1u), 254u) - 150 + 160;  // the first bit that counts, 11 .. 264
-    const int k = at >> 5, s = at & 31;
-    const unsigned w0 = kBits[k], w1 = kBits[k + 1], w2 = kBits[k + 2], w3 = kBits[k + 3];
-    const unsigned hi = __funnelshift_l(w1, w0, s), mid = __funnelshift_l(w2, w1, s), lo = __funnelshift_l(w3, w2, s);
-    const unsigned long long low = (unsigned long long)m * lo;
-    const unsigned long long frac = ((unsigned long long)(m * hi) << 32) + (unsigned long long)m * mid + (low >> 32) +
-                                    (low >> 31 & 1u);
-    return (long long)((u >> 31) ? 0ull - frac : frac);
-}
-
 constexpr int kMaxThreads = 320;
 
-template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
+// kNorm: queries and keys are first divided by their head's root mean square and
+// multiplied by its weights, in fp32 like the rotation that follows, one rounding
+// for both.  A head's units then sit in `lanes` adjacent lanes (a power of two,
+// the last of them idle where a head has fewer units), which add up their squares.
+template <typename T, bool kInterleaved, bool kNorm>
+__global__ void __launch_bounds__(kMaxThreads, kNorm ? 3 : 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
     // [2 tokens]: cosines of pairs 8c .. 8c+3, 8c+4 .. 8c+7, then the sines
     // alike, [4][unit c], so that a warp's reads are consecutive
     __shared__ float4 s_cs[2][4][kRotaryMaxDim / 16];
@@ -88,14 +65,22 @@ __global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_con
     const int tid = threadIdx.x;
     const int upr = p.head_dim / 16;  // units of a head; the first rot_dim / 16 are turned
     const int half = p.rot_dim / 2;
-    const int c = tid % upr;
-    const int row0 = tid / upr, rows_step = blockDim.x / upr;
+    const int lanes = kNorm ? norm_lanes(upr) : upr;
+    const int c = tid % lanes;
+    const int row0 = tid / lanes, rows_step = blockDim.x / lanes;
     const int rows_qk = p.num_heads + p.num_kv_heads, rows = rows_qk + p.num_kv_heads;
     const bool turned = c < p.rot_dim / 16;
     // element offsets of the unit's two vectors inside a head (the values' too: e0 and e1 cover the row either way)
     const int e0 = turned && !kInterleaved ? c * 8 : c * 16;
     const int e1 = turned && !kInterleaved ? half + c * 8 : e0 + 8;
-    const bool active = row0 < rows_step;  // threads past the last whole row of units move nothing
+    // threads past the last whole row of units, and lanes past a head's units, move nothing
+    const bool active = row0 < rows_step && (!kNorm || c < upr);
+
+    // kNorm: the weights of queries and of keys, and the lanes of this thread's head
+    __shared__ float4 s_w[kNorm ? 2 : 1][kNorm ? kRotaryMaxDim / 4 : 1];
+    const unsigned mates = (lanes < 32 ? (1u << lanes) - 1u : kFull) << ((tid & 31) & ~(lanes - 1) & 31);
+
+    const float per_dim = 1.f / (float)p.head_dim;
 
     pdl_wait();
     pdl_trigger();  // what follows may be placed; it waits for these writes
@@ -113,10 +98,8 @@ __global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_con
     if (mine < half) frac = turns_of(mine, finite);
     if (mine + (int)blockDim.x < half) frac2 = turns_of(mine + blockDim.x, finite2);
     auto angle = [&](int i, long long fr, bool ok, int pos, int buf) {
-        const unsigned long long ang = (unsigned long long)fr * (unsigned long long)(long long)pos;
-        const int top = (int)(unsigned)((ang + 0x80000000ull) >> 32);
         float sn, cs;
-        sincospif((float)top * 4.656612873077393e-10f, &sn, &cs);  // top * 2^-31 half turns
+        turn_sincos(fr, pos, sn, cs);
         if (!ok) sn = cs = __int_as_float(0x7fc00000);
         float *q = reinterpret_cast<float *>(s_cs[buf]);
         constexpr int plane = kRotaryMaxDim / 16 * 4;
@@ -145,11 +128,18 @@ __global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_con
         va = ldg_stream(s + e0);
         vb = ldg_stream(s + e1);
     }
+    if constexpr (kNorm) {
+        for (int i = tid; i < 2 * p.head_dim; i += blockDim.x) {
+            const bool of_key = i >= p.head_dim;
+            const int d = i - (of_key ? p.head_dim : 0);
+            reinterpret_cast<float *>(s_w[of_key])[d] = to_float(static_cast<const T *>(of_key ? p.key_norm : p.query_norm)[d]);
+        }
+    }
     prepare(t, 0);
     __syncthreads();
     for (; t < p.num_tokens; t += gridDim.x, buf ^= 1) {
         const int t_next = t + gridDim.x;
-        if (active) {
+        if (active || kNorm) {
             const long long dst = s_dst[buf];
             float cs[8], sn[8];
             if (turned) {
@@ -164,16 +154,34 @@ __global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_con
                 // the next unit's vectors, of this token or the next
                 const bool more = row + rows_step < rows;
                 uint4 na = va, nb = vb;
-                if (more || t_next < p.num_tokens) {
+                if (active && (more || t_next < p.num_tokens)) {
                     const T *s = more ? src_of(t, row + rows_step) : src_of(t_next, row0);
                     na = ldg_stream(s + e0);
                     nb = ldg_stream(s + e1);
                 }
-                if (turned && row < rows_qk) {
+                if ((turned || kNorm) && row < rows_qk) {
                     float a[8], b[8];
                     unpack8<T>(va, a);
                     unpack8<T>(vb, b);
-                    if (kInterleaved) {
+                    if constexpr (kNorm) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) sum = fmaf(a[k], a[k], fmaf(b[k], b[k], sum));
+                        for (int m = lanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(mates, sum, m);
+                        const float r = __frsqrt_rn(fmaf(sum, per_dim, p.eps));
+                        const float *w = reinterpret_cast<const float *>(s_w[row >= p.num_heads]);
+                        if (active) {
+#pragma unroll
+                            for (int k = 0; k < 8; k += 4) {
+                                const float4 x = *reinterpret_cast<const float4 *>(w + e0 + k);
+                                const float4 y = *reinterpret_cast<const float4 *>(w + e1 + k);
+                                a[k] *= r * x.x, a[k + 1] *= r * x.y, a[k + 2] *= r * x.z, a[k + 3] *= r * x.w;
+                                b[k] *= r * y.x, b[k + 1] *= r * y.y, b[k + 2] *= r * y.z, b[k + 3] *= r * y.w;
+                            }
+                        }
+                    }
+                    if (kNorm && !turned) {
+                    } else if (kInterleaved) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float x = a[2 * k], y = a[2 * k + 1], z = b[2 * k], w = b[2 * k + 1];
@@ -194,7 +202,8 @@ __global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_con
                     vb = pack8<T>(b);
                 }
                 T *out = nullptr;
-                if (row < p.num_heads) {
+                if (kNorm && !active) {
+                } else if (row < p.num_heads) {
                     out = static_cast<T *>(p.query_out) + t * p.query_out_stride + row * p.head_dim;
                 } else if (dst >= 0) {
                     const bool is_v = row >= rows_qk;
@@ -214,9 +223,9 @@ __global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_con
     }
 }
 
-template <typename T, bool kInterleaved>
+template <typename T, bool kInterleaved, bool kNorm>
 int launch_t(const RotaryParams &p, int threads, cudaStream_t stream) {
-    auto kern = rotary_kernel<T, kInterleaved>;
+    auto kern = rotary_kernel<T, kInterleaved, kNorm>;
     static std::atomic<int> resident[kMaxThreads / 32 + 1];  // CTAs an SM holds, by block size; asked for once
     int n = resident[threads / 32].load(std::memory_order_relaxed);
     if (n == 0) {
@@ -232,12 +241,15 @@ int launch_t(const RotaryParams &p, int threads, cudaStream_t stream) {
 int launch_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream) {
     // A token's units take one pass of up to kMaxThreads threads; the grid
     // is one wave of resident CTAs, which walk the tokens.
-    const int units = (p.num_heads + 2 * p.num_kv_heads) * (p.head_dim / 16);
+    const bool norm = p.query_norm != nullptr;
+    const int upr = p.head_dim / 16;
+    const int units = (p.num_heads + 2 * p.num_kv_heads) * (norm ? norm_lanes(upr) : upr);
     const int passes = (units + kMaxThreads - 1) / kMaxThreads;
     const int threads = std::max(64, ((units + passes - 1) / passes + 31) / 32 * 32);
-    if (dt == PA_BF16) return p.interleaved ? launch_t<__nv_bfloat16, true>(p, threads, stream)
-                                             : launch_t<__nv_bfloat16, false>(p, threads, stream);
-    return p.interleaved ? launch_t<__half, true>(p, threads, stream) : launch_t<__half, false>(p, threads, stream);
+#define PA_ROTARY(TT, II) (norm ? launch_t<TT, II, true>(p, threads, stream) : launch_t<TT, II, false>(p, threads, stream))
+    if (dt == PA_BF16) return p.interleaved ? PA_ROTARY(__nv_bfloat16, true) : PA_ROTARY(__nv_bfloat16, false);
+    return p.interleaved ? PA_ROTARY(__half, true) : PA_ROTARY(__half, false);
+#undef PA_ROTARY
 }
 
 }  // namespace pa
