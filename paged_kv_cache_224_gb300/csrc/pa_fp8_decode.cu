@@ -180,9 +180,11 @@ int fp8_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int head
 
 int launch_decode_fp8(pa_dtype dt, int head_dim, int block_size, int group, const Fp8DecodeParams &p,
                       cudaStream_t stream) {
-    (void)block_size;
-    cudaError_t e;
-    if (dt == PA_BF16) e = head_dim == 128 ? decode_d<__nv_bfloat16, 128>(group, p, stream) : decode_d<__nv_bfloat16, 64>(group, p, stream);
+    int rc = head_dim == 128 ? launch_decode_fp8_tc(dt, block_size, group, p, stream) : PA_ERR_UNSUPPORTED;
+    if (rc != PA_OK && rc != PA_ERR_UNSUPPORTED) return rc;
+    cudaError_t e = cudaSuccess;
+    if (rc == PA_OK) ;
+    else if (dt == PA_BF16) e = head_dim == 128 ? decode_d<__nv_bfloat16, 128>(group, p, stream) : decode_d<__nv_bfloat16, 64>(group, p, stream);
     else e = head_dim == 128 ? decode_d<__half, 128>(group, p, stream) : decode_d<__half, 64>(group, p, stream);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     if (p.d.max_partitions == 1) return PA_OK;

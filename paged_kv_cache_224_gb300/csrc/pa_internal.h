@@ -216,6 +216,9 @@ struct Fp8DecodeParams {
 };
 int launch_decode_fp8(pa_dtype dt, int head_dim, int block_size, int group, const Fp8DecodeParams &p,
                       cudaStream_t stream);
+// The same on the tensor cores at head_dim 128, without the merge; PA_ERR_UNSUPPORTED
+// where a tensor map does not reach.
+int launch_decode_fp8_tc(pa_dtype dt, int block_size, int group, const Fp8DecodeParams &p, cudaStream_t stream);
 int fp8_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                          int max_context_len);
 // The codes of the sequences' first blocks as values of dt, laid end to end: block
