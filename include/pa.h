@@ -554,21 +554,27 @@ PA_API int pa_rotary_and_cache_fp8(void *query_out, int64_t query_out_stride, co
 
 /*
  * pa_decode_fp8 -- pa_decode over an 8-bit cache: softmax(scale * q . k) v with the
- * cached values as above, sums in fp32, the output rounded once to dtype.
- * Arguments, shapes, partition_tokens and data errors as for pa_decode (invalid table
- * entries are flagged and the keys they would supply are left out).
+ * cached values as above, sums in fp32, the output rounded once to dtype.  On the
+ * tensor cores for all shapes: scores are exact up to fp32 sums, a softmax weight
+ * enters the weighted sum with 12 bits, down to 2^-33 of the largest.  A query with an
+ * infinity or NaN gives NaN.
+ * Arguments, shapes and data errors as for pa_decode (invalid table entries are flagged
+ * and the keys they would supply are left out), without partition_tokens: contexts are
+ * cut where that shares the batch out evenly, so that a row's last bits depend on the
+ * batch that it is in.  The same call gives the same bits.
  *   workspace      >= pa_decode_fp8_workspace_bytes(...) bytes, 256-byte aligned,
- *                  scratch (may be NULL when that is 0)
- * max_blocks_per_seq * block_size must stay below 2^31 - 256.
+ *                  scratch (may be NULL when that is 0); its size depends on the device
+ * max_blocks_per_seq * block_size, num_seqs * num_heads and num_blocks * num_kv_heads *
+ * block_size must stay below 2^31 - 256.
  */
 PA_API size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                                            int block_size, int max_context_len, int partition_tokens);
+                                            int block_size, int max_context_len);
 PA_API int pa_decode_fp8(void *out, const void *query, const uint8_t *k_cache, const uint8_t *v_cache,
                          const uint8_t *k_scales, const uint8_t *v_scales, const int32_t *block_tables,
                          int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
                          int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_context_len,
-                         float scale, int partition_tokens, pa_dtype dtype, void *workspace, size_t workspace_bytes,
-                         int *d_err, void *stream);
+                         float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes, int *d_err,
+                         void *stream);
 
 /*
  * pa_prefill_batch_fp8 -- pa_prefill_batch over an 8-bit cache: causal attention of

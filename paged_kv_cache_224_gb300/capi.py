@@ -146,9 +146,9 @@ def lib() -> ctypes.CDLL:
         L.pa_reshape_and_cache_fp8.restype = i
         L.pa_rotary_and_cache_fp8.argtypes = [p, i64, p, i64, p, i64, p, i64] + [p] * 8 + [i, i, i, p, p, f] + [i] * 7 + [p, p]
         L.pa_rotary_and_cache_fp8.restype = i
-        L.pa_decode_fp8_workspace_bytes.argtypes = [i] * 7
+        L.pa_decode_fp8_workspace_bytes.argtypes = [i] * 6
         L.pa_decode_fp8_workspace_bytes.restype = sz
-        L.pa_decode_fp8.argtypes = [p] * 7 + [i, p] + [i] * 7 + [f, i, i, p, sz, p, p]
+        L.pa_decode_fp8.argtypes = [p] * 7 + [i, p] + [i] * 7 + [f, i, p, sz, p, p]
         L.pa_decode_fp8.restype = i
         L.pa_prefill_batch_fp8_workspace_bytes.argtypes = [p, p] + [i] * 5
         L.pa_prefill_batch_fp8_workspace_bytes.restype = sz
@@ -893,23 +893,21 @@ def pa_rotary_and_cache_fp8(query_out, query, key, value, k_cache, v_cache, k_sc
           v_scales.data_ptr(), *rest, _opt(d_err), _raw_stream(dev, stream))
 
 
-def pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
-                                  partition_tokens=0) -> int:
-    return lib().pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
-                                               partition_tokens)
+def pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len) -> int:
+    return lib().pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len)
 
 
-def decode_fp8_workspace(query, num_kv_heads, block_size, max_context_len, partition_tokens=0, stream=None):
+def decode_fp8_workspace(query, num_kv_heads, block_size, max_context_len, stream=None):
     """Allocate (with torch) a workspace big enough for ``pa_decode_fp8`` on ``stream``
     (None: the current one)."""
     B, Hq, D = query.shape
     with torch.cuda.device(query.device):
-        n = pa_decode_fp8_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len, partition_tokens)
+        n = pa_decode_fp8_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len)
     return _scratch(query.device, n, stream)
 
 
 def pa_decode_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, max_context_len,
-                  partition_tokens=0, workspace=None, d_err=None, stream=None):
+                  workspace=None, d_err=None, stream=None):
     """``pa_decode`` over an 8-bit cache: out/query [B][Hq][D]; caches float8_e4m3fn
     [NB][Hkv][bs][D] with scales float8_e8m0fnu (or uint8) [NB][Hkv]; block_tables
     int32 [B][MB]; context_lens int32 [B].  ``workspace`` defaults to a fresh one."""
@@ -926,12 +924,11 @@ def pa_decode_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables
             context_lens.shape != (B,):
         raise ValueError("shape mismatch")
     if workspace is None:
-        workspace = decode_fp8_workspace(query, Hkv, bs, max_context_len, partition_tokens, stream)
+        workspace = decode_fp8_workspace(query, Hkv, bs, max_context_len, stream)
     _call("pa_decode_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-          context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), int(partition_tokens),
-          _dt_int(dt), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _opt(d_err),
-          _raw_stream(dev, stream))
+          context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), _dt_int(dt),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _opt(d_err), _raw_stream(dev, stream))
 
 
 def _lens32(prefix_lens, chunk_lens):

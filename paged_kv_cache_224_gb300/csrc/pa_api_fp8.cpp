@@ -86,29 +86,20 @@ int store_fp8(pa::RotaryParams &p, uint8_t *k_scales, uint8_t *v_scales, pa_dtyp
     return pa::launch_store_fp8(dtype, p, static_cast<cudaStream_t>(stream));
 }
 
-// Partition length of the decode, 0 for a bad one, and the partials' workspace.
+// The decode's workspace: what each (sequence, kv head) was cut into, the partials'
+// accumulators and (max, sum) pairs.  None where every context is a single tile.
 struct DecodeWs {
-    int pt, slots;
-    size_t acc = 0, ml = 0;
-    DecodeWs(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
-             int partition_tokens) {
-        pt = 0;
-        if (partition_tokens < 0 || partition_tokens % block_size) return;
-        const int longest = std::max(max_context_len, 1);
-        if (partition_tokens) {
-            // at most what holds the longest length: the kernels add a length to it in 32 bits
-            const long long whole = ((long long)longest + block_size - 1) / block_size * block_size;
-            pt = (int)std::min<long long>(partition_tokens, whole);
-        } else {
-            pt = pa::fp8_partition_tokens(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len);
-        }
-        slots = (int)(((long long)longest + pt - 1) / pt);
-        if (slots == 1) return;
-        const size_t n = (size_t)num_seqs * num_heads * slots;
+    int ctas;
+    size_t units = 0, acc = 0, ml = 0;
+    DecodeWs(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_context_len) {
+        ctas = pa::fp8_decode_ctas(num_seqs, num_kv_heads, max_context_len);
+        if (max_context_len <= 128) return;
+        const size_t n = (size_t)2 * ctas * (num_heads / num_kv_heads);
+        units = round256((size_t)num_seqs * num_kv_heads * 2 * sizeof(int));
         acc = round256(n * head_dim * sizeof(float));
         ml = round256(n * 2 * sizeof(float));
     }
-    size_t total() const { return acc + ml; }
+    size_t total() const { return units + acc + ml; }
 };
 
 // The prefill's own workspace for a launch of up to kPrefillMaxSeqs chunks, then the
@@ -202,18 +193,17 @@ int pa_reshape_and_cache_fp8(const void *key, const void *value, uint8_t *k_cach
 }
 
 size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                                     int max_context_len, int partition_tokens) {
+                                     int max_context_len) {
     if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
-        block_size <= 0 || max_context_len < 0)
+        !good_block(block_size) || max_context_len < 0)
         return 0;
-    const DecodeWs w(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_tokens);
-    return w.pt > 0 ? w.total() : 0;
+    return DecodeWs(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len).total();
 }
 
 int pa_decode_fp8(void *out, const void *query, const uint8_t *k_cache, const uint8_t *v_cache, const uint8_t *k_scales,
                   const uint8_t *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
                   const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                  int num_blocks, int max_context_len, float scale, int partition_tokens, pa_dtype dtype, void *workspace,
+                  int num_blocks, int max_context_len, float scale, pa_dtype dtype, void *workspace,
                   size_t workspace_bytes, int *d_err, void *stream) {
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 ||
         max_blocks_per_seq <= 0 || max_context_len < 0 || !good_dtype(dtype))
@@ -225,10 +215,12 @@ int pa_decode_fp8(void *out, const void *query, const uint8_t *k_cache, const ui
         return PA_ERR_INVALID_ARG;
     const int group = num_heads / num_kv_heads;
     if ((head_dim != 64 && head_dim != 128) || !good_block(block_size) || !good_group(group)) return PA_ERR_UNSUPPORTED;
-    if ((long long)max_blocks_per_seq * block_size > 0x7fffff00LL) return PA_ERR_UNSUPPORTED;
+    // tokens of a table, rows of a pool (TMA coordinates) and query heads are counted in 32 bits
+    if ((long long)max_blocks_per_seq * block_size > 0x7fffff00LL || (long long)num_seqs * num_heads > 0x7fffff00LL ||
+        (long long)num_blocks * num_kv_heads > 0x7fffff00LL / block_size)
+        return PA_ERR_UNSUPPORTED;
     if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGNMENT;
-    const DecodeWs w(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_tokens);
-    if (w.pt <= 0) return PA_ERR_OUT_OF_RANGE;
+    const DecodeWs w(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len);
     if (w.total() > 0) {
         if (!workspace || workspace_bytes < w.total()) return PA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return PA_ERR_ALIGNMENT;
@@ -249,18 +241,20 @@ int pa_decode_fp8(void *out, const void *query, const uint8_t *k_cache, const ui
     d.num_blocks = num_blocks;
     d.max_context_len = max_context_len;
     d.block_size = block_size;
-    d.partition_tokens = w.pt;
-    d.max_partitions = w.slots;
     d.scale_log2 = scale * 1.4426950408889634f;
     d.grp_size = 1;
     d.grp_inner = group;
     d.table_stride = max_blocks_per_seq;
-    d.slots = w.slots;
-    d.ws_acc = static_cast<float *>(workspace);
-    d.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + w.acc);
+    if (w.total() > 0) {
+        char *base = static_cast<char *>(workspace);
+        p.units = reinterpret_cast<int2 *>(base);
+        d.ws_acc = reinterpret_cast<float *>(base + w.units);
+        d.ws_ml = reinterpret_cast<float2 *>(base + w.units + w.acc);
+    }
+    p.ctas = w.ctas;
     p.k_scales = k_scales;
     p.v_scales = v_scales;
-    return pa::launch_decode_fp8(dtype, head_dim, block_size, group, p, static_cast<cudaStream_t>(stream));
+    return pa::launch_decode_fp8(dtype, head_dim, group, p, static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_prefill_batch_fp8_workspace_bytes(const int *prefix_lens, const int *chunk_lens, int num_seqs, int num_heads,

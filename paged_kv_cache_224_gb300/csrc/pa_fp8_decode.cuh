@@ -1,0 +1,776 @@
+// Device code of the decode over an 8-bit cache; see pa_fp8_decode.cu for the design.
+#pragma once
+
+#include <cuda.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "pa_fp8.cuh"
+#include "pa_internal.h"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace d8 {
+
+constexpr int kKeys = 128;               // keys per tile (M of the QK^T MMA)
+constexpr int kThreads = 224;            // producer, MMA issuer, four softmax warps, scales
+constexpr int kScaleRing = 8;            // tiles whose blocks' scales are held
+constexpr int kLens = 256;               // context lengths held from the first sequence on
+constexpr float kRescale = 8.0f;         // log2 units a maximum may lag behind
+constexpr float kLift = 7.0f;            // weights are 2^(z - M + kLift), at most 2^15
+constexpr int kQPieces = 3, kPPieces = 4;
+
+// G heads of a kv head take GP rows a piece; N is the four pieces' rows.  At
+// head_dim 64 a 128-byte row of V holds two keys: O^T has the sums over the even
+// keys in its first 64 rows and over the odd ones in the others, each of them right in
+// that half of the columns whose weights are its keys'.
+template <int D, int G>
+struct Lay {
+    static constexpr int kPar = 128 / D;                    // keys in a 128-byte row of V
+    static constexpr int GP = G <= 4 ? 4 : 8;
+    static constexpr int N = 4 * GP, NO = N * kPar;         // columns of S^T and of O^T
+    static constexpr uint32_t kCols = 2 * N + NO <= 64 ? 64 : 128;  // TMEM: S^T x 2 buffers, O^T
+    static constexpr uint32_t kColO = 2 * N;
+    static constexpr int kSlot = kKeys * D;                 // one K or V tile
+    static constexpr int S = D == 128 ? 6 : 12;             // ring slots: 96 KB, two CTAs to an SM
+    static constexpr int kRowP = kKeys / kPar;              // bytes of a row of P^T: a tile's keys of one parity
+    static constexpr int kOffQ = S * kSlot;                 // [N][D]
+    static constexpr int kOffP = kOffQ + N * D;             // 2 x [NO][kRowP]
+    static constexpr int kP = NO * kRowP;
+    static constexpr int kOffSc = kOffP + 2 * kP;           // [kScaleRing][16 blocks] of float4
+    static constexpr int kOffBar = kOffSc + kScaleRing * 16 * 16;
+    static constexpr int kBars = 2 * S + 7 + 2 * kScaleRing;
+    static constexpr int kOffLen = kOffBar + (kBars * 8 + 8 + 15) / 16 * 16;
+    static constexpr int kOffXch = kOffLen + kLens * 4 + 64;  // [2][4 warps][GP] maxima, [4][GP] sums, [GP] query scales, [G][64] sums of odd keys
+    static constexpr int kUsed = kOffXch + (2 * 4 * GP + 4 * GP + GP + (kPar == 2 ? G * 64 : 0)) * 4;
+    static constexpr int kAlloc = kUsed + 1024;             // room to align the base to 1 KB
+};
+
+// kind::f8f6f4, fp32 accumulator: A e4m3, B e4m3 or e5m2.
+__host__ __device__ constexpr uint32_t instr_desc8(bool b_e5m2, bool a_mn_major, int m, int n) {
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+// As desc_hi, for 64-byte swizzling (value 4 at bit 61).
+__host__ __device__ constexpr uint32_t desc_hi64(uint32_t sbo) { return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (4u << 29); }
+
+__device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// 2-D tensor copy global -> shared of the box at (0, row), completing bytes on `bar`.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int row, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void sts8(uint32_t addr, unsigned v) {
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, unsigned a, unsigned b) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// Byte `at` of row `row` in rows of W bytes, swizzled over W bytes (W = 64 or 128).
+template <int W>
+__device__ __forceinline__ uint32_t swizzled(int row, int at) {
+    const int x = W == 128 ? row & 7 : (row >> 1) & 3;
+    return row * W + ((((at >> 4) ^ x) << 4) | (at & 15));
+}
+
+// Two values as e5m2 codes, and what those stand for: e5m2 is the upper byte of an fp16.
+__device__ __forceinline__ unsigned e5m2x2(float a, float b) {
+    return (unsigned)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ float2 from_e5m2x2(unsigned two) {
+    const unsigned w = __byte_perm(two, 0u, 0x1404);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// Reduce G values of every lane across the warp; lane l ends with the result for
+// value l / (32 / G).
+template <bool kMax, int G>
+__device__ __forceinline__ float warp_scatter(const float (&v)[G], int lane) {
+    auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+    float a[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) a[i] = v[i];
+    int m = 16;
+#pragma unroll
+    for (int n = G; n > 1; n >>= 1, m >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int k = 0; k < n / 2; ++k) {
+            const float keep = up ? a[k + n / 2] : a[k], send = up ? a[k] : a[k + n / 2];
+            a[k] = op(keep, __shfl_xor_sync(kFull, send, m));
+        }
+    }
+#pragma unroll
+    for (; m > 0; m >>= 1) a[0] = op(a[0], __shfl_xor_sync(kFull, a[0], m));
+    return a[0];
+}
+
+// The call's `total` key tiles lie end to end, sequence by sequence and kv head by kv
+// head; CTA c of n (n <= total, so that each has one) has those from share(c) to
+// share(c + 1), and owner(t) is the CTA that has tile t.
+__device__ __forceinline__ long long share(long long total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int owner(long long total, int n, long long t) { return (int)(((t + 1) * n - 1) / total); }
+
+// A CTA's tiles of one (sequence, kv head).  `slot`: where its partial goes, -1 if it
+// is the whole; a CTA's first piece has slot 2c, a last one that is not its first 2c + 1.
+struct Piece {
+    int s, kvh;
+    int tile, n;      // first tile within the sequence, tiles
+    int ntok;         // tokens from the first tile on
+    int slot;
+    int pieces;       // of the (sequence, kv head), known to the first of them
+};
+
+// Walks a CTA's pieces; every role of the CTA has one and sees the same.
+struct Walk {
+    long long at, end, total;  // the next tile of the call, the CTA's end, all tiles
+    int ctas;                  // CTAs that have tiles
+    int s, kvh, tile, len;
+    int s0;                    // sequence whose length is lens[0]
+    bool first;
+};
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kKeys - 1) / kKeys; }
+
+__device__ __forceinline__ int clamped_len(const DecodeParams &p, int s) {
+    const int cap = min(p.max_context_len, p.max_blocks_per_seq * p.block_size);
+    return min(max(p.context_lens[s], 0), cap);
+}
+
+__device__ __forceinline__ bool next_piece(const DecodeParams &p, const int *lens, Walk &w, Piece &q) {
+    if (w.at >= w.end) return false;
+    while (w.len == 0) {  // (tiles are left, so a sequence with some follows)
+        ++w.s;
+        w.len = w.s - w.s0 < kLens ? lens[w.s - w.s0] : clamped_len(p, w.s);
+        w.kvh = w.tile = 0;
+    }
+    const int whole = tiles_of(w.len);
+    q.s = w.s;
+    q.kvh = w.kvh;
+    q.tile = w.tile;
+    q.n = (int)min((long long)(whole - w.tile), w.end - w.at);
+    q.ntok = min(w.len - w.tile * kKeys, q.n * kKeys);
+    q.slot = q.n == whole ? -1 : 2 * (int)blockIdx.x + (w.first ? 0 : 1);
+    q.pieces = q.n == whole || w.tile > 0 ? 1 : owner(w.total, w.ctas, w.at + whole - 1) - (int)blockIdx.x + 1;
+    w.first = false;
+    w.at += q.n;
+    w.tile += q.n;
+    if (w.tile == whole) {
+        w.tile = 0;
+        if (++w.kvh == p.num_kv_heads) {
+            w.kvh = 0;
+            w.len = 0;
+        }
+    }
+    return true;
+}
+
+// The walk's start, by all threads: a scan of the sequences' tiles, the CTA's share of
+// them, and the sequence that it begins in.  Sequences without tokens get their zeros here.
+template <typename T>
+__device__ __forceinline__ Walk begin(const Fp8DecodeParams &fp, int head_dim, int *lens, long long *scan) {
+    const DecodeParams &p = fp.d;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int a = min(tid * per, p.num_seqs), b = min(a + per, p.num_seqs);
+    long long mine = 0;
+    for (int s = a; s < b; ++s) {
+        const int len = clamped_len(p, s);
+        if (blockIdx.x == 0 && len != p.context_lens[s]) flag_error(p.d_err, PA_DEVERR_CONTEXT_RANGE);
+        mine += tiles_of(len);
+    }
+    long long upto = mine;  // inclusive
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(kFull, upto, m);
+        if (lane >= m) upto += o;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    long long before = upto - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const long long x = scan[w];
+        if (w < warp) before += x;
+        total += x;
+    }
+    __syncthreads();
+    total *= p.num_kv_heads;
+    Walk w;
+    w.total = total;
+    w.ctas = (int)min((long long)gridDim.x, total);
+    const bool has = (int)blockIdx.x < w.ctas;
+    const long long t0 = w.at = has ? share(total, w.ctas, blockIdx.x) : 0;
+    w.end = has ? share(total, w.ctas, blockIdx.x + 1) : 0;
+    int *start = reinterpret_cast<int *>(scan);  // sequence, kv head, tile
+    if (has && t0 >= before * p.num_kv_heads && t0 < (before + mine) * p.num_kv_heads) {
+        for (int s = a; s < b; ++s) {
+            const int n = tiles_of(clamped_len(p, s));
+            if (t0 < (before + n) * p.num_kv_heads) {
+                const long long rest = t0 - before * p.num_kv_heads;
+                start[0] = s;
+                start[1] = (int)(rest / n);
+                start[2] = (int)(rest % n);
+                break;
+            }
+            before += n;
+        }
+    }
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+        if (clamped_len(p, s) > 0) continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (size_t)s * p.num_heads * head_dim);
+        for (int i = tid; i < p.num_heads * head_dim / 8; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
+        if (fp.units)
+            for (int i = tid; i < p.num_kv_heads; i += kThreads) fp.units[(size_t)s * p.num_kv_heads + i] = make_int2(-1, 1);
+    }
+    __syncthreads();
+    w.first = true;
+    w.s = w.s0 = has ? start[0] : 0;
+    w.kvh = has ? start[1] : 0;
+    w.tile = has ? start[2] : 0;
+    if (has)
+        for (int i = tid; i < kLens && w.s0 + i < p.num_seqs; i += kThreads) lens[i] = clamped_len(p, w.s0 + i);
+    __syncthreads();
+    w.len = has ? lens[0] : 0;
+    return w;
+}
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams fp, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv) {
+    using L = Lay<D, G>;
+    constexpr int S = L::S, GP = L::GP, N = L::N, NO = L::NO;
+    const DecodeParams &p = fp.d;
+    extern __shared__ unsigned char smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw = smem_addr(smem_raw), sb = (raw + 1023u) & ~1023u;  // swizzle atoms start on 1 KB
+    unsigned char *smem = smem_raw + (sb - raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);  // [S] TMA -> MMA
+    uint64_t *empty = full + S;                                        // [S] MMA -> TMA
+    uint64_t *q_full = empty + S;                                      // softmax threads -> MMA (Q^T written)
+    uint64_t *s_full = q_full + 1;                                     // [2] MMA -> softmax (S^T of a tile ready)
+    uint64_t *p_full = s_full + 2;                                     // [2] softmax -> MMA (P^T written, O rescaled)
+    uint64_t *pv_done = p_full + 2;                                    // [2] MMA -> softmax (PV of a tile complete)
+    uint64_t *sc_full = pv_done + 2;                                   // [kScaleRing] scales -> softmax
+    uint64_t *sc_empty = sc_full + kScaleRing;                         // [kScaleRing] softmax -> scales
+    volatile uint32_t *holder = reinterpret_cast<volatile uint32_t *>(sc_empty + kScaleRing);
+    int *lens = reinterpret_cast<int *>(smem + L::kOffLen);
+    float4 *scales = reinterpret_cast<float4 *>(smem + L::kOffSc);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * S; ++i) mbar_init(&full[i], 1);
+        mbar_init(q_full, 128);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&s_full[b], 1);
+            mbar_init(&p_full[b], 128);
+            mbar_init(&pv_done[b], 1);
+        }
+        for (int i = 0; i < kScaleRing; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_empty[i], 4);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(const_cast<uint32_t *>(holder))),
+                     "r"(L::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();     // the kernel before this one on the stream (e.g. the cache write) has finished
+    pdl_trigger();  // the merge may be scheduled once every CTA of this grid has started
+    Walk walk = begin<T>(fp, D, lens, reinterpret_cast<long long *>(lens + kLens));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *holder;
+    const int shift = __ffs(p.block_size) - 1;  // block_size is a power of two, 8 .. 128
+    const int per_tile = kKeys >> shift;        // blocks per tile
+    Piece q;
+
+    if (warp == 0) {
+        // ============================================================ producer
+        const int oob = p.num_blocks * p.num_kv_heads * p.block_size;  // first row past the pool: zero fill
+        const uint64_t pol = policy_evict_first();
+        const int per_chunk = 32 / per_tile;  // tiles of 32 table entries
+        int item = 0;
+        auto load = [&](const CUtensorMap *map, int y) {
+            const int sl = item % S;
+            if (lane == 0) {
+                if (item >= S) wait_or_flag(&empty[sl], (uint32_t)(item / S - 1) & 1u, p.d_err);
+                mbar_arrive_expect_tx(&full[sl], (uint32_t)L::kSlot);
+            }
+            __syncwarp();
+            if (lane < per_tile) tma_rows(sb + sl * L::kSlot + lane * p.block_size * D, map, y, &full[sl], pol);
+            ++item;
+        };
+        while (next_piece(p, lens, walk, q)) {
+            // ring items in consumption order: K(0), then K(j), V(j-1) for j >= 1, then V(last)
+            const int32_t *table = p.block_tables + (size_t)q.s * p.table_stride + q.tile * per_tile;
+            const int nblk = (q.ntok + p.block_size - 1) >> shift;
+            // table entries 32 at a time, one per lane, a chunk ahead of use
+            auto chunk = [&](int c) { return c * 32 + lane < nblk ? table[c * 32 + lane] : -1; };
+            int ent_cur = chunk(0), ent_nxt = chunk(1);
+            int y_prev = oob;
+            for (int j = 0; j < q.n; ++j) {
+                const int in = j & (per_chunk - 1);
+                if (j > 0 && in == 0) {
+                    ent_cur = ent_nxt;
+                    ent_nxt = chunk(j / per_chunk + 1);
+                }
+                const int e = __shfl_sync(kFull, ent_cur, in * per_tile + (lane & (per_tile - 1)));
+                int y = oob;
+                if (lane < per_tile && j * per_tile + lane < nblk) {
+                    if (e >= 0 && e < p.num_blocks) y = (e * p.num_kv_heads + q.kvh) << shift;
+                    else flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
+                }
+                load(&tmk, y);
+                if (j >= 1) load(&tmv, y_prev / L::kPar);
+                y_prev = y;
+            }
+            load(&tmv, y_prev / L::kPar);
+        }
+        // copies still in flight (only after a timeout) land before the CTA ends
+        if (lane == 0)
+            for (int i = max(0, item - S); i < item; ++i) mbar_wait(&full[i % S], (uint32_t)(i / S) & 1u);
+    } else if (warp == 1) {
+        // ============================================================ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_qk = instr_desc8(false, false, kKeys, N);
+            constexpr uint32_t id_pv = instr_desc8(true, true, 128, NO);
+            constexpr uint32_t hi_v = desc_hi(1024);  // 128-byte rows: groups of 8 are 1 KB apart
+            constexpr uint32_t hi = D == 128 ? hi_v : desc_hi64(512);  // K, Q^T, P^T: rows of D, D and kRowP = D bytes
+            static_assert(L::kRowP == D, "P^T is swizzled like K and Q^T");
+            // one swizzle row wide: the leading offset is unused
+            const uint32_t kv_lo0 = desc_lo(sb, 16), q_lo = desc_lo(sb + L::kOffQ, 16), p_lo0 = desc_lo(sb + L::kOffP, 16);
+            int ib = 0, g = 0, pieces = 0;  // ring items, tiles and pieces so far
+            while (next_piece(p, lens, walk, q)) {
+                wait_or_flag(q_full, (uint32_t)pieces & 1u, p.d_err);
+                tc_fence_after();
+                for (int j = 0; j <= q.n; ++j) {
+                    if (j < q.n) {
+                        // S^T(j) = K(j) Q^T into buffer (g + j) & 1 (its previous tile's
+                        // softmax finished before the PV issued last iteration)
+                        const int it = ib + (j == 0 ? 0 : 2 * j - 1), sl = it % S, b = (g + j) & 1;
+                        wait_or_flag(&full[sl], (uint32_t)(it / S) & 1u, p.d_err);
+                        tc_fence_after();
+                        const uint32_t k_lo = kv_lo0 + ((uint32_t)(sl * L::kSlot) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 32; ++kk)
+                            mma_f8(tmem + b * N, desc_of(k_lo + kk * 2, hi), desc_of(q_lo + kk * 2, hi), id_qk, kk > 0);
+                        mma_commit(&s_full[b]);
+                        mma_commit(&empty[sl]);
+                    }
+                    if (j >= 1) {
+                        // O^T += V^T(j-1) P^T(j-1)
+                        const int gg = g + j - 1, b = gg & 1;
+                        wait_or_flag(&p_full[b], (uint32_t)(gg >> 1) & 1u, p.d_err);
+                        const int it = ib + (j < q.n ? 2 * j : 2 * j - 1), sl = it % S;
+                        wait_or_flag(&full[sl], (uint32_t)(it / S) & 1u, p.d_err);
+                        tc_fence_after();
+                        const uint32_t v_lo = kv_lo0 + ((uint32_t)(sl * L::kSlot) >> 4);
+                        const uint32_t p_lo = p_lo0 + ((uint32_t)(b * L::kP) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 32; ++kk)
+                            mma_f8(tmem + L::kColO, desc_of(v_lo + kk * 256, hi_v), desc_of(p_lo + kk * 2, hi), id_pv,
+                                   j > 1 || kk > 0);
+                        mma_commit(&pv_done[b]);
+                        mma_commit(&empty[sl]);
+                    }
+                }
+                ib += 2 * q.n;
+                g += q.n;
+                ++pieces;
+            }
+        }
+    } else if (warp == 6) {
+        // ============================================================ scales
+        // of every block of a tile: (2^ek, ev, 2^(-ev)); a block outside the pool has
+        // (0, -inf, 0), so that its keys (zeros) weigh nothing
+        int g = 0;
+        while (next_piece(p, lens, walk, q)) {
+            const int32_t *table = p.block_tables + (size_t)q.s * p.table_stride + q.tile * per_tile;
+            const int nblk = (q.ntok + p.block_size - 1) >> shift;
+            const int per_chunk = 32 / per_tile;
+            auto entry = [&](int c) { return c * 32 + lane < nblk ? table[c * 32 + lane] : -1; };
+            auto fetch = [&](int e, unsigned &kb, unsigned &vb) {
+                kb = vb = 256u;
+                if (e >= 0 && e < p.num_blocks) {
+                    const size_t at = (size_t)e * p.num_kv_heads + q.kvh;
+                    kb = fp.k_scales[at];
+                    vb = fp.v_scales[at];
+                }
+            };
+            // entries two chunks ahead, scales one
+            unsigned kb, vb, kn, vn;
+            int e1 = entry(1), e2 = entry(2);
+            fetch(entry(0), kb, vb);
+            for (int j = 0; j < q.n; ++j, ++g) {
+                const int in = j & (per_chunk - 1);
+                if (in == 0) {
+                    if (j > 0) kb = kn, vb = vn;
+                    fetch(e1, kn, vn);
+                    e1 = e2;
+                    e2 = entry(j / per_chunk + 3);
+                }
+                const int r = g % kScaleRing;
+                if (g >= kScaleRing) {
+                    if (lane == 0) wait_or_flag(&sc_empty[r], (uint32_t)(g / kScaleRing - 1) & 1u, p.d_err);
+                    __syncwarp();
+                }
+                if (lane / per_tile == in) {
+                    float4 v = make_float4(0.f, -INFINITY, 0.f, 0.f);
+                    if (kb < 256u) v = make_float4(scale_of(kb), log_scale_of(vb), vb == 255u ? scale_of(255u) : scale_of(254u - vb), 0.f);
+                    scales[r * 16 + (lane & (per_tile - 1))] = v;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&sc_full[r]);
+            }
+        }
+    } else {
+        // ============================================================ softmax
+        const int quarter = warp & 3;         // TMEM lanes 32*quarter .. +31
+        const int t = quarter * 32 + lane;    // key of the tile (S^T row), row of O^T
+        const int sw = warp - 2;              // index among the softmax warps
+        const int par = t / D, d = t % D;     // parity of the keys whose sums, and dimension that, O^T's row has
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t col_o = L::kColO + par * N;
+        float *xmax = reinterpret_cast<float *>(smem + L::kOffXch);
+        float *xsum = xmax + 2 * 4 * GP, *qscale = xsum + 4 * GP, *odd = qscale + GP;
+        int g0 = 0;
+        while (next_piece(p, lens, walk, q)) {
+            const size_t row0 = (size_t)q.s * p.num_heads + (size_t)q.kvh * G;
+            {
+                // Q^T: each head over a power of two that brings its largest element to
+                // 128 .. 256, as three e4m3 pieces, each the residual of those before
+                // times 2^4: 12 bits, as many as fp16 has, and the products are exact.
+                // (The previous piece's QKs have all completed: its last S was read.)
+                constexpr int kPer = D / 16;       // dimensions of a thread, 16 threads a head
+                const int h = t >> 4, c = t & 15;
+                float x[8];
+                const T *src = static_cast<const T *>(p.query) + (row0 + (h < G ? h : 0)) * D + c * kPer;
+                if constexpr (kPer == 8) {
+                    unpack8<T>(*reinterpret_cast<const uint4 *>(src), x);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                    Elem<T>::unpack2(u.x, x[0], x[1]);
+                    Elem<T>::unpack2(u.y, x[2], x[3]);
+                    x[4] = x[5] = x[6] = x[7] = 0.f;
+                }
+                float amax = 0.f;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, counted(x[i]));
+#pragma unroll
+                for (int m = 8; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
+                const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100) - 7;
+                const float f = __uint_as_float((unsigned)(127 - e) << 23);
+                if (h < G) {
+                    if (c == 0) qscale[h] = __uint_as_float((unsigned)(127 + e) << 23) * p.scale_log2;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) x[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] * f : __uint_as_float(0x7fc00000u);
+#pragma unroll
+                    for (int pc = 0; pc < kQPieces; ++pc) {
+                        const unsigned lo = codes4(x[0], x[1], x[2], x[3]), hi = codes4(x[4], x[5], x[6], x[7]);
+                        const uint32_t at = sb + L::kOffQ + swizzled<D>(pc * GP + h, c * kPer);
+                        if constexpr (kPer == 8) sts64(at, lo, hi);
+                        else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(lo) : "memory");
+                        const float2 v0 = values2(lo & 0xffffu), v1 = values2(lo >> 16);
+                        x[0] = (x[0] - v0.x) * 16.f, x[1] = (x[1] - v0.y) * 16.f;
+                        x[2] = (x[2] - v1.x) * 16.f, x[3] = (x[3] - v1.y) * 16.f;
+                        if constexpr (kPer == 8) {
+                            const float2 v2 = values2(hi & 0xffffu), v3 = values2(hi >> 16);
+                            x[4] = (x[4] - v2.x) * 16.f, x[5] = (x[5] - v2.y) * 16.f;
+                            x[6] = (x[6] - v3.x) * 16.f, x[7] = (x[7] - v3.y) * 16.f;
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive1(q_full);
+                named_bar_sync(1, 128);  // qscale
+            }
+            float qf[G], m_run[G], l_part[G];
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                qf[h] = qscale[h];
+                m_run[h] = -INFINITY;
+                l_part[h] = 0.f;
+            }
+            for (int j = 0; j < q.n; ++j) {
+                const int g = g0 + j, b = g & 1, r = g % kScaleRing;
+                const bool valid = j * kKeys + t < q.ntok;
+                wait_or_flag(&sc_full[r], (uint32_t)(g / kScaleRing) & 1u, p.d_err);
+                const float4 sc = scales[r * 16 + (t >> shift)];
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&sc_empty[r]);
+                wait_or_flag(&s_full[b], (uint32_t)(g >> 1) & 1u, p.d_err);
+                tc_fence_after();
+                float z[G];
+                {
+                    float s0[16];
+                    tmem_ld16(tmem + lane_off + b * N, s0);
+                    if constexpr (GP == 4) {
+#pragma unroll
+                        for (int h = 0; h < G; ++h) z[h] = fmaf(fmaf(s0[8 + h], 0.0625f, s0[4 + h]), 0.0625f, s0[h]);
+                    } else {
+                        float s1[8];
+                        tmem_ld8(tmem + lane_off + b * N + 16, s1);
+#pragma unroll
+                        for (int h = 0; h < G; ++h) z[h] = fmaf(fmaf(s1[h], 0.0625f, s0[8 + h]), 0.0625f, s0[h]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < G; ++h) z[h] = valid ? fmaf(z[h], sc.x * qf[h], sc.y) : -INFINITY;
+                }
+                // each head's maximum over the tile's 128 keys
+                const float wmax = warp_scatter<true, G>(z, lane);
+                if ((lane & (32 / G - 1)) == 0) xmax[(b * 4 + sw) * GP + lane / (32 / G)] = wmax;
+                named_bar_sync(1, 128);
+                float tmax[GP];
+                {
+                    const float4 *x = reinterpret_cast<const float4 *>(xmax + b * 4 * GP);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+#pragma unroll
+                        for (int k = 0; k < GP / 4; ++k) {
+                            const float4 v = x[w * (GP / 4) + k];
+                            tmax[4 * k] = w ? fmaxf(tmax[4 * k], v.x) : v.x;
+                            tmax[4 * k + 1] = w ? fmaxf(tmax[4 * k + 1], v.y) : v.y;
+                            tmax[4 * k + 2] = w ? fmaxf(tmax[4 * k + 2], v.z) : v.z;
+                            tmax[4 * k + 3] = w ? fmaxf(tmax[4 * k + 3], v.w) : v.w;
+                        }
+                }
+                // rescale when a maximum has grown by more than 2^8 (the same decision in every thread)
+                bool grow = false;
+                float alpha[GP];
+#pragma unroll
+                for (int h = 0; h < GP; ++h) alpha[h] = 1.f;
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    const float nm = tmax[h] > m_run[h] + kRescale ? tmax[h] : m_run[h];
+                    alpha[h] = m_run[h] == -INFINITY ? 0.f : fast_exp2(m_run[h] - nm);
+                    grow |= nm != m_run[h];
+                    m_run[h] = nm;
+                }
+                if (grow && j > 0) {
+                    // O must hold the PV of tile j-1 before it is scaled
+                    wait_or_flag(&pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1u, p.d_err);
+                    tc_fence_after();
+#pragma unroll
+                    for (int i0 = 0; i0 < N; i0 += 16) {
+                        float o[16];
+                        tmem_ld16(tmem + lane_off + col_o + i0, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= alpha[(i0 + i) % GP];
+                        tmem_st16(tmem + lane_off + col_o + i0, o);
+                    }
+#pragma unroll
+                    for (int h = 0; h < G; ++h) l_part[h] *= alpha[h];
+                }
+                float pr[G + (G & 1)];
+                if constexpr (G & 1) pr[G] = 0.f;
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    // (no NaN while every key so far is left out)
+                    pr[h] = z[h] == -INFINITY ? 0.f : fast_exp2(z[h] - m_run[h] + kLift);
+                    l_part[h] = fmaf(pr[h], valid ? sc.z : 0.f, l_part[h]);
+                }
+                // P^T buffer b is free once the PV of tile j-2 completed
+                if (j >= 2) wait_or_flag(&pv_done[b], (uint32_t)((g - 2) >> 1) & 1u, p.d_err);
+                {
+                    // each weight as four e5m2 pieces, each the rounded residual of those
+                    // before times 2^3: 12 bits from 2^15 down, and never coarser than 2^-26
+                    const uint32_t pb = sb + L::kOffP + b * L::kP;
+                    const int kp = t % L::kPar, at = t / L::kPar;  // the key's parity, and its place among that parity's
+#pragma unroll
+                    for (int pc = 0; pc < kPPieces; ++pc) {
+#pragma unroll
+                        for (int h = 0; h < G; h += 2) {
+                            const unsigned two = e5m2x2(pr[h], pr[h + 1]);
+                            const int n = kp * N + pc * GP + h;
+                            sts8(pb + swizzled<L::kRowP>(n, at), two);
+                            if (h + 1 < G) sts8(pb + swizzled<L::kRowP>(n + 1, at), two >> 8);
+                            if (pc + 1 < kPPieces) {
+                                const float2 a = from_e5m2x2(two);
+                                pr[h] = (pr[h] - a.x) * 8.f;
+                                pr[h + 1] = (pr[h + 1] - a.y) * 8.f;
+                            }
+                        }
+                    }
+                }
+                if (j == q.n - 1 && !valid) {
+                    // this key's V row holds whatever the pool has past the context
+                    // (possibly NaN, and 0 * NaN poisons O): zero it
+                    const int it = 2 * g + 1, sl = it % S;  // V of a piece's last tile is its last item
+                    wait_or_flag(&full[sl], (uint32_t)(it / S) & 1u, p.d_err);
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c)
+                        sts128(sb + sl * L::kSlot + swizzled<128>(t / L::kPar, (t % L::kPar) * D + c * 16), zero);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive1(&p_full[b]);
+            }
+            g0 += q.n;
+
+            // row sums over the 128 key lanes, then the four warps
+            const float wsum = warp_scatter<false, G>(l_part, lane);
+            if ((lane & (32 / G - 1)) == 0) xsum[sw * GP + lane / (32 / G)] = wsum;
+            const int gl = g0 - 1;
+            wait_or_flag(&pv_done[gl & 1], (uint32_t)(gl >> 1) & 1u, p.d_err);
+            tc_fence_after();
+            float v[G];
+            {
+                float o[N];
+#pragma unroll
+                for (int i0 = 0; i0 < N; i0 += 16)
+                    tmem_ld16(tmem + lane_off + col_o + i0, *reinterpret_cast<float(*)[16]>(&o[i0]));
+#pragma unroll
+                for (int h = 0; h < G; ++h)
+                    v[h] = fmaf(fmaf(fmaf(o[3 * GP + h], 0.125f, o[2 * GP + h]), 0.125f, o[GP + h]), 0.125f, o[h]);
+            }
+            tc_fence_before();  // the next piece's first PV overwrites O
+            if constexpr (L::kPar == 2) {
+                if (par) {
+#pragma unroll
+                    for (int h = 0; h < G; ++h) odd[h * 64 + d] = v[h];
+                }
+            }
+            named_bar_sync(1, 128);
+            if (par == 0) {
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    if constexpr (L::kPar == 2) v[h] += odd[h * 64 + d];
+                    const float lsum = (xsum[h] + xsum[GP + h]) + (xsum[2 * GP + h] + xsum[3 * GP + h]);
+                    if (q.slot < 0) {
+                        static_cast<T *>(p.out)[(row0 + h) * D + d] = (T)(lsum != 0.f ? v[h] / lsum : 0.f);
+                    } else {
+                        const size_t at = (size_t)q.slot * G + h;
+                        p.ws_acc[at * D + d] = v[h];
+                        if (d == h) p.ws_ml[at] = make_float2(m_run[h] == -INFINITY ? kEmptyMax : m_run[h], lsum);
+                    }
+                }
+            }
+            // (the next piece's exchanges through xsum and odd come after its own barriers)
+            // the piece with the first tile says where the partials are
+            if (fp.units && q.tile == 0 && t == 0)
+                fp.units[(size_t)q.s * p.num_kv_heads + q.kvh] = make_int2(q.slot, q.pieces);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols) : "memory");
+    }
+}
+
+// Log-sum-exp merge of the pieces of what was cut, one warp per (sequence, query head):
+//   M = max m_i,  w_i = 2^(m_i - M),  out = sum w_i acc_i / sum w_i l_i.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) merge_fp8_kernel(const __grid_constant__ Fp8DecodeParams fp) {
+    constexpr int V = D / 32;  // values per lane
+    const DecodeParams &p = fp.d;
+    pdl_wait();                // the decode kernel's partials are complete and visible
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (long long)p.num_seqs * p.num_heads) return;
+    const int G = p.grp_inner, h = (int)(row % G);  // rows of a (sequence, kv head) are adjacent
+    const int2 u = fp.units[row / G];
+    if (u.y <= 1) return;
+    auto slot = [&](int i) { return (size_t)(i ? 2 * ((u.x >> 1) + i) : u.x) * G + h; };
+    float M = kEmptyMax;
+    for (int i = lane; i < u.y; i += 32) M = fmaxf(M, p.ws_ml[slot(i)].x);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, m));
+    float lsum = 0.f, o[V];
+#pragma unroll
+    for (int d = 0; d < V; ++d) o[d] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < u.y; ++i) {
+        const size_t at = slot(i);
+        const float2 ml = p.ws_ml[at];
+        const float w = fast_exp2(ml.x - M);
+        lsum = fmaf(w, ml.y, lsum);
+        const float2 *a = reinterpret_cast<const float2 *>(p.ws_acc + at * D + lane * V);
+#pragma unroll
+        for (int d = 0; d < V / 2; ++d) {
+            const float2 x = a[d];
+            o[2 * d] = fmaf(w, x.x, o[2 * d]);
+            o[2 * d + 1] = fmaf(w, x.y, o[2 * d + 1]);
+        }
+    }
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + row * D + lane * V);
+#pragma unroll
+    for (int d = 0; d < V / 2; ++d)
+        dst[d] = lsum != 0.f ? Elem<T>::pack2(o[2 * d] / lsum, o[2 * d + 1] / lsum) : 0u;
+}
+
+// ---- host side -------------------------------------------------------------
+
+// The pool as rows of `width` bytes, a block of a kv head one box of `rows` of them.
+inline bool make_rows_map(CUtensorMap *map, const void *pool, long long all_rows, int width, int rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)all_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)width};
+    const cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, int G>
+int launch_t(const Fp8DecodeParams &p, cudaStream_t stream) {
+    auto kern = decode_fp8_kernel<T, D, G>;
+    using L = Lay<D, G>;
+    static std::atomic<uint64_t> attr_done{0};
+    if (ensure_smem_attr(kern, L::kAlloc, attr_done) != PA_OK) return PA_ERR_CUDA;
+    const long long rows = (long long)p.d.num_blocks * p.d.num_kv_heads * p.d.block_size;
+    CUtensorMap tmk, tmv;
+    if (!make_rows_map(&tmk, p.d.k_cache, rows, D, p.d.block_size) ||
+        !make_rows_map(&tmv, p.d.v_cache, rows / L::kPar, 128, p.d.block_size / L::kPar))
+        return PA_ERR_CUDA;
+    if (launch_pdl(kern, dim3(p.ctas), dim3(kThreads), L::kAlloc, stream, p, tmk, tmv) != cudaSuccess) return PA_ERR_CUDA;
+    if (!p.units) return PA_OK;
+    const long long heads = (long long)p.d.num_seqs * p.d.num_heads;
+    return launch_pdl(merge_fp8_kernel<T, D>, dim3((unsigned)((heads + 3) / 4)), dim3(128), 0, stream, p) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+template <typename T, int D>
+int launch_group(int group, const Fp8DecodeParams &p, cudaStream_t stream) {
+    return group == 1   ? launch_t<T, D, 1>(p, stream)
+           : group == 2 ? launch_t<T, D, 2>(p, stream)
+           : group == 4 ? launch_t<T, D, 4>(p, stream)
+                        : launch_t<T, D, 8>(p, stream);
+}
+
+template <typename T>
+int launch_dtype(int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream) {
+    return head_dim == 128 ? launch_group<T, 128>(group, p, stream) : launch_group<T, 64>(group, p, stream);
+}
+
+}  // namespace d8
+}  // namespace pa

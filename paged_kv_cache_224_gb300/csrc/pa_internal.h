@@ -208,19 +208,16 @@ int weights_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int 
 // a row of `width` totals.  one_table: flags sequences of a row whose table rows differ.
 int launch_weights_merge(pa_dtype dt, int head_dim, int group, const DecodeParams &p, const float *weights,
                          float *weights_out, int width, int queries_per_row, bool one_table, cudaStream_t stream);
-// Decode over an 8-bit cache, with the merge of the partials.
+// Decode over an 8-bit cache, with the merge of what is cut (pa_fp8_decode.cu).
 struct Fp8DecodeParams {
-    DecodeParams d;
+    DecodeParams d;              // ws_acc, ws_ml: [2 * ctas slots][group]
     const uint8_t *k_scales;     // [NB][Hkv]
     const uint8_t *v_scales;
+    int2 *units;                 // [B][Hkv] (slot of the first piece, pieces); null where nothing can be cut
+    int ctas;
 };
-int launch_decode_fp8(pa_dtype dt, int head_dim, int block_size, int group, const Fp8DecodeParams &p,
-                      cudaStream_t stream);
-// The same on the tensor cores at head_dim 128, without the merge; PA_ERR_UNSUPPORTED
-// where a tensor map does not reach.
-int launch_decode_fp8_tc(pa_dtype dt, int block_size, int group, const Fp8DecodeParams &p, cudaStream_t stream);
-int fp8_partition_tokens(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                         int max_context_len);
+int fp8_decode_ctas(int num_seqs, int num_kv_heads, int max_context_len);
+int launch_decode_fp8(pa_dtype dt, int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
 // The codes of the sequences' first blocks as values of dt, laid end to end: block
 // j of sequence i becomes block first[i] + j of k_out and v_out, whose own table is
 // `table` (the number itself, or -1 where the sequence's entry is outside the pool,

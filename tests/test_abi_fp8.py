@@ -75,9 +75,9 @@ def test_store_refusals(lib):
 
 
 def decode(lib, out=BUF, q=BUF, kc=BUF, vc=BUF, ks=BUF, vs=BUF, bt=BUF, mb=8, lens=BUF, B=4, Hq=8, Hkv=2, D=128, bs=16, NB=64,
-           ml=100, scale=0.1, pt=0, dt=1, ws=BUF, wsb=1 << 30):
+           ml=100, scale=0.1, dt=1, ws=BUF, wsb=1 << 30):
     return lib.pa_decode_fp8(P(out), P(q), P(kc), P(vc), P(ks), P(vs), P(bt), mb, P(lens), B, Hq, Hkv, D, bs, NB, ml, F(scale),
-                             pt, dt, P(ws), wsb, None, None)
+                             dt, P(ws), wsb, None, None)
 
 
 def test_decode_refusals(lib):
@@ -87,14 +87,21 @@ def test_decode_refusals(lib):
     assert decode(lib, Hq=7) == -1 and decode(lib, dt=9) == -1 and decode(lib, mb=0) == -1 and decode(lib, ml=-1) == -1
     assert decode(lib, D=96) == -2 and decode(lib, bs=24) == -2 and decode(lib, Hq=32) == -2 and decode(lib, Hq=6) == -2
     assert decode(lib, mb=1 << 28) == -2                    # a table of 2^32 tokens
-    assert decode(lib, scale=float("inf")) == -3 and decode(lib, pt=24) == -3 and decode(lib, pt=-16) == -3
+    assert decode(lib, NB=1 << 27) == -2                    # a pool of 2^32 rows
+    assert decode(lib, B=1 << 29) == -2
+    assert decode(lib, scale=float("inf")) == -3
     assert decode(lib, q=BUF + 2) == -6 and decode(lib, kc=BUF + 8) == -6
-    need = lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 16, 100, 64)
-    assert need == 2 * 4 * 8 * (128 + 2) * 4                # two partitions of each of 32 rows
-    assert decode(lib, pt=64, ws=0) == -5 and decode(lib, pt=64, wsb=need - 1) == -5 and decode(lib, pt=64, ws=BUF + 16) == -6
-    assert lib.pa_decode_fp8_workspace_bytes(4, 7, 2, 128, 16, 100, 0) == 0
-    assert lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 16, 100, 24) == 0
-    assert lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 16, 100, 1 << 30) == 0
+    # contexts of a single tile are never cut
+    assert lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 16, 128) == 0
+    # 4 sequences of 2 tiles, 2 kv heads: 16 CTAs, two partials each of 4 heads
+    need = lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 16, 200)
+    assert need == 256 + 2 * 16 * 4 * (128 + 2) * 4
+    assert decode(lib, ml=200, ws=0) == -5 and decode(lib, ml=200, wsb=need - 1) == -5
+    assert decode(lib, ml=200, ws=BUF + 16) == -6
+    # two CTAs to each of (without a device) 152 SMs, however large the batch
+    assert lib.pa_decode_fp8_workspace_bytes(256, 32, 8, 128, 16, 4096) == 256 * 8 * 8 + 2 * 304 * 4 * (128 + 2) * 4
+    assert lib.pa_decode_fp8_workspace_bytes(4, 7, 2, 128, 16, 200) == 0
+    assert lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 24, 200) == 0
 
 
 def prefill(lib, out=BUF, q=BUF, kc=BUF, vc=BUF, ks=BUF, vs=BUF, bt=BUF, mb=8, prefix=(64, 0), chunk=(20, 30), Hq=8, Hkv=2, D=128,

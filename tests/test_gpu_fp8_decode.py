@@ -78,10 +78,29 @@ def test_decode(G, D, bs, dtype):
 
 @pytest.mark.parametrize("D,G", [(128, 4), (128, 8), (64, 8), (64, 1)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("pt", [0, 256, 64, 1 << 30])
-def test_partitions(D, G, dtype, pt):
-    c = make([1500, 3, 0, 257, 64, 1024], G, 1, D, 16, dtype, seed=3 + D + G, poison=True)
-    check(c, dtype, partition_tokens=pt)
+@pytest.mark.parametrize("lens,Hkv", [([1500, 3, 0, 257, 64, 1024], 1),      # every tile a CTA of its own
+                                      ([5000, 0, 0, 129], 8),                # shares of one and of two tiles
+                                      ([40] * 300 + [3000, 0] + [130] * 40, 3),   # more sequences than are held at a time
+                                      ([0, 0, 0, 128, 0], 2)])
+def test_shares(D, G, dtype, lens, Hkv):
+    c = make(lens, G * Hkv, Hkv, D, 16, dtype, seed=3 + D + G, poison=True)
+    if len(lens) > 100:  # the first and last ones, and those around the long one
+        c2 = decode(c)
+        kv, vv = ref8.values(c["kc"], c["ks"]), ref8.values(c["vc"], c["vs"])
+        for i in (0, 1, 7, 299, 300, 301, 302, 341):
+            near(c2[i], c["q"][i].cpu().double(), ref8.rows_of(kv, c["bt"][i], lens[i]), ref8.rows_of(vv, c["bt"][i], lens[i]),
+                 c["scale"], dtype, lens[i])
+    else:
+        check(c, dtype)
+
+
+def test_a_row_alone_and_in_a_batch():
+    """Cut differently, the same up to fp32 sums and one rounding."""
+    c = make([2500, 700, 1, 90], 8, 2, 128, 16, "bf16", seed=40)
+    out = decode(c)
+    for i, n in enumerate(c["lens"].tolist()):
+        one = dict(c, q=c["q"][i:i + 1], bt=c["bt"][i:i + 1].contiguous(), lens=c["lens"][i:i + 1], most=n)
+        assert bool(((decode(one).float() - out[i].float()).abs() <= 2.0 ** -7 * out[i].float().abs() + 2.0 ** -12).all())
 
 
 @pytest.mark.parametrize("D,G", [(128, 2), (128, 8), (64, 4)])
@@ -130,13 +149,12 @@ def test_no_context_and_tables_that_hold_nothing():
         good = check(c, "bf16").clone()
         c["bt"][0] = -5
         c["bt"][1] = 1 << 20
-        for pt in (0, 64):
-            err = torch.zeros(1, dtype=torch.int32, device=DEV)
-            out = decode(c, err, partition_tokens=pt)
-            torch.cuda.synchronize()
-            assert int(err.item()) == pa.capi.DEVERR["block_range"]
-            assert not bool(out[:2].any())
-            assert bool(((out[2].float() - good[2].float()).abs() <= 2.0 ** -7 * good[2].float().abs() + 2.0 ** -12).all())
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = decode(c, err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == pa.capi.DEVERR["block_range"]
+        assert not bool(out[:2].any())
+        assert bool(((out[2].float() - good[2].float()).abs() <= 2.0 ** -7 * good[2].float().abs() + 2.0 ** -12).all())
 
 
 @pytest.mark.parametrize("D,G,bs", [(128, 8, 16), (128, 1, 8), (64, 2, 16)])
@@ -255,7 +273,6 @@ def test_wrong_tensors_are_refused():
                     (TypeError, dict(block_tables=c["bt"].long())), (TypeError, dict(context_lens=c["lens"].long())),
                     (ValueError, dict(context_lens=c["lens"][:1])), (ValueError, dict(block_tables=c["bt"].cpu())),
                     (ValueError, dict(out=torch.zeros_like(c["q"])[:1])), (pa.PAError, dict(scale=float("nan"))),
-                    (pa.PAError, dict(partition_tokens=24)),
                     (pa.PAError, dict(max_context_len=100000, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)))):
         with pytest.raises(exc):
             pa.pa_decode_fp8(**{**a, **kw})
