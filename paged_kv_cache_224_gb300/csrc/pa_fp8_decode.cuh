@@ -33,17 +33,20 @@ struct Lay {
     static constexpr uint32_t kCols = 2 * N + NO <= 64 ? 64 : 128;  // TMEM: S^T x 2 buffers, O^T
     static constexpr uint32_t kColO = 2 * N;
     static constexpr int kSlot = kKeys * D;                 // one K or V tile
-    static constexpr int S = D == 128 ? 6 : 12;             // ring slots: 96 KB, two CTAs to an SM
+    static constexpr int S = (GP == 4 ? 6 : 5) * kPar;      // ring slots: 96 or 80 KB, two CTAs to an SM
     static constexpr int kRowP = kKeys / kPar;              // bytes of a row of P^T: a tile's keys of one parity
-    static constexpr int kOffQ = S * kSlot;                 // [N][D]
-    static constexpr int kOffP = kOffQ + N * D;             // 2 x [NO][kRowP]
+    // 2 x [3 GP rows][D]; the MMAs read N rows, the last GP of them whatever follows:
+    // columns that nobody reads
+    static constexpr int kOffQ = S * kSlot;
+    static constexpr int kQ = (kQPieces * GP + 7) / 8 * 8 * D;
+    static constexpr int kOffP = kOffQ + 2 * kQ;            // 2 x [NO][kRowP]
     static constexpr int kP = NO * kRowP;
     static constexpr int kOffSc = kOffP + 2 * kP;           // [kScaleRing][16 blocks] of float4
     static constexpr int kOffBar = kOffSc + kScaleRing * 16 * 16;
-    static constexpr int kBars = 2 * S + 7 + 2 * kScaleRing;
+    static constexpr int kBars = 2 * S + 10 + 2 * kScaleRing;
     static constexpr int kOffLen = kOffBar + (kBars * 8 + 8 + 15) / 16 * 16;
-    static constexpr int kOffXch = kOffLen + kLens * 4 + 64;  // [2][4 warps][GP] maxima, [4][GP] sums, [GP] query scales, [G][64] sums of odd keys
-    static constexpr int kUsed = kOffXch + (2 * 4 * GP + 4 * GP + GP + (kPar == 2 ? G * 64 : 0)) * 4;
+    static constexpr int kOffXch = kOffLen + kLens * 4 + 64;  // [2][4 warps][GP] maxima, [4][GP] sums, [2][GP] query scales, [G][64] sums of odd keys
+    static constexpr int kUsed = kOffXch + (2 * 4 * GP + 4 * GP + 2 * GP + (kPar == 2 ? G * 64 : 0)) * 4;
     static constexpr int kAlloc = kUsed + 1024;             // room to align the base to 1 KB
 };
 
@@ -75,12 +78,20 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, i
 __device__ __forceinline__ void sts8(uint32_t addr, unsigned v) {
     asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void sts64(uint32_t addr, unsigned a, unsigned b) {
-    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
+}
+
+// wait_or_flag with the polling out of line: the roles' code has to stay in the
+// instruction cache together, and most waits find their phase complete.
+static __device__ __noinline__ void poll_or_flag(uint64_t *bar, uint32_t parity, int *d_err) {
+    for (uint32_t i = 0; i < kMaxPolls; ++i)
+        if (mbar_try_wait(bar, parity)) return;
+    flag_error(d_err, PA_DEVERR_TIMEOUT);
+}
+__device__ __forceinline__ void await(uint64_t *bar, uint32_t parity, int *d_err) {
+    if (!mbar_test(bar, parity)) poll_or_flag(bar, parity, d_err);
 }
 
 // Byte `at` of row `row` in rows of W bytes, swizzled over W bytes (W = 64 or 128).
@@ -135,7 +146,8 @@ struct Piece {
     int tile, n;      // first tile within the sequence, tiles
     int ntok;         // tokens from the first tile on
     int slot;
-    int pieces;       // of the (sequence, kv head), known to the first of them
+    long long at;     // first tile within the call
+    int whole;        // tiles of the (sequence, kv head)
 };
 
 // Walks a CTA's pieces; every role of the CTA has one and sees the same.
@@ -168,7 +180,8 @@ __device__ __forceinline__ bool next_piece(const DecodeParams &p, const int *len
     q.n = (int)min((long long)(whole - w.tile), w.end - w.at);
     q.ntok = min(w.len - w.tile * kKeys, q.n * kKeys);
     q.slot = q.n == whole ? -1 : 2 * (int)blockIdx.x + (w.first ? 0 : 1);
-    q.pieces = q.n == whole || w.tile > 0 ? 1 : owner(w.total, w.ctas, w.at + whole - 1) - (int)blockIdx.x + 1;
+    q.at = w.at;
+    q.whole = whole;
     w.first = false;
     w.at += q.n;
     w.tile += q.n;
@@ -265,19 +278,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     unsigned char *smem = smem_raw + (sb - raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);  // [S] TMA -> MMA
     uint64_t *empty = full + S;                                        // [S] MMA -> TMA
-    uint64_t *q_full = empty + S;                                      // softmax threads -> MMA (Q^T written)
-    uint64_t *s_full = q_full + 1;                                     // [2] MMA -> softmax (S^T of a tile ready)
+    uint64_t *q_full = empty + S;                                      // [2] helper -> MMA, softmax (Q^T written)
+    uint64_t *q_empty = q_full + 2;                                    // [2] MMA, softmax -> helper
+    uint64_t *s_full = q_empty + 2;                                    // [2] MMA -> softmax (S^T of a tile ready)
     uint64_t *p_full = s_full + 2;                                     // [2] softmax -> MMA (P^T written, O rescaled)
     uint64_t *pv_done = p_full + 2;                                    // [2] MMA -> softmax (PV of a tile complete)
-    uint64_t *sc_full = pv_done + 2;                                   // [kScaleRing] scales -> softmax
-    uint64_t *sc_empty = sc_full + kScaleRing;                         // [kScaleRing] softmax -> scales
+    uint64_t *sc_full = pv_done + 2;                                   // [kScaleRing] helper -> softmax
+    uint64_t *sc_empty = sc_full + kScaleRing;                         // [kScaleRing] softmax -> helper
     volatile uint32_t *holder = reinterpret_cast<volatile uint32_t *>(sc_empty + kScaleRing);
     int *lens = reinterpret_cast<int *>(smem + L::kOffLen);
     float4 *scales = reinterpret_cast<float4 *>(smem + L::kOffSc);
+    float *xmax = reinterpret_cast<float *>(smem + L::kOffXch);
+    float *xsum = xmax + 2 * 4 * GP, *qscale = xsum + 4 * GP, *odd = qscale + 2 * GP;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * S; ++i) mbar_init(&full[i], 1);
-        mbar_init(q_full, 128);
         for (int b = 0; b < 2; ++b) {
+            mbar_init(&q_full[b], 1);
+            mbar_init(&q_empty[b], 1 + 4);  // the MMA thread's commit and the softmax warps
             mbar_init(&s_full[b], 1);
             mbar_init(&p_full[b], 128);
             mbar_init(&pv_done[b], 1);
@@ -315,21 +332,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto load = [&](const CUtensorMap *map, int y) {
             const int sl = item % S;
             if (lane == 0) {
-                if (item >= S) wait_or_flag(&empty[sl], (uint32_t)(item / S - 1) & 1u, p.d_err);
+                if (item >= S) await(&empty[sl], (uint32_t)(item / S - 1) & 1u, p.d_err);
                 mbar_arrive_expect_tx(&full[sl], (uint32_t)L::kSlot);
             }
             __syncwarp();
             if (lane < per_tile) tma_rows(sb + sl * L::kSlot + lane * p.block_size * D, map, y, &full[sl], pol);
             ++item;
         };
+        // ring items in consumption order, whatever piece a tile is of: K(0), then K(g),
+        // V(g-1) for g >= 1, then V(last)
+        int y_prev = -1;
         while (next_piece(p, lens, walk, q)) {
-            // ring items in consumption order: K(0), then K(j), V(j-1) for j >= 1, then V(last)
             const int32_t *table = p.block_tables + (size_t)q.s * p.table_stride + q.tile * per_tile;
             const int nblk = (q.ntok + p.block_size - 1) >> shift;
             // table entries 32 at a time, one per lane, a chunk ahead of use
             auto chunk = [&](int c) { return c * 32 + lane < nblk ? table[c * 32 + lane] : -1; };
             int ent_cur = chunk(0), ent_nxt = chunk(1);
-            int y_prev = oob;
             for (int j = 0; j < q.n; ++j) {
                 const int in = j & (per_chunk - 1);
                 if (j > 0 && in == 0) {
@@ -343,11 +361,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     else flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
                 }
                 load(&tmk, y);
-                if (j >= 1) load(&tmv, y_prev / L::kPar);
+                if (y_prev >= 0) load(&tmv, y_prev / L::kPar);
                 y_prev = y;
             }
-            load(&tmv, y_prev / L::kPar);
         }
+        if (y_prev >= 0) load(&tmv, y_prev / L::kPar);
         // copies still in flight (only after a timeout) land before the CTA ends
         if (lane == 0)
             for (int i = max(0, item - S); i < item; ++i) mbar_wait(&full[i % S], (uint32_t)(i / S) & 1u);
@@ -361,51 +379,53 @@ __global__ void __launch_bounds__(kThreads, 2)
             static_assert(L::kRowP == D, "P^T is swizzled like K and Q^T");
             // one swizzle row wide: the leading offset is unused
             const uint32_t kv_lo0 = desc_lo(sb, 16), q_lo = desc_lo(sb + L::kOffQ, 16), p_lo0 = desc_lo(sb + L::kOffP, 16);
-            int ib = 0, g = 0, pieces = 0;  // ring items, tiles and pieces so far
-            while (next_piece(p, lens, walk, q)) {
-                wait_or_flag(q_full, (uint32_t)pieces & 1u, p.d_err);
+            // O^T (+)= V^T(g) P^T(g); `item`: V's place in the ring
+            auto pv = [&](int g, int item, bool first) {
+                const int b = g & 1, sl = item % S;
+                await(&p_full[b], (uint32_t)(g >> 1) & 1u, p.d_err);
+                await(&full[sl], (uint32_t)(item / S) & 1u, p.d_err);
                 tc_fence_after();
-                for (int j = 0; j <= q.n; ++j) {
-                    if (j < q.n) {
-                        // S^T(j) = K(j) Q^T into buffer (g + j) & 1 (its previous tile's
-                        // softmax finished before the PV issued last iteration)
-                        const int it = ib + (j == 0 ? 0 : 2 * j - 1), sl = it % S, b = (g + j) & 1;
-                        wait_or_flag(&full[sl], (uint32_t)(it / S) & 1u, p.d_err);
-                        tc_fence_after();
-                        const uint32_t k_lo = kv_lo0 + ((uint32_t)(sl * L::kSlot) >> 4);
+                const uint32_t v_lo = kv_lo0 + ((uint32_t)(sl * L::kSlot) >> 4);
+                const uint32_t p_lo = p_lo0 + ((uint32_t)(b * L::kP) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 32; ++kk)
-                            mma_f8(tmem + b * N, desc_of(k_lo + kk * 2, hi), desc_of(q_lo + kk * 2, hi), id_qk, kk > 0);
-                        mma_commit(&s_full[b]);
-                        mma_commit(&empty[sl]);
-                    }
-                    if (j >= 1) {
-                        // O^T += V^T(j-1) P^T(j-1)
-                        const int gg = g + j - 1, b = gg & 1;
-                        wait_or_flag(&p_full[b], (uint32_t)(gg >> 1) & 1u, p.d_err);
-                        const int it = ib + (j < q.n ? 2 * j : 2 * j - 1), sl = it % S;
-                        wait_or_flag(&full[sl], (uint32_t)(it / S) & 1u, p.d_err);
-                        tc_fence_after();
-                        const uint32_t v_lo = kv_lo0 + ((uint32_t)(sl * L::kSlot) >> 4);
-                        const uint32_t p_lo = p_lo0 + ((uint32_t)(b * L::kP) >> 4);
+                for (int kk = 0; kk < D / 32; ++kk)
+                    mma_f8(tmem + L::kColO, desc_of(v_lo + kk * 256, hi_v), desc_of(p_lo + kk * 2, hi), id_pv, !first || kk > 0);
+                mma_commit(&pv_done[b]);
+                mma_commit(&empty[sl]);
+            };
+            int g = 0, pieces = 0;  // tiles and pieces so far
+            bool first = false;     // whether tile g - 1 is its piece's first
+            while (next_piece(p, lens, walk, q)) {
+                const int qb = pieces & 1;
+                await(&q_full[qb], (uint32_t)(pieces >> 1) & 1u, p.d_err);
+                tc_fence_after();
+                for (int j = 0; j < q.n; ++j, ++g) {
+                    // S^T(g) = K(g) Q^T into buffer g & 1 (its previous tile's softmax
+                    // finished before the PV issued last iteration)
+                    const int it = g == 0 ? 0 : 2 * g - 1, sl = it % S, b = g & 1;
+                    await(&full[sl], (uint32_t)(it / S) & 1u, p.d_err);
+                    tc_fence_after();
+                    const uint32_t k_lo = kv_lo0 + ((uint32_t)(sl * L::kSlot) >> 4);
+                    const uint32_t qq = q_lo + ((uint32_t)(qb * L::kQ) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 32; ++kk)
-                            mma_f8(tmem + L::kColO, desc_of(v_lo + kk * 256, hi_v), desc_of(p_lo + kk * 2, hi), id_pv,
-                                   j > 1 || kk > 0);
-                        mma_commit(&pv_done[b]);
-                        mma_commit(&empty[sl]);
-                    }
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        mma_f8(tmem + b * N, desc_of(k_lo + kk * 2, hi), desc_of(qq + kk * 2, hi), id_qk, kk > 0);
+                    mma_commit(&s_full[b]);
+                    mma_commit(&empty[sl]);
+                    if (j == q.n - 1) mma_commit(&q_empty[qb]);
+                    if (g > 0) pv(g - 1, 2 * g, first);
+                    first = j == 0;
                 }
-                ib += 2 * q.n;
-                g += q.n;
                 ++pieces;
             }
+            if (g > 0) pv(g - 1, 2 * g - 1, first);
         }
     } else if (warp == 6) {
-        // ============================================================ scales
-        // of every block of a tile: (2^ek, ev, 2^(-ev)); a block outside the pool has
-        // (0, -inf, 0), so that its keys (zeros) weigh nothing
-        int g = 0;
+        // ============================================================ helper
+        // Q^T of each piece, a piece ahead, and of every block of a tile (2^ek, ev,
+        // 2^(-ev)), up to kScaleRing tiles ahead; a block outside the pool has (0, -inf,
+        // 0), so that its keys (zeros) weigh nothing
+        int g = 0, pieces = 0;
         while (next_piece(p, lens, walk, q)) {
             const int32_t *table = p.block_tables + (size_t)q.s * p.table_stride + q.tile * per_tile;
             const int nblk = (q.ntok + p.block_size - 1) >> shift;
@@ -421,8 +441,60 @@ __global__ void __launch_bounds__(kThreads, 2)
             };
             // entries two chunks ahead, scales one
             unsigned kb, vb, kn, vn;
+            const int e0 = entry(0);
             int e1 = entry(1), e2 = entry(2);
-            fetch(entry(0), kb, vb);
+            fetch(e0, kb, vb);
+            // Q^T: each head over a power of two that brings its largest element to
+            // 128 .. 256, as three e4m3 pieces, each the residual of those before times
+            // 2^4: 12 bits, as many as fp16 has, and the products are exact
+            const int qb = pieces & 1;
+            if (pieces >= 2) {
+                if (lane == 0) await(&q_empty[qb], (uint32_t)((pieces >> 1) - 1) & 1u, p.d_err);
+                __syncwarp();
+            }
+            {
+                // (rolled up: what runs once a piece should not push the tiles' code out of
+                // the instruction cache, and the second reads come from L1)
+                constexpr int kLanes = 32 / G;  // of a head, four dimensions at a time
+                const int h = lane / kLanes, d0 = lane % kLanes * 4;
+                const T *src = static_cast<const T *>(p.query) + ((size_t)q.s * p.num_heads + (size_t)q.kvh * G + h) * D;
+                float x[4], amax = 0.f;
+                auto four = [&](int d) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(src + d);
+                    Elem<T>::unpack2(u.x, x[0], x[1]);
+                    Elem<T>::unpack2(u.y, x[2], x[3]);
+                };
+#pragma unroll 4
+                for (int d = d0; d < D; d += 4 * kLanes) {
+                    four(d);
+                    amax = fmaxf(amax, fmaxf(fmaxf(counted(x[0]), counted(x[1])), fmaxf(counted(x[2]), counted(x[3]))));
+                }
+#pragma unroll
+                for (int m = kLanes / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
+                const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100) - 7;
+                const float f = __uint_as_float((unsigned)(127 - e) << 23);
+                if (d0 == 0) qscale[qb * GP + h] = __uint_as_float((unsigned)(127 + e) << 23) * p.scale_log2;
+#pragma unroll 1
+                for (int d = d0; d < D; d += 4 * kLanes) {
+                    four(d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] * f : __uint_as_float(0x7fc00000u);
+#pragma unroll
+                    for (int pc = 0; pc < kQPieces; ++pc) {
+                        const unsigned lo = codes2(x[0], x[1]), hi2 = codes2(x[2], x[3]);
+                        const float2 v0 = values2(lo), v1 = values2(hi2);
+                        x[0] = (x[0] - v0.x) * 16.f, x[1] = (x[1] - v0.y) * 16.f;
+                        x[2] = (x[2] - v1.x) * 16.f, x[3] = (x[3] - v1.y) * 16.f;
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + L::kOffQ + qb * L::kQ + swizzled<D>(pc * GP + h, d)),
+                                     "r"(lo | hi2 << 16)
+                                     : "memory");
+                    }
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&q_full[qb]);
+            ++pieces;
             for (int j = 0; j < q.n; ++j, ++g) {
                 const int in = j & (per_chunk - 1);
                 if (in == 0) {
@@ -433,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 const int r = g % kScaleRing;
                 if (g >= kScaleRing) {
-                    if (lane == 0) wait_or_flag(&sc_empty[r], (uint32_t)(g / kScaleRing - 1) & 1u, p.d_err);
+                    if (lane == 0) await(&sc_empty[r], (uint32_t)(g / kScaleRing - 1) & 1u, p.d_err);
                     __syncwarp();
                 }
                 if (lane / per_tile == in) {
@@ -453,74 +525,29 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int par = t / D, d = t % D;     // parity of the keys whose sums, and dimension that, O^T's row has
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t col_o = L::kColO + par * N;
-        float *xmax = reinterpret_cast<float *>(smem + L::kOffXch);
-        float *xsum = xmax + 2 * 4 * GP, *qscale = xsum + 4 * GP, *odd = qscale + GP;
-        int g0 = 0;
+        int g0 = 0, pieces = 0;
         while (next_piece(p, lens, walk, q)) {
             const size_t row0 = (size_t)q.s * p.num_heads + (size_t)q.kvh * G;
-            {
-                // Q^T: each head over a power of two that brings its largest element to
-                // 128 .. 256, as three e4m3 pieces, each the residual of those before
-                // times 2^4: 12 bits, as many as fp16 has, and the products are exact.
-                // (The previous piece's QKs have all completed: its last S was read.)
-                constexpr int kPer = D / 16;       // dimensions of a thread, 16 threads a head
-                const int h = t >> 4, c = t & 15;
-                float x[8];
-                const T *src = static_cast<const T *>(p.query) + (row0 + (h < G ? h : 0)) * D + c * kPer;
-                if constexpr (kPer == 8) {
-                    unpack8<T>(*reinterpret_cast<const uint4 *>(src), x);
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(src);
-                    Elem<T>::unpack2(u.x, x[0], x[1]);
-                    Elem<T>::unpack2(u.y, x[2], x[3]);
-                    x[4] = x[5] = x[6] = x[7] = 0.f;
-                }
-                float amax = 0.f;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, counted(x[i]));
-#pragma unroll
-                for (int m = 8; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
-                const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100) - 7;
-                const float f = __uint_as_float((unsigned)(127 - e) << 23);
-                if (h < G) {
-                    if (c == 0) qscale[h] = __uint_as_float((unsigned)(127 + e) << 23) * p.scale_log2;
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) x[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] * f : __uint_as_float(0x7fc00000u);
-#pragma unroll
-                    for (int pc = 0; pc < kQPieces; ++pc) {
-                        const unsigned lo = codes4(x[0], x[1], x[2], x[3]), hi = codes4(x[4], x[5], x[6], x[7]);
-                        const uint32_t at = sb + L::kOffQ + swizzled<D>(pc * GP + h, c * kPer);
-                        if constexpr (kPer == 8) sts64(at, lo, hi);
-                        else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(lo) : "memory");
-                        const float2 v0 = values2(lo & 0xffffu), v1 = values2(lo >> 16);
-                        x[0] = (x[0] - v0.x) * 16.f, x[1] = (x[1] - v0.y) * 16.f;
-                        x[2] = (x[2] - v1.x) * 16.f, x[3] = (x[3] - v1.y) * 16.f;
-                        if constexpr (kPer == 8) {
-                            const float2 v2 = values2(hi & 0xffffu), v3 = values2(hi >> 16);
-                            x[4] = (x[4] - v2.x) * 16.f, x[5] = (x[5] - v2.y) * 16.f;
-                            x[6] = (x[6] - v3.x) * 16.f, x[7] = (x[7] - v3.y) * 16.f;
-                        }
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive1(q_full);
-                named_bar_sync(1, 128);  // qscale
-            }
+            const int qb = pieces & 1;
+            await(&q_full[qb], (uint32_t)(pieces >> 1) & 1u, p.d_err);
             float qf[G], m_run[G], l_part[G];
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-                qf[h] = qscale[h];
+                qf[h] = qscale[qb * GP + h];
                 m_run[h] = -INFINITY;
                 l_part[h] = 0.f;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&q_empty[qb]);
+            ++pieces;
             for (int j = 0; j < q.n; ++j) {
                 const int g = g0 + j, b = g & 1, r = g % kScaleRing;
                 const bool valid = j * kKeys + t < q.ntok;
-                wait_or_flag(&sc_full[r], (uint32_t)(g / kScaleRing) & 1u, p.d_err);
+                await(&sc_full[r], (uint32_t)(g / kScaleRing) & 1u, p.d_err);
                 const float4 sc = scales[r * 16 + (t >> shift)];
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(&sc_empty[r]);
-                wait_or_flag(&s_full[b], (uint32_t)(g >> 1) & 1u, p.d_err);
+                await(&s_full[b], (uint32_t)(g >> 1) & 1u, p.d_err);
                 tc_fence_after();
                 float z[G];
                 {
@@ -570,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 if (grow && j > 0) {
                     // O must hold the PV of tile j-1 before it is scaled
-                    wait_or_flag(&pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1u, p.d_err);
+                    await(&pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1u, p.d_err);
                     tc_fence_after();
 #pragma unroll
                     for (int i0 = 0; i0 < N; i0 += 16) {
@@ -592,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     l_part[h] = fmaf(pr[h], valid ? sc.z : 0.f, l_part[h]);
                 }
                 // P^T buffer b is free once the PV of tile j-2 completed
-                if (j >= 2) wait_or_flag(&pv_done[b], (uint32_t)((g - 2) >> 1) & 1u, p.d_err);
+                if (j >= 2) await(&pv_done[b], (uint32_t)((g - 2) >> 1) & 1u, p.d_err);
                 {
                     // each weight as four e5m2 pieces, each the rounded residual of those
                     // before times 2^3: 12 bits from 2^15 down, and never coarser than 2^-26
@@ -617,8 +644,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (j == q.n - 1 && !valid) {
                     // this key's V row holds whatever the pool has past the context
                     // (possibly NaN, and 0 * NaN poisons O): zero it
-                    const int it = 2 * g + 1, sl = it % S;  // V of a piece's last tile is its last item
-                    wait_or_flag(&full[sl], (uint32_t)(it / S) & 1u, p.d_err);
+                    const int it = walk.at >= walk.end ? 2 * g + 1 : 2 * g + 2, sl = it % S;  // (the CTA's last V is the last item)
+                    await(&full[sl], (uint32_t)(it / S) & 1u, p.d_err);
                     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c)
@@ -635,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float wsum = warp_scatter<false, G>(l_part, lane);
             if ((lane & (32 / G - 1)) == 0) xsum[sw * GP + lane / (32 / G)] = wsum;
             const int gl = g0 - 1;
-            wait_or_flag(&pv_done[gl & 1], (uint32_t)(gl >> 1) & 1u, p.d_err);
+            await(&pv_done[gl & 1], (uint32_t)(gl >> 1) & 1u, p.d_err);
             tc_fence_after();
             float v[G];
             {
@@ -661,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if constexpr (L::kPar == 2) v[h] += odd[h * 64 + d];
                     const float lsum = (xsum[h] + xsum[GP + h]) + (xsum[2 * GP + h] + xsum[3 * GP + h]);
                     if (q.slot < 0) {
-                        static_cast<T *>(p.out)[(row0 + h) * D + d] = (T)(lsum != 0.f ? v[h] / lsum : 0.f);
+                        static_cast<T *>(p.out)[(row0 + h) * D + d] = (T)(lsum != 0.f ? __fdividef(v[h], lsum) : 0.f);
                     } else {
                         const size_t at = (size_t)q.slot * G + h;
                         p.ws_acc[at * D + d] = v[h];
@@ -669,10 +696,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
             }
-            // (the next piece's exchanges through xsum and odd come after its own barriers)
+            // (the next piece's sums go to xsum and odd after its own tiles' barriers)
             // the piece with the first tile says where the partials are
             if (fp.units && q.tile == 0 && t == 0)
-                fp.units[(size_t)q.s * p.num_kv_heads + q.kvh] = make_int2(q.slot, q.pieces);
+                fp.units[(size_t)q.s * p.num_kv_heads + q.kvh] =
+                    make_int2(q.slot, q.slot < 0 ? 1 : owner(walk.total, walk.ctas, q.at + q.whole - 1) - (int)blockIdx.x + 1);
         }
     }
     tc_fence_before();
