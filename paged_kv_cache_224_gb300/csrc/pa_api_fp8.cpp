@@ -92,7 +92,7 @@ struct DecodeWs {
     int ctas;
     size_t units = 0, acc = 0, ml = 0;
     DecodeWs(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_context_len) {
-        ctas = pa::fp8_decode_ctas(num_seqs, num_kv_heads, max_context_len);
+        ctas = pa::fp8_decode_ctas(num_seqs, num_kv_heads, num_heads / num_kv_heads, head_dim, max_context_len);
         if (max_context_len <= 128) return;
         const size_t n = (size_t)2 * ctas * (num_heads / num_kv_heads);
         units = round256((size_t)num_seqs * num_kv_heads * 2 * sizeof(int));

@@ -39,9 +39,9 @@ namespace pa {
 int launch_decode_fp8_bf16(int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
 int launch_decode_fp8_f16(int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
 
-int fp8_decode_ctas(int num_seqs, int num_kv_heads, int max_context_len) {
+int fp8_decode_ctas(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len) {
     const long long tiles = (long long)num_seqs * num_kv_heads * (((long long)max_context_len + 127) / 128);
-    const long long most = 2LL * sm_count();
+    const long long most = (long long)d8::ctas_per_sm(head_dim, group) * sm_count();
     return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }
 

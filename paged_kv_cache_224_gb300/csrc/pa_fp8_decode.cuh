@@ -33,7 +33,8 @@ struct Lay {
     static constexpr uint32_t kCols = 2 * N + NO <= 64 ? 64 : 128;  // TMEM: S^T x 2 buffers, O^T
     static constexpr uint32_t kColO = 2 * N;
     static constexpr int kSlot = kKeys * D;                 // one K or V tile
-    static constexpr int S = (GP == 4 ? 6 : 5) * kPar;      // ring slots: 96 or 80 KB, two CTAs to an SM
+    static constexpr int kCtas = ctas_per_sm(D, G);
+    static constexpr int S = D == 128 ? (GP == 4 ? 6 : 5) : (GP == 4 ? 6 : 10);  // ring slots: 96, 80 and 48 KB, 80 KB
     static constexpr int kRowP = kKeys / kPar;              // bytes of a row of P^T: a tile's keys of one parity
     // 2 x [3 GP rows][D]; the MMAs read N rows, the last GP of them whatever follows:
     // columns that nobody reads
@@ -45,8 +46,8 @@ struct Lay {
     static constexpr int kOffBar = kOffSc + kScaleRing * 16 * 16;
     static constexpr int kBars = 2 * S + 10 + 2 * kScaleRing;
     static constexpr int kOffLen = kOffBar + (kBars * 8 + 8 + 15) / 16 * 16;
-    static constexpr int kOffXch = kOffLen + kLens * 4 + 64;  // [2][4 warps][GP] maxima, [4][GP] sums, [2][GP] query scales, [G][64] sums of odd keys
-    static constexpr int kUsed = kOffXch + (2 * 4 * GP + 4 * GP + 2 * GP + (kPar == 2 ? G * 64 : 0)) * 4;
+    static constexpr int kOffXch = kOffLen + kLens * 4 + 64;  // [4 warps][GP] maxima, [4][GP] sums, [2][GP] query scales, [G][64] sums of odd keys
+    static constexpr int kUsed = kOffXch + (4 * GP + 4 * GP + 2 * GP + (kPar == 2 ? G * 64 : 0)) * 4;
     static constexpr int kAlloc = kUsed + 1024;             // room to align the base to 1 KB
 };
 
@@ -92,6 +93,18 @@ static __device__ __noinline__ void poll_or_flag(uint64_t *bar, uint32_t parity,
 }
 __device__ __forceinline__ void await(uint64_t *bar, uint32_t parity, int *d_err) {
     if (!mbar_test(bar, parity)) poll_or_flag(bar, parity, d_err);
+}
+
+// Barrier `id` over `count` threads, which all learn whether any of them came with `mine`.
+__device__ __forceinline__ bool bar_any(int id, int count, bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+        "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(count), "r"((uint32_t)mine)
+        : "memory");
+    return any != 0;
 }
 
 // Byte `at` of row `row` in rows of W bytes, swizzled over W bytes (W = 64 or 128).
@@ -266,7 +279,7 @@ __device__ __forceinline__ Walk begin(const Fp8DecodeParams &fp, int head_dim, i
 }
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
     decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams fp, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
     using L = Lay<D, G>;
@@ -289,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int *lens = reinterpret_cast<int *>(smem + L::kOffLen);
     float4 *scales = reinterpret_cast<float4 *>(smem + L::kOffSc);
     float *xmax = reinterpret_cast<float *>(smem + L::kOffXch);
-    float *xsum = xmax + 2 * 4 * GP, *qscale = xsum + 4 * GP, *odd = qscale + 2 * GP;
+    float *xsum = xmax + 4 * GP, *qscale = xsum + 4 * GP, *odd = qscale + 2 * GP;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * S; ++i) mbar_init(&full[i], 1);
         for (int b = 0; b < 2; ++b) {
@@ -565,50 +578,41 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int h = 0; h < G; ++h) z[h] = valid ? fmaf(z[h], sc.x * qf[h], sc.y) : -INFINITY;
                 }
-                // each head's maximum over the tile's 128 keys
-                const float wmax = warp_scatter<true, G>(z, lane);
-                if ((lane & (32 / G - 1)) == 0) xmax[(b * 4 + sw) * GP + lane / (32 / G)] = wmax;
-                named_bar_sync(1, 128);
-                float tmax[GP];
-                {
-                    const float4 *x = reinterpret_cast<const float4 *>(xmax + b * 4 * GP);
+                // The maxima that weights are relative to move only when some key is more
+                // than 2^8 above them (and at a piece's first keys): one barrier tells
+                // every thread whether any has seen that.
+                bool over = false;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w)
+                for (int h = 0; h < G; ++h) over |= z[h] > m_run[h] + kRescale;
+                if (bar_any(1, 128, over)) {
+                    const float wmax = warp_scatter<true, G>(z, lane);
+                    if ((lane & (32 / G - 1)) == 0) xmax[sw * GP + lane / (32 / G)] = wmax;
+                    named_bar_sync(1, 128);
+                    float alpha[GP];
 #pragma unroll
-                        for (int k = 0; k < GP / 4; ++k) {
-                            const float4 v = x[w * (GP / 4) + k];
-                            tmax[4 * k] = w ? fmaxf(tmax[4 * k], v.x) : v.x;
-                            tmax[4 * k + 1] = w ? fmaxf(tmax[4 * k + 1], v.y) : v.y;
-                            tmax[4 * k + 2] = w ? fmaxf(tmax[4 * k + 2], v.z) : v.z;
-                            tmax[4 * k + 3] = w ? fmaxf(tmax[4 * k + 3], v.w) : v.w;
-                        }
-                }
-                // rescale when a maximum has grown by more than 2^8 (the same decision in every thread)
-                bool grow = false;
-                float alpha[GP];
+                    for (int h = 0; h < GP; ++h) alpha[h] = 1.f;
 #pragma unroll
-                for (int h = 0; h < GP; ++h) alpha[h] = 1.f;
-#pragma unroll
-                for (int h = 0; h < G; ++h) {
-                    const float nm = tmax[h] > m_run[h] + kRescale ? tmax[h] : m_run[h];
-                    alpha[h] = m_run[h] == -INFINITY ? 0.f : fast_exp2(m_run[h] - nm);
-                    grow |= nm != m_run[h];
-                    m_run[h] = nm;
-                }
-                if (grow && j > 0) {
-                    // O must hold the PV of tile j-1 before it is scaled
-                    await(&pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1u, p.d_err);
-                    tc_fence_after();
-#pragma unroll
-                    for (int i0 = 0; i0 < N; i0 += 16) {
-                        float o[16];
-                        tmem_ld16(tmem + lane_off + col_o + i0, o);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= alpha[(i0 + i) % GP];
-                        tmem_st16(tmem + lane_off + col_o + i0, o);
+                    for (int h = 0; h < G; ++h) {
+                        const float tmax = fmaxf(fmaxf(xmax[h], xmax[GP + h]), fmaxf(xmax[2 * GP + h], xmax[3 * GP + h]));
+                        const float nm = tmax > m_run[h] + kRescale ? tmax : m_run[h];
+                        alpha[h] = m_run[h] == -INFINITY ? 0.f : fast_exp2(m_run[h] - nm);
+                        l_part[h] *= alpha[h];
+                        m_run[h] = nm;
                     }
+                    if (j > 0) {
+                        // O must hold the PV of tile g-1 before it is scaled
+                        await(&pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1u, p.d_err);
+                        tc_fence_after();
 #pragma unroll
-                    for (int h = 0; h < G; ++h) l_part[h] *= alpha[h];
+                        for (int i0 = 0; i0 < N; i0 += 16) {
+                            float o[16];
+                            tmem_ld16(tmem + lane_off + col_o + i0, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= alpha[(i0 + i) % GP];
+                            tmem_st16(tmem + lane_off + col_o + i0, o);
+                        }
+                        tmem_wait_st();
+                    }
                 }
                 float pr[G + (G & 1)];
                 if constexpr (G & 1) pr[G] = 0.f;
@@ -652,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                         sts128(sb + sl * L::kSlot + swizzled<128>(t / L::kPar, (t % L::kPar) * D + c * 16), zero);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive1(&p_full[b]);
             }
@@ -713,12 +716,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Log-sum-exp merge of the pieces of what was cut, one warp per (sequence, query head):
 //   M = max m_i,  w_i = 2^(m_i - M),  out = sum w_i acc_i / sum w_i l_i.
+// (It does not let the kernel behind it start early: a decode placed beside the last of
+// these CTAs finds less room than its grid counts on, and what does not fit runs after
+// the rest.  256 contexts of 2048 tokens, 8/8 heads of 64: 144 us, against 88.)
 template <typename T, int D>
 __global__ void __launch_bounds__(128) merge_fp8_kernel(const __grid_constant__ Fp8DecodeParams fp) {
     constexpr int V = D / 32;  // values per lane
     const DecodeParams &p = fp.d;
     pdl_wait();                // the decode kernel's partials are complete and visible
-    pdl_trigger();
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= (long long)p.num_seqs * p.num_heads) return;

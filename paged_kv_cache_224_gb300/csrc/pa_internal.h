@@ -216,7 +216,11 @@ struct Fp8DecodeParams {
     int2 *units;                 // [B][Hkv] (slot of the first piece, pieces); null where nothing can be cut
     int ctas;
 };
-int fp8_decode_ctas(int num_seqs, int num_kv_heads, int max_context_len);
+int fp8_decode_ctas(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len);
+namespace d8 {
+// CTAs of the decode over an 8-bit cache that an SM holds.
+constexpr int ctas_per_sm(int head_dim, int group) { return head_dim == 64 && group <= 4 ? 3 : 2; }
+}  // namespace d8
 int launch_decode_fp8(pa_dtype dt, int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
 // The codes of the sequences' first blocks as values of dt, laid end to end: block
 // j of sequence i becomes block first[i] + j of k_out and v_out, whose own table is
