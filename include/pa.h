@@ -642,8 +642,9 @@ PA_API int pa_selftest_bounded_wait(int max_polls, int *d_err, long long *d_cycl
  *              on entry is ignored; it must not be shared with work that
  *              overlaps the call on the device.
  * num_pairs above PA_COPY_MAX_PAIRS returns PA_ERR_OUT_OF_RANGE; a missing
- * or too small workspace returns PA_ERR_WORKSPACE.  Three launches (clear
- * the table, count, copy).
+ * or too small workspace returns PA_ERR_WORKSPACE.  One launch up to 1024
+ * pairs (each copy looks through the list), three beyond (clear the table,
+ * count, copy).
  */
 #define PA_COPY_MAX_PAIRS (1 << 26)
 PA_API size_t pa_copy_blocks_workspace_bytes(int num_pairs);

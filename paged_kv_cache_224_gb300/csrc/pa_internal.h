@@ -155,6 +155,7 @@ struct RotaryParams {
     // 8-bit cache: k_cache and v_cache hold codes, these their scales [NB][Hkv]
     uint8_t *k_scales;
     uint8_t *v_scales;
+    int tokens_per_cta;          // of the 8-bit cache write, 1 .. 32
 };
 
 // One eviction (see pa_evict): the kernels mark, select and copy.
