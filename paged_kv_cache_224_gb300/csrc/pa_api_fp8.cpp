@@ -49,7 +49,7 @@ int rotary_params(pa::RotaryParams &p, void *query_out, int64_t query_out_stride
         (rot_dim > 0 && (!positions || !inv_freq)))
         return PA_ERR_INVALID_ARG;
     if (!aligned16(query_out) || !aligned16(query) || !aligned16(key) || !aligned16(value) || !aligned16(k_cache) ||
-        !aligned16(v_cache) || (query_out_stride | query_stride | key_stride | value_stride) % 8)
+        !aligned16(v_cache) || !aligned16(query_norm) || !aligned16(key_norm) || (query_out_stride | query_stride | key_stride | value_stride) % 8)
         return PA_ERR_ALIGNMENT;
     p.query_out = query_out;
     p.query = query;
@@ -159,7 +159,7 @@ int pa_norm_rotary_and_cache(void *query_out, int64_t query_out_stride, const vo
     if (num_heads == 0) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PA_OK;
     if (!query_norm) return PA_ERR_INVALID_ARG;
-    return pa::launch_rotary(dtype, p, static_cast<cudaStream_t>(stream));
+    return pa::launch_norm_rotary(dtype, p, static_cast<cudaStream_t>(stream));
 }
 
 int pa_rotary_and_cache_fp8(void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,

@@ -42,6 +42,12 @@ __device__ __forceinline__ float holdable(float x) {
     return finite ? x : __uint_as_float(0x7fc00000u);
 }
 
+// Bits of the largest magnitude that holdable() leaves as it is.
+template <typename T>
+__device__ __forceinline__ unsigned top_held() {
+    return std::is_same<T, __half>::value ? 0x47700000u : 0x7f7fffffu;  // 61440, the largest float
+}
+
 // |x|, or 0 where it is not finite: what counts towards a scale.
 __device__ __forceinline__ float counted(float x) {
     const float a = fabsf(x);

@@ -28,16 +28,19 @@ namespace {
 
 constexpr int kHeadsPerCta = 4;
 constexpr int kStoreThreads = 64 * kHeadsPerCta;  // at most
-constexpr int kPasses = 4;                        // rows that a lane holds at a time
 
-template <typename T, bool kInterleaved, bool kNorm>
-__global__ void __launch_bounds__(kStoreThreads, 2) store_fp8_kernel(const __grid_constant__ RotaryParams p) {
+// kPasses: rows that a lane holds at a time.
+template <typename T, bool kInterleaved, bool kNorm, int kPasses>
+__global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8_kernel(const __grid_constant__ RotaryParams p) {
     __shared__ int s_tok[kStoreMaxBlock];   // token of each row, -1: not written
     __shared__ int s_row[kStoreMaxBlock];   // the written rows
     __shared__ int s_rows, s_late;
     __shared__ unsigned s_heads;            // tokens that may be the first of their block
-    __shared__ float2 s_cs[kPasses * 32 * 8];  // [rows of a chunk][rot_dim / 2]: 8 pairs a lane at most
-    __shared__ float s_w[kNorm ? kRotaryMaxDim : 1];
+    // [rows of a chunk][4 planes][units]: cosines of pairs 8c .. 8c+3, 8c+4 .. 8c+7, then
+    // the sines alike, so that a row's lanes read side by side
+    __shared__ float4 s_cs[kPasses * 32 * 4];
+    __shared__ long long s_frac[kRotaryMaxDim / 2];  // turns per position, 2^-64
+    __shared__ bool s_odd[kRotaryMaxDim / 2];        // whose frequency is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = p.block_size, D = p.head_dim, shift = __ffs(bs) - 1;
     const int head0 = blockIdx.y * kHeadsPerCta, heads = min(kHeadsPerCta, p.num_kv_heads - head0);
@@ -46,6 +49,7 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_fp8_kernel(const __gri
     // waits for it at the end; any other launch starts when what was before it is done)
     // Of this CTA's tokens, those that do not follow another one of their block:
     const int first = blockIdx.x * p.tokens_per_cta;
+    const int upr = D / 16, half = p.rot_dim / 2, lanes = norm_lanes(upr);
     if (warp == 0) {
         const int t = first + lane;
         bool head = lane < p.tokens_per_cta && t < p.num_tokens;
@@ -60,6 +64,11 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_fp8_kernel(const __gri
         }
         const unsigned m = __ballot_sync(kFull, head);
         if (lane == 0) s_heads = m;
+    }
+    for (int i = tid; i < half; i += blockDim.x) {
+        const float f = p.inv_freq[i];
+        s_odd[i] = !isfinite(f);
+        s_frac[i] = turn_fraction(f);
     }
     __syncthreads();
     for (unsigned heads_left = s_heads; heads_left; heads_left &= heads_left - 1) {
@@ -90,7 +99,7 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_fp8_kernel(const __gri
         const int odd = (int)(reinterpret_cast<uintptr_t>(p.slots) >> 3 & 1u);  // slots before the first 16-byte boundary
         const longlong2 *pairs = reinterpret_cast<const longlong2 *>(p.slots + odd);
         const int npairs = (p.num_tokens - odd) / 2;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = tid; i < npairs; i += blockDim.x) {
             const longlong2 v = pairs[i];
             look(v.x, odd + 2 * i);
@@ -110,10 +119,7 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_fp8_kernel(const __gri
             }
             if (lane == 0) s_rows = n;
         }
-        if constexpr (kNorm)
-            for (int i = tid; i < D; i += blockDim.x) s_w[i] = to_float(static_cast<const T *>(p.key_norm)[i]);
         __syncthreads();
-        const int upr = D / 16, half = p.rot_dim / 2, lanes = norm_lanes(upr);
         const int c = lane % lanes, k0 = lane / lanes, per_warp = 32 / lanes;  // rows k0, + per_warp, ... are this lane's
         const int per_chunk = kPasses * per_warp;
         const int nrows = s_rows, chunks = (nrows + per_chunk - 1) / per_chunk;
@@ -122,9 +128,16 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_fp8_kernel(const __gri
         const int e0 = turned && !kInterleaved ? c * 8 : c * 16;
         const int e1 = turned && !kInterleaved ? half + c * 8 : e0 + 8;
         const float per_dim = 1.f / (float)D;
+        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+        if (kNorm && which == 0 && c < upr) {
+            w0 = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key_norm) + e0);
+            w1 = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key_norm) + e1);
+        }
+
         float a[kPasses][8], b[kPasses][8];  // the units of this lane's rows, as they are to be held
         auto rows_of = [&](int ch) { return min(per_chunk, nrows - ch * per_chunk); };
-        // a chunk's units: their loads, the angles meanwhile (by all warps), then the arithmetic
+        // a chunk's units: their loads, the angles meanwhile (by all warps), then the
+        // arithmetic; returns the largest magnitude of this lane's (lanes without a row have 0)
         auto compute = [&](int ch) {
             const int n = rows_of(ch);
             uint4 va[kPasses], vb[kPasses];
@@ -140,14 +153,19 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_fp8_kernel(const __gri
             }
             if (half > 0) {
                 __syncthreads();  // the angles of the chunk before are read
-                for (int i = tid; i < n * half; i += blockDim.x) {
-                    const int k = i / half, pair = i - k * half;
-                    const float f = p.inv_freq[pair];
+                const int by_row = blockDim.x / half, by_pair = blockDim.x - by_row * half;
+                int k = tid / half, pair = tid - k * half;
+                while (k < n) {
                     float sn, cs;
-                    turn_sincos(turn_fraction(f),
+                    turn_sincos(s_frac[pair],
                                 p.positions[(long long)p.pair_axis[pair] * p.num_tokens + s_tok[s_row[ch * per_chunk + k]]], sn, cs);
-                    if (!isfinite(f)) sn = cs = __int_as_float(0x7fc00000);
-                    s_cs[i] = make_float2(cs, sn);
+                    if (s_odd[pair]) sn = cs = __int_as_float(0x7fc00000);
+                    float *q = reinterpret_cast<float *>(s_cs) + k * 2 * half + (pair >> 2 & 1) * (half / 2) + (pair >> 3) * 4 + (pair & 3);
+                    q[0] = cs;
+                    q[half] = sn;
+                    k += by_row;
+                    pair += by_pair;
+                    if (pair >= half) pair -= half, ++k;
                 }
                 __syncthreads();
             }
@@ -156,60 +174,48 @@ __global__ void __launch_bounds__(kStoreThreads, 2) store_fp8_kernel(const __gri
                 unpack8<T>(va[i], a[i]);
                 unpack8<T>(vb[i], b[i]);
                 if (which == 0) {
-                    if constexpr (kNorm) {
-                        float sum = 0.f;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) sum = fmaf(a[i][x], a[i][x], fmaf(b[i][x], b[i][x], sum));
-                        for (int m = lanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(kFull, sum, m);
-                        const float r = __frsqrt_rn(fmaf(sum, per_dim, p.eps));
-                        if (c < upr) {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                a[i][x] *= r * s_w[e0 + x];
-                                b[i][x] *= r * s_w[e1 + x];
-                            }
-                        }
-                    }
+                    if constexpr (kNorm) norm_unit<T>(a[i], b[i], lanes, per_dim, p.eps, w0, w1);
                     const int k = k0 + i * per_warp;
                     if (turned && k < n) {
-                        const float2 *q = s_cs + k * half + c * 8;
-                        if (kInterleaved) {
+                        float cs[8], sn[8];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float u = a[i][2 * x], v = a[i][2 * x + 1], z = b[i][2 * x], w = b[i][2 * x + 1];
-                                a[i][2 * x] = fmaf(u, q[x].x, -(v * q[x].y));
-                                a[i][2 * x + 1] = fmaf(v, q[x].x, u * q[x].y);
-                                b[i][2 * x] = fmaf(z, q[4 + x].x, -(w * q[4 + x].y));
-                                b[i][2 * x + 1] = fmaf(w, q[4 + x].x, z * q[4 + x].y);
-                            }
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const float u = a[i][x], v = b[i][x];
-                                a[i][x] = fmaf(u, q[x].x, -(v * q[x].y));
-                                b[i][x] = fmaf(v, q[x].x, u * q[x].y);
-                            }
+                        for (int x = 0; x < 2; ++x) {
+                            const float4 u = s_cs[k * (half / 2) + x * (half / 8) + c], v = s_cs[k * (half / 2) + (2 + x) * (half / 8) + c];
+                            cs[4 * x] = u.x, cs[4 * x + 1] = u.y, cs[4 * x + 2] = u.z, cs[4 * x + 3] = u.w;
+                            sn[4 * x] = v.x, sn[4 * x + 1] = v.y, sn[4 * x + 2] = v.z, sn[4 * x + 3] = v.w;
                         }
+                        turn_unit<kInterleaved>(a[i], b[i], cs, sn);
                     }
                 }
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    a[i][x] = holdable<T>(a[i][x]);
-                    b[i][x] = holdable<T>(b[i][x]);
-                }
             }
-        };
-        // ---- the largest magnitude (lanes without a row or a unit have zeros)
-        float amax = 0.f;
-        for (int ch = 0; ch < chunks; ++ch) {
-            compute(ch);
+            // (the bits of magnitudes order as they do, infinities and NaN above all)
+            unsigned top = 0u;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i)
-                if (k0 + i * per_warp < rows_of(ch) && c < upr) {
+                if (k0 + i * per_warp < n && c < upr) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) amax = fmaxf(amax, fmaxf(counted(a[i][x]), counted(b[i][x])));
+                    for (int x = 0; x < 8; ++x)
+                        top = max(top, max(__float_as_uint(a[i][x]) & 0x7fffffffu, __float_as_uint(b[i][x]) & 0x7fffffffu));
                 }
-        }
+            if (__any_sync(kFull, top > top_held<T>())) {  // rare: what cannot be held as it is
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const bool on = k0 + i * per_warp < n && c < upr;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        a[i][x] = holdable<T>(a[i][x]);
+                        b[i][x] = holdable<T>(b[i][x]);
+                        if (on) most = fmaxf(most, fmaxf(counted(a[i][x]), counted(b[i][x])));
+                    }
+                }
+                return most;
+            }
+            return __uint_as_float(top);
+        };
+        // ---- the largest magnitude
+        float amax = 0.f;
+        for (int ch = 0; ch < chunks; ++ch) amax = fmaxf(amax, compute(ch));
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
         // ---- the scale, and the rows that it moves
@@ -308,20 +314,28 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const __grid_constant__
 
 // After this call's query kernel (`beside`) it may start while that one runs; else not
 // before everything that was queued has ended.
-template <typename T, bool kInterleaved, bool kNorm>
+template <typename T, bool kInterleaved, bool kNorm, int kPasses>
 cudaError_t store_t(const RotaryParams &p, bool beside, cudaStream_t stream) {
     const unsigned splits = (unsigned)((p.num_kv_heads + kHeadsPerCta - 1) / kHeadsPerCta);
     const dim3 grid((unsigned)((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta), splits);
     const dim3 block(64 * std::min(kHeadsPerCta, p.num_kv_heads));
-    if (beside) return launch_pdl(store_fp8_kernel<T, kInterleaved, kNorm>, grid, block, 0, stream, p);
-    store_fp8_kernel<T, kInterleaved, kNorm><<<grid, block, 0, stream>>>(p);
+    auto kern = store_fp8_kernel<T, kInterleaved, kNorm, kPasses>;
+    if (beside) return launch_pdl(kern, grid, block, 0, stream, p);
+    kern<<<grid, block, 0, stream>>>(p);
     return cudaPeekAtLastError();
+}
+
+template <typename T, bool kInterleaved, bool kNorm>
+cudaError_t store_passes(const RotaryParams &p, bool beside, cudaStream_t stream) {
+    return p.tokens_per_cta == 1 ? store_t<T, kInterleaved, kNorm, 1>(p, beside, stream)
+                                 : store_t<T, kInterleaved, kNorm, 4>(p, beside, stream);
 }
 
 template <typename T>
 cudaError_t store_dtype(const RotaryParams &p, bool beside, cudaStream_t stream) {
-    if (p.key_norm) return p.interleaved ? store_t<T, true, true>(p, beside, stream) : store_t<T, false, true>(p, beside, stream);
-    return p.interleaved ? store_t<T, true, false>(p, beside, stream) : store_t<T, false, false>(p, beside, stream);
+    if (p.key_norm)
+        return p.interleaved ? store_passes<T, true, true>(p, beside, stream) : store_passes<T, false, true>(p, beside, stream);
+    return p.interleaved ? store_passes<T, true, false>(p, beside, stream) : store_passes<T, false, false>(p, beside, stream);
 }
 
 }  // namespace
@@ -330,7 +344,7 @@ int launch_store_fp8(pa_dtype dt, const RotaryParams &p, cudaStream_t stream) {
     if (p.num_heads > 0) {
         RotaryParams q = p;
         q.num_kv_heads = 0;
-        const int rc = launch_rotary(dt, q, stream);
+        const int rc = q.query_norm ? launch_norm_rotary(dt, q, stream) : launch_rotary(dt, q, stream);
         if (rc != PA_OK) return rc;
     }
     const bool beside = p.num_heads > 0;

@@ -244,6 +244,8 @@ int launch_reshape_and_cache(const void *key, const void *value, void *k_cache, 
                              const int64_t *slots, int num_tokens, int num_kv_heads, int head_dim,
                              int block_size, int num_blocks, int *d_err, cudaStream_t stream);
 int launch_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream);
+// With the norms whose weights p has; num_kv_heads may be 0.
+int launch_norm_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream);
 // Keys (normed and rotated as p says) and values into an 8-bit cache, then the
 // queries as launch_rotary does; block_size up to kStoreMaxBlock.
 constexpr int kStoreMaxBlock = 128;

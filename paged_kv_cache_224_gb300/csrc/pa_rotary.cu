@@ -38,26 +38,10 @@
 namespace pa {
 namespace {
 
-// A token's kv head 0 row: element offset in the caches, or -1 for none.
-__device__ __forceinline__ long long cache_row(const RotaryParams &p, long long slot) {
-    if (slot < 0) return -1;
-    if (slot >= (long long)p.num_blocks * p.block_size) {
-        flag_error(p.d_err, PA_DEVERR_SLOT_RANGE);
-        return -1;
-    }
-    // most pools have fewer than 2^32 slots, and a 32-bit division costs a third
-    const long long blk = (slot >> 32) ? slot / p.block_size : (long long)((unsigned)slot / (unsigned)p.block_size);
-    return (blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size)) * p.head_dim;
-}
-
 constexpr int kMaxThreads = 320;
 
-// kNorm: queries and keys are first divided by their head's root mean square and
-// multiplied by its weights, in fp32 like the rotation that follows, one rounding
-// for both.  A head's units then sit in `lanes` adjacent lanes (a power of two,
-// the last of them idle where a head has fewer units), which add up their squares.
-template <typename T, bool kInterleaved, bool kNorm>
-__global__ void __launch_bounds__(kMaxThreads, kNorm ? 3 : 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kMaxThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
     // [2 tokens]: cosines of pairs 8c .. 8c+3, 8c+4 .. 8c+7, then the sines
     // alike, [4][unit c], so that a warp's reads are consecutive
     __shared__ float4 s_cs[2][4][kRotaryMaxDim / 16];
@@ -65,22 +49,14 @@ __global__ void __launch_bounds__(kMaxThreads, kNorm ? 3 : 4) rotary_kernel(cons
     const int tid = threadIdx.x;
     const int upr = p.head_dim / 16;  // units of a head; the first rot_dim / 16 are turned
     const int half = p.rot_dim / 2;
-    const int lanes = kNorm ? norm_lanes(upr) : upr;
-    const int c = tid % lanes;
-    const int row0 = tid / lanes, rows_step = blockDim.x / lanes;
+    const int c = tid % upr;
+    const int row0 = tid / upr, rows_step = blockDim.x / upr;
     const int rows_qk = p.num_heads + p.num_kv_heads, rows = rows_qk + p.num_kv_heads;
     const bool turned = c < p.rot_dim / 16;
     // element offsets of the unit's two vectors inside a head (the values' too: e0 and e1 cover the row either way)
     const int e0 = turned && !kInterleaved ? c * 8 : c * 16;
     const int e1 = turned && !kInterleaved ? half + c * 8 : e0 + 8;
-    // threads past the last whole row of units, and lanes past a head's units, move nothing
-    const bool active = row0 < rows_step && (!kNorm || c < upr);
-
-    // kNorm: the weights of queries and of keys, and the lanes of this thread's head
-    __shared__ float4 s_w[kNorm ? 2 : 1][kNorm ? kRotaryMaxDim / 4 : 1];
-    const unsigned mates = (lanes < 32 ? (1u << lanes) - 1u : kFull) << ((tid & 31) & ~(lanes - 1) & 31);
-
-    const float per_dim = 1.f / (float)p.head_dim;
+    const bool active = row0 < rows_step;  // threads past the last whole row of units move nothing
 
     pdl_wait();
     pdl_trigger();  // what follows may be placed; it waits for these writes
@@ -128,18 +104,11 @@ __global__ void __launch_bounds__(kMaxThreads, kNorm ? 3 : 4) rotary_kernel(cons
         va = ldg_stream(s + e0);
         vb = ldg_stream(s + e1);
     }
-    if constexpr (kNorm) {
-        for (int i = tid; i < 2 * p.head_dim; i += blockDim.x) {
-            const bool of_key = i >= p.head_dim;
-            const int d = i - (of_key ? p.head_dim : 0);
-            reinterpret_cast<float *>(s_w[of_key])[d] = to_float(static_cast<const T *>(of_key ? p.key_norm : p.query_norm)[d]);
-        }
-    }
     prepare(t, 0);
     __syncthreads();
     for (; t < p.num_tokens; t += gridDim.x, buf ^= 1) {
         const int t_next = t + gridDim.x;
-        if (active || kNorm) {
+        if (active) {
             const long long dst = s_dst[buf];
             float cs[8], sn[8];
             if (turned) {
@@ -154,34 +123,16 @@ __global__ void __launch_bounds__(kMaxThreads, kNorm ? 3 : 4) rotary_kernel(cons
                 // the next unit's vectors, of this token or the next
                 const bool more = row + rows_step < rows;
                 uint4 na = va, nb = vb;
-                if (active && (more || t_next < p.num_tokens)) {
+                if (more || t_next < p.num_tokens) {
                     const T *s = more ? src_of(t, row + rows_step) : src_of(t_next, row0);
                     na = ldg_stream(s + e0);
                     nb = ldg_stream(s + e1);
                 }
-                if ((turned || kNorm) && row < rows_qk) {
+                if (turned && row < rows_qk) {
                     float a[8], b[8];
                     unpack8<T>(va, a);
                     unpack8<T>(vb, b);
-                    if constexpr (kNorm) {
-                        float sum = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) sum = fmaf(a[k], a[k], fmaf(b[k], b[k], sum));
-                        for (int m = lanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(mates, sum, m);
-                        const float r = __frsqrt_rn(fmaf(sum, per_dim, p.eps));
-                        const float *w = reinterpret_cast<const float *>(s_w[row >= p.num_heads]);
-                        if (active) {
-#pragma unroll
-                            for (int k = 0; k < 8; k += 4) {
-                                const float4 x = *reinterpret_cast<const float4 *>(w + e0 + k);
-                                const float4 y = *reinterpret_cast<const float4 *>(w + e1 + k);
-                                a[k] *= r * x.x, a[k + 1] *= r * x.y, a[k + 2] *= r * x.z, a[k + 3] *= r * x.w;
-                                b[k] *= r * y.x, b[k + 1] *= r * y.y, b[k + 2] *= r * y.z, b[k + 3] *= r * y.w;
-                            }
-                        }
-                    }
-                    if (kNorm && !turned) {
-                    } else if (kInterleaved) {
+                    if (kInterleaved) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float x = a[2 * k], y = a[2 * k + 1], z = b[2 * k], w = b[2 * k + 1];
@@ -202,8 +153,7 @@ __global__ void __launch_bounds__(kMaxThreads, kNorm ? 3 : 4) rotary_kernel(cons
                     vb = pack8<T>(b);
                 }
                 T *out = nullptr;
-                if (kNorm && !active) {
-                } else if (row < p.num_heads) {
+                if (row < p.num_heads) {
                     out = static_cast<T *>(p.query_out) + t * p.query_out_stride + row * p.head_dim;
                 } else if (dst >= 0) {
                     const bool is_v = row >= rows_qk;
@@ -223,9 +173,9 @@ __global__ void __launch_bounds__(kMaxThreads, kNorm ? 3 : 4) rotary_kernel(cons
     }
 }
 
-template <typename T, bool kInterleaved, bool kNorm>
+template <typename T, bool kInterleaved>
 int launch_t(const RotaryParams &p, int threads, cudaStream_t stream) {
-    auto kern = rotary_kernel<T, kInterleaved, kNorm>;
+    auto kern = rotary_kernel<T, kInterleaved>;
     static std::atomic<int> resident[kMaxThreads / 32 + 1];  // CTAs an SM holds, by block size; asked for once
     int n = resident[threads / 32].load(std::memory_order_relaxed);
     if (n == 0) {
@@ -241,15 +191,12 @@ int launch_t(const RotaryParams &p, int threads, cudaStream_t stream) {
 int launch_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream) {
     // A token's units take one pass of up to kMaxThreads threads; the grid
     // is one wave of resident CTAs, which walk the tokens.
-    const bool norm = p.query_norm != nullptr;
-    const int upr = p.head_dim / 16;
-    const int units = (p.num_heads + 2 * p.num_kv_heads) * (norm ? norm_lanes(upr) : upr);
+    const int units = (p.num_heads + 2 * p.num_kv_heads) * (p.head_dim / 16);
     const int passes = (units + kMaxThreads - 1) / kMaxThreads;
     const int threads = std::max(64, ((units + passes - 1) / passes + 31) / 32 * 32);
-#define PA_ROTARY(TT, II) (norm ? launch_t<TT, II, true>(p, threads, stream) : launch_t<TT, II, false>(p, threads, stream))
-    if (dt == PA_BF16) return p.interleaved ? PA_ROTARY(__nv_bfloat16, true) : PA_ROTARY(__nv_bfloat16, false);
-    return p.interleaved ? PA_ROTARY(__half, true) : PA_ROTARY(__half, false);
-#undef PA_ROTARY
+    if (dt == PA_BF16) return p.interleaved ? launch_t<__nv_bfloat16, true>(p, threads, stream)
+                                             : launch_t<__nv_bfloat16, false>(p, threads, stream);
+    return p.interleaved ? launch_t<__half, true>(p, threads, stream) : launch_t<__half, false>(p, threads, stream);
 }
 
 }  // namespace pa

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "pa_device.cuh"
+#include "pa_internal.h"
 
 namespace pa {
 
@@ -12,6 +13,18 @@ __device__ __forceinline__ uint4 ldg_stream(const void *p) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
+}
+
+// A token's kv head 0 row: element offset in the caches, or -1 for none.
+__device__ __forceinline__ long long cache_row(const RotaryParams &p, long long slot) {
+    if (slot < 0) return -1;
+    if (slot >= (long long)p.num_blocks * p.block_size) {
+        flag_error(p.d_err, PA_DEVERR_SLOT_RANGE);
+        return -1;
+    }
+    // most pools have fewer than 2^32 slots, and a 32-bit division costs a third
+    const long long blk = (slot >> 32) ? slot / p.block_size : (long long)((unsigned)slot / (unsigned)p.block_size);
+    return (blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size)) * p.head_dim;
 }
 
 // f / (2 pi) modulo 1, in 2^-64, to half a unit, for finite f.  With f = m 2^e
@@ -47,7 +60,56 @@ __host__ __device__ constexpr int norm_lanes(int units) {
     return units <= 1 ? 1 : units <= 2 ? 2 : units <= 4 ? 4 : units <= 8 ? 8 : 16;
 }
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+// Turn the pairs of a unit (two vectors of a head) by its cosines and sines.
+template <bool kInterleaved>
+__device__ __forceinline__ void turn_unit(float (&a)[8], float (&b)[8], const float (&cs)[8], const float (&sn)[8]) {
+    if (kInterleaved) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float x = a[2 * k], y = a[2 * k + 1], z = b[2 * k], w = b[2 * k + 1];
+            a[2 * k] = fmaf(x, cs[k], -(y * sn[k]));
+            a[2 * k + 1] = fmaf(y, cs[k], x * sn[k]);
+            b[2 * k] = fmaf(z, cs[4 + k], -(w * sn[4 + k]));
+            b[2 * k + 1] = fmaf(w, cs[4 + k], z * sn[4 + k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float x = a[k], y = b[k];
+            a[k] = fmaf(x, cs[k], -(y * sn[k]));
+            b[k] = fmaf(y, cs[k], x * sn[k]);
+        }
+    }
+}
+
+// 1 / sqrt(x), within 2^-22.9 of itself.
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Divide a head, held by `lanes` adjacent lanes, by its root mean square and multiply it
+// by its weights (w0, w1: those of the unit's two vectors).
+template <typename T>
+__device__ __forceinline__ void norm_unit(float (&a)[8], float (&b)[8], int lanes, float per_dim, float eps, const uint4 &w0,
+                                          const uint4 &w1) {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        s0 = fmaf(a[k], a[k], s0);
+        s1 = fmaf(b[k], b[k], s1);
+    }
+    float sum = s0 + s1;
+    for (int m = lanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(kFull, sum, m);
+    const float r = rsqrt_approx(fmaf(sum, per_dim, eps));
+    float w[8];
+    unpack8<T>(w0, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = a[k] * r * w[k];
+    unpack8<T>(w1, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = b[k] * r * w[k];
+}
 
 }  // namespace pa

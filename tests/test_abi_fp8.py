@@ -54,7 +54,7 @@ def test_rotary_refusals(lib, call):
     assert call(lib, D=64, R=128) == -3
     assert call(lib, axis=[0] * 63 + [1]) == -3
     assert call(lib, qs=1016) == -3 and call(lib, ks=0) == -3
-    assert call(lib, qs=1028) == -6 and call(lib, v=BUF + 8) == -6
+    assert call(lib, qs=1028) == -6 and call(lib, v=BUF + 8) == -6 and call(lib, kn=BUF + 2) == -6
 
 
 def test_norms_are_required_where_they_are_the_point(lib):
