@@ -610,6 +610,23 @@ PA_API int pa_copy_blocks_fp8(uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_sca
                               int num_blocks, void *workspace, size_t workspace_bytes, int *d_err, void *stream);
 
 /*
+ * pa_call_packed -- one of the calls above with its arguments in an array, for callers
+ * whose foreign-function interface costs more per argument than these calls' kernels
+ * take (the Python binding): args[i] is argument i of the call's prototype, a pointer or
+ * integer as a 64-bit integer, a float as a double.  Results and errors are the call's;
+ * PA_ERR_INVALID_ARG for an unknown call or a null array.
+ */
+enum {
+    PA_CALL_NORM_ROTARY_AND_CACHE = 0,
+    PA_CALL_ROTARY_AND_CACHE_FP8 = 1,
+    PA_CALL_RESHAPE_AND_CACHE_FP8 = 2,
+    PA_CALL_DECODE_FP8 = 3,
+    PA_CALL_PREFILL_BATCH_FP8 = 4,
+    PA_CALL_COPY_BLOCKS_FP8 = 5
+};
+PA_API int pa_call_packed(int call, const int64_t *args);
+
+/*
  * Failure detection.  Every wait inside the kernels (on TMA copies, MMA
  * completions, other warps) is bounded: after pa_bounded_wait_polls() polls
  * it gives up, ORs PA_DEVERR_TIMEOUT into *d_err and lets the kernel finish,

@@ -12,6 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -37,7 +38,7 @@ EXPORTED = ("pa_status_string", "pa_reshape_and_cache", "pa_decode_partition_tok
             "pa_decode_common_prefix", "pa_bm_evict_sequence", "pa_bm_evict_sequences",
             "pa_norm_rotary_and_cache", "pa_reshape_and_cache_fp8", "pa_rotary_and_cache_fp8",
             "pa_decode_fp8_workspace_bytes", "pa_decode_fp8", "pa_prefill_batch_fp8_workspace_bytes",
-            "pa_prefill_batch_fp8", "pa_copy_blocks_fp8")
+            "pa_prefill_batch_fp8", "pa_copy_blocks_fp8", "pa_call_packed")
 PA_ERR_NO_BLOCKS = -8
 PA_ERR_SCRATCH_LIMIT = -7
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -156,6 +157,8 @@ def lib() -> ctypes.CDLL:
         L.pa_prefill_batch_fp8.restype = i
         L.pa_copy_blocks_fp8.argtypes = [p] * 5 + [i] * 5 + [p, sz, p, p]
         L.pa_copy_blocks_fp8.restype = i
+        L.pa_call_packed.argtypes = [i, ctypes.c_char_p]
+        L.pa_call_packed.restype = i
         L.pa_bounded_wait_polls.argtypes = []
         L.pa_bounded_wait_polls.restype = i
         L.pa_selftest_bounded_wait.argtypes = [i, p, p, p]
@@ -771,6 +774,39 @@ def pa_decode_common_prefix(out, query, k_cache, v_cache, block_tables, context_
 # ---- head norms, and caches of 8 bits ---------------------------------------------
 
 
+# (number in the C interface's pa_call_packed, the arguments' layout): a ctypes call
+# with thirty arguments costs more than these calls' kernels take
+_PACKED = {
+    "pa_norm_rotary_and_cache": (0, struct.Struct("=19qd9q").pack),
+    "pa_rotary_and_cache_fp8": (1, struct.Struct("=21qd9q").pack),
+    "pa_reshape_and_cache_fp8": (2, struct.Struct("=15q").pack),
+    "pa_decode_fp8": (3, struct.Struct("=16qd5q").pack),
+    "pa_prefill_batch_fp8": (4, struct.Struct("=16qd5q").pack),
+    "pa_copy_blocks_fp8": (5, struct.Struct("=14q").pack),
+}
+_packed = None
+
+
+def _call_packed(name, index, *args) -> None:
+    """``_call`` through ``pa_call_packed`` (pointers and integers as ints, None not allowed)."""
+    global _packed
+    if _packed is None:
+        _packed = lib().pa_call_packed
+    number, pack = _PACKED[name]
+    if _current_device() == index:
+        rc = _packed(number, pack(*args))
+    else:
+        with torch.cuda.device(index):
+            rc = _packed(number, pack(*args))
+    if rc:
+        raise PAError(name, rc)
+
+
+def _at(t) -> int:
+    """The address of ``t``, 0 for None."""
+    return 0 if t is None else t.data_ptr()
+
+
 def _dt_int(dtype) -> int:
     if dtype is torch.bfloat16:
         return PA_BF16
@@ -781,7 +817,8 @@ def _dt_int(dtype) -> int:
 
 def _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq, query_norm,
                  key_norm, eps, pair_axis, interleaved):
-    """The arguments up to value_stride, and from positions to eps, of a rotary call."""
+    """The arguments up to value_stride, those from positions to dtype, and the array
+    that pair_axis points into, of a rotary call."""
     if slot_mapping.dtype is not _I64:
         raise TypeError("slot_mapping must be int64")
     if query.dim() != 3:
@@ -804,10 +841,9 @@ def _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, position
         axes = pshape[0] if len(pshape) == 2 else 1
         half = inv_freq.shape[0]
     if pair_axis is not None:
-        ax = np.asarray(pair_axis, dtype=np.int32)
+        ax = np.ascontiguousarray(pair_axis, dtype=np.int32)
         if ax.shape != (half,):
             raise ValueError("pair_axis must name an axis for every pair")
-        ax = ax.tobytes()
     if (query_norm is None) != (key_norm is None):
         raise ValueError("query_norm and key_norm go together")
     if query_norm is not None:
@@ -819,9 +855,9 @@ def _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, position
     rows = (query_out.data_ptr(), _token_rows(dev, dt, query_out, qshape, qrow), query.data_ptr(),
             _token_rows(dev, dt, query, qshape, qrow), key.data_ptr(), _token_rows(dev, dt, key, kshape, krow),
             value.data_ptr(), _token_rows(dev, dt, value, kshape, krow))
-    rest = (_opt(positions), slot_mapping.data_ptr(), _opt(inv_freq), ax, axes, 2 * half, 1 if interleaved else 0,
-            _opt(query_norm), _opt(key_norm), float(eps), T, Hq, Hkv, D, bs, NB, _dt_int(dt))
-    return rows, rest
+    rest = (_at(positions), slot_mapping.data_ptr(), _at(inv_freq), 0 if ax is None else ax.ctypes.data, axes, 2 * half,
+            1 if interleaved else 0, _at(query_norm), _at(key_norm), float(eps), T, Hq, Hkv, D, bs, NB, _dt_int(dt))
+    return rows, rest, ax
 
 
 def pa_norm_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, query_norm,
@@ -837,9 +873,9 @@ def pa_norm_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, pos
     NB, Hkv, bs, D = shape = k_cache.shape
     if v_cache.shape != shape or query_norm is None or key_norm is None:
         raise ValueError("two caches of one shape and both norms are needed")
-    rows, rest = _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq,
-                              query_norm, key_norm, eps, pair_axis, interleaved)
-    _call("pa_norm_rotary_and_cache", dev, *rows, k_cache.data_ptr(), v_cache.data_ptr(), *rest, _opt(d_err),
+    rows, rest, kept = _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq,
+                                    query_norm, key_norm, eps, pair_axis, interleaved)
+    _call_packed("pa_norm_rotary_and_cache", dev, *rows, k_cache.data_ptr(), v_cache.data_ptr(), *rest, _at(d_err),
           _raw_stream(dev, stream))
 
 
@@ -873,9 +909,9 @@ def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scales, v_scales, s
     T = key.shape[0]
     if key.shape != (T, Hkv, D) or value.shape != key.shape or slot_mapping.shape != (T,):
         raise ValueError("shape mismatch")
-    _call("pa_reshape_and_cache_fp8", dev, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _call_packed("pa_reshape_and_cache_fp8", dev, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, bs, NB, _dt_int(key.dtype),
-          _opt(d_err), _raw_stream(dev, stream))
+          _at(d_err), _raw_stream(dev, stream))
 
 
 def pa_rotary_and_cache_fp8(query_out, query, key, value, k_cache, v_cache, k_scales, v_scales, positions, slot_mapping,
@@ -887,10 +923,10 @@ def pa_rotary_and_cache_fp8(query_out, query, key, value, k_cache, v_cache, k_sc
     dev = _index(k_cache)
     _checked(dev, k_cache, v_cache, k_scales, v_scales, positions, slot_mapping, inv_freq, query_norm, key_norm, d_err)
     NB, Hkv, bs, D = _cache8(k_cache, v_cache, k_scales, v_scales)
-    rows, rest = _rotary_args(dev, query.dtype, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping,
+    rows, rest, kept = _rotary_args(dev, query.dtype, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping,
                               inv_freq, query_norm, key_norm, eps, pair_axis, interleaved)
-    _call("pa_rotary_and_cache_fp8", dev, *rows, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-          v_scales.data_ptr(), *rest, _opt(d_err), _raw_stream(dev, stream))
+    _call_packed("pa_rotary_and_cache_fp8", dev, *rows, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+          v_scales.data_ptr(), *rest, _at(d_err), _raw_stream(dev, stream))
 
 
 def pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len) -> int:
@@ -925,10 +961,10 @@ def pa_decode_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables
         raise ValueError("shape mismatch")
     if workspace is None:
         workspace = decode_fp8_workspace(query, Hkv, bs, max_context_len, stream)
-    _call("pa_decode_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _call_packed("pa_decode_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
           context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), _dt_int(dt),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _opt(d_err), _raw_stream(dev, stream))
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _at(d_err), _raw_stream(dev, stream))
 
 
 def _lens32(prefix_lens, chunk_lens):
@@ -970,10 +1006,10 @@ def pa_prefill_batch_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block
         raise ValueError("shape mismatch")
     if workspace is None:
         workspace = prefill_fp8_workspace(query, k_cache, pl, cl, stream)
-    _call("pa_prefill_batch_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _call_packed("pa_prefill_batch_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], pl.ctypes.data,
           cl.ctypes.data, n, Hq, Hkv, D, bs, NB, float(scale), _dt_int(dt), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), _opt(d_err), _raw_stream(dev, stream))
+          workspace.numel() * workspace.element_size(), _at(d_err), _raw_stream(dev, stream))
 
 
 def pa_copy_blocks_fp8(k_cache, v_cache, k_scales, v_scales, pairs, workspace=None, d_err=None, stream=None):
@@ -989,6 +1025,6 @@ def pa_copy_blocks_fp8(k_cache, v_cache, k_scales, v_scales, pairs, workspace=No
     n = pairs.shape[0] if pairs.numel() else 0
     if workspace is None:
         workspace = _scratch(k_cache.device, pa_copy_blocks_workspace_bytes(n), stream)
-    _call("pa_copy_blocks_fp8", dev, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+    _call_packed("pa_copy_blocks_fp8", dev, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
           pairs.data_ptr(), n, Hkv, D, bs, NB, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          _opt(d_err), _raw_stream(dev, stream))
+          _at(d_err), _raw_stream(dev, stream))
