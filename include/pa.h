@@ -613,8 +613,9 @@ PA_API int pa_copy_blocks_fp8(uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_sca
  * pa_call_packed -- one of the calls above with its arguments in an array, for callers
  * whose foreign-function interface costs more per argument than these calls' kernels
  * take (the Python binding): args[i] is argument i of the call's prototype, a pointer or
- * integer as a 64-bit integer, a float as a double.  Results and errors are the call's;
- * PA_ERR_INVALID_ARG for an unknown call or a null array.
+ * integer as a 64-bit integer, a float as a double.  A host array (pair_axis, prefix_lens,
+ * chunk_lens) may lie behind the arguments: -k points k bytes into args.  Results and
+ * errors are the call's; PA_ERR_INVALID_ARG for an unknown call or a null array.
  */
 enum {
     PA_CALL_NORM_ROTARY_AND_CACHE = 0,

@@ -787,17 +787,19 @@ _PACKED = {
 _packed = None
 
 
-def _call_packed(name, index, *args) -> None:
-    """``_call`` through ``pa_call_packed`` (pointers and integers as ints, None not allowed)."""
+def _call_packed(name, index, *args, tail=b"") -> None:
+    """``_call`` through ``pa_call_packed`` (pointers and integers as ints, None not
+    allowed); ``tail``: host arrays, which arguments of -8 * (number of arguments) and
+    below point into."""
     global _packed
     if _packed is None:
         _packed = lib().pa_call_packed
     number, pack = _PACKED[name]
     if _current_device() == index:
-        rc = _packed(number, pack(*args))
+        rc = _packed(number, pack(*args) + tail)
     else:
         with torch.cuda.device(index):
-            rc = _packed(number, pack(*args))
+            rc = _packed(number, pack(*args) + tail)
     if rc:
         raise PAError(name, rc)
 
@@ -815,10 +817,10 @@ def _dt_int(dtype) -> int:
     raise TypeError(f"unsupported dtype {dtype}")
 
 
-def _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq, query_norm,
+def _rotary_args(count, dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq, query_norm,
                  key_norm, eps, pair_axis, interleaved):
-    """The arguments up to value_stride, those from positions to dtype, and the array
-    that pair_axis points into, of a rotary call."""
+    """The arguments up to value_stride, those from positions to dtype, and pair_axis as
+    bytes behind them, of a rotary call of ``count`` arguments."""
     if slot_mapping.dtype is not _I64:
         raise TypeError("slot_mapping must be int64")
     if query.dim() != 3:
@@ -827,7 +829,7 @@ def _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, position
     T, Hq, _ = qshape
     if slot_mapping.shape != (T,) or qshape[2] != D:
         raise ValueError("shape mismatch")
-    half, axes, ax = 0, 1, None
+    half, axes, ax = 0, 1, b""
     if inv_freq is not None:
         if inv_freq.dtype is not _F32:
             raise TypeError("inv_freq must be float32")
@@ -841,9 +843,10 @@ def _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, position
         axes = pshape[0] if len(pshape) == 2 else 1
         half = inv_freq.shape[0]
     if pair_axis is not None:
-        ax = np.ascontiguousarray(pair_axis, dtype=np.int32)
+        ax = np.asarray(pair_axis, dtype=np.int32)
         if ax.shape != (half,):
             raise ValueError("pair_axis must name an axis for every pair")
+        ax = ax.tobytes()
     if (query_norm is None) != (key_norm is None):
         raise ValueError("query_norm and key_norm go together")
     if query_norm is not None:
@@ -855,7 +858,7 @@ def _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, position
     rows = (query_out.data_ptr(), _token_rows(dev, dt, query_out, qshape, qrow), query.data_ptr(),
             _token_rows(dev, dt, query, qshape, qrow), key.data_ptr(), _token_rows(dev, dt, key, kshape, krow),
             value.data_ptr(), _token_rows(dev, dt, value, kshape, krow))
-    rest = (_at(positions), slot_mapping.data_ptr(), _at(inv_freq), 0 if ax is None else ax.ctypes.data, axes, 2 * half,
+    rest = (_at(positions), slot_mapping.data_ptr(), _at(inv_freq), -8 * count if ax else 0, axes, 2 * half,
             1 if interleaved else 0, _at(query_norm), _at(key_norm), float(eps), T, Hq, Hkv, D, bs, NB, _dt_int(dt))
     return rows, rest, ax
 
@@ -873,10 +876,10 @@ def pa_norm_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, pos
     NB, Hkv, bs, D = shape = k_cache.shape
     if v_cache.shape != shape or query_norm is None or key_norm is None:
         raise ValueError("two caches of one shape and both norms are needed")
-    rows, rest, kept = _rotary_args(dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq,
+    rows, rest, ax = _rotary_args(29, dev, dt, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping, inv_freq,
                                     query_norm, key_norm, eps, pair_axis, interleaved)
     _call_packed("pa_norm_rotary_and_cache", dev, *rows, k_cache.data_ptr(), v_cache.data_ptr(), *rest, _at(d_err),
-          _raw_stream(dev, stream))
+                 _raw_stream(dev, stream), tail=ax)
 
 
 _E4M3, _SCALES = torch.float8_e4m3fn, (torch.float8_e8m0fnu, torch.uint8)
@@ -910,8 +913,8 @@ def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, k_scales, v_scales, s
     if key.shape != (T, Hkv, D) or value.shape != key.shape or slot_mapping.shape != (T,):
         raise ValueError("shape mismatch")
     _call_packed("pa_reshape_and_cache_fp8", dev, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, bs, NB, _dt_int(key.dtype),
-          _at(d_err), _raw_stream(dev, stream))
+                 k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, bs, NB, _dt_int(key.dtype),
+                 _at(d_err), _raw_stream(dev, stream))
 
 
 def pa_rotary_and_cache_fp8(query_out, query, key, value, k_cache, v_cache, k_scales, v_scales, positions, slot_mapping,
@@ -923,10 +926,10 @@ def pa_rotary_and_cache_fp8(query_out, query, key, value, k_cache, v_cache, k_sc
     dev = _index(k_cache)
     _checked(dev, k_cache, v_cache, k_scales, v_scales, positions, slot_mapping, inv_freq, query_norm, key_norm, d_err)
     NB, Hkv, bs, D = _cache8(k_cache, v_cache, k_scales, v_scales)
-    rows, rest, kept = _rotary_args(dev, query.dtype, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping,
-                              inv_freq, query_norm, key_norm, eps, pair_axis, interleaved)
+    rows, rest, ax = _rotary_args(31, dev, query.dtype, query_out, query, key, value, NB, Hkv, bs, D, positions, slot_mapping,
+                                  inv_freq, query_norm, key_norm, eps, pair_axis, interleaved)
     _call_packed("pa_rotary_and_cache_fp8", dev, *rows, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-          v_scales.data_ptr(), *rest, _at(d_err), _raw_stream(dev, stream))
+                 v_scales.data_ptr(), *rest, _at(d_err), _raw_stream(dev, stream), tail=ax)
 
 
 def pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len) -> int:
@@ -962,9 +965,9 @@ def pa_decode_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables
     if workspace is None:
         workspace = decode_fp8_workspace(query, Hkv, bs, max_context_len, stream)
     _call_packed("pa_decode_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-          context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), _dt_int(dt),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _at(d_err), _raw_stream(dev, stream))
+                 k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+                 context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, int(max_context_len), float(scale), _dt_int(dt),
+                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _at(d_err), _raw_stream(dev, stream))
 
 
 def _lens32(prefix_lens, chunk_lens):
@@ -1007,9 +1010,10 @@ def pa_prefill_batch_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block
     if workspace is None:
         workspace = prefill_fp8_workspace(query, k_cache, pl, cl, stream)
     _call_packed("pa_prefill_batch_fp8", dev, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], pl.ctypes.data,
-          cl.ctypes.data, n, Hq, Hkv, D, bs, NB, float(scale), _dt_int(dt), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), _at(d_err), _raw_stream(dev, stream))
+                 k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], -8 * 22,
+                 -8 * 22 - 4 * n, n, Hq, Hkv, D, bs, NB, float(scale), _dt_int(dt), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), _at(d_err), _raw_stream(dev, stream),
+                 tail=pl.tobytes() + cl.tobytes())
 
 
 def pa_copy_blocks_fp8(k_cache, v_cache, k_scales, v_scales, pairs, workspace=None, d_err=None, stream=None):
@@ -1026,5 +1030,5 @@ def pa_copy_blocks_fp8(k_cache, v_cache, k_scales, v_scales, pairs, workspace=No
     if workspace is None:
         workspace = _scratch(k_cache.device, pa_copy_blocks_workspace_bytes(n), stream)
     _call_packed("pa_copy_blocks_fp8", dev, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-          pairs.data_ptr(), n, Hkv, D, bs, NB, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          _at(d_err), _raw_stream(dev, stream))
+                 pairs.data_ptr(), n, Hkv, D, bs, NB, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                 _at(d_err), _raw_stream(dev, stream))

@@ -39,10 +39,12 @@ int rotary_params(pa::RotaryParams &p, void *query_out, int64_t query_out_stride
         return PA_ERR_OUT_OF_RANGE;
     if (!std::isfinite(eps) || eps < 0.f) return PA_ERR_OUT_OF_RANGE;
     if ((query_norm == nullptr) != (key_norm == nullptr)) return PA_ERR_INVALID_ARG;
+    p.one_axis = 1;
     for (int i = 0; i < rot_dim / 2; ++i) {
         const int a = pair_axis ? pair_axis[i] : 0;
         if (a < 0 || a >= num_axes) return PA_ERR_OUT_OF_RANGE;
         p.pair_axis[i] = (uint8_t)a;
+        if (a) p.one_axis = 0;
     }
     p.num_tokens = num_tokens;
     if (num_tokens == 0) return PA_OK;
@@ -364,7 +366,7 @@ int pa_copy_blocks_fp8(uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_scales, ui
 }
 
 // One call with its arguments in an array, in the order of its prototype: pointers and
-// integers as 64-bit integers, floats as doubles.
+// integers as 64-bit integers, floats as doubles, host arrays behind the arguments.
 int pa_call_packed(int call, const int64_t *a) {
     if (!a) return PA_ERR_INVALID_ARG;
     const auto I = [a](int k) { return (int)a[k]; };
@@ -376,16 +378,20 @@ int pa_call_packed(int call, const int64_t *a) {
     const auto P = [a](int k) { return reinterpret_cast<void *>(a[k]); };
     const auto U8 = [a](int k) { return reinterpret_cast<uint8_t *>(a[k]); };
     const auto I32 = [a](int k) { return reinterpret_cast<int32_t *>(a[k]); };
+    const auto H32 = [a](int k) {  // host integers, maybe behind the arguments
+        const char *tail = reinterpret_cast<const char *>(a);
+        return a[k] < 0 ? reinterpret_cast<const int *>(tail - a[k]) : reinterpret_cast<const int *>(a[k]);
+    };
     const auto I64 = [a](int k) { return reinterpret_cast<int64_t *>(a[k]); };
     const auto F32 = [a](int k) { return reinterpret_cast<float *>(a[k]); };
     switch (call) {
         case PA_CALL_NORM_ROTARY_AND_CACHE:
             return pa_norm_rotary_and_cache(P(0), a[1], P(2), a[3], P(4), a[5], P(6), a[7], P(8), P(9), I32(10), I64(11),
-                                            F32(12), I32(13), I(14), I(15), I(16), P(17), P(18), F(19), I(20), I(21), I(22),
+                                            F32(12), H32(13), I(14), I(15), I(16), P(17), P(18), F(19), I(20), I(21), I(22),
                                             I(23), I(24), I(25), (pa_dtype)I(26), I32(27), P(28));
         case PA_CALL_ROTARY_AND_CACHE_FP8:
             return pa_rotary_and_cache_fp8(P(0), a[1], P(2), a[3], P(4), a[5], P(6), a[7], U8(8), U8(9), U8(10), U8(11),
-                                           I32(12), I64(13), F32(14), I32(15), I(16), I(17), I(18), P(19), P(20), F(21),
+                                           I32(12), I64(13), F32(14), H32(15), I(16), I(17), I(18), P(19), P(20), F(21),
                                            I(22), I(23), I(24), I(25), I(26), I(27), (pa_dtype)I(28), I32(29), P(30));
         case PA_CALL_RESHAPE_AND_CACHE_FP8:
             return pa_reshape_and_cache_fp8(P(0), P(1), U8(2), U8(3), U8(4), U8(5), I64(6), I(7), I(8), I(9), I(10), I(11),
@@ -394,7 +400,7 @@ int pa_call_packed(int call, const int64_t *a) {
             return pa_decode_fp8(P(0), P(1), U8(2), U8(3), U8(4), U8(5), I32(6), I(7), I32(8), I(9), I(10), I(11), I(12),
                                  I(13), I(14), I(15), F(16), (pa_dtype)I(17), P(18), (size_t)a[19], I32(20), P(21));
         case PA_CALL_PREFILL_BATCH_FP8:
-            return pa_prefill_batch_fp8(P(0), P(1), U8(2), U8(3), U8(4), U8(5), I32(6), I(7), I32(8), I32(9), I(10), I(11),
+            return pa_prefill_batch_fp8(P(0), P(1), U8(2), U8(3), U8(4), U8(5), I32(6), I(7), H32(8), H32(9), I(10), I(11),
                                         I(12), I(13), I(14), I(15), F(16), (pa_dtype)I(17), P(18), (size_t)a[19], I32(20),
                                         P(21));
         case PA_CALL_COPY_BLOCKS_FP8:

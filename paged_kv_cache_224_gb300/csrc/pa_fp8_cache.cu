@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
     __shared__ float4 s_cs[kPasses * 32 * 4];
     __shared__ long long s_frac[kRotaryMaxDim / 2];  // turns per position, 2^-64
     __shared__ bool s_odd[kRotaryMaxDim / 2];        // whose frequency is not finite
+    __shared__ uint8_t s_axis[kRotaryMaxDim / 2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = p.block_size, D = p.head_dim, shift = __ffs(bs) - 1;
     const int head0 = blockIdx.y * kHeadsPerCta, heads = min(kHeadsPerCta, p.num_kv_heads - head0);
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
         const float f = p.inv_freq[i];
         s_odd[i] = !isfinite(f);
         s_frac[i] = turn_fraction(f);
+        s_axis[i] = p.one_axis ? 0 : p.pair_axis[i];
     }
     __syncthreads();
     for (unsigned heads_left = s_heads; heads_left; heads_left &= heads_left - 1) {
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
                 while (k < n) {
                     float sn, cs;
                     turn_sincos(s_frac[pair],
-                                p.positions[(long long)p.pair_axis[pair] * p.num_tokens + s_tok[s_row[ch * per_chunk + k]]], sn, cs);
+                                p.positions[(long long)s_axis[pair] * p.num_tokens + s_tok[s_row[ch * per_chunk + k]]], sn, cs);
                     if (s_odd[pair]) sn = cs = __int_as_float(0x7fc00000);
                     float *q = reinterpret_cast<float *>(s_cs) + k * 2 * half + (pair >> 2 & 1) * (half / 2) + (pair >> 3) * 4 + (pair & 3);
                     q[0] = cs;

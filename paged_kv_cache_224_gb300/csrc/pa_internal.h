@@ -148,6 +148,7 @@ struct RotaryParams {
     int num_tokens, num_heads, num_kv_heads, head_dim, rot_dim, interleaved;
     int block_size, num_blocks;
     uint8_t pair_axis[kRotaryMaxDim / 2];
+    int one_axis;                // whether every pair's axis is 0 (lanes that index pair_axis each their own way wait for one another)
     // RMS norms of the heads before they are rotated, or null
     const void *query_norm;      // [head_dim] dtype
     const void *key_norm;

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) norm_rotary_kernel(const __gri
         for (int i = lane; i < half; i += 32) {
             const float f = p.inv_freq[i];
             float x, y;
-            turn_sincos(turn_fraction(f), p.positions[(long long)p.pair_axis[i] * p.num_tokens + t], y, x);
+            turn_sincos(turn_fraction(f), p.positions[(p.one_axis ? 0LL : (long long)p.pair_axis[i] * p.num_tokens) + t], y, x);
             if (!isfinite(f)) x = y = __int_as_float(0x7fc00000);
             const int at = (i >> 2 & 1) * kPlane * 4 + (i >> 3) * 4 + (i & 3);
             q[at] = x;
