@@ -536,8 +536,10 @@ PA_API int pa_norm_rotary_and_cache(void *query_out, int64_t query_out_stride, c
  *   arguments      as for pa_reshape_and_cache and pa_rotary_and_cache; k_scales and
  *                  v_scales are read and written; query_norm, key_norm and eps as for
  *                  pa_norm_rotary_and_cache, or both norms NULL for none
- * Supported: head_dim a multiple of 16 up to 256, block_size in {8, 16, 32, 64, 128}.
- * num_tokens == 0 is a no-op.
+ * Supported: head_dim a multiple of 16 up to 256, block_size in {8, 16, 32, 64, 128}, up
+ * to 65535 kv heads.  num_tokens == 0 is a no-op.
+ * Reading.  The attention calls take scales from 2^-64 (byte 63) on, which is what the
+ * writing calls leave; caches filled in another way keep to that too.
  */
 PA_API int pa_reshape_and_cache_fp8(const void *key, const void *value, uint8_t *k_cache, uint8_t *v_cache,
                                     uint8_t *k_scales, uint8_t *v_scales, const int64_t *slot_mapping, int num_tokens,

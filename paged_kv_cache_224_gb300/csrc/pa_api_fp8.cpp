@@ -82,7 +82,7 @@ int rotary_params(pa::RotaryParams &p, void *query_out, int64_t query_out_stride
 }
 
 int store_fp8(pa::RotaryParams &p, uint8_t *k_scales, uint8_t *v_scales, pa_dtype dtype, void *stream) {
-    if (!good_block(p.block_size)) return PA_ERR_UNSUPPORTED;
+    if (!good_block(p.block_size) || p.num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
     if (!k_scales || !v_scales || k_scales == v_scales || p.k_cache == p.v_cache) return PA_ERR_INVALID_ARG;
     p.k_scales = k_scales;
     p.v_scales = v_scales;

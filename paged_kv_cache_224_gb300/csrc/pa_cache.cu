@@ -73,8 +73,9 @@ int launch_reshape_and_cache(const void *key, const void *value, void *k_cache, 
 // inside the pool are counted; an id outside it cannot equal a valid dst),
 // and each copy CTA then looks its dst up once -- O(n) work for n pairs
 // instead of every CTA scanning the whole list.  Up to kCowScan pairs the list is
-// short enough for that scan (16 KB from L2), and the table's two launches are saved:
-// 224 pairs of 8-bit blocks of 40 heads 21.5 -> 12.3 us, one pair 12.3 -> 8.2.
+// short enough for that scan (16 KB from L2), and the table's two launches are saved.
+// Scan / table, replayed, us: 1 pair of 8 heads of 16 rows of 128 bytes 2.8 / 4.9, 1024
+// pairs 8.5 / 16.3; of 40 heads of 256-byte rows 2.9 / 6.2 and 62 / 71.
 
 struct CowEntry {
     unsigned int key;   // block id, or kCowEmpty

@@ -318,6 +318,9 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
         }
         fence_barrier_init();
     }
+    pdl_wait();     // the kernel before this one on the stream (e.g. the cache write) has finished
+    // (not before the wait: a kernel that is still to allocate tensor memory on this SM
+    // would wait for this one, and this one for that)
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(const_cast<uint32_t *>(holder))),
@@ -325,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_wait();     // the kernel before this one on the stream (e.g. the cache write) has finished
     pdl_trigger();  // the merge may be scheduled once every CTA of this grid has started
     Walk walk = begin<T>(fp, D, lens, reinterpret_cast<long long *>(lens + kLens));
     tc_fence_before();

@@ -63,6 +63,7 @@ def test_norms_are_required_where_they_are_the_point(lib):
 
 def test_store_refusals(lib):
     assert rotary8(lib, bs=5) == -2 and rotary8(lib, bs=256) == -2
+    assert rotary8(lib, Hkv=65536, D=16, R=16, ks=1 << 20, vs=1 << 20) == -2
     assert rotary8(lib, ksc=0) == -1 and rotary8(lib, vsc=0) == -1
     assert rotary8(lib, vsc=BUF) == -1 and rotary8(lib, vc=BUF) == -1     # one buffer for both
 

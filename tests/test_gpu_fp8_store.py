@@ -239,6 +239,28 @@ def test_query_in_place_strided_and_one_dimensional_positions():
     assert torch.equal(c["q"], want)
 
 
+@pytest.mark.parametrize("T", [1, 2, 7, 64, 700])
+def test_slots_that_begin_between_16_byte_boundaries(T):
+    """(as a slice of a step's slot mapping does)"""
+    c = make(T, 4, 2, 64, 64, "bf16", 16, "scattered" if T > 2 else "step", seed=12 + T, norm=True)
+    home = torch.full((T + 1,), 3, dtype=torch.int64, device=DEV)   # the slot before would clash
+    home[1:] = c["slots"]
+    c["slots"] = home[1:]
+    check(c, 64, True, "bf16")
+
+
+def test_two_runs_of_one_block_far_apart():
+    """Tokens of one block at the call's two ends, and a slot that three of them name."""
+    T = 900
+    c = make(T, 2, 3, 64, 64, "f16", 16, "run", seed=13, norm=False)
+    b = int(c["slots"][0]) // 16
+    c["slots"][T - 5:] = torch.tensor([b * 16 + 9, b * 16 + 3, b * 16 + 3, b * 16 + 15, b * 16 + 9], device=DEV)
+    c["slots"][450] = b * 16 + 3
+    check(c, 64, False, "f16")
+    c["slots"][:16] = c["slots"][:16].flip(0)
+    check(c, 64, False, "f16")
+
+
 def test_same_bits_on_another_stream_and_replayed():
     c = make(64, 8, 2, 128, 128, "bf16", 16, "onward", seed=11, norm=True)
     start = [x.clone() for x in (c["kc"], c["vc"], c["ks"], c["vs"])]
