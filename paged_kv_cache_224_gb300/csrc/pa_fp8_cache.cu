@@ -26,8 +26,8 @@
 namespace pa {
 namespace {
 
-constexpr int kHeadsPerCta = 4;
-constexpr int kStoreThreads = 64 * kHeadsPerCta;  // at most
+constexpr int kHeadsPerCta = 8;
+constexpr int kStoreThreads = 32 * kHeadsPerCta;  // at most
 
 // kPasses: rows that a lane holds at a time.
 template <typename T, bool kInterleaved, bool kNorm, int kPasses>
@@ -76,17 +76,17 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
     for (unsigned heads_left = s_heads; heads_left; heads_left &= heads_left - 1) {
         const int t0 = first + __ffs(heads_left) - 1;
         const long long slot = p.slots[t0], blk = slot >> shift, base = blk << shift;
-        // this warp's head, and whether it has the values (the last heads' CTA may have idle warps)
-        const bool busy = warp < 2 * heads;
-        const int which = busy ? warp / heads : 1, h = head0 + warp % heads;
-        const T *src = (which ? static_cast<const T *>(p.value) : static_cast<const T *>(p.key)) + (long long)h * D;
-        const long long stride = which ? p.value_stride : p.key_stride;
-        uint8_t *scale = (which ? p.v_scales : p.k_scales) + blk * p.num_kv_heads + h;
-        uint8_t *tile = static_cast<uint8_t *>(which ? p.v_cache : p.k_cache) + (blk * p.num_kv_heads + h) * bs * D;
-        const int old = busy ? (int)*scale - 127 : 0;
+        // this warp's head (the last heads' CTA may have idle warps), its tiles and scales
+        const bool busy = warp < heads;
+        const int h = head0 + (busy ? warp : 0);
+        const long long at = blk * p.num_kv_heads + h;
+        auto tile_of = [&](int which) { return static_cast<uint8_t *>(which ? p.v_cache : p.k_cache) + at * bs * D; };
+        auto scale_at = [&](int which) { return (which ? p.v_scales : p.k_scales) + at; };
+        const int old_k = (int)*scale_at(0) - 127, old_v = (int)*scale_at(1) - 127;
         // rows that may have to move: on their way while the slots are looked through
         if (busy && slot != base)
-            for (int i = lane * 128; i < bs * D; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(tile + i));
+            for (int i = lane * 128; i < 2 * bs * D; i += 32 * 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(i < bs * D ? tile_of(0) + i : tile_of(1) + (i - bs * D)));
         __syncthreads();  // what the block before left in shared memory is read
         for (int i = tid; i < bs; i += blockDim.x) s_tok[i] = -1;
         if (tid == 0) s_late = 0;
@@ -131,18 +131,17 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
         const int e1 = turned && !kInterleaved ? half + c * 8 : e0 + 8;
         const float per_dim = 1.f / (float)D;
         uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-        if (kNorm && which == 0 && c < upr) {
+        if (kNorm && c < upr) {
             w0 = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key_norm) + e0);
             w1 = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key_norm) + e1);
         }
 
-        float a[kPasses][8], b[kPasses][8];  // the units of this lane's rows, as they are to be held
         auto rows_of = [&](int ch) { return min(per_chunk, nrows - ch * per_chunk); };
-        // a chunk's units: their loads, the angles meanwhile (by all warps), then the
-        // arithmetic; returns the largest magnitude of this lane's (lanes without a row have 0)
-        auto compute = [&](int ch) {
+        // the units of this lane's rows of a chunk, of keys or values
+        auto load = [&](int which, int ch, uint4(&va)[kPasses], uint4(&vb)[kPasses]) {
             const int n = rows_of(ch);
-            uint4 va[kPasses], vb[kPasses];
+            const T *src = (which ? static_cast<const T *>(p.value) : static_cast<const T *>(p.key)) + (long long)h * D;
+            const long long stride = which ? p.value_stride : p.key_stride;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int k = k0 + i * per_warp;
@@ -153,24 +152,31 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
                     vb[i] = *reinterpret_cast<const uint4 *>(row + e1);
                 }
             }
-            if (half > 0) {
-                __syncthreads();  // the angles of the chunk before are read
-                const int by_row = blockDim.x / half, by_pair = blockDim.x - by_row * half;
-                int k = tid / half, pair = tid - k * half;
-                while (k < n) {
-                    float sn, cs;
-                    turn_sincos(s_frac[pair],
-                                p.positions[(long long)s_axis[pair] * p.num_tokens + s_tok[s_row[ch * per_chunk + k]]], sn, cs);
-                    if (s_odd[pair]) sn = cs = __int_as_float(0x7fc00000);
-                    float *q = reinterpret_cast<float *>(s_cs) + k * 2 * half + (pair >> 2 & 1) * (half / 2) + (pair >> 3) * 4 + (pair & 3);
-                    q[0] = cs;
-                    q[half] = sn;
-                    k += by_row;
-                    pair += by_pair;
-                    if (pair >= half) pair -= half, ++k;
-                }
-                __syncthreads();
+        };
+        // the angles of a chunk's rows, by all warps
+        auto angles = [&](int ch) {
+            if (half == 0) return;
+            const int n = rows_of(ch);
+            __syncthreads();  // the angles of the chunk before are read
+            const int by_row = blockDim.x / half, by_pair = blockDim.x - by_row * half;
+            int k = tid / half, pair = tid - k * half;
+            while (k < n) {
+                float sn, cs;
+                turn_sincos(s_frac[pair], p.positions[(long long)s_axis[pair] * p.num_tokens + s_tok[s_row[ch * per_chunk + k]]], sn, cs);
+                if (s_odd[pair]) sn = cs = __int_as_float(0x7fc00000);
+                float *q = reinterpret_cast<float *>(s_cs) + k * 2 * half + (pair >> 2 & 1) * (half / 2) + (pair >> 3) * 4 + (pair & 3);
+                q[0] = cs;
+                q[half] = sn;
+                k += by_row;
+                pair += by_pair;
+                if (pair >= half) pair -= half, ++k;
             }
+            __syncthreads();
+        };
+        float a[kPasses][8], b[kPasses][8];  // the units of this lane's rows, as they are to be held
+        // returns the largest magnitude among them (0 for lanes without a row)
+        auto compute = [&](int which, int ch, const uint4(&va)[kPasses], const uint4(&vb)[kPasses]) {
+            const int n = rows_of(ch);
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 unpack8<T>(va[i], a[i]);
@@ -215,41 +221,64 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
             }
             return __uint_as_float(top);
         };
-        // ---- the largest magnitude
-        float amax = 0.f;
-        for (int ch = 0; ch < chunks; ++ch) amax = fmaxf(amax, compute(ch));
+        // the scale that the lanes' largest magnitudes ask for, and the rows that it moves;
+        // returns what brings values to codes
+        auto settle = [&](int which, float amax, int old) {
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
-        // ---- the scale, and the rows that it moves
-        const int need = scale_exponent(amax), e = fresh ? need : max(old, need);
-        if (busy && lane == 0) *scale = (uint8_t)(e + 127);
-        if (busy && !fresh && e > old) {
-            const float down = __uint_as_float((unsigned)(max(old - e, -32) + 127) << 23);
-            for (int i = lane; i < bs * upr; i += 32) {
-                if (s_tok[i / upr] >= 0) continue;
-                uint4 *q = reinterpret_cast<uint4 *>(tile) + i;
-                float f[16];
-                values16(*q, f);
+            for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
+            const int need = scale_exponent(amax), e = fresh ? need : max(old, need);
+            if (busy && lane == 0) *scale_at(which) = (uint8_t)(e + 127);
+            if (busy && !fresh && e > old) {
+                const float down = __uint_as_float((unsigned)(max(old - e, -32) + 127) << 23);
+                for (int i = lane; i < bs * upr; i += 32) {
+                    if (s_tok[i / upr] >= 0) continue;
+                    uint4 *q = reinterpret_cast<uint4 *>(tile_of(which)) + i;
+                    float f[16];
+                    values16(*q, f);
 #pragma unroll
-                for (int x = 0; x < 16; ++x) f[x] *= down;
-                *q = make_uint4(codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7]), codes4(f[8], f[9], f[10], f[11]),
-                                codes4(f[12], f[13], f[14], f[15]));
+                    for (int x = 0; x < 16; ++x) f[x] *= down;
+                    *q = make_uint4(codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7]),
+                                    codes4(f[8], f[9], f[10], f[11]), codes4(f[12], f[13], f[14], f[15]));
+                }
             }
-        }
-        // ---- the codes, of the last chunk from registers
-        const float up = __uint_as_float((unsigned)(127 - e) << 23);
-        for (int ch = chunks - 1; ch >= 0; --ch) {
-            if (ch < chunks - 1) compute(ch);
+            return __uint_as_float((unsigned)(127 - e) << 23);
+        };
+        // the codes of the units that are held
+        auto put = [&](int which, int ch, float up) {
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int k = k0 + i * per_warp;
                 if (busy && k < rows_of(ch) && c < upr) {
-                    uint8_t *row = tile + s_row[ch * per_chunk + k] * D;
+                    uint8_t *row = tile_of(which) + s_row[ch * per_chunk + k] * D;
                     const float(&x)[8] = a[i], (&y)[8] = b[i];
                     *reinterpret_cast<uint2 *>(row + e0) =
                         make_uint2(codes4(x[0] * up, x[1] * up, x[2] * up, x[3] * up), codes4(x[4] * up, x[5] * up, x[6] * up, x[7] * up));
                     *reinterpret_cast<uint2 *>(row + e1) =
                         make_uint2(codes4(y[0] * up, y[1] * up, y[2] * up, y[3] * up), codes4(y[4] * up, y[5] * up, y[6] * up, y[7] * up));
+                }
+            }
+        };
+        uint4 ka[kPasses], kb[kPasses], va[kPasses], vb[kPasses];
+        if (chunks == 1) {
+            load(0, 0, ka, kb);
+            load(1, 0, va, vb);
+            angles(0);
+            put(0, 0, settle(0, compute(0, 0, ka, kb), old_k));
+            put(1, 0, settle(1, compute(1, 0, va, vb), old_v));
+        } else {
+#pragma unroll 1
+            for (int which = 0; which < 2; ++which) {
+                float amax = 0.f;
+#pragma unroll 1
+                for (int step = 0; step < 2 * chunks - 1; ++step) {
+                    // chunks upwards for the largest magnitude, then down again for the codes, the last one once
+                    const int ch = step < chunks ? step : 2 * chunks - 2 - step;
+                    load(which, ch, va, vb);
+                    if (which == 0) angles(ch);
+                    const float most = compute(which, ch, va, vb);
+                    if (step < chunks) amax = fmaxf(amax, most);
+                    if (step == chunks - 1) amax = settle(which, amax, which ? old_v : old_k);
+                    if (step >= chunks - 1) put(which, ch, amax);
                 }
             }
         }
@@ -320,7 +349,7 @@ template <typename T, bool kInterleaved, bool kNorm, int kPasses>
 cudaError_t store_t(const RotaryParams &p, bool beside, cudaStream_t stream) {
     const unsigned splits = (unsigned)((p.num_kv_heads + kHeadsPerCta - 1) / kHeadsPerCta);
     const dim3 grid((unsigned)((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta), splits);
-    const dim3 block(64 * std::min(kHeadsPerCta, p.num_kv_heads));
+    const dim3 block(32 * std::min(kHeadsPerCta, p.num_kv_heads));
     auto kern = store_fp8_kernel<T, kInterleaved, kNorm, kPasses>;
     if (beside) return launch_pdl(kern, grid, block, 0, stream, p);
     kern<<<grid, block, 0, stream>>>(p);
