@@ -1,8 +1,7 @@
 // Writing and reading back an 8-bit cache.
 //
-// store_fp8_kernel: one CTA per block that the call's tokens write to, and up to
-// kHeadsPerCta kv heads of it, a warp for each head's keys and for its values.  The CTA
-// of the first token that names a block finds all the call's tokens for it (the later one
+// store_fp8_kernel: a CTA has the blocks that up to 16 of the call's tokens are the first
+// to name, and up to kHeadsPerCta kv heads of them, a warp for each.  It finds all the call's tokens for it (the later one
 // where two name the same slot), normalises and rotates their keys, and then decides
 // the scale of each head:
 //   need = the least e with amax <= 448 * 2^e, over the written rows
@@ -11,11 +10,18 @@
 // Rows that were there before are moved to a scale that grew, code by code.
 //
 // HBM-bound for prompts, latency-bound for steps of single tokens.  A warp has all of
-// its rows' loads under way at once (16 rows of 128 values) while the angles are
-// computed, and keeps the values in registers between the maximum and the codes; only
-// blocks with more rows than that are read twice.  To find a block's tokens every CTA
-// reads the whole slot mapping, 8 bytes a token from L2 (8192 tokens: 64 KB beside the
-// 96 KB of keys and values that four heads of 16 tokens have).
+// its rows' loads under way at once (16 rows of 128 values, keys and values) while the
+// angles are computed, and keeps the values in registers between the maximum and the
+// codes; only blocks with more rows than that are read twice.  To find a block's tokens
+// every CTA reads the whole slot mapping, 8 bytes a token from L2 (8192 tokens: 64 KB
+// beside the 64 KB of keys and values that eight heads of 16 tokens have).
+// With the queries' kernel, which it starts beside: 8192 tokens of 64/8 heads of 128,
+// bf16, 64.5 us, 73% of the copy rate (the queries alone take 45); 1021 of 40/40 heads,
+// fp16, 20; a step of 256 tokens 8 on the device.  Rows read a second time for the codes
+// took 108 and 51 us; a CTA per token, of which most had nothing to do, 114 and 38; a warp
+// for keys and one for values, four heads to a CTA, 74 and 24; the rows computed before
+// the slots are looked through 80 and 33 (every later run of a block does so in vain); two
+// warps to a head's keys 81 and 28.  Looking through the slots costs 3 us of the 64.5.
 #include <algorithm>
 #include <type_traits>
 
@@ -379,11 +385,11 @@ int launch_store_fp8(pa_dtype dt, const RotaryParams &p, cudaStream_t stream) {
         if (rc != PA_OK) return rc;
     }
     const bool beside = p.num_heads > 0;
-    // One token to a CTA while that gives no more than four CTAs to an SM (a step of
+    // One token to a CTA while that gives no more than two to four CTAs to an SM (a step of
     // single tokens), up to 16 beyond (a prompt, where one of 16 begins a block).
     RotaryParams q = p;
     const long long all = (long long)p.num_tokens * ((p.num_kv_heads + kHeadsPerCta - 1) / kHeadsPerCta);
-    q.tokens_per_cta = (int)std::min(16LL, std::max(1LL, all / (4LL * sm_count())));
+    q.tokens_per_cta = (int)std::min(16LL, std::max(1LL, all / (2LL * sm_count())));
     const cudaError_t e = dt == PA_BF16 ? store_dtype<__nv_bfloat16>(q, beside, stream) : store_dtype<__half>(q, beside, stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

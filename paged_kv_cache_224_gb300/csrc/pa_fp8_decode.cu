@@ -30,7 +30,18 @@
 //   warps 2-5 softmax, one thread per key (= TMEM lane): scores, maxima over the tile,
 //             O rescaled only when a maximum has grown by 2^8, weights to shared memory;
 //             at a piece's end one thread per dimension writes the output or the partial;
-//   warp 6    the scales of each tile's blocks, up to eight tiles ahead.
+//   warp 6    the next piece's queries, and the scales of each tile's blocks up to eight
+//             tiles ahead.
+// At head_dim 64, where a tile is 16 KB, three CTAs to an SM (two with eight heads).
+//
+// Measured (bf16, us, share of the copy rate): 256 contexts of up to 4096 tokens, 32/8
+// heads of 128, 176, 94%; eight of 32768 to 131072, 64/8 heads, 207, 98%; 256 of 2048, 8/8
+// heads of 64, 87, 90%, 64/8 heads of 64, 132, 60% (bound by the softmax warps).  On the
+// way (the first two cases): on the CUDA cores 1088 and 2367; one unit (sequence, kv head,
+// 1024 tokens) a CTA 203 and 228; equal shares 196 and 216.  What runs once a piece was
+// kept small after 256 contexts of 2048 tokens with 64/8 heads had taken 234, not 168: the
+// roles' code did not stay in the instruction cache together.  A vote instead of every
+// tile's maxima: 1024 contexts of 512 tokens, 64/8 heads, 197 -> 188.
 // All waits are bounded; a wait that gives up flags PA_DEVERR_TIMEOUT.
 #include "pa_internal.h"
 

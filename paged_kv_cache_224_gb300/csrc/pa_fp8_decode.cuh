@@ -34,7 +34,7 @@ struct Lay {
     static constexpr uint32_t kColO = 2 * N;
     static constexpr int kSlot = kKeys * D;                 // one K or V tile
     static constexpr int kCtas = ctas_per_sm(D, G);
-    static constexpr int S = D == 128 ? (GP == 4 ? 6 : 5) : (GP == 4 ? 6 : 10);  // ring slots: 96, 80 and 48 KB, 80 KB
+    static constexpr int S = GP == 8 ? 5 * kPar : 6;        // ring slots: 80 KB, else 96 KB (48 KB at head_dim 64)
     static constexpr int kRowP = kKeys / kPar;              // bytes of a row of P^T: a tile's keys of one parity
     // 2 x [3 GP rows][D]; the MMAs read N rows, the last GP of them whatever follows:
     // columns that nobody reads
@@ -46,7 +46,8 @@ struct Lay {
     static constexpr int kOffBar = kOffSc + kScaleRing * 16 * 16;
     static constexpr int kBars = 2 * S + 10 + 2 * kScaleRing;
     static constexpr int kOffLen = kOffBar + (kBars * 8 + 8 + 15) / 16 * 16;
-    static constexpr int kOffXch = kOffLen + kLens * 4 + 64;  // [4 warps][GP] maxima, [4][GP] sums, [2][GP] query scales, [G][64] sums of odd keys
+    // [4 warps][GP] maxima, [4][GP] sums, [2][GP] query scales, [G][64] sums of odd keys
+    static constexpr int kOffXch = kOffLen + kLens * 4 + 64;
     static constexpr int kUsed = kOffXch + (4 * GP + 4 * GP + 2 * GP + (kPar == 2 ? G * 64 : 0)) * 4;
     static constexpr int kAlloc = kUsed + 1024;             // room to align the base to 1 KB
 };
@@ -181,8 +182,11 @@ __device__ __forceinline__ int clamped_len(const DecodeParams &p, int s) {
 
 __device__ __forceinline__ bool next_piece(const DecodeParams &p, const int *lens, Walk &w, Piece &q) {
     if (w.at >= w.end) return false;
-    while (w.len == 0) {  // (tiles are left, so a sequence with some follows)
-        ++w.s;
+    while (w.len == 0) {  // (tiles are left, so a sequence with some follows, unless the lengths changed meanwhile)
+        if (++w.s >= p.num_seqs) {
+            w.at = w.end;
+            return false;
+        }
         w.len = w.s - w.s0 < kLens ? lens[w.s - w.s0] : clamped_len(p, w.s);
         w.kvh = w.tile = 0;
     }
