@@ -1,9 +1,9 @@
 // Writing and reading back an 8-bit cache.
 //
 // store_fp8_kernel: a CTA has the blocks that up to 16 of the call's tokens are the first
-// to name, and up to kHeadsPerCta kv heads of them, a warp for each.  It finds all the call's tokens for it (the later one
-// where two name the same slot), normalises and rotates their keys, and then decides
-// the scale of each head:
+// to name, and up to kHeadsPerCta kv heads of them, a warp for each.  For each block it
+// finds all the call's tokens (the later one where two name the same slot), normalises
+// and rotates their keys, and then decides the scale of each head:
 //   need = the least e with amax <= 448 * 2^e, over the written rows
 //   e    = need where the block's first row is among them (the block starts afresh),
 //          else max(the old e, need)
@@ -385,8 +385,11 @@ int launch_store_fp8(pa_dtype dt, const RotaryParams &p, cudaStream_t stream) {
         if (rc != PA_OK) return rc;
     }
     const bool beside = p.num_heads > 0;
-    // One token to a CTA while that gives no more than two to four CTAs to an SM (a step of
-    // single tokens), up to 16 beyond (a prompt, where one of 16 begins a block).
+    // One token to a CTA while that gives no more than four CTAs to an SM (a step of
+    // single tokens), up to 16 beyond (a prompt, where one of 16 begins a block).  With one
+    // token the variant that holds one row a lane, of half the registers, leaves room for
+    // all CTAs at once: a step of 256 tokens 8 us, with four rows a lane 14; a prompt with
+    // it reads its rows twice.
     RotaryParams q = p;
     const long long all = (long long)p.num_tokens * ((p.num_kv_heads + kHeadsPerCta - 1) / kHeadsPerCta);
     q.tokens_per_cta = (int)std::min(16LL, std::max(1LL, all / (2LL * sm_count())));

@@ -220,7 +220,10 @@ struct Fp8DecodeParams {
 };
 int fp8_decode_ctas(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len);
 namespace d8 {
-// CTAs of the decode over an 8-bit cache that an SM holds.
+// CTAs of the decode over an 8-bit cache that an SM holds.  At head_dim 64 a tile is 16 KB
+// and two CTAs wait for their softmax: 256 contexts of 2048 tokens, 8/8 heads, 112 us with
+// two and 88 with three; with eight heads a kv head three CTAs' registers do not suffice
+// (146 us, with two 132).
 constexpr int ctas_per_sm(int head_dim, int group) { return head_dim == 64 && group <= 4 ? 3 : 2; }
 }  // namespace d8
 int launch_decode_fp8(pa_dtype dt, int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
