@@ -127,6 +127,31 @@ def test_peaked_and_flat_weights(D, G):
     check(c, "f16")
 
 
+@pytest.mark.parametrize("D,G", [(128, 1), (128, 8), (64, 2)])
+@pytest.mark.parametrize("gap", [9.0, 14.0, 18.0])
+def test_many_small_weights_beside_a_large_one(D, G, gap):
+    """One key `gap` above 6000 others in the exponent: what those add up to is what they
+    have of the output (the first key's value is zero), although each weighs e^-gap."""
+    n = 6000
+    c = make([n], G, 1, D, 16, "f16", seed=35, spread=0.0)
+    kc, vc = c["kc"].view(torch.uint8), c["vc"].view(torch.uint8)
+    t = c["bt"][0].long()
+    kc.zero_()
+    one = int(torch.tensor(1.0).to(torch.float8_e4m3fn).view(torch.uint8))
+    kc[t[0], :, 0] = one
+    vc[:] = one
+    vc[t[0], :, 0] = 0
+    c["ks"].view(torch.uint8).fill_(127)
+    c["vs"].view(torch.uint8).fill_(127)
+    c["scale"] = 1.0
+    c["q"].fill_(gap / D)
+    out = check(c, "f16")
+    s = (c["q"][0, 0].double().sum()).item()
+    want = (n - 1) * math.exp(-s) / (1 + (n - 1) * math.exp(-s))
+    # the output's own rounding, the weights' 2^-12 and the sums'
+    assert abs(float(out[0, 0, 0]) - want) <= want * (2.0 ** -11 + 2.0 ** -12 + 2 * n * 2.0 ** -24 + 2.0 ** -16) + 2.0 ** -25
+
+
 @pytest.mark.parametrize("D,G", [(128, 8), (64, 4)])
 def test_rising_scores(D, G):
     """Later keys far above earlier ones: the running maximum moves all the way."""
