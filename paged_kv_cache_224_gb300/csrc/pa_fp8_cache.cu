@@ -296,8 +296,10 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
 
 // ---- reading back ------------------------------------------------------------
 
-// CTA (b, piece): piece of block b of the laid-out sequences, four vectors of 16 codes a
-// thread, all on their way together, each into two vectors of 16-bit values.
+// CTA (b, piece): piece of block b of the laid-out sequences, four vectors of 8 codes a
+// thread, all on their way together, each into one vector of 16-bit values, side by side
+// with its neighbours' (vectors of 16 codes, whose two halves are stored 32 bytes apart
+// from lane to lane, cost a chunk after 8192 tokens 3 us more, eight of those 9).
 constexpr int kExpandVectors = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) expand_fp8_kernel(const __grid_constant__ Fp8ExpandParams p) {
@@ -320,32 +322,25 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const __grid_constant__
         if (!ok) flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
     }
     if (!ok) return;
-    const int per_head = p.block_size * p.head_dim / 16, n = p.num_kv_heads * per_head;
+    const int per_head = p.block_size * p.head_dim / 8, n = p.num_kv_heads * per_head;
     const size_t src0 = (size_t)blk * n, dst0 = (size_t)at * n;
     const int i0 = blockIdx.y * (256 * kExpandVectors) + tid;
-    uint4 u[kExpandVectors];
+    uint2 u[kExpandVectors];
     float scale[kExpandVectors];
 #pragma unroll
     for (int k = 0; k < kExpandVectors; ++k) {
         const int i = i0 + k * 256, j = i >= n ? i - n : i;
         if (i >= 2 * n) continue;
-        u[k] = reinterpret_cast<const uint4 *>(i >= n ? p.v_cache : p.k_cache)[src0 + j];
+        u[k] = reinterpret_cast<const uint2 *>(i >= n ? p.v_cache : p.k_cache)[src0 + j];
         scale[k] = scale_of((i >= n ? p.v_scales : p.k_scales)[(size_t)blk * p.num_kv_heads + j / per_head]);
     }
 #pragma unroll
     for (int k = 0; k < kExpandVectors; ++k) {
         const int i = i0 + k * 256, j = i >= n ? i - n : i;
         if (i >= 2 * n) continue;
-        float f[16], a[8], b[8];
-        values16(u[k], f);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            a[x] = f[x] * scale[k];
-            b[x] = f[8 + x] * scale[k];
-        }
-        uint4 *dst = reinterpret_cast<uint4 *>(i >= n ? p.v_out : p.k_out) + (dst0 + j) * 2;
-        dst[0] = pack8<T>(a);
-        dst[1] = pack8<T>(b);
+        const float2 a = values2(u[k].x & 0xffffu), b = values2(u[k].x >> 16), c = values2(u[k].y & 0xffffu), d = values2(u[k].y >> 16);
+        const float f = scale[k], x[8] = {a.x * f, a.y * f, b.x * f, b.y * f, c.x * f, c.y * f, d.x * f, d.y * f};
+        reinterpret_cast<uint4 *>(i >= n ? p.v_out : p.k_out)[dst0 + j] = pack8<T>(x);
     }
 }
 
@@ -400,7 +395,7 @@ int launch_store_fp8(pa_dtype dt, const RotaryParams &p, cudaStream_t stream) {
 int launch_expand_fp8(pa_dtype dt, const Fp8ExpandParams &p, cudaStream_t stream) {
     const int blocks = p.first[p.num_seqs];
     if (blocks == 0) return PA_OK;
-    const long long vectors = 2LL * p.num_kv_heads * p.block_size * p.head_dim / 16;
+    const long long vectors = 2LL * p.num_kv_heads * p.block_size * p.head_dim / 8;
     const long long pieces = (vectors + 256 * kExpandVectors - 1) / (256 * kExpandVectors);
     if (pieces > 65535) return PA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks, (unsigned)pieces);
