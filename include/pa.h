@@ -564,8 +564,14 @@ PA_API int pa_rotary_and_cache_fp8(void *query_out, int64_t query_out_stride, co
  * and the keys they would supply are left out), without partition_tokens: contexts are
  * cut where that shares the batch out evenly, so that a row's last bits depend on the
  * batch that it is in.  The same call gives the same bits.
- *   workspace      >= pa_decode_fp8_workspace_bytes(...) bytes, 256-byte aligned,
- *                  scratch (may be NULL when that is 0); its size depends on the device
+ *   workspace      >= pa_decode_fp8_workspace_bytes(...) bytes, 256-byte aligned (may
+ *                  be NULL when that is 0; its size depends on the device), ZERO-FILLED
+ *                  before its first use: its first 4 KB hold counters that every call
+ *                  that completes leaves at zero again, so one workspace serves every
+ *                  later call whose sizes it covers (after a call that set
+ *                  PA_DEVERR_TIMEOUT, or whose context_lens were written while it
+ *                  ran, zero-fill it again).  Not to be shared with work
+ *                  that overlaps the call on the device
  * max_blocks_per_seq * block_size, num_seqs * num_heads and num_blocks * num_kv_heads *
  * block_size must stay below 2^31 - 256.
  */

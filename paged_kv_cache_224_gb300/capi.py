@@ -937,12 +937,12 @@ def pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, b
 
 
 def decode_fp8_workspace(query, num_kv_heads, block_size, max_context_len, stream=None):
-    """Allocate (with torch) a workspace big enough for ``pa_decode_fp8`` on ``stream``
-    (None: the current one)."""
+    """A zero-filled workspace big enough for ``pa_decode_fp8`` (zero-filled once, on
+    ``stream`` or the current one; the calls keep it usable)."""
     B, Hq, D = query.shape
     with torch.cuda.device(query.device):
         n = pa_decode_fp8_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len)
-    return _scratch(query.device, n, stream)
+    return _scratch(query.device, n, stream, torch.zeros)
 
 
 def pa_decode_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, max_context_len,

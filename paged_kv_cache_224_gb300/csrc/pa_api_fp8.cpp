@@ -89,20 +89,20 @@ int store_fp8(pa::RotaryParams &p, uint8_t *k_scales, uint8_t *v_scales, pa_dtyp
     return pa::launch_store_fp8(dtype, p, static_cast<cudaStream_t>(stream));
 }
 
-// The decode's workspace: what each (sequence, kv head) was cut into, the partials'
-// accumulators and (max, sum) pairs.  None where every context is a single tile.
+// The decode's workspace: counters (where they are does not depend on the call), the
+// partials' accumulators and (max, sum) pairs.  None where every context is a single tile.
 struct DecodeWs {
     int ctas;
-    size_t units = 0, acc = 0, ml = 0;
+    size_t counters = 0, acc = 0, ml = 0;
     DecodeWs(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_context_len) {
         ctas = pa::fp8_decode_ctas(num_seqs, num_kv_heads, num_heads / num_kv_heads, head_dim, max_context_len);
         if (max_context_len <= 128) return;
         const size_t n = (size_t)2 * ctas * (num_heads / num_kv_heads);
-        units = round256((size_t)num_seqs * num_kv_heads * 2 * sizeof(int));
+        counters = pa::kFp8MaxCtas * sizeof(unsigned);
         acc = round256(n * head_dim * sizeof(float));
         ml = round256(n * 2 * sizeof(float));
     }
-    size_t total() const { return units + acc + ml; }
+    size_t total() const { return counters + acc + ml; }
 };
 
 // The prefill's own workspace for a launch of up to kPrefillMaxSeqs chunks, then the
@@ -250,9 +250,9 @@ int pa_decode_fp8(void *out, const void *query, const uint8_t *k_cache, const ui
     d.table_stride = max_blocks_per_seq;
     if (w.total() > 0) {
         char *base = static_cast<char *>(workspace);
-        p.units = reinterpret_cast<int2 *>(base);
-        d.ws_acc = reinterpret_cast<float *>(base + w.units);
-        d.ws_ml = reinterpret_cast<float2 *>(base + w.units + w.acc);
+        p.counters = reinterpret_cast<unsigned *>(base);
+        d.ws_acc = reinterpret_cast<float *>(base + w.counters);
+        d.ws_ml = reinterpret_cast<float2 *>(base + w.counters + w.acc);
     }
     p.ctas = w.ctas;
     p.k_scales = k_scales;

@@ -22,7 +22,7 @@
 // HBM-bound: every code is read once, and 128 keys of a kv head are 32 KB.  The call's
 // tiles of 128 keys lie end to end and every CTA, two to an SM, takes an equal share of
 // them, whatever the lengths are: one start per CTA, no tail, and no more than two
-// partials per CTA for the merge.  A CTA is
+// partials per CTA, which the last CTA to finish one of a unit's pieces merges.  A CTA is
 //   warp 0    TMA producer: one copy per (block, K or V) into a ring of 96 KB, tiles in
 //             the order that the MMAs take them, running on from one sequence to the next;
 //   warp 1    MMA issuer (one thread): QK^T of tile j into one of two S buffers, then
@@ -35,14 +35,18 @@
 // At head_dim 64, where a tile is 16 KB, three CTAs to an SM (two with eight heads).
 //
 // Measured (bf16, us, share of the copy rate): 256 contexts of up to 4096 tokens, 32/8
-// heads of 128, 176, 94%; eight of 32768 to 131072, 64/8 heads, 207, 98%; 256 of 2048, 8/8
-// heads of 64, 87, 90%, 64/8 heads of 64, 132, 60% (bound by the softmax warps).  On the
+// heads of 128, 176, 94%; eight of 32768 to 131072, 64/8 heads, 207, 98%; 256 of 2048, 32/8
+// heads of 64, 91.5, 86%, 64/8 heads of 64, 131, 60% (bound by the softmax warps).  On the
 // way (the first two cases): on the CUDA cores 1088 and 2367; one unit (sequence, kv head,
 // 1024 tokens) a CTA 203 and 228; equal shares 196 and 216.  What runs once a piece was
 // kept small after 256 contexts of 2048 tokens with 64/8 heads had taken 234, not 168: the
 // roles' code did not stay in the instruction cache together.  A vote instead of every
-// tile's maxima: 1024 contexts of 512 tokens, 64/8 heads, 197 -> 188.
+// tile's maxima: 1024 contexts of 512 tokens, 64/8 heads, 197 -> 188.  The merge at the end of
+// this kernel, not in one behind it: 188 -> 183, one context of 4096, 32/8 heads, 15.1 -> 11.5.
 // All waits are bounded; a wait that gives up flags PA_DEVERR_TIMEOUT.
+#include <algorithm>
+#include <cmath>
+
 #include "pa_internal.h"
 
 namespace pa {
@@ -50,10 +54,16 @@ namespace pa {
 int launch_decode_fp8_bf16(int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
 int launch_decode_fp8_f16(int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
 
+// As many CTAs as the SMs hold, but at most 4 sqrt(tiles) to a (sequence, kv head) of the
+// greatest length: its pieces are merged by one CTA, and with p pieces that takes as long
+// as p grows, the pieces themselves as tiles / p does.  One context of 131072 tokens, 8/1
+// heads: 35 us by all 304 CTAs (1024 tiles), 28.6 by up to 6 sqrt(tiles), 25.2 by 4 or 3,
+// 27.5 by 2; of 16384: 20.0, 16.3, 15.1, 15.4.  64/8 heads reach all 304 either way.
 int fp8_decode_ctas(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len) {
-    const long long tiles = (long long)num_seqs * num_kv_heads * (((long long)max_context_len + 127) / 128);
-    const long long most = (long long)d8::ctas_per_sm(head_dim, group) * sm_count();
-    return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most);
+    const long long units = (long long)num_seqs * num_kv_heads, tiles = ((long long)max_context_len + 127) / 128;
+    const long long pieces = std::min(tiles, (long long)std::ceil(4.0 * std::sqrt((double)tiles)));
+    const long long most = std::min((long long)d8::ctas_per_sm(head_dim, group) * sm_count(), (long long)kFp8MaxCtas);
+    return (int)std::max(1LL, std::min(most, units * pieces));
 }
 
 int launch_decode_fp8(pa_dtype dt, int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream) {

@@ -46,10 +46,12 @@ struct Lay {
     static constexpr int kOffBar = kOffSc + kScaleRing * 16 * 16;
     static constexpr int kBars = 2 * S + 10 + 2 * kScaleRing;
     static constexpr int kOffLen = kOffBar + (kBars * 8 + 8 + 15) / 16 * 16;
-    // [4 warps][GP] maxima, [4][GP] sums, [2][GP] query scales, [G][64] sums of odd keys
+    // [4 warps][GP] maxima, [4][GP] sums, [2][GP] query scales, [G][64] sums of odd keys, [2] of Cut
     static constexpr int kOffXch = kOffLen + kLens * 4 + 64;
-    static constexpr int kUsed = kOffXch + (4 * GP + 4 * GP + 2 * GP + (kPar == 2 ? G * 64 : 0)) * 4;
+    static constexpr int kUsed = kOffXch + (4 * GP + 4 * GP + 2 * GP + (kPar == 2 ? G * 64 : 0)) * 4 + 2 * 32;
     static constexpr int kAlloc = kUsed + 1024;             // room to align the base to 1 KB
+    // (what a merge keeps goes where the tiles were; two units' weights never do together)
+    static_assert((kThreads / 32 * G * D + G + kFp8MaxCtas * G) * 4 <= S * kSlot, "the merge's sums and weights");
 };
 
 // kind::f8f6f4, fp32 accumulator: A e4m3, B e4m3 or e5m2.
@@ -267,8 +269,6 @@ __device__ __forceinline__ Walk begin(const Fp8DecodeParams &fp, int head_dim, i
         if (clamped_len(p, s) > 0) continue;
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (size_t)s * p.num_heads * head_dim);
         for (int i = tid; i < p.num_heads * head_dim / 8; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
-        if (fp.units)
-            for (int i = tid; i < p.num_kv_heads; i += kThreads) fp.units[(size_t)s * p.num_kv_heads + i] = make_int2(-1, 1);
     }
     __syncthreads();
     w.first = true;
@@ -280,6 +280,120 @@ __device__ __forceinline__ Walk begin(const Fp8DecodeParams &fp, int head_dim, i
     __syncthreads();
     w.len = has ? lens[0] : 0;
     return w;
+}
+
+// A unit (sequence, kv head) that the shares cut, as a CTA that has a piece of it sees it.
+struct Cut {
+    long long from;  // its first tile within the call
+    int whole;  // its tiles
+    int row0;   // its first row of the output
+    int lead;   // CTA that has its first piece; piece i is of CTA lead + i
+    int n;      // pieces; 0: no such unit
+    int first;  // slot of the first piece (piece i > 0 has the even slot of its CTA); -1 once another CTA merges it
+    int pad;
+};
+
+// Log-sum-exp merge of a unit's pieces by all warps:
+//   M = max m_i,  w_i = 2^(m_i - M),  out = sum w_i acc_i / sum w_i l_i.
+// A warp has a head for the weights, a lane a piece; then a warp has every kWarps-th
+// piece, whole, and the warps' sums are added up.  `work`: the ring, which has served.
+// (Loads go past L1, which may hold what an earlier call left.  Inlined: with this and
+// merge_few out of line 256 contexts of 2048 tokens, 64/8 heads of 64, took 138 us, not 131.)
+template <typename T, int D, int G>
+__device__ __forceinline__ void merge_many(const DecodeParams &p, const Cut &c, float *work) {
+    using V = typename std::conditional<D == 128, float4, float2>::type;
+    constexpr int kWarps = kThreads / 32, kN = D / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float *sums = work, *total = sums + kWarps * G * D, *weight = total + G;  // [kWarps][G][D], [G], [n][G]
+    auto slot = [&](int i) { return (size_t)(i ? 2 * (c.lead + i) : c.first) * G; };
+#pragma unroll 1
+    for (int h = warp; h < G; h += kWarps) {
+        float M = kEmptyMax, l = 0.f;
+        for (int i = lane; i < c.n; i += 32) {
+            const float2 ml = __ldcg(&p.ws_ml[slot(i) + h]);
+            const float top = fmaxf(M, ml.x);
+            l = fmaf(l, fast_exp2(M - top), fast_exp2(ml.x - top) * ml.y);
+            M = top;
+            weight[i * G + h] = ml.x;
+        }
+        float top = M;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+        l *= fast_exp2(M - top);
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
+        for (int i = lane; i < c.n; i += 32) weight[i * G + h] = fast_exp2(weight[i * G + h] - top);
+        if (lane == 0) total[h] = l;
+    }
+    __syncthreads();
+    if (warp < c.n) {
+        float o[G][kN] = {};
+#pragma unroll (16 / G)
+        for (int i = warp; i < c.n; i += kWarps) {
+            const V *src = reinterpret_cast<const V *>(p.ws_acc + slot(i) * D) + lane;
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                const V v = __ldcg(src + h * 32);
+                const float w = weight[i * G + h];
+#pragma unroll
+                for (int k = 0; k < kN; ++k) o[h][k] = fmaf(w, reinterpret_cast<const float *>(&v)[k], o[h][k]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+            *reinterpret_cast<V *>(sums + (warp * G + h) * D + lane * kN) = *reinterpret_cast<const V *>(o[h]);
+    }
+    __syncthreads();
+    for (int e = tid; e < G * D / 2; e += kThreads) {
+        float2 x = make_float2(0.f, 0.f);
+        for (int w = 0; w < min(c.n, kWarps); ++w) {
+            const float2 y = reinterpret_cast<const float2 *>(sums)[w * (G * D / 2) + e];
+            x.x += y.x, x.y += y.y;
+        }
+        const float l = total[e / (D / 2)];
+        reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + (size_t)c.row0 * D)[e] = l != 0.f ? Elem<T>::pack2(x.x / l, x.y / l) : 0u;
+    }
+    __syncthreads();  // (the next unit's weights and sums go to the same place)
+}
+
+// The same of up to kFew pieces by single threads, four dimensions each, with everything
+// loaded at once: most cuts in a large batch are in two.  (32 contexts of 700 tokens, 32/8
+// heads: 17.0 us by merge_many alone, 15.0 by both.)
+constexpr int kFew = 4;
+template <typename T, int D, int G>
+__device__ __forceinline__ void merge_few(const DecodeParams &p, const Cut *cuts) {
+#pragma unroll 1
+    for (int e = threadIdx.x; e < 2 * G * (D / 4); e += kThreads) {
+        const int k = e >= G * (D / 4), f = e - k * G * (D / 4), h = f / (D / 4);
+        const Cut c = cuts[k];
+        if (c.n == 0 || c.n > kFew || c.first < 0) continue;
+        float2 ml[kFew];
+        float4 v[kFew];
+        float M = kEmptyMax, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            ml[i] = make_float2(kEmptyMax, 0.f);
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < c.n) {
+                const size_t at = (size_t)(i ? 2 * (c.lead + i) : c.first) * G;
+                ml[i] = __ldcg(&p.ws_ml[at + h]);
+                v[i] = __ldcg(reinterpret_cast<const float4 *>(p.ws_acc + at * D) + f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) M = fmaxf(M, ml[i].x);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            const float w = fast_exp2(ml[i].x - M);
+            l = fmaf(w, ml[i].y, l);
+            o.x = fmaf(w, v[i].x, o.x), o.y = fmaf(w, v[i].y, o.y);
+            o.z = fmaf(w, v[i].z, o.z), o.w = fmaf(w, v[i].w, o.w);
+        }
+        uint2 out = make_uint2(0u, 0u);
+        if (l != 0.f) out = make_uint2(Elem<T>::pack2(o.x / l, o.y / l), Elem<T>::pack2(o.z / l, o.w / l));
+        reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (size_t)c.row0 * D)[f] = out;
+    }
 }
 
 template <typename T, int D, int G>
@@ -307,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
     float4 *scales = reinterpret_cast<float4 *>(smem + L::kOffSc);
     float *xmax = reinterpret_cast<float *>(smem + L::kOffXch);
     float *xsum = xmax + 4 * GP, *qscale = xsum + 4 * GP, *odd = qscale + 2 * GP;
+    Cut *cuts = reinterpret_cast<Cut *>(odd + (L::kPar == 2 ? G * 64 : 0));  // [2], of the pieces with slots 2c and 2c + 1
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * S; ++i) mbar_init(&full[i], 1);
         for (int b = 0; b < 2; ++b) {
@@ -321,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
             mbar_init(&sc_empty[i], 4);
         }
         fence_barrier_init();
+        cuts[0].n = cuts[1].n = cuts[0].whole = cuts[1].whole = 0;
     }
     pdl_wait();     // the kernel before this one on the stream (e.g. the cache write) has finished
     // (not before the wait: a kernel that is still to allocate tensor memory on this SM
@@ -332,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_trigger();  // the merge may be scheduled once every CTA of this grid has started
+    pdl_trigger();  // what follows may be placed; it waits for these writes
     Walk walk = begin<T>(fp, D, lens, reinterpret_cast<long long *>(lens + kLens));
     tc_fence_before();
     __syncthreads();
@@ -514,6 +630,12 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
             __syncwarp();
             if (lane == 0) mbar_arrive1(&q_full[qb]);
             ++pieces;
+            if (q.slot >= 0 && lane == 0) {
+                Cut &c = cuts[q.slot & 1];
+                c.from = q.at - q.tile;
+                c.whole = q.whole;
+                c.row0 = q.s * p.num_heads + q.kvh * G;
+            }
             for (int j = 0; j < q.n; ++j, ++g) {
                 const int in = j & (per_chunk - 1);
                 if (in == 0) {
@@ -535,6 +657,14 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(&sc_full[r]);
             }
+        }
+        // (here and not with its piece: the divisions are a lot of code)
+        __syncwarp();
+        if (lane < 2 && cuts[lane].whole > 0) {
+            Cut &c = cuts[lane];
+            c.lead = owner(walk.total, walk.ctas, c.from);
+            c.n = owner(walk.total, walk.ctas, c.from + c.whole - 1) - c.lead + 1;
+            c.first = share(walk.total, walk.ctas, c.lead) == c.from ? 2 * c.lead : 2 * c.lead + 1;
         }
     } else {
         // ============================================================ softmax
@@ -706,62 +836,29 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                 }
             }
             // (the next piece's sums go to xsum and odd after its own tiles' barriers)
-            // the piece with the first tile says where the partials are
-            if (fp.units && q.tile == 0 && t == 0)
-                fp.units[(size_t)q.s * p.num_kv_heads + q.kvh] =
-                    make_int2(q.slot, q.slot < 0 ? 1 : owner(walk.total, walk.ctas, q.at + q.whole - 1) - (int)blockIdx.x + 1);
         }
     }
     tc_fence_before();
+    __threadfence();  // the partials, before the counts below
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols) : "memory");
     }
-}
-
-// Log-sum-exp merge of the pieces of what was cut, one warp per (sequence, query head):
-//   M = max m_i,  w_i = 2^(m_i - M),  out = sum w_i acc_i / sum w_i l_i.
-// (It does not let the kernel behind it start early: a decode placed beside the last of
-// these CTAs finds less room than its grid counts on, and what does not fit runs after
-// the rest.  256 contexts of 2048 tokens, 8/8 heads of 64: 144 us, against 88.)
-template <typename T, int D>
-__global__ void __launch_bounds__(128) merge_fp8_kernel(const __grid_constant__ Fp8DecodeParams fp) {
-    constexpr int V = D / 32;  // values per lane
-    const DecodeParams &p = fp.d;
-    pdl_wait();                // the decode kernel's partials are complete and visible
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (long long)p.num_seqs * p.num_heads) return;
-    const int G = p.grp_inner, h = (int)(row % G);  // rows of a (sequence, kv head) are adjacent
-    const int2 u = fp.units[row / G];
-    if (u.y <= 1) return;
-    auto slot = [&](int i) { return (size_t)(i ? 2 * ((u.x >> 1) + i) : u.x) * G + h; };
-    float M = kEmptyMax;
-    for (int i = lane; i < u.y; i += 32) M = fmaxf(M, p.ws_ml[slot(i)].x);
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, m));
-    float lsum = 0.f, o[V];
-#pragma unroll
-    for (int d = 0; d < V; ++d) o[d] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < u.y; ++i) {
-        const size_t at = slot(i);
-        const float2 ml = p.ws_ml[at];
-        const float w = fast_exp2(ml.x - M);
-        lsum = fmaf(w, ml.y, lsum);
-        const float2 *a = reinterpret_cast<const float2 *>(p.ws_acc + at * D + lane * V);
-#pragma unroll
-        for (int d = 0; d < V / 2; ++d) {
-            const float2 x = a[d];
-            o[2 * d] = fmaf(w, x.x, o[2 * d]);
-            o[2 * d + 1] = fmaf(w, x.y, o[2 * d + 1]);
-        }
+    if (cuts[0].n == 0 && cuts[1].n == 0) return;
+    // The last CTA to get here of those that have a unit's pieces merges them.  Which that
+    // is does not change the result: the sums are the same.
+    if (threadIdx.x < 2) {
+        Cut &c = cuts[threadIdx.x];
+        // (counts to n - 1 and then from 0 again: nothing is left for the next call)
+        if (c.n > 0 && atomicInc(fp.counters + c.lead, (unsigned)(c.n - 1)) != (unsigned)(c.n - 1)) c.first = -1;
+        __threadfence();
     }
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + row * D + lane * V);
-#pragma unroll
-    for (int d = 0; d < V / 2; ++d)
-        dst[d] = lsum != 0.f ? Elem<T>::pack2(o[2 * d] / lsum, o[2 * d + 1] / lsum) : 0u;
+    __syncthreads();
+    merge_few<T, D, G>(p, cuts);
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k)
+        if (cuts[k].n > kFew && cuts[k].first >= 0) merge_many<T, D, G>(p, cuts[k], reinterpret_cast<float *>(smem));
 }
 
 // ---- host side -------------------------------------------------------------
@@ -790,12 +887,7 @@ int launch_t(const Fp8DecodeParams &p, cudaStream_t stream) {
     if (!make_rows_map(&tmk, p.d.k_cache, rows, D, p.d.block_size) ||
         !make_rows_map(&tmv, p.d.v_cache, rows / L::kPar, 128, p.d.block_size / L::kPar))
         return PA_ERR_CUDA;
-    if (launch_pdl(kern, dim3(p.ctas), dim3(kThreads), L::kAlloc, stream, p, tmk, tmv) != cudaSuccess) return PA_ERR_CUDA;
-    if (!p.units) return PA_OK;
-    const long long heads = (long long)p.d.num_seqs * p.d.num_heads;
-    return launch_pdl(merge_fp8_kernel<T, D>, dim3((unsigned)((heads + 3) / 4)), dim3(128), 0, stream, p) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    return launch_pdl(kern, dim3(p.ctas), dim3(kThreads), L::kAlloc, stream, p, tmk, tmv) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <typename T, int D>

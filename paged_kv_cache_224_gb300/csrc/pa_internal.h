@@ -215,9 +215,10 @@ struct Fp8DecodeParams {
     DecodeParams d;              // ws_acc, ws_ml: [2 * ctas slots][group]
     const uint8_t *k_scales;     // [NB][Hkv]
     const uint8_t *v_scales;
-    int2 *units;                 // [B][Hkv] (slot of the first piece, pieces); null where nothing can be cut
+    unsigned *counters;          // [CTAs] of the unit that a CTA is the first of several to have pieces of; zero
     int ctas;
 };
+constexpr int kFp8MaxCtas = 1024;
 int fp8_decode_ctas(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len);
 namespace d8 {
 // CTAs of the decode over an 8-bit cache that an SM holds.  At head_dim 64 a tile is 16 KB

@@ -96,11 +96,11 @@ def test_decode_refusals(lib):
     assert lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 16, 128) == 0
     # 4 sequences of 2 tiles, 2 kv heads: 16 CTAs, two partials each of 4 heads
     need = lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 16, 200)
-    assert need == 256 + 2 * 16 * 4 * (128 + 2) * 4
+    assert need == 4096 + 2 * 16 * 4 * (128 + 2) * 4
     assert decode(lib, ml=200, ws=0) == -5 and decode(lib, ml=200, wsb=need - 1) == -5
     assert decode(lib, ml=200, ws=BUF + 16) == -6
     # two CTAs to each of (without a device) 152 SMs, however large the batch
-    assert lib.pa_decode_fp8_workspace_bytes(256, 32, 8, 128, 16, 4096) == 256 * 8 * 8 + 2 * 304 * 4 * (128 + 2) * 4
+    assert lib.pa_decode_fp8_workspace_bytes(256, 32, 8, 128, 16, 4096) == 4096 + 2 * 304 * 4 * (128 + 2) * 4
     assert lib.pa_decode_fp8_workspace_bytes(4, 7, 2, 128, 16, 200) == 0
     assert lib.pa_decode_fp8_workspace_bytes(4, 8, 2, 128, 24, 200) == 0
 

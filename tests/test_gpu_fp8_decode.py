@@ -94,6 +94,27 @@ def test_shares(D, G, dtype, lens, Hkv):
         check(c, dtype)
 
 
+def test_one_workspace_for_calls_of_all_sizes():
+    """The counters that tell who merges are at zero after every call."""
+    big = make([5000, 0, 3, 129, 1024], 8 * 2, 2, 128, 16, "bf16", seed=41)
+    small = make([200, 700], 8 * 2, 2, 128, 16, "bf16", seed=42)
+    ws = pa.decode_fp8_workspace(big["q"], 2, 16, big["most"])
+    a, b = check(big, "bf16", workspace=ws).clone(), check(small, "bf16", workspace=ws).clone()
+    for _ in range(5):
+        assert torch.equal(decode(big, workspace=ws), a)
+        assert torch.equal(decode(small, workspace=ws), b)
+    torch.cuda.synchronize()
+    assert not bool(ws[:4096].any())
+
+
+@pytest.mark.parametrize("D,G,Hkv", [(128, 8, 1), (128, 2, 1), (64, 4, 1)])
+def test_one_long_context_in_many_pieces(D, G, Hkv):
+    c = make([40000], G * Hkv, Hkv, D, 64, "bf16", seed=43)
+    out = check(c, "bf16")
+    for _ in range(3):
+        assert torch.equal(decode(c), out)   # whoever merges
+
+
 def test_a_row_alone_and_in_a_batch():
     """Cut differently, the same up to fp32 sums and one rounding."""
     c = make([2500, 700, 1, 90], 8, 2, 128, 16, "bf16", seed=40)
