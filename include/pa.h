@@ -589,7 +589,8 @@ PA_API int pa_decode_fp8(void *out, const void *query, const uint8_t *k_cache, c
  * prompt chunks whose own keys and values are in the cache already.  The sequences'
  * cached values are laid out once in dtype (exact: every code times its scale is a
  * bf16 value, and an fp16 one as far as fp16 reaches) and attended as pa_prefill_batch
- * does, with its numerics.
+ * does, but with each softmax weight as two values of dtype (its rounded value and what
+ * the rounding left), so that the output's is the only rounding that counts.
  *   prefix_lens, chunk_lens  int [num_seqs], HOST memory
  *   workspace      >= pa_prefill_batch_fp8_workspace_bytes(...) bytes, 256-byte
  *                  aligned, required; its content on entry is ignored; not to be shared

@@ -127,7 +127,7 @@ struct PrefillWs {
             }
         }
         pre = round256(pre);
-        table = round256((size_t)blocks * sizeof(int32_t));
+        table = round256((size_t)blocks * (block_size / pa::kExpandRows) * sizeof(int32_t));
         pool = round256((size_t)blocks * num_kv_heads * block_size * head_dim * 2);
     }
     size_t total() const { return pre + table + 2 * pool; }
@@ -324,6 +324,7 @@ int pa_prefill_batch_fp8(void *out, const void *query, const uint8_t *k_cache, c
     p.scale_log2 = scale * 1.4426950408889634f;
     p.query_rows = (int)rows;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int parts = block_size / pa::kExpandRows;
     int row = 0;
     for (int i = 0; i < num_seqs; ++i) {
         if (chunk_lens[i] > 0) {
@@ -331,7 +332,7 @@ int pa_prefill_batch_fp8(void *out, const void *query, const uint8_t *k_cache, c
             x.tables[n] = block_tables + (size_t)i * max_blocks_per_seq;
             x.first[n + 1] = x.first[n] + (prefix_lens[i] + chunk_lens[i] - 1) / block_size + 1;
             pa::PrefillSeq &q = p.seqs[n];
-            q.block_table = x.table + x.first[n];
+            q.block_table = x.table + (size_t)x.first[n] * parts;
             q.prefix_len = prefix_lens[i];
             q.chunk_len = chunk_lens[i];
             q.row_start = row;
@@ -339,9 +340,9 @@ int pa_prefill_batch_fp8(void *out, const void *query, const uint8_t *k_cache, c
         row += chunk_lens[i];
         if (p.num_seqs == pa::kPrefillMaxSeqs || (i == num_seqs - 1 && p.num_seqs > 0)) {
             x.num_seqs = p.num_seqs;
-            p.num_blocks = x.first[p.num_seqs];
+            p.num_blocks = x.first[p.num_seqs] * parts;
             int rc = pa::launch_expand_fp8(dtype, x, st);
-            if (rc == PA_OK) rc = pa::launch_prefill(dtype, head_dim, block_size, group, p, workspace, w.pre, st);
+            if (rc == PA_OK) rc = pa::launch_prefill(dtype, head_dim, pa::kExpandRows, group, p, workspace, w.pre, st, true);
             if (rc != PA_OK) return rc;
             p.num_seqs = 0;
         }

@@ -317,12 +317,14 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const __grid_constant__
     }
     const int blk = p.tables[lo][at - p.first[lo]];
     const bool ok = blk >= 0 && blk < p.num_blocks;
-    if (tid == 0 && blockIdx.y == 0) {
-        p.table[at] = ok ? at : -1;
-        if (!ok) flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
+    const int parts = p.block_size / kExpandRows;
+    if (blockIdx.y == 0) {
+        for (int i = tid; i < parts; i += 256) p.table[at * parts + i] = ok ? at * parts + i : -1;
+        if (tid == 0 && !ok) flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
     }
     if (!ok) return;
     const int per_head = p.block_size * p.head_dim / 8, n = p.num_kv_heads * per_head;
+    const int per_part = kExpandRows * p.head_dim / 8;
     const size_t src0 = (size_t)blk * n, dst0 = (size_t)at * n;
     const int i0 = blockIdx.y * (256 * kExpandVectors) + tid;
     uint2 u[kExpandVectors];
@@ -340,7 +342,10 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const __grid_constant__
         if (i >= 2 * n) continue;
         const float2 a = values2(u[k].x & 0xffffu), b = values2(u[k].x >> 16), c = values2(u[k].y & 0xffffu), d = values2(u[k].y >> 16);
         const float f = scale[k], x[8] = {a.x * f, a.y * f, b.x * f, b.y * f, c.x * f, c.y * f, d.x * f, d.y * f};
-        reinterpret_cast<uint4 *>(i >= n ? p.v_out : p.k_out)[dst0 + j] = pack8<T>(x);
+        // vector j is `rest` of its head, in the head's part rest / per_part
+        const int head = j / per_head, rest = j - head * per_head, part = rest / per_part;
+        const int dst = (part * p.num_kv_heads + head) * per_part + (rest - part * per_part);
+        reinterpret_cast<uint4 *>(i >= n ? p.v_out : p.k_out)[dst0 + dst] = pack8<T>(x);
     }
 }
 

@@ -156,7 +156,7 @@ struct RotaryParams {
     // 8-bit cache: k_cache and v_cache hold codes, these their scales [NB][Hkv]
     uint8_t *k_scales;
     uint8_t *v_scales;
-    int tokens_per_cta;          // of the 8-bit cache write, 1 .. 32
+    int tokens_per_cta;          // of the 8-bit cache write, 1 .. 16
 };
 
 // One eviction (see pa_evict): the kernels mark, select and copy.
@@ -228,10 +228,12 @@ namespace d8 {
 constexpr int ctas_per_sm(int head_dim, int group) { return head_dim == 64 && group <= 4 ? 3 : 2; }
 }  // namespace d8
 int launch_decode_fp8(pa_dtype dt, int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
-// The codes of the sequences' first blocks as values of dt, laid end to end: block
-// j of sequence i becomes block first[i] + j of k_out and v_out, whose own table is
-// `table` (the number itself, or -1 where the sequence's entry is outside the pool,
+// The codes of the sequences' first blocks as values of dt, laid end to end in blocks of
+// kExpandRows rows: with n = block_size / kExpandRows, block j of sequence i becomes
+// blocks n (first[i] + j) to n (first[i] + j) + n - 1 of k_out and v_out, whose own table
+// is `table` (the number itself, or -1 where the sequence's entry is outside the pool,
 // which is flagged).  Also clears num_zero words at zero.
+constexpr int kExpandRows = 16;
 struct Fp8ExpandParams {
     const uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
     void *k_out, *v_out;
@@ -251,8 +253,9 @@ int launch_reshape_and_cache(const void *key, const void *value, void *k_cache, 
 int launch_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream);
 // With the norms whose weights p has; num_kv_heads may be 0.
 int launch_norm_rotary(pa_dtype dt, const RotaryParams &p, cudaStream_t stream);
-// Keys (normed and rotated as p says) and values into an 8-bit cache, then the
-// queries as launch_rotary does; block_size up to kStoreMaxBlock.
+// Keys (normed and rotated as p says) and values into an 8-bit cache, beside the
+// queries' kernel (launch_rotary's or launch_norm_rotary's), which is launched first;
+// block_size up to kStoreMaxBlock.
 constexpr int kStoreMaxBlock = 128;
 int launch_store_fp8(pa_dtype dt, const RotaryParams &p, cudaStream_t stream);
 int launch_evict(const EvictParams &p, cudaStream_t stream);
@@ -280,8 +283,11 @@ size_t prefill_workspace_bytes(int num_seqs, long long total_chunk_len, int grou
 // Where its counters begin (the same on every call); they reach to its end.
 size_t prefill_counters_offset();
 // workspace may be NULL (or too small): each CTA then computes one whole unit.
+// two: softmax weights as two 16-bit values, for block_size kExpandRows.
 int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const PrefillParams &p,
-                   void *workspace, size_t workspace_bytes, cudaStream_t stream);
+                   void *workspace, size_t workspace_bytes, cudaStream_t stream, bool two = false);
+// (of launch_prefill: the launch itself)
+int launch_prefill_two(pa_dtype dt, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
 // Attention of a batch over long shared prefixes (pa_decode_common_prefix):
 // `groups` groups of group_size consecutive sequences, each over the first
 // prefix_tokens tokens of its first sequence's table, and every sequence over

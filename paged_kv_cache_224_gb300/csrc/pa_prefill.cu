@@ -7,38 +7,6 @@ namespace pa {
 namespace {
 using namespace pf;
 
-template <typename T, int BS, int G>
-__global__ void __launch_bounds__(kThreads, 1)
-    prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
-    pdl_wait();  // the kernel before this one on the stream (the chunk's cache write) has finished
-    prefill_cta<T, BS, G>(p, tmk, tmv, tmq, (int)blockIdx.x, (int)gridDim.x);
-}
-
-template <typename T, int BS, int G>
-int launch_tc_t(const PrefillParams &p, unsigned grid, cudaStream_t stream) {
-    auto kern = prefill_tc_kernel<T, BS, G>;
-    static std::atomic<uint64_t> attr_done{0};
-    if (ensure_smem_attr(kern, kSmemAlloc, attr_done) != PA_OK) return PA_ERR_CUDA;
-    const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-    CUtensorMap tmk, tmv, tmq;
-    if (!make_pool_map(&tmk, p.k_cache, p, BS, bf16) || !make_pool_map(&tmv, p.v_cache, p, BS, bf16) ||
-        !make_query_map(&tmq, p, G, bf16))
-        return PA_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemAlloc;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    // programmatic dependent launch: scheduled while the cache write drains
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv, tmq) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-}
-
 template <typename T>
 int launch_tc_dtype(int block_size, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream) {
 #define PA_TC_CASE(BB, GG) \
@@ -63,7 +31,7 @@ size_t prefill_workspace_bytes(int num_seqs, long long total_chunk_len, int grou
 size_t prefill_counters_offset() { return prefill_ws(sm_count(), 1).cnt_off(); }
 
 int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const PrefillParams &p_in,
-                   void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+                   void *workspace, size_t workspace_bytes, cudaStream_t stream, bool two) {
     if (head_dim != kD) return PA_ERR_UNSUPPORTED;
     // TMA row coordinates are 32-bit
     if ((long long)p_in.num_blocks * p_in.num_kv_heads * block_size >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
@@ -103,6 +71,7 @@ int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const P
         p.split = 0;
         grid = (unsigned)units;
     }
+    if (two) return block_size == kExpandRows ? launch_prefill_two(dt, group, p, grid, stream) : PA_ERR_UNSUPPORTED;
     return dt == PA_BF16 ? launch_tc_dtype<__nv_bfloat16>(block_size, group, p, grid, stream)
                          : launch_tc_dtype<__half>(block_size, group, p, grid, stream);
 }

@@ -75,8 +75,8 @@
 //
 // kTwoP instances send each softmax weight to its product with V as two 16-bit
 // values, the rounded one and what the rounding left over (a second set of MMAs
-// on the same columns of O), where the others round it once.  A Q tile 1 without
-// rows gets no MMAs and no softmax there, so a unit of up to 128 rows has less
+// on the same columns of O), where the others round it once.  With kPrefix, a Q tile 1
+// without rows gets no MMAs and no softmax there, so a unit of up to 128 rows has less
 // for the tensor pipe than two whole Q tiles.  (Handing that tile the second
 // values instead, its rows a copy of tile 0's, took as long or longer: 32 to 35 us
 // against 32 where one value takes 28, 16 positions of 4 heads over 8191 tokens.)
@@ -372,7 +372,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
     static_assert(kNK % BS == 0 && BS % 8 == 0 && 32 % kBlocksPerTile == 0, "block_size");
     static_assert(kM % G == 0, "group");
     static_assert(kPrefix || !kWindow, "a window leaves partials");
-    static_assert(kPrefix || !kTwoP, "Q tile 1 may be left out of partials only");
+    constexpr bool kLeaveOut = kTwoP && kPrefix;  // (Q tile 1 may be left out of partials only)
 
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -537,7 +537,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     --sc;
                     continue;
                 }
-                const bool both = !kTwoP || second_tile<G>(p, sg);  // else nothing is issued for Q tile 1
+                const bool both = !kLeaveOut || second_tile<G>(p, sg);  // else nothing is issued for Q tile 1
                 if (lane == 0) wait_or_flag(q_full, (uint32_t)sc & 1u, p.d_err);
                 for (int k = 0; k <= nt; ++k) {
                     const int gt = tc + k;  // this CTA's tile count
@@ -695,7 +695,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     jn = kend / kNK;
                 }
                 // no last tile (and no register for it): this Q tile has no rows
-                if (kTwoP && g == kQT - 1 && !second_tile<G>(p, sg)) jn = -1;
+                if (kLeaveOut && g == kQT - 1 && !second_tile<G>(p, sg)) jn = -1;
             }
             if constexpr (kWindow) {
                 if (nt == 0) {
@@ -736,7 +736,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     // and on the segment's last tile, both QKs of it have read Q
                     if (k == nt - 1) mbar_arrive1(q_empty);
                 }
-                if constexpr (kTwoP) {
+                if constexpr (kLeaveOut) {
                     if (jn < 0) {
                         named_bar_arrive(kBarP + g, 160);
                         continue;
@@ -877,7 +877,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 const size_t out_row = (size_t)(q.row_start + rw.ipos) * p.num_heads + sg.h * G + rw.head;
                 T *orow = static_cast<T *>(p.out) + out_row * kD;
                 if constexpr (kPrefix) {
-                    if (!kTwoP || jn >= 0)
+                    if (!kLeaveOut || jn >= 0)
                         store_partial(p.part_o, p.part_ml, out_row * p.part_slots, rw.valid, tO, cta, sg.x_unit,
                                       p.total_tiles, ncta, m_run, l_run);
                 } else if (sg.t0 == 0 && sg.t1 == sg.n) {
@@ -985,6 +985,40 @@ inline int prefill_schedule(PrefillParams &p, int group, long long *units_out) {
     p.total_tiles = (int)tiles;
     *units_out = units;
     return PA_OK;
+}
+
+// ---- the chunked-prefill kernel ----------------------------------------------
+
+template <typename T, int BS, int G, bool kTwoP>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
+    pdl_wait();  // the kernel before this one on the stream (the chunk's cache write) has finished
+    prefill_cta<T, BS, G, false, false, false, kTwoP>(p, tmk, tmv, tmq, (int)blockIdx.x, (int)gridDim.x);
+}
+
+template <typename T, int BS, int G, bool kTwoP = false>
+inline int launch_tc_t(const PrefillParams &p, unsigned grid, cudaStream_t stream) {
+    auto kern = prefill_tc_kernel<T, BS, G, kTwoP>;
+    static std::atomic<uint64_t> attr_done{0};
+    if (ensure_smem_attr(kern, kSmemAlloc, attr_done) != PA_OK) return PA_ERR_CUDA;
+    const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    CUtensorMap tmk, tmv, tmq;
+    if (!make_pool_map(&tmk, p.k_cache, p, BS, bf16) || !make_pool_map(&tmv, p.v_cache, p, BS, bf16) ||
+        !make_query_map(&tmq, p, G, bf16))
+        return PA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemAlloc;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    // programmatic dependent launch: scheduled while the cache write drains
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv, tmq) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace pf
