@@ -13,8 +13,10 @@
 //   O^T[128][NO] += V^T[128][keys] . P^T    (V read in place, MN-major)
 // An 8-bit operand on the other side would leave a query or a weight 3 or 4 bits, so
 // each goes in as several rows of N, every one the rounded residual of those before
-// times a power of two: queries as three e4m3 rows (12 bits, what fp16 has and more
-// than bf16 has: scores are as exact as fp32 sums), weights as four e5m2 rows (12
+// times a power of two: queries as four e4m3 rows (16 bits, and for elements below the
+// head's largest 2^-32 of that: scores are as exact as fp32 sums unless the keys meet a
+// query's largest elements with next to nothing; with three rows an element of 10^4 beside
+// N(0, 0.02^2) took the small ones' scores off by 1%), weights as four e5m2 rows (12
 // bits; e5m2 for its range, so that what a key 2^-30 below the largest adds still
 // counts: a long context may hold very many of them).  N is padded to 16 by the
 // MMA anyway (32 for eight heads).

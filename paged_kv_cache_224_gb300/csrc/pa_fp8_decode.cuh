@@ -19,7 +19,8 @@ constexpr int kScaleRing = 8;            // tiles whose blocks' scales are held
 constexpr int kLens = 256;               // context lengths held from the first sequence on
 constexpr float kRescale = 8.0f;         // log2 units a maximum may lag behind
 constexpr float kLift = 7.0f;            // weights are 2^(z - M + kLift), at most 2^15
-constexpr int kQPieces = 3, kPPieces = 4;
+constexpr int kQPieces = 4, kPPieces = 4;
+constexpr float kQStep = 32.0f;          // from one piece of a query to the next
 
 // G heads of a kv head take GP rows a piece; N is the four pieces' rows.  At
 // head_dim 64 a 128-byte row of V holds two keys: O^T has the sums over the even
@@ -36,11 +37,9 @@ struct Lay {
     static constexpr int kCtas = ctas_per_sm(D, G);
     static constexpr int S = GP == 8 ? 5 * kPar : 6;        // ring slots: 80 KB, else 96 KB (48 KB at head_dim 64)
     static constexpr int kRowP = kKeys / kPar;              // bytes of a row of P^T: a tile's keys of one parity
-    // 2 x [3 GP rows][D]; the MMAs read N rows, the last GP of them whatever follows:
-    // columns that nobody reads
     static constexpr int kOffQ = S * kSlot;
-    static constexpr int kQ = (kQPieces * GP + 7) / 8 * 8 * D;
-    static constexpr int kOffP = kOffQ + 2 * kQ;            // 2 x [NO][kRowP]
+    static constexpr int kQ = N * D;
+    static constexpr int kOffP = kOffQ + 2 * kQ;            // 2 x [N][D], then 2 x [NO][kRowP]
     static constexpr int kP = NO * kRowP;
     static constexpr int kOffSc = kOffP + 2 * kP;           // [kScaleRing][16 blocks] of float4
     static constexpr int kOffBar = kOffSc + kScaleRing * 16 * 16;
@@ -580,8 +579,10 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
             int e1 = entry(1), e2 = entry(2);
             fetch(e0, kb, vb);
             // Q^T: each head over a power of two that brings its largest element to
-            // 128 .. 256, as three e4m3 pieces, each the residual of those before times
-            // 2^4: 12 bits, as many as fp16 has, and the products are exact
+            // 128 .. 256, as four e4m3 pieces, each the residual of those before times
+            // 2^5 (of up to 8, so up to 256): the last one's step is 2^-24.  fp16 elements
+            // are exact down to 2^-21 of the largest one's power of two, bf16 down to
+            // 2^-24, what is smaller to 2^-32 of it, and the products are exact
             const int qb = pieces & 1;
             if (pieces >= 2) {
                 if (lane == 0) await(&q_empty[qb], (uint32_t)((pieces >> 1) - 1) & 1u, p.d_err);
@@ -618,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                     for (int pc = 0; pc < kQPieces; ++pc) {
                         const unsigned lo = codes2(x[0], x[1]), hi2 = codes2(x[2], x[3]);
                         const float2 v0 = values2(lo), v1 = values2(hi2);
-                        x[0] = (x[0] - v0.x) * 16.f, x[1] = (x[1] - v0.y) * 16.f;
-                        x[2] = (x[2] - v1.x) * 16.f, x[3] = (x[3] - v1.y) * 16.f;
+                        x[0] = (x[0] - v0.x) * kQStep, x[1] = (x[1] - v0.y) * kQStep;
+                        x[2] = (x[2] - v1.x) * kQStep, x[3] = (x[3] - v1.y) * kQStep;
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + L::kOffQ + qb * L::kQ + swizzled<D>(pc * GP + h, d)),
                                      "r"(lo | hi2 << 16)
                                      : "memory");
@@ -702,14 +703,17 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                 {
                     float s0[16];
                     tmem_ld16(tmem + lane_off + b * N, s0);
+                    auto join = [](float a, float b, float c, float d) {
+                        return fmaf(fmaf(fmaf(d, 1 / kQStep, c), 1 / kQStep, b), 1 / kQStep, a);
+                    };
                     if constexpr (GP == 4) {
 #pragma unroll
-                        for (int h = 0; h < G; ++h) z[h] = fmaf(fmaf(s0[8 + h], 0.0625f, s0[4 + h]), 0.0625f, s0[h]);
+                        for (int h = 0; h < G; ++h) z[h] = join(s0[h], s0[4 + h], s0[8 + h], s0[12 + h]);
                     } else {
-                        float s1[8];
-                        tmem_ld8(tmem + lane_off + b * N + 16, s1);
+                        float s1[16];
+                        tmem_ld16(tmem + lane_off + b * N + 16, s1);
 #pragma unroll
-                        for (int h = 0; h < G; ++h) z[h] = fmaf(fmaf(s1[h], 0.0625f, s0[8 + h]), 0.0625f, s0[h]);
+                        for (int h = 0; h < G; ++h) z[h] = join(s0[h], s0[8 + h], s1[h], s1[8 + h]);
                     }
 #pragma unroll
                     for (int h = 0; h < G; ++h) z[h] = valid ? fmaf(z[h], sc.x * qf[h], sc.y) : -INFINITY;
