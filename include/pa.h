@@ -559,9 +559,10 @@ PA_API int pa_rotary_and_cache_fp8(void *query_out, int64_t query_out_stride, co
  * cached values as above, sums in fp32, the output rounded once to dtype.  On the
  * tensor cores for all shapes: scores are fp32 sums of exact products, of a query whose
  * elements are exact unless they are below 2^-21 (fp16) or 2^-24 (bf16) of their head's
- * largest one, and then off by up to 2^-32 of that one; a softmax weight enters the
- * weighted sum with 12 bits, down to 2^-33 of the largest.  A query with an infinity or
- * NaN gives NaN.
+ * largest one, and then off by up to 2^-32 of that one.  A softmax weight, times its
+ * block's value scale, enters the weighted sum off by up to 2^-12 of itself or 2^-37 of
+ * the largest such product, the greater of the two; into the sum of weights that divides
+ * it, in fp32.  A query with an infinity or NaN gives NaN.
  * Arguments, shapes and data errors as for pa_decode (invalid table entries are flagged
  * and the keys they would supply are left out), without partition_tokens: contexts are
  * cut where that shares the batch out evenly, so that a row's last bits depend on the

@@ -17,8 +17,8 @@
 // head's largest 2^-32 of that: scores are as exact as fp32 sums unless the keys meet a
 // query's largest elements with next to nothing; with three rows an element of 10^4 beside
 // N(0, 0.02^2) took the small ones' scores off by 1%), weights as four e5m2 rows (12
-// bits; e5m2 for its range, so that what a key 2^-30 below the largest adds still
-// counts: a long context may hold very many of them).  N is padded to 16 by the
+// bits down to 2^-25 of the largest weight, off by 2^-37 of that below; e5m2 for its
+// range: a long context may hold very many small weights, all rounded alike).  N is padded to 16 by the
 // MMA anyway (32 for eight heads).
 //
 // HBM-bound: every code is read once, and 128 keys of a kv head are 32 KB.  The call's
@@ -30,7 +30,7 @@
 //   warp 1    MMA issuer (one thread): QK^T of tile j into one of two S buffers, then
 //             O += P V of tile j-1;
 //   warps 2-5 softmax, one thread per key (= TMEM lane): scores, maxima over the tile,
-//             O rescaled only when a maximum has grown by 2^8, weights to shared memory;
+//             O rescaled only when a maximum has grown by 2^4, weights to shared memory;
 //             at a piece's end one thread per dimension writes the output or the partial;
 //   warp 6    the next piece's queries, and the scales of each tile's blocks up to eight
 //             tiles ahead.

@@ -17,8 +17,11 @@ constexpr int kKeys = 128;               // keys per tile (M of the QK^T MMA)
 constexpr int kThreads = 224;            // producer, MMA issuer, four softmax warps, scales
 constexpr int kScaleRing = 8;            // tiles whose blocks' scales are held
 constexpr int kLens = 256;               // context lengths held from the first sequence on
-constexpr float kRescale = 8.0f;         // log2 units a maximum may lag behind
-constexpr float kLift = 7.0f;            // weights are 2^(z - M + kLift), at most 2^15
+// A maximum may lag 2^kRescale behind and weights are 2^(z - M + kLift), at most 2^15.  The
+// last row of a weight ends at 2^-26, whatever the lift: a shorter lag is more bits for
+// small weights.  (Lags of 8 and 4 take the same time.)
+constexpr float kRescale = 4.0f;
+constexpr float kLift = 11.0f;
 constexpr int kQPieces = 4, kPPieces = 4;
 constexpr float kQStep = 32.0f;          // from one piece of a query to the next
 
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                     for (int h = 0; h < G; ++h) z[h] = valid ? fmaf(z[h], sc.x * qf[h], sc.y) : -INFINITY;
                 }
                 // The maxima that weights are relative to move only when some key is more
-                // than 2^8 above them (and at a piece's first keys): one barrier tells
+                // than 2^kRescale above them (and at a piece's first keys): one barrier tells
                 // every thread whether any has seen that.
                 bool over = false;
 #pragma unroll
@@ -766,7 +769,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                 if (j >= 2) await(&pv_done[b], (uint32_t)((g - 2) >> 1) & 1u, p.d_err);
                 {
                     // each weight as four e5m2 pieces, each the rounded residual of those
-                    // before times 2^3: 12 bits from 2^15 down, and never coarser than 2^-26
+                    // before times 2^3: off by 2^-12 of itself or 2^-26, the greater: 12
+                    // bits down to 2^-25 of a weight at the maximum, and 2^-37 of that below
                     const uint32_t pb = sb + L::kOffP + b * L::kP;
                     const int kp = t % L::kPar, at = t / L::kPar;  // the key's parity, and its place among that parity's
 #pragma unroll
