@@ -6,7 +6,9 @@
 //     z_j = s_j + ev_j,   o = sum_j 2^(z_j - M) * (codes of v_j),
 //     l = sum_j 2^(z_j - M) * 2^(-ev_j),   M the running maximum of z,
 // and out = o / l: the scales of the values only move exponents, and however far the
-// scales of two blocks are apart, the terms of o are as exact as their weights.
+// scales of two blocks are apart, the terms of o are as exact as their weights.  The
+// terms of l are 2^(s_j - M) in one step where 2^(z_j - M) would be too small for fp32
+// (scales from 2^-64 to 2^120 occur), and l is moved from one M to another in two halves.
 //
 // The codes go to the MMAs as they lie in memory, with keys as the M dimension:
 //   S^T[128 keys][N] = K[128 keys][D] . Q^T

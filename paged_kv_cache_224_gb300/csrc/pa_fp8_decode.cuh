@@ -22,6 +22,7 @@ constexpr int kLens = 256;               // context lengths held from the first 
 // small weights.  (Lags of 8 and 4 take the same time.)
 constexpr float kRescale = 4.0f;
 constexpr float kLift = 11.0f;
+constexpr float kLowest = -110.0f;       // log2 of the least weight for O; 2^-ev brings it up to 2^64 higher in l
 constexpr int kQPieces = 4, kPPieces = 4;
 constexpr float kQStep = 32.0f;          // from one piece of a query to the next
 
@@ -126,6 +127,13 @@ __device__ __forceinline__ unsigned e5m2x2(float a, float b) {
 __device__ __forceinline__ float2 from_e5m2x2(unsigned two) {
     const unsigned w = __byte_perm(two, 0u, 0x1404);
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// l 2^d for d <= 0 and a sum of weights l: scales of the values enter the maxima, so that
+// where they are far apart l may be as large as 2^d is small.
+__device__ __forceinline__ float moved(float l, float d) {
+    const float half = fast_exp2(0.5f * d);
+    return l * half * half;
 }
 
 // Reduce G values of every lane across the warp; lane l ends with the result for
@@ -314,14 +322,14 @@ __device__ __forceinline__ void merge_many(const DecodeParams &p, const Cut &c, 
         for (int i = lane; i < c.n; i += 32) {
             const float2 ml = __ldcg(&p.ws_ml[slot(i) + h]);
             const float top = fmaxf(M, ml.x);
-            l = fmaf(l, fast_exp2(M - top), fast_exp2(ml.x - top) * ml.y);
+            l = moved(l, M - top) + moved(ml.y, ml.x - top);
             M = top;
             weight[i * G + h] = ml.x;
         }
         float top = M;
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-        l *= fast_exp2(M - top);
+        l = moved(l, M - top);
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
         for (int i = lane; i < c.n; i += 32) weight[i * G + h] = fast_exp2(weight[i * G + h] - top);
@@ -388,7 +396,7 @@ __device__ __forceinline__ void merge_few(const DecodeParams &p, const Cut *cuts
 #pragma unroll
         for (int i = 0; i < kFew; ++i) {
             const float w = fast_exp2(ml[i].x - M);
-            l = fmaf(w, ml[i].y, l);
+            l += moved(ml[i].y, ml[i].x - M);
             o.x = fmaf(w, v[i].x, o.x), o.y = fmaf(w, v[i].y, o.y);
             o.z = fmaf(w, v[i].z, o.z), o.w = fmaf(w, v[i].w, o.w);
         }
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
 #pragma unroll
             for (int h = 0; h < G; ++h) {
                 qf[h] = qscale[qb * GP + h];
-                m_run[h] = -INFINITY;
+                m_run[h] = kEmptyMax;
                 l_part[h] = 0.f;
             }
             __syncwarp();
@@ -738,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                     for (int h = 0; h < G; ++h) {
                         const float tmax = fmaxf(fmaxf(xmax[h], xmax[GP + h]), fmaxf(xmax[2 * GP + h], xmax[3 * GP + h]));
                         const float nm = tmax > m_run[h] + kRescale ? tmax : m_run[h];
-                        alpha[h] = m_run[h] == -INFINITY ? 0.f : fast_exp2(m_run[h] - nm);
-                        l_part[h] *= alpha[h];
+                        alpha[h] = fast_exp2(m_run[h] - nm);
+                        l_part[h] = moved(l_part[h], m_run[h] - nm);
                         m_run[h] = nm;
                     }
                     if (j > 0) {
@@ -758,12 +766,24 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                     }
                 }
                 float pr[G + (G & 1)];
+                bool low = false;
                 if constexpr (G & 1) pr[G] = 0.f;
 #pragma unroll
                 for (int h = 0; h < G; ++h) {
-                    // (no NaN while every key so far is left out)
-                    pr[h] = z[h] == -INFINITY ? 0.f : fast_exp2(z[h] - m_run[h] + kLift);
+                    const float x = z[h] - m_run[h] + kLift;
+                    low |= x < kLowest;
+                    pr[h] = x < kLowest ? 0.f : fast_exp2(x);
                     l_part[h] = fmaf(pr[h], valid ? sc.z : 0.f, l_part[h]);
+                }
+                // A key whose values' scale is far below the largest one's may weigh
+                // nothing for O and count for l all the same: 2^(x - ev) in one step.
+                // (2^60, so that the smallest are not flushed to zero.)
+                if (low) {
+#pragma unroll
+                    for (int h = 0; h < G; ++h) {
+                        const float x = z[h] - m_run[h] + kLift;
+                        if (x < kLowest && z[h] > -INFINITY) l_part[h] = fmaf(fast_exp2(x - sc.y + 60.f), 0x1p-60f, l_part[h]);
+                    }
                 }
                 // P^T buffer b is free once the PV of tile j-2 completed
                 if (j >= 2) await(&pv_done[b], (uint32_t)((g - 2) >> 1) & 1u, p.d_err);
@@ -839,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, G>::kCtas)
                     } else {
                         const size_t at = (size_t)q.slot * G + h;
                         p.ws_acc[at * D + d] = v[h];
-                        if (d == h) p.ws_ml[at] = make_float2(m_run[h] == -INFINITY ? kEmptyMax : m_run[h], lsum);
+                        if (d == h) p.ws_ml[at] = make_float2(m_run[h], lsum);
                     }
                 }
             }
