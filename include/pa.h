@@ -627,7 +627,8 @@ PA_API int pa_copy_blocks_fp8(uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_sca
  * take (the Python binding): args[i] is argument i of the call's prototype, a pointer or
  * integer as a 64-bit integer, a float as a double.  A host array (pair_axis, prefix_lens,
  * chunk_lens) may lie behind the arguments: -k points k bytes into args.  Results and
- * errors are the call's; PA_ERR_INVALID_ARG for an unknown call or a null array.
+ * errors are the call's; PA_ERR_INVALID_ARG for an unknown call or a null array,
+ * PA_ERR_OUT_OF_RANGE for an int that does not fit 32 bits.
  */
 enum {
     PA_CALL_NORM_ROTARY_AND_CACHE = 0,

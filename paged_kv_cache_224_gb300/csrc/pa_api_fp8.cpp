@@ -369,7 +369,13 @@ int pa_copy_blocks_fp8(uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_scales, ui
 // One call with its arguments in an array, in the order of its prototype: pointers and
 // integers as 64-bit integers, floats as doubles, host arrays behind the arguments.
 int pa_call_packed(int call, const int64_t *a) {
-    if (!a) return PA_ERR_INVALID_ARG;
+    // the arguments that are ints (bit i: argument i), of each call
+    static constexpr uint32_t kInts[] = {0x07f1c000u, 0x1fc70000u, 0x00001f80u, 0x0002fe80u, 0x0002fc80u, 0x000003e0u};
+    if (!a || call < 0 || call > PA_CALL_COPY_BLOCKS_FP8) return PA_ERR_INVALID_ARG;
+    for (uint32_t left = kInts[call]; left; left &= left - 1) {
+        const int64_t v = a[__builtin_ctz(left)];
+        if (v != (int32_t)v) return PA_ERR_OUT_OF_RANGE;
+    }
     const auto I = [a](int k) { return (int)a[k]; };
     const auto F = [a](int k) {
         double d;
