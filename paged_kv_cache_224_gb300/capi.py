@@ -970,9 +970,16 @@ def pa_decode_fp8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables
                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _at(d_err), _raw_stream(dev, stream))
 
 
+def _int32s(lens):
+    a = np.asarray(lens)
+    b = np.ascontiguousarray(a, dtype=np.int32)
+    if a is not b and not np.array_equal(a, b):
+        raise ValueError("lengths must be whole numbers of 32 bits")
+    return b
+
+
 def _lens32(prefix_lens, chunk_lens):
-    pl = np.ascontiguousarray(prefix_lens, dtype=np.int32)
-    cl = np.ascontiguousarray(chunk_lens, dtype=np.int32)
+    pl, cl = _int32s(prefix_lens), _int32s(chunk_lens)
     if pl.ndim != 1 or pl.shape != cl.shape:
         raise ValueError("prefix_lens and chunk_lens must name the same sequences")
     return pl, cl
