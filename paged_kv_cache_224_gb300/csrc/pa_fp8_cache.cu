@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kStoreThreads, kPasses == 1 ? 4 : 2) store_fp8
                                     codes4(f[8], f[9], f[10], f[11]), codes4(f[12], f[13], f[14], f[15]));
                 }
             }
-            return __uint_as_float((unsigned)(127 - e) << 23);
+            return scale_of(min((unsigned)(127 - e), 255u));  // (2^-127 beside a scale of 2^127, NaN beside NaN)
         };
         // the codes of the units that are held
         auto put = [&](int which, int ch, float up) {
