@@ -495,8 +495,9 @@ PA_API int pa_decode_common_prefix(void *out, const void *query, const void *k_c
  * queries and keys head by head: before the rotation each head of query and key
  * becomes
  *   x[d] / sqrt(mean(x^2) + eps) * norm[d],   d < head_dim
- * in fp32 like the rotation, so that each result is rounded once.  Values pass
- * unchanged.
+ * in fp32 like the rotation, so that each result is rounded once.  That holds for heads
+ * whose root mean square is below 2^59, and above 2^-50 or eps above 2^-80: fp32 does not
+ * hold the squares of what bf16 has beyond.  Values pass unchanged.
  *   query_norm, key_norm  [head_dim] dtype (device), both required
  *   eps            finite, >= 0
  * Everything else as for pa_rotary_and_cache.

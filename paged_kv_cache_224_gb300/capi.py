@@ -866,8 +866,8 @@ def _rotary_args(count, dev, dt, query_out, query, key, value, NB, Hkv, bs, D, p
 def pa_norm_rotary_and_cache(query_out, query, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, query_norm,
                              key_norm, eps, pair_axis=None, interleaved=False, d_err=None, stream=None):
     """``pa_rotary_and_cache`` with an RMS norm of every query and key head before
-    the rotation: query_norm, key_norm [D] weights of the cache's dtype.  inv_freq
-    and positions may be None (norms alone)."""
+    the rotation: query_norm, key_norm [D] weights of the cache's dtype; squares are
+    summed in fp32.  inv_freq and positions may be None (norms alone)."""
     dev = _index(k_cache)
     _checked(dev, k_cache, v_cache, positions, slot_mapping, inv_freq, query_norm, key_norm, d_err)
     dt = k_cache.dtype
