@@ -591,10 +591,14 @@ PA_API int pa_decode_fp8(void *out, const void *query, const uint8_t *k_cache, c
 /*
  * pa_prefill_batch_fp8 -- pa_prefill_batch over an 8-bit cache: causal attention of
  * prompt chunks whose own keys and values are in the cache already.  The sequences'
- * cached values are laid out once in dtype (exact: every code times its scale is a
- * bf16 value, and an fp16 one as far as fp16 reaches) and attended as pa_prefill_batch
- * does, but with each softmax weight as two values of dtype (its rounded value and what
- * the rounding left), so that the output's is the only rounding that counts.
+ * cached values are laid out once in 16 bits and attended as pa_prefill_batch does, but
+ * with softmax weights of more bits than dtype has, so that the output's rounding is the
+ * only one that counts.
+ *   bf16  keys exact; values in fp16 over the greatest scale among each 128 keys of a
+ *         sequence's kv head: exact where a value's scale is not below 2^-22 of that one,
+ *         off by up to 2^-32 of it elsewhere; weights off by up to 2^-12 of themselves or
+ *         2^-32 of the largest, times scales
+ *   fp16  keys and values exact as far as fp16 reaches; weights as two fp16 values
  *   prefix_lens, chunk_lens  int [num_seqs], HOST memory
  *   workspace      >= pa_prefill_batch_fp8_workspace_bytes(...) bytes, 256-byte
  *                  aligned, required; its content on entry is ignored; not to be shared

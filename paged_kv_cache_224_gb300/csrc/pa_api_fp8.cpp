@@ -323,6 +323,11 @@ int pa_prefill_batch_fp8(void *out, const void *query, const uint8_t *k_cache, c
     p.num_kv_heads = num_kv_heads;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.query_rows = (int)rows;
+    p.v_scales = v_scales;
+    p.tables = block_tables;
+    p.table_stride = max_blocks_per_seq;
+    p.pool_blocks = num_blocks;
+    p.block_shift = __builtin_ctz(block_size);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int parts = block_size / pa::kExpandRows;
     int row = 0;
@@ -336,6 +341,7 @@ int pa_prefill_batch_fp8(void *out, const void *query, const uint8_t *k_cache, c
             q.prefix_len = prefix_lens[i];
             q.chunk_len = chunk_lens[i];
             q.row_start = row;
+            q.table_row = i;
         }
         row += chunk_lens[i];
         if (p.num_seqs == pa::kPrefillMaxSeqs || (i == num_seqs - 1 && p.num_seqs > 0)) {

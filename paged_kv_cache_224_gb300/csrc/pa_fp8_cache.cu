@@ -323,29 +323,57 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const __grid_constant__
         if (tid == 0 && !ok) flag_error(p.d_err, PA_DEVERR_BLOCK_RANGE);
     }
     if (!ok) return;
-    const int per_head = p.block_size * p.head_dim / 8, n = p.num_kv_heads * per_head;
-    const int per_part = kExpandRows * p.head_dim / 8;
+    // vectors of a head's block and of a part of it: powers of two, like block_size and head_dim
+    const int head_bits = __ffs(p.block_size * p.head_dim / 8) - 1, part_bits = __ffs(kExpandRows * p.head_dim / 8) - 1;
+    const int n = p.num_kv_heads << head_bits;
     const size_t src0 = (size_t)blk * n, dst0 = (size_t)at * n;
     const int i0 = blockIdx.y * (256 * kExpandVectors) + tid;
     uint2 u[kExpandVectors];
-    float scale[kExpandVectors];
 #pragma unroll
     for (int k = 0; k < kExpandVectors; ++k) {
         const int i = i0 + k * 256, j = i >= n ? i - n : i;
-        if (i >= 2 * n) continue;
-        u[k] = reinterpret_cast<const uint2 *>(i >= n ? p.v_cache : p.k_cache)[src0 + j];
-        scale[k] = scale_of((i >= n ? p.v_scales : p.k_scales)[(size_t)blk * p.num_kv_heads + j / per_head]);
+        if (i < 2 * n) u[k] = reinterpret_cast<const uint2 *>(i >= n ? p.v_cache : p.k_cache)[src0 + j];
+    }
+    // the greatest scales of the tile that this block is in, of the heads whose values these are
+    constexpr bool kOver = std::is_same<T, __nv_bfloat16>::value;
+    __shared__ int s_top[256 * kExpandVectors / 128 + 1];  // (a head has 128 vectors at least)
+    const int from = max((int)blockIdx.y * 256 * kExpandVectors - n, 0);
+    const int to = min((int)(blockIdx.y + 1) * 256 * kExpandVectors, 2 * n) - n;  // (none: <= 0)
+    const int head0 = from >> head_bits;
+    if (kOver && to > 0) {
+        const int heads = ((to - 1) >> head_bits) - head0 + 1, blocks = p.first[lo + 1] - p.first[lo];
+        const int per_tile = kExpandTile / p.block_size, b = ((at - p.first[lo]) & -per_tile) + (tid & 7);
+        // eight lanes a head, one of them a block of the tile
+        for (int h = tid >> 3; h - (tid >> 3) < heads; h += 32) {
+            unsigned byte = 0u;
+            if (h < heads && (tid & 7) < per_tile && b < blocks) {
+                const int blk2 = p.tables[lo][b];
+                if (blk2 >= 0 && blk2 < p.num_blocks) byte = p.v_scales[(size_t)blk2 * p.num_kv_heads + head0 + h];
+            }
+            if (byte == 255u) byte = 0u;
+#pragma unroll
+            for (int m = 4; m > 0; m >>= 1) byte = max(byte, __shfl_xor_sync(kFull, byte, m));
+            if (h < heads && (tid & 7) == 0) s_top[h] = (int)byte;
+        }
+        __syncthreads();
     }
 #pragma unroll
     for (int k = 0; k < kExpandVectors; ++k) {
         const int i = i0 + k * 256, j = i >= n ? i - n : i;
         if (i >= 2 * n) continue;
+        const bool is_v = i >= n;
+        const int head = j >> head_bits, rest = j & ((1 << head_bits) - 1);
+        const unsigned byte = (is_v ? p.v_scales : p.k_scales)[(size_t)blk * p.num_kv_heads + head];
+        float f = scale_of(byte);
+        if (kOver && is_v) {
+            // (exact down to 2^-22 of the greatest scale, nothing below 2^-41)
+            const int e = (int)byte - s_top[head - head0] + kValueLift + 127;
+            f = byte == 255u ? f : e > 0 ? scale_of((unsigned)e) : 0.f;
+        }
         const float2 a = values2(u[k].x & 0xffffu), b = values2(u[k].x >> 16), c = values2(u[k].y & 0xffffu), d = values2(u[k].y >> 16);
-        const float f = scale[k], x[8] = {a.x * f, a.y * f, b.x * f, b.y * f, c.x * f, c.y * f, d.x * f, d.y * f};
-        // vector j is `rest` of its head, in the head's part rest / per_part
-        const int head = j / per_head, rest = j - head * per_head, part = rest / per_part;
-        const int dst = (part * p.num_kv_heads + head) * per_part + (rest - part * per_part);
-        reinterpret_cast<uint4 *>(i >= n ? p.v_out : p.k_out)[dst0 + dst] = pack8<T>(x);
+        const float x[8] = {a.x * f, a.y * f, b.x * f, b.y * f, c.x * f, c.y * f, d.x * f, d.y * f};
+        const int dst = ((((rest >> part_bits) * p.num_kv_heads) + head) << part_bits) + (rest & ((1 << part_bits) - 1));
+        reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out)[dst0 + dst] = kOver && is_v ? pack8<__half>(x) : pack8<T>(x);
     }
 }
 

@@ -129,13 +129,6 @@ __device__ __forceinline__ float2 from_e5m2x2(unsigned two) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// l 2^d for d <= 0 and a sum of weights l: scales of the values enter the maxima, so that
-// where they are far apart l may be as large as 2^d is small.
-__device__ __forceinline__ float moved(float l, float d) {
-    const float half = fast_exp2(0.5f * d);
-    return l * half * half;
-}
-
 // Reduce G values of every lane across the warp; lane l ends with the result for
 // value l / (32 / G).
 template <bool kMax, int G>

@@ -88,6 +88,7 @@ struct PrefillSeq {
     int tiles_per_head;          // key tiles of all its row tiles for one kv head
     int tile_start;              // global index of its first key tile
     int unit_start;              // global index of its first unit
+    int table_row;               // 8-bit cache: row of `tables`
 };
 
 constexpr int kPrefillMaxSeqs = 64;  // sequences per launch (kernel-parameter table)
@@ -116,6 +117,11 @@ struct PrefillParams {
     int len_cap, row_base;
     float *scores;
     long long score_stride;
+    // V is an 8-bit cache's, over the greatest scale of a tile (kScaled): v_scales
+    // [pool_blocks][kv head], by the cache's own block tables, blocks of 2^block_shift rows
+    const uint8_t *v_scales;
+    const int32_t *tables;
+    int table_stride, pool_blocks, block_shift;
     PrefillSeq seqs[kPrefillMaxSeqs];
 };
 
@@ -228,12 +234,14 @@ namespace d8 {
 constexpr int ctas_per_sm(int head_dim, int group) { return head_dim == 64 && group <= 4 ? 3 : 2; }
 }  // namespace d8
 int launch_decode_fp8(pa_dtype dt, int head_dim, int group, const Fp8DecodeParams &p, cudaStream_t stream);
-// The codes of the sequences' first blocks as values of dt, laid end to end in blocks of
-// kExpandRows rows: with n = block_size / kExpandRows, block j of sequence i becomes
+// The sequences' first blocks as values of dt (V for bf16: in fp16, over 2^(E - kValueLift),
+// E the greatest exponent of a scale among a tile's kExpandTile keys), laid end to end in
+// blocks of kExpandRows rows: with n = block_size / kExpandRows, block j of sequence i becomes
 // blocks n (first[i] + j) to n (first[i] + j) + n - 1 of k_out and v_out, whose own table
 // is `table` (the number itself, or -1 where the sequence's entry is outside the pool,
 // which is flagged).  Also clears num_zero words at zero.
-constexpr int kExpandRows = 16;
+constexpr int kExpandRows = 16, kExpandTile = 128;
+constexpr int kValueLift = 7;  // brings the largest code, 448, to 57344, short of fp16's largest value
 struct Fp8ExpandParams {
     const uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
     void *k_out, *v_out;
@@ -283,11 +291,11 @@ size_t prefill_workspace_bytes(int num_seqs, long long total_chunk_len, int grou
 // Where its counters begin (the same on every call); they reach to its end.
 size_t prefill_counters_offset();
 // workspace may be NULL (or too small): each CTA then computes one whole unit.
-// two: softmax weights as two 16-bit values, for block_size kExpandRows.
+// fp8: over what launch_expand_fp8 laid out (block_size kExpandRows).
 int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const PrefillParams &p,
-                   void *workspace, size_t workspace_bytes, cudaStream_t stream, bool two = false);
+                   void *workspace, size_t workspace_bytes, cudaStream_t stream, bool fp8 = false);
 // (of launch_prefill: the launch itself)
-int launch_prefill_two(pa_dtype dt, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
+int launch_prefill_fp8(pa_dtype dt, int group, const PrefillParams &p, unsigned grid, cudaStream_t stream);
 // Attention of a batch over long shared prefixes (pa_decode_common_prefix):
 // `groups` groups of group_size consecutive sequences, each over the first
 // prefix_tokens tokens of its first sequence's table, and every sequence over

@@ -31,7 +31,7 @@ size_t prefill_workspace_bytes(int num_seqs, long long total_chunk_len, int grou
 size_t prefill_counters_offset() { return prefill_ws(sm_count(), 1).cnt_off(); }
 
 int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const PrefillParams &p_in,
-                   void *workspace, size_t workspace_bytes, cudaStream_t stream, bool two) {
+                   void *workspace, size_t workspace_bytes, cudaStream_t stream, bool fp8) {
     if (head_dim != kD) return PA_ERR_UNSUPPORTED;
     // TMA row coordinates are 32-bit
     if ((long long)p_in.num_blocks * p_in.num_kv_heads * block_size >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
@@ -71,7 +71,7 @@ int launch_prefill(pa_dtype dt, int head_dim, int block_size, int group, const P
         p.split = 0;
         grid = (unsigned)units;
     }
-    if (two) return block_size == kExpandRows ? launch_prefill_two(dt, group, p, grid, stream) : PA_ERR_UNSUPPORTED;
+    if (fp8) return block_size == kExpandRows ? launch_prefill_fp8(dt, group, p, grid, stream) : PA_ERR_UNSUPPORTED;
     return dt == PA_BF16 ? launch_tc_dtype<__nv_bfloat16>(block_size, group, p, grid, stream)
                          : launch_tc_dtype<__half>(block_size, group, p, grid, stream);
 }

@@ -80,13 +80,20 @@
 // for the tensor pipe than two whole Q tiles.  (Handing that tile the second
 // values instead, its rows a copy of tile 0's, took as long or longer: 32 to 35 us
 // against 32 where one value takes 28, 16 positions of 4 heads over 8191 tokens.)
+//
+// kScaled instances (bf16 models, pa_prefill_fp8.cu) have an 8-bit cache's values as V in
+// fp16, over 2^(E - 7), E the greatest exponent of a scale among the tile's 128 keys.
+// With z = s + E in log2 units
+//   o = sum 2^(z - M) * V,   l = sum 2^(z - M) * 2^(-E),   M the running maximum of z,
+// and out = 2^(-7) o / l, whatever the scales of different tiles are.  Weights are fp16 then,
+// lifted by 2^7 (M lags by up to 2^8): off by 2^-12 of themselves, or 2^-32 of the largest.
 #pragma once
 
 #include <cuda.h>
 
 #include <type_traits>
 
-#include "pa_device.cuh"
+#include "pa_fp8.cuh"
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
 
@@ -108,6 +115,9 @@ constexpr int kOffBar = kOffKV + kSlots * kKVTile;         // 224 KB
 constexpr int kSmemUsed = kOffBar + 256;
 constexpr int kSmemAlloc = kSmemUsed + 1024;               // room to align the base to 1 KB
 constexpr int kThreads = 64 + kQT * 128 + 32;
+// kScaled: weights are 2^(z - M + 7), at most 2^15; a tile's that are below kLeastSum
+// together, so that none is above 2^kLowSum, are added up apart
+constexpr float kWeightLift = 7.0f, kLeastSum = 0x1p-100f, kLowSum = -99.0f;
 // TMEM columns: S of each Q tile (128 fp32; P overwrites its first 64 columns
 // as 128 packed pairs), O of each Q tile (128 fp32)
 constexpr uint32_t kColS = 0, kColO = 256;
@@ -231,7 +241,9 @@ __device__ __forceinline__ int cta_of(int x, long long W, long long N) { return 
 //   * Otherwise it publishes (partial, fence, count); the segment whose count
 //     completes the unit merges, everything read from the workspace and the
 //     fold accumulated in its O columns.
-template <typename T>
+// (kWide: kScaled instances, whose sums of weights may be as large as a step from one
+// maximum to the next is small)
+template <typename T, bool kWide>
 __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, unsigned *counter, T *orow, bool valid,
                                             uint32_t tO, uint32_t tS, bool last_seg, int g, int t, int slot, int my_cta,
                                             int c_lo, int c_hi, int x_unit, long long W, long long N, float m_run,
@@ -278,7 +290,11 @@ __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, uns
         const float m_new = fmaxf(m_acc, ml.x);
         const float a = m_acc == -INFINITY ? 0.f : fast_exp2(m_acc - m_new);  // rescales what is accumulated
         const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m_new);
-        lsum = lsum * a + ml.y * w;
+        if constexpr (kWide) {
+            lsum = (m_acc == -INFINITY ? 0.f : moved(lsum, m_acc - m_new)) + (ml.x == -INFINITY ? 0.f : moved(ml.y, ml.x - m_new));
+        } else {
+            lsum = lsum * a + ml.y * w;
+        }
         m_acc = m_new;
 #pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
@@ -318,7 +334,7 @@ __device__ __noinline__ void finish_partial(float4 *part_o, float2 *part_ml, uns
         }
         tmem_wait_st();
     }
-    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    const float inv = lsum > 0.f ? (kWide ? 1.f / (1 << kValueLift) : 1.f) / lsum : 0.f;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float v[32];
@@ -364,7 +380,7 @@ static __device__ __noinline__ void store_partial(float *part_o, float2 *part_ml
 // Returns the CTA's TMEM base; with kKeepTmem (the one-launch step, whose
 // prefill CTAs go on to decode) the allocation is left for the caller to free.
 template <typename T, int BS, int G, bool kKeepTmem = false, bool kPrefix = false, bool kWindow = false,
-          bool kTwoP = false>
+          bool kTwoP = false, bool kScaled = false>
 __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CUtensorMap &tmk,
                                                 const CUtensorMap &tmv, const CUtensorMap &tmq, int cta, int ncta) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -372,6 +388,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
     static_assert(kNK % BS == 0 && BS % 8 == 0 && 32 % kBlocksPerTile == 0, "block_size");
     static_assert(kM % G == 0, "group");
     static_assert(kPrefix || !kWindow, "a window leaves partials");
+    static_assert(!kScaled || (BS == kExpandRows && !kPrefix && !kTwoP), "codes are laid out for prompt chunks");
     constexpr bool kLeaveOut = kTwoP && kPrefix;  // (Q tile 1 may be left out of partials only)
 
     extern __shared__ unsigned char smem_raw[];
@@ -520,7 +537,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
         // phase is long complete.
         {
             constexpr uint32_t idesc_qk = instr_desc(kBf16, false, false, kM, kNK);
-            constexpr uint32_t idesc_pv = instr_desc(kBf16, false, true, kM, kD);
+            constexpr uint32_t idesc_pv = instr_desc(kBf16 && !kScaled, false, true, kM, kD);
             constexpr uint32_t hi_q = desc_hi(1024);   // Q: 8-row groups 1 KB apart
             constexpr uint32_t hi_kv = desc_hi(2048);  // K, V: 8-key groups 2 KB apart
             // descriptor low words of Q tile 0 and of slot 0's K and V; the
@@ -669,6 +686,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             [[maybe_unused]] int adv;                       // kWindow: tiles of the schedule
             [[maybe_unused]] float *srow = nullptr;         // kWindow: this row's kept scores, or none
             [[maybe_unused]] const int32_t *wtable = nullptr;
+            [[maybe_unused]] int trow = 0, kvh = 0, last = 0;  // kScaled: row of the tables, kv head, the sequence's last key
             {
                 const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
                 const PrefillSeq &q = p.seqs[sg.si];
@@ -694,6 +712,11 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     kend = sg.longest - 1;
                     jn = kend / kNK;
                 }
+                if constexpr (kScaled) {
+                    trow = q.table_row;
+                    kvh = sg.h;
+                    last = q.prefix_len + q.chunk_len - 1;
+                }
                 // no last tile (and no register for it): this Q tile has no rows
                 if (kLeaveOut && g == kQT - 1 && !second_tile<G>(p, sg)) jn = -1;
             }
@@ -713,6 +736,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             }
 
             float m_run = -INFINITY;  // running max in scaled log2 units
+            [[maybe_unused]] float l_sum = 0.f, rest = 0.f;  // kScaled: row sum; a tile's, where that is rare
             float2 l2[4];             // row sum as four pairs of partial sums
 #pragma unroll
             for (int e = 0; e < 4; ++e) l2[e] = make_float2(0.f, 0.f);
@@ -723,6 +747,14 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     const int b = j * kBlocksPerTile + lane;
                     if (lane < kBlocksPerTile && b * BS <= kend) went = wtable[b];
                     else went = 0;
+                }
+                // kScaled: lane i has the scale of the tile's keys 16 i .. 16 i + 15, fetched
+                // behind the wait; 0 for none, and for NaN, which the values are themselves
+                [[maybe_unused]] unsigned byte = 0u;
+                if constexpr (kScaled) {
+                    const int key = j * kNK + (lane & 7) * kExpandRows;
+                    const int blk = key <= last ? p.tables[(size_t)trow * p.table_stride + (key >> p.block_shift)] : -1;
+                    if (blk >= 0 && blk < p.pool_blocks) byte = p.v_scales[(size_t)blk * p.num_kv_heads + kvh];
                 }
                 wait_or_flag(&s_full[g], (uint32_t)gt & 1u, p.d_err);
                 tc_fence_after();
@@ -742,6 +774,8 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                         continue;
                     }
                 }
+                [[maybe_unused]] int top_byte = 0;  // kScaled: E + 127
+                if constexpr (kScaled) top_byte = (int)__reduce_max_sync(kFull, byte == 255u ? 0u : byte);
                 // causal mask only on tiles that reach past some row's limit
                 const int kb = j * kNK;
                 const bool need_mask = kb + kNK - 1 > plim_min;
@@ -780,16 +814,33 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                     for (int e = 0; e < 8; ++e) mx8[e] = fmax3(mx8[e], s[c + e], s[c + 8 + e]);
                 }
                 float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-                mx *= csc;
+                mx = kScaled ? fmaf(mx, csc, (float)(top_byte - 127)) : mx * csc;
 
                 // Lazy rescale: the maximum moves only when it grew by more than
                 // 2^8.  The TMEM loads and stores of O are warp-collective, so the
                 // warp decides together: lanes whose maximum did not grow scale by 1.
                 const bool up = mx > m_run + 8.0f;
-                const bool any_up = __any_sync(kFull, up);
+                // kScaled, rare: a tile whose scales are so far below others' that its 2^(z - M)
+                // are too small for fp32.  They count for l all the same.
+                const bool low = kScaled && mx < m_run - kWeightLift + kLowSum && mx > -INFINITY;
+                bool any_up = __any_sync(kFull, up || low);
+                if constexpr (kScaled) {
+                    if (any_up) {
+                        any_up = __any_sync(kFull, up);
+                        // 2^(s - M) in one step, and 2^60 up, for the smallest of these
+                        if (__any_sync(kFull, low)) {
+                            rest = 0.f;
+#pragma unroll
+                            for (int c = 0; c < kNK; ++c) rest += fast_exp2(fmaf(s[c], csc, kWeightLift + 60.f - m_run));
+                            if (!low) rest = 0.f;  // (without a maximum yet it would be NaN)
+                        }
+                        __syncwarp();
+                    }
+                }
                 float alpha = 1.f;  // factor for what was accumulated against the old maximum
                 if (up) {
                     alpha = m_run == -INFINITY ? 0.f : fast_exp2(m_run - mx);
+                    if constexpr (kScaled) l_sum = m_run == -INFINITY ? 0.f : moved(l_sum, m_run - mx);
                     m_run = mx;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) l2[e] = __fmul2_rn(l2[e], make_float2(alpha, alpha));
@@ -803,7 +854,12 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 // a unit's last tiles that starts past the row's position) has
                 // no maximum yet: its weights are 2^-inf = 0.
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                const float2 csc2 = make_float2(csc, csc), negm2 = make_float2(-m_use, -m_use);
+                const float minus = kScaled ? (float)(top_byte - 127) + kWeightLift - m_use : -m_use;
+                const float2 csc2 = make_float2(csc, csc), negm2 = make_float2(minus, minus);
+                if constexpr (kScaled) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) l2[e] = make_float2(0.f, 0.f);  // (of this tile)
+                }
 #pragma unroll
                 for (int h = 0; h < kNK / 16; ++h) {
                     uint32_t pk[8];
@@ -814,7 +870,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                         const float2 a = __ffma2_rn(make_float2(s[kk], s[kk + 1]), csc2, negm2);
                         const float2 e2 = make_float2(fast_exp2(a.x), fast_exp2(a.y));
                         l2[c & 3] = __fadd2_rn(l2[c & 3], e2);
-                        pk[c] = Elem<T>::pack2(e2.x, e2.y);
+                        pk[c] = Elem<typename std::conditional<kScaled, __half, T>::type>::pack2(e2.x, e2.y);
                         if constexpr (kTwoP) {
                             // what the rounding left, rounded itself, goes over S's other
                             // 64 columns: together about twice the type's bits
@@ -858,6 +914,12 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                 tmem_wait_st();
                 tc_fence_before();
                 named_bar_arrive(kBarP + g, 160);
+                if constexpr (kScaled) {  // (while the tensor cores take P)
+                    const float w =
+                        ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) + ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
+                    l_sum = w < kLeastSum ? fmaf(rest, 0x1p-60f, l_sum) : fmaf(w, scale_of(254u - top_byte), l_sum);
+                    rest = 0.f;
+                }
             }
 
             // ---- end of the segment.  O (unnormalised) is complete in TMEM; it
@@ -869,7 +931,7 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
             int x_next = x + nt;
             if constexpr (kWindow) x_next = x + adv;
             const float l_run =
-                ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) + ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
+                kScaled ? l_sum : ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) + ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
             {
                 const Seg sg = seg_at<G, kPrefix, kWindow>(p, x, x1);
                 const PrefillSeq &q = p.seqs[sg.si];
@@ -882,13 +944,13 @@ __device__ __forceinline__ uint32_t prefill_cta(const PrefillParams &p, const CU
                                       p.total_tiles, ncta, m_run, l_run);
                 } else if (sg.t0 == 0 && sg.t1 == sg.n) {
                     // the whole unit: normalise, round once, store
-                    store_out(orow, l_run > 0.f ? 1.f / l_run : 0.f, rw.valid);
+                    store_out(orow, l_run > 0.f ? (kScaled ? 1.f / (1 << kValueLift) : 1.f) / l_run : 0.f, rw.valid);
                 } else {
                     // part of a unit: write the partial to this CTA's slot (0 for
                     // the first segment of its range, 1 for the last), count it,
                     // and if it is the unit's last to arrive, merge all of them
                     const long long Wt = p.total_tiles, Nc = ncta;
-                    finish_partial<T>(reinterpret_cast<float4 *>(p.part_o), p.part_ml, &p.counters[sg.unit * kQT + g],
+                    finish_partial<T, kScaled>(reinterpret_cast<float4 *>(p.part_o), p.part_ml, &p.counters[sg.unit * kQT + g],
                                       orow, rw.valid, tO, tS, x_next >= x1, g, t, 2 * cta + (sc == 0 ? 0 : 1),
                                       cta, cta_of(sg.x_unit, Wt, Nc), cta_of(sg.x_unit + sg.n - 1, Wt, Nc),
                                       sg.x_unit, Wt, Nc, m_run, l_run, merge_flag);
@@ -989,22 +1051,22 @@ inline int prefill_schedule(PrefillParams &p, int group, long long *units_out) {
 
 // ---- the chunked-prefill kernel ----------------------------------------------
 
-template <typename T, int BS, int G, bool kTwoP>
+template <typename T, int BS, int G, bool kTwoP, bool kScaled>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
     pdl_wait();  // the kernel before this one on the stream (the chunk's cache write) has finished
-    prefill_cta<T, BS, G, false, false, false, kTwoP>(p, tmk, tmv, tmq, (int)blockIdx.x, (int)gridDim.x);
+    prefill_cta<T, BS, G, false, false, false, kTwoP, kScaled>(p, tmk, tmv, tmq, (int)blockIdx.x, (int)gridDim.x);
 }
 
-template <typename T, int BS, int G, bool kTwoP = false>
+template <typename T, int BS, int G, bool kTwoP = false, bool kScaled = false>
 inline int launch_tc_t(const PrefillParams &p, unsigned grid, cudaStream_t stream) {
-    auto kern = prefill_tc_kernel<T, BS, G, kTwoP>;
+    auto kern = prefill_tc_kernel<T, BS, G, kTwoP, kScaled>;
     static std::atomic<uint64_t> attr_done{0};
     if (ensure_smem_attr(kern, kSmemAlloc, attr_done) != PA_OK) return PA_ERR_CUDA;
     const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     CUtensorMap tmk, tmv, tmq;
-    if (!make_pool_map(&tmk, p.k_cache, p, BS, bf16) || !make_pool_map(&tmv, p.v_cache, p, BS, bf16) ||
+    if (!make_pool_map(&tmk, p.k_cache, p, BS, bf16) || !make_pool_map(&tmv, p.v_cache, p, BS, bf16 && !kScaled) ||
         !make_query_map(&tmq, p, G, bf16))
         return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
