@@ -72,8 +72,8 @@ def load_traffic(kernel_key: str, sources):
 # headers it includes), for the traffic entries' hashes.
 DECODE_SOURCES = ["pa_decode.cuh", "pa_device.cuh"]
 DECODE_TC_SOURCES = ["pa_decode_tc.cuh", "pa_decode_tc.cu", "pa_tcgen05.cuh", "pa_device.cuh"]
-PREFILL_SOURCES = ["pa_prefill.cu", "pa_prefill.cuh", "pa_tcgen05.cuh", "pa_device.cuh"]
-MIXED_SOURCES = ["pa_mixed.cuh", "pa_mixed_bf16.cu", "pa_prefill.cuh", "pa_decode_tc.cuh", "pa_tcgen05.cuh",
+PREFILL_SOURCES = ["pa_prefill.cu", "pa_prefill.cuh", "pa_fp8.cuh", "pa_tcgen05.cuh", "pa_device.cuh"]
+MIXED_SOURCES = ["pa_mixed.cuh", "pa_mixed_bf16.cu", "pa_prefill.cuh", "pa_fp8.cuh", "pa_decode_tc.cuh", "pa_tcgen05.cuh",
                  "pa_device.cuh"]
 
 

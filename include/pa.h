@@ -539,6 +539,10 @@ PA_API int pa_norm_rotary_and_cache(void *query_out, int64_t query_out_stride, c
  *                  pa_norm_rotary_and_cache, or both norms NULL for none
  * Supported: head_dim a multiple of 16 up to 256, block_size in {8, 16, 32, 64, 128}, up
  * to 65535 kv heads.  num_tokens == 0 is a no-op.
+ * To find a block's tokens the slots of the whole call are looked through once a block (and
+ * once more for every eight kv heads, and for a token behind padding or behind one of
+ * another block): next to nothing up to some 8192 tokens, but it grows with their square.
+ * Longer prompts are written faster in several calls.
  * Reading.  The attention calls take scales from 2^-64 (byte 63) on, which is what the
  * writing calls leave; caches filled in another way keep to that too.
  */
@@ -575,7 +579,10 @@ PA_API int pa_rotary_and_cache_fp8(void *query_out, int64_t query_out_stride, co
  *                  later call whose sizes it covers (after a call that set
  *                  PA_DEVERR_TIMEOUT, or whose context_lens were written while it
  *                  ran, zero-fill it again).  Not to be shared with work
- *                  that overlaps the call on the device
+ *                  that overlaps the call on the device, nor, without zero-filling
+ *                  those 4 KB again, with other calls between two of these: counters
+ *                  that another call left anything in are not noticed, and contexts
+ *                  that were cut stay unwritten
  * max_blocks_per_seq * block_size, num_seqs * num_heads and num_blocks * num_kv_heads *
  * block_size must stay below 2^31 - 256.
  */

@@ -938,7 +938,8 @@ def pa_decode_fp8_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, b
 
 def decode_fp8_workspace(query, num_kv_heads, block_size, max_context_len, stream=None):
     """A zero-filled workspace big enough for ``pa_decode_fp8`` (zero-filled once, on
-    ``stream`` or the current one; the calls keep it usable)."""
+    ``stream`` or the current one; the calls keep it usable, as long as nothing else
+    writes its first 4 KB in between)."""
     B, Hq, D = query.shape
     with torch.cuda.device(query.device):
         n = pa_decode_fp8_workspace_bytes(B, Hq, num_kv_heads, D, block_size, max_context_len)

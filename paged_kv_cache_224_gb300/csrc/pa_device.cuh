@@ -203,13 +203,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-// l 2^d for d <= 0 and a sum of weights l, in two halves: where scales of the values enter
-// the maxima and are far apart, l may be as large as 2^d is small.
-__device__ __forceinline__ float moved(float l, float d) {
-    const float half = fast_exp2(0.5f * d);
-    return l * half * half;
-}
-
 // The G scores that are kept of one key.
 template <int G>
 __device__ __forceinline__ void load_scores(const float *a, float (&x)[G]) {

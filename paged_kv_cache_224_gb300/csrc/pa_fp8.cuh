@@ -74,4 +74,11 @@ __device__ __forceinline__ void values16(const uint4 &u, float (&f)[16]) {
     }
 }
 
+// l 2^d for d <= 0 and a sum of weights l, in two halves: where scales of the values enter
+// the maxima and are far apart, l may be as large as 2^d is small.
+__device__ __forceinline__ float moved(float l, float d) {
+    const float half = fast_exp2(0.5f * d);
+    return l * half * half;
+}
+
 }  // namespace pa

@@ -21,7 +21,11 @@
 // took 108 and 51 us; a CTA per token, of which most had nothing to do, 114 and 38; a warp
 // for keys and one for values, four heads to a CTA, 74 and 24; the rows computed before
 // the slots are looked through 80 and 33 (every later run of a block does so in vain); two
-// warps to a head's keys 81 and 28.  Looking through the slots costs 3 us of the 64.5.
+// warps to a head's keys 81 and 28.  Looking through the slots costs 3 us of the 64.5, and
+// grows with the square of the tokens: without rotation, 8 kv heads of 128, blocks of 16,
+// bf16, 8192 tokens 15.2 us, 32768 84, 131072 648 (floors 7.4, 29.6, 118.5); with 40 kv heads
+// 74, 380, 3193; blocks of 8 half as much again to twice; every fourth token padding 26, 178,
+// 1894.  8192 tokens in blocks of their own 151 (1 kv head 160: a single warp looks).
 #include <algorithm>
 #include <type_traits>
 
@@ -413,11 +417,16 @@ int launch_store_fp8(pa_dtype dt, const RotaryParams &p, cudaStream_t stream) {
         if (rc != PA_OK) return rc;
     }
     const bool beside = p.num_heads > 0;
-    // One token to a CTA while that gives no more than four CTAs to an SM (a step of
-    // single tokens), up to 16 beyond (a prompt, where one of 16 begins a block).  With one
-    // token the variant that holds one row a lane, of half the registers, leaves room for
-    // all CTAs at once: a step of 256 tokens 8 us, with four rows a lane 14; a prompt with
-    // it reads its rows twice.
+    // One token to a CTA while that gives no more than four CTAs to an SM, up to 16 beyond
+    // (a prompt, where one of 16 begins a block).  With one token, the variant that holds one
+    // row a lane, of half the registers, leaves room for all CTAs at once: right for a step
+    // of single tokens; a block's rows it reads twice, in chunks.  Both sides (the host does
+    // not see the slots), bf16, heads of 128, replayed, us, one row / four rows a lane:
+    //                                        step        run of one sequence
+    //   without rotation, 256 tokens, 2 kv   4.2 / 5.4     9.0 / 5.7
+    //                     256         8      4.5 / 5.5    10.9 / 7.1
+    //                     600         8      6.2 / 9.9    13.8 / 7.5
+    //   norms, rotation,  256         8      8.8 / 9.9    16.7 / 11.0
     RotaryParams q = p;
     const long long all = (long long)p.num_tokens * ((p.num_kv_heads + kHeadsPerCta - 1) / kHeadsPerCta);
     q.tokens_per_cta = (int)std::min(16LL, std::max(1LL, all / (2LL * sm_count())));

@@ -39,8 +39,8 @@
 // At head_dim 64, where a tile is 16 KB, three CTAs to an SM (two with eight heads).
 //
 // Measured (bf16, us, share of the copy rate): 256 contexts of up to 4096 tokens, 32/8
-// heads of 128, 176, 94%; eight of 32768 to 131072, 64/8 heads, 207, 98%; 256 of 2048, 32/8
-// heads of 64, 91.5, 86%, 64/8 heads of 64, 131, 60% (bound by the softmax warps).  On the
+// heads of 128, 177, 94%; eight of 32768 to 131072, 64/8 heads, 209, 97%; 256 of 2048, 32/8
+// heads of 64, 91.5, 86%, 64/8 heads of 64, 132, 60% (bound by the softmax warps).  On the
 // way (the first two cases): on the CUDA cores 1088 and 2367; one unit (sequence, kv head,
 // 1024 tokens) a CTA 203 and 228; equal shares 196 and 216.  What runs once a piece was
 // kept small after 256 contexts of 2048 tokens with 64/8 heads had taken 234, not 168: the
