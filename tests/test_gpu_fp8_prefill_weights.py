@@ -5,10 +5,10 @@ outputs stay within one rounding of the exact ones.
 Tolerance, by arithmetic.  u = half a step of the type, relative.  In f16 a weight P goes in
 as hi + lo, hi = rn(P), lo = rn(P - hi): off by p = u^2, relative, or by 2^-25 where lo is
 below f16's normal range (the sum of the weights is 1 at least).  In bf16 it goes in as one
-f16 value, the cached values in f16 too: off by p = 2^-12, u / 16, or 2^-32.  A score is off by D 2^-23 A, A the
-largest scaled sum of |q_i k_i| (the tensor cores may truncate), a weight by twice that
-relatively, plus 2^-19 for the exponentials, sums and division, plus 2^-23 a key for the
-product with V.  With W = sum w |v|:
+f16 value, the cached values in f16 too: off by p = 2^-12, u / 16, or 2^-32.  A score is off
+by D 2^-23 A, A the largest scaled sum of |q_i k_i| (the tensor cores may truncate), a weight
+by twice that relatively, plus 2^-19 for the exponentials, sums and division, plus 2^-23 a
+key for the product with V.  With W = sum w |v|:
   delta = W (p + 4 D 2^-23 A + 2^-19 + n 2^-22) + n 2^-25 max |v|,
 and the result is rounded once: |got - ref| <= delta + u (|ref| + delta).  Queries are
 small, so that A is: one 16-bit value for a weight would be off by u W / 2, above that."""
